@@ -8,7 +8,9 @@ gfx950, the calls raise.
 
 The functions carry the C names: `blr_expand_signs`, `blr_forward`,
 `blr_forward_noalloc`, `blr_backward`, `blr_backward_signs`, `blr_plane_linear`, `blr_sumsq`, `blr_workspace_bytes`,
-plus the profiling calls; `all_finite` and `next_gscale` are the host side
+the token routing (`blr_route_sort`, `blr_route_gather`, `blr_route_combine`, `blr_route_combine_backward`) and the
+low-rank adapters beside a layer (`blr_adapters_forward`, `blr_adapters_backward`), plus the profiling calls;
+`all_finite` and `next_gscale` are the host side
 of the finite check and the power-of-two loss scale.
 """
 from __future__ import annotations
@@ -64,6 +66,23 @@ def load():
     lib.blr_plane_linear.restype = i32
     lib.blr_sumsq.argtypes = [p, i64, p, i32, p]
     lib.blr_sumsq.restype = i32
+    lib.blr_route_workspace_bytes.argtypes = [i64, i64]
+    lib.blr_route_workspace_bytes.restype = sz
+    lib.blr_route_sort.argtypes = [i64, i64, p, p, p, p, p, sz, p]
+    lib.blr_route_sort.restype = i32
+    lib.blr_route_gather.argtypes = [i64, i64, i64, i64, i32, p, p, p, p, p]
+    lib.blr_route_gather.restype = i32
+    lib.blr_route_combine.argtypes = [i64, i64, i64, i64, i32, p, p, p, p, p, i32, p]
+    lib.blr_route_combine.restype = i32
+    lib.blr_route_combine_backward.argtypes = [i64, i64, i64, i64, i32, p, p, p, p, p, p, p, p]
+    lib.blr_route_combine_backward.restype = i32
+    lib.blr_adapters_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+    lib.blr_adapters_workspace_bytes.restype = sz
+    lib.blr_adapters_forward.argtypes = [i64, i64, i64, i64, i64, i32, i32, p, p, p, p, p, p, p, i32, p, p, sz, p]
+    lib.blr_adapters_forward.restype = i32
+    lib.blr_adapters_backward.argtypes = [i64, i64, i64, i64, i64, i32, i32, p, p, p, p, p, p, p, p, p, p, i32, p, i32,
+                                          p, sz, p]
+    lib.blr_adapters_backward.restype = i32
     lib.blr_profile_enable.argtypes = [i32]
     lib.blr_profile_enable.restype = i32
     lib.blr_profile_read.argtypes = [ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(i64),
@@ -368,6 +387,268 @@ def blr_plane_linear(x, plane, scale: float = 1.0, *, y=None, stream=None):
     return y
 
 
+def _wide():
+    """The element types of rows and adapters; their places are their numbers
+    in the C ABI."""
+    import torch
+    return (torch.float32, torch.float16, torch.bfloat16)
+
+
+def _apart(outputs, others):
+    """No output shares memory with another argument."""
+    spans = [(n, t.data_ptr(), t.numel() * t.element_size()) for n, t in others if t is not None]
+    for n, t in outputs:
+        if t is None:
+            continue
+        at, size = t.data_ptr(), t.numel() * t.element_size()
+        for m, b, bs in spans:
+            if at < b + bs and b < at + size:
+                raise ValueError(f"{n} shares memory with {m}")
+        spans.append((n, at, size))
+
+
+def _launch(name, dev, stream, *args):
+    """The C call `name` on the tensors' own device, on its current stream
+    unless one is given."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    handle = ctypes.c_void_p(stream.cuda_stream)
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, handle), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, handle), name)
+
+
+def _same_device(dev, tensors):
+    for n, t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{n} is on {t.device}, expected {dev}")
+
+
+def workspace_route(pairs: int, experts: int, device=None):
+    import torch
+    n = int(load().blr_route_workspace_bytes(pairs, experts))
+    if n == 0:
+        raise BlrError(-2, "blr_route_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def blr_route_sort(ids, experts: int, *, offsets=None, order=None, slot=None, ws=None, stream=None):
+    """Sort the pairs of ids [T] or [T][k] (int32) by expert; an id outside
+    [0, experts) means none. Returns (offsets [experts + 1], order [T k], slot
+    in the shape of ids): the plan that the gather, the combine and the
+    adapters take."""
+    import torch
+    i32 = (torch.int32,)
+    _need(ids, "ids", i32)
+    if ids.dim() not in (1, 2):
+        raise ValueError(f"ids has shape {tuple(ids.shape)}, expected [T] or [T][k]")
+    dev, n = ids.device, ids.numel()
+    new = lambda shape: torch.empty(shape, dtype=torch.int32, device=dev)  # noqa: E731
+    offsets = new(experts + 1) if offsets is None else _need(offsets, "offsets", i32, (experts + 1,))
+    order = new(n) if order is None else _need(order, "order", i32, (n,))
+    slot = new(ids.shape) if slot is None else _need(slot, "slot", i32, ids.shape)
+    ws = workspace_route(n, experts, dev) if ws is None else _need(ws, "ws", (torch.uint8,))
+    out = [("offsets", offsets), ("order", order), ("slot", slot), ("ws", ws)]
+    _same_device(dev, out)
+    _apart(out, [("ids", ids)])
+    _launch("blr_route_sort", dev, stream, n, experts, _ptr(ids), _ptr(offsets), _ptr(order), _ptr(slot), _ptr(ws),
+            ws.numel())
+    return offsets, order, slot
+
+
+def _route_shapes(offsets, slot):
+    import torch
+    _need(offsets, "offsets", (torch.int32,))
+    _need(slot, "slot", (torch.int32,))
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError(f"offsets has shape {tuple(offsets.shape)}, expected [experts + 1]")
+    if slot.dim() not in (1, 2):
+        raise ValueError(f"slot has shape {tuple(slot.shape)}, expected [T] or [T][k]")
+    return slot.shape[0], (slot.shape[1] if slot.dim() == 2 else 1), offsets.numel() - 1
+
+
+def _rows(t, name, n):
+    """Width of t, rows [n][d] of one of the wide types."""
+    _need(t, name, _wide())
+    if t.dim() != 2 or t.shape[0] != n:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({n}, d)")
+    return t.shape[1]
+
+
+def blr_route_gather(x, offsets, slot, *, rows=None, stream=None):
+    """Rows by expert: rows[slot[t][j]] = x[t], zero where the pair is not
+    placed. Returns rows [T k][d]. Its gradient is blr_route_combine without
+    weights."""
+    import torch
+    T, k, E = _route_shapes(offsets, slot)
+    d = _rows(x, "x", T)
+    rows = torch.empty((T * k, d), dtype=x.dtype, device=x.device) if rows is None else \
+        _need(rows, "rows", (x.dtype,), (T * k, d))
+    ins = [("x", x), ("offsets", offsets), ("slot", slot)]
+    _same_device(x.device, ins + [("rows", rows)])
+    _apart([("rows", rows)], ins)
+    _launch("blr_route_gather", x.device, stream, T, k, E, d, _wide().index(x.dtype), _ptr(x), _ptr(offsets), _ptr(slot), _ptr(rows))
+    return rows
+
+
+def blr_route_combine(z, offsets, slot, weights=None, *, y=None, accumulate_y=False, stream=None):
+    """Experts' rows back into tokens: y[t] (+)= sum_j w[t][j] z[slot[t][j]]
+    over the placed pairs; weights [T][k] f32, or None for ones. y is
+    overwritten unless accumulate_y. Returns y [T][d]."""
+    import torch
+    T, k, E = _route_shapes(offsets, slot)
+    d = _rows(z, "z", T * k)
+    if weights is not None:
+        _need(weights, "weights", (torch.float32,), slot.shape)
+    if y is None and accumulate_y:
+        raise ValueError("accumulate_y needs y")
+    y = torch.empty((T, d), dtype=z.dtype, device=z.device) if y is None else _need(y, "y", (z.dtype,), (T, d))
+    ins = [("z", z), ("offsets", offsets), ("slot", slot), ("weights", weights)]
+    _same_device(z.device, ins + [("y", y)])
+    _apart([("y", y)], ins)
+    _launch("blr_route_combine", z.device, stream, T, k, E, d, _wide().index(z.dtype), _ptr(z), _ptr(offsets), _ptr(slot),
+            _ptr(weights), _ptr(y), int(bool(accumulate_y)))
+    return y
+
+
+def blr_route_combine_backward(dy, z, offsets, slot, weights=None, *, dz=None, dw=None, stream=None):
+    """Gradient of blr_route_combine: dz[slot[t][j]] = w[t][j] dy[t] and, with
+    weights, dw[t][j] = dy[t] . z[slot[t][j]], both zero where the pair is not
+    placed. Returns (dz [T k][d], dw [T][k]), dw None without weights (z may
+    then be None)."""
+    import torch
+    T, k, E = _route_shapes(offsets, slot)
+    d = _rows(dy, "dy", T)
+    if weights is not None:
+        _need(weights, "weights", (torch.float32,), slot.shape)
+        dw = torch.empty(slot.shape, dtype=torch.float32, device=dy.device) if dw is None else \
+            _need(dw, "dw", (torch.float32,), slot.shape)
+    elif dw is not None:
+        raise ValueError("dw needs weights")
+    if z is not None or dw is not None:
+        _need(z, "z", (dy.dtype,), (T * k, d))
+    dz = torch.empty((T * k, d), dtype=dy.dtype, device=dy.device) if dz is None else \
+        _need(dz, "dz", (dy.dtype,), (T * k, d))
+    ins = [("dy", dy), ("z", z), ("offsets", offsets), ("slot", slot), ("weights", weights)]
+    out = [("dz", dz), ("dw", dw)]
+    _same_device(dy.device, ins + out)
+    _apart(out, ins)
+    _launch("blr_route_combine_backward", dy.device, stream, T, k, E, d, _wide().index(dy.dtype),
+            _ptr(dy), _ptr(z), _ptr(offsets), _ptr(slot), _ptr(weights), _ptr(dz), _ptr(dw))
+    return dz, dw
+
+
+def workspace_adapters(M: int, d_in: int, d_out: int, r: int, adapters: int, device=None):
+    import torch
+    n = int(load().blr_adapters_workspace_bytes(M, d_in, d_out, r, adapters))
+    if n == 0:
+        raise BlrError(-2, "blr_adapters_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _adapters_shapes(first, name, down, up, offsets, order, scale):
+    """Checks what both adapter calls share; `first` is x or dy. Returns
+    (M, d_in, d_out, r, E, act, wt)."""
+    import torch
+    wide = _wide()
+    _need(first, name, wide)
+    _need(down, "down", wide)
+    _need(up, "up", (down.dtype,))
+    if first.dim() != 2 or down.dim() != 3 or up.dim() != 3:
+        raise ValueError(f"{name}, down and up are [M][d], [E][r][d_in] and [E][d_out][r]")
+    E, r, d_in = down.shape
+    d_out = up.shape[1]
+    _need(up, "up", (down.dtype,), (E, d_out, r))
+    M = first.shape[0]
+    _need(offsets, "offsets", (torch.int32,), (E + 1,))
+    if order is not None:
+        _need(order, "order", (torch.int32,), (M,))
+    if scale is not None:
+        _need(scale, "scale", (torch.float32,), (E,))
+    return M, d_in, d_out, r, E, wide.index(first.dtype), wide.index(down.dtype)
+
+
+def blr_adapters_forward(x, down, up, offsets, order=None, scale=None, *, y=None, accumulate_y=False, tape_s=None,
+                         keep_tape=False, ws=None, stream=None):
+    """Low-rank adapters of many requests at once: y[t] (+)= scale_e (x[t]
+    down[e]^T) up[e]^T for each row t with adapter e. x [M][d_in]; down
+    [E][r][d_in]; up [E][d_out][r]; (offsets, order) of
+    blr_route_sort(adapter of each row, E), order None when the rows lie by
+    adapter already. Beside a shared projection give its result as y with
+    accumulate_y. The tape x down[e]^T [M][r], which the backward reads, is
+    kept when tape_s is given or keep_tape is set. Returns (y, tape_s)."""
+    import torch
+    M, d_in, d_out, r, E, act, wt = _adapters_shapes(x, "x", down, up, offsets, order, scale)
+    _need(x, "x", (x.dtype,), (M, d_in))
+    dev = x.device
+    if y is None and accumulate_y:
+        raise ValueError("accumulate_y needs y")
+    y = torch.empty((M, d_out), dtype=x.dtype, device=dev) if y is None else _need(y, "y", (x.dtype,), (M, d_out))
+    if tape_s is not None:
+        _need(tape_s, "tape_s", (torch.float32,), (M, r))
+    elif keep_tape:
+        tape_s = torch.empty((M, r), dtype=torch.float32, device=dev)
+    ws = workspace_adapters(M, d_in, d_out, r, E, dev) if ws is None else _need(ws, "ws", (torch.uint8,))
+    ins = [("x", x), ("down", down), ("up", up), ("offsets", offsets), ("order", order), ("scale", scale)]
+    out = [("y", y), ("tape_s", tape_s), ("ws", ws)]
+    _same_device(dev, ins + out)
+    _apart(out, ins)
+    _launch("blr_adapters_forward", dev, stream, M, d_in, d_out, r, E, act, wt, _ptr(x), _ptr(down), _ptr(up),
+            _ptr(offsets), _ptr(order), _ptr(scale), _ptr(y), int(bool(accumulate_y)), _ptr(tape_s), _ptr(ws),
+            ws.numel())
+    return y, tape_s
+
+
+def blr_adapters_backward(x, dy, down, up, offsets, order=None, scale=None, tape_s=None, *, grad_down=None,
+                          grad_up=None, accumulate_grads=False, grads=True, dx=None, accumulate_dx=False,
+                          need_dx=True, ws=None, stream=None):
+    """Backward of blr_adapters_forward: dx, and the f32 gradients grad_down
+    [E][r][d_in] and grad_up [E][d_out][r] of every adapter (zero for one
+    without rows). grads=False forms dx alone (x and tape_s may then be None),
+    need_dx=False the gradients alone. Outputs not given are allocated;
+    overwritten unless accumulate_grads / accumulate_dx. Returns (grad_down,
+    grad_up, dx), None for what was not formed."""
+    import torch
+    M, d_in, d_out, r, E, act, wt = _adapters_shapes(dy, "dy", down, up, offsets, order, scale)
+    f32 = (torch.float32,)
+    _need(dy, "dy", (dy.dtype,), (M, d_out))
+    dev = dy.device
+    if x is not None or grads:
+        _need(x, "x", (dy.dtype,), (M, d_in))
+    if tape_s is not None or grads:
+        _need(tape_s, "tape_s", f32, (M, r))
+    if (accumulate_grads and (grad_down is None or grad_up is None)) or (accumulate_dx and dx is None):
+        raise ValueError("what is accumulated into has to be given")
+    if grads:
+        grad_down = torch.empty((E, r, d_in), dtype=torch.float32, device=dev) if grad_down is None else \
+            _need(grad_down, "grad_down", f32, (E, r, d_in))
+        grad_up = torch.empty((E, d_out, r), dtype=torch.float32, device=dev) if grad_up is None else \
+            _need(grad_up, "grad_up", f32, (E, d_out, r))
+    elif grad_down is not None or grad_up is not None:
+        raise ValueError("grad_down and grad_up are given, but grads is False")
+    if need_dx:
+        dx = torch.empty((M, d_in), dtype=dy.dtype, device=dev) if dx is None else \
+            _need(dx, "dx", (dy.dtype,), (M, d_in))
+    elif dx is not None:
+        raise ValueError("dx is given, but need_dx is False")
+    ws = workspace_adapters(M, d_in, d_out, r, E, dev) if ws is None else _need(ws, "ws", (torch.uint8,))
+    ins = [("x", x), ("dy", dy), ("down", down), ("up", up), ("offsets", offsets), ("order", order),
+           ("scale", scale), ("tape_s", tape_s)]
+    out = [("grad_down", grad_down), ("grad_up", grad_up), ("dx", dx), ("ws", ws)]
+    _same_device(dev, ins + out)
+    _apart(out, ins)
+    _launch("blr_adapters_backward", dev, stream, M, d_in, d_out, r, E, act, wt, _ptr(x), _ptr(dy), _ptr(down),
+            _ptr(up), _ptr(offsets), _ptr(order), _ptr(scale), _ptr(tape_s), _ptr(grad_down), _ptr(grad_up),
+            int(bool(accumulate_grads)), _ptr(dx), int(bool(accumulate_dx)), _ptr(ws), ws.numel())
+    return grad_down, grad_up, dx
+
+
 def blr_sumsq(a, nparts: int = 64, stream=None) -> float:
     """Sum of squares of a float32 tensor: nparts device partials, added on
     the host in f64 (the page's `sumsq`). Synchronises the stream."""
@@ -401,7 +682,7 @@ def blr_profile_reset():
     _check(load().blr_profile_reset(), "blr_profile_reset")
 
 
-def blr_profile_read(max_kinds: int = 16) -> dict[str, tuple[int, float]]:
+def blr_profile_read(max_kinds: int = 64) -> dict[str, tuple[int, float]]:
     """{kernel name: (launches, total ms)} of the timed launches so far."""
     names = (ctypes.c_char_p * max_kinds)()
     counts = (ctypes.c_int64 * max_kinds)()

@@ -6,11 +6,15 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", f) for f in ("blr_kernels.hip", "blr_api.hip")]
-HEADERS = [os.path.join(HERE, "csrc", "blr_internal.h"), os.path.join(ROOT, "include", "blr.h")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("blr_kernels.hip", "blr_route.hip", "blr_adapters.hip",
+                                                     "blr_api.hip")]
+HEADERS = [os.path.join(HERE, "csrc", f) for f in ("blr_internal.h", "blr_vec.h")] + \
+    [os.path.join(ROOT, "include", "blr.h")]
 LIB = os.path.join(HERE, "libblr.so")
 ARCH = "gfx950"
 
@@ -33,14 +37,21 @@ def flags() -> list[str]:
 
 
 def build(verbose: bool = False) -> str:
-    tmp = LIB + ".tmp"
-    cmd = [hipcc()] + flags() + ["-o", tmp] + SOURCES
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError(f"hipcc failed with status {r.returncode}")
+    def run(cmd: list[str]):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError(f"hipcc failed with status {r.returncode}")
+
+    # the sources side by side, then one link
+    with tempfile.TemporaryDirectory() as d, ThreadPoolExecutor(len(SOURCES)) as pool:
+        objects = [os.path.join(d, os.path.basename(src) + ".o") for src in SOURCES]
+        list(pool.map(lambda so: run([hipcc()] + [f for f in flags() if f != "-shared"] + ["-c", "-o", so[1], so[0]]),
+                      zip(SOURCES, objects)))
+        tmp = LIB + ".tmp"
+        run([hipcc()] + flags() + ["-o", tmp] + objects)
     os.replace(tmp, LIB)
     return LIB
 

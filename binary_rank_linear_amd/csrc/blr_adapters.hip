@@ -1,0 +1,484 @@
+// Low-rank adapters of many requests at once, for gfx950. Row t with adapter
+// e (A_e [r][d_in], B_e [d_out][r], factor c_e):
+//
+//   forward   s = x A_e^T          y (+)= c_e s B_e^T
+//   backward  ds = c_e dy B_e      dx (+)= ds A_e
+//             dA_e (+)= sum_t ds^T x      dB_e (+)= c_e sum_t dy^T s
+//
+// Rows are taken by the plan of the sort (blr_route.hip): a workgroup has a
+// tile of rows of one adapter, found from offsets by every wave for itself.
+// All products run on the f32 matrix instruction: operands of 16 bits are
+// exact in f32, and s, ds and the gradients keep 32 bits throughout.
+//
+// v_mfma_f32_16x16x4_f32, D += A B: lane l = 16 q + c gives A[c][q] and
+// B[q][c], and holds D[4 q + i][c], i < 4. Which column of a product a k index
+// stands for is free as long as A and B agree; the loads below use that to
+// read four consecutive elements per lane.
+#include "blr_internal.h"
+#include "blr_vec.h"
+
+namespace blr {
+
+namespace {
+
+constexpr int TM = ADAPT_TM;
+
+__device__ __forceinline__ vf4 mfma4(float a, float b, vf4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
+// A tile of one group of the plan; group E is the rows without an adapter.
+struct Tile {
+    int e;      // -1: the grid has more tiles than the plan
+    int p0;     // first position
+    int cnt;    // positions
+    int j, of;  // this tile is the j-th of the group's `of`
+    int slot;   // tiles of earlier groups that have several
+};
+
+// Tile b of tiles of tm positions over groups 0 .. groups-1 (wave-uniform).
+// Offsets out of order or out of range cannot lead outside [0, M).
+__device__ Tile find_tile(const AdaptPlan &plan, int groups, int tm, int b) {
+    const int lane = threadIdx.x & 63;
+    int run = 0, many = 0;
+    for (int base = 0; base < groups; base += 64) {
+        const int e = base + lane;
+        int lo = 0, cnt = 0;
+        if (e < groups) {
+            lo = plan.offsets[e];
+            const int hi = e < plan.E ? plan.offsets[e + 1] : plan.M;
+            lo = lo < 0 ? 0 : lo > plan.M ? plan.M : lo;
+            cnt = (hi > plan.M ? plan.M : hi) - lo;
+            cnt = cnt < 0 ? 0 : cnt;
+        }
+        const int nt = cnt / tm + (cnt % tm ? 1 : 0);
+        const int several = nt > 1 ? nt : 0;
+        int incl = nt, mincl = several;
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) {
+            const int u = __shfl_up(incl, o), v = __shfl_up(mincl, o);
+            if (lane >= o) {
+                incl += u;
+                mincl += v;
+            }
+        }
+        const uint64_t past = __ballot(run + incl > b);
+        if (past) {
+            const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)past) - 1);
+            Tile t;
+            t.e = base + l;
+            t.of = __builtin_amdgcn_readlane(nt, l);
+            t.j = b - run - (__builtin_amdgcn_readlane(incl, l) - t.of);
+            t.p0 = __builtin_amdgcn_readlane(lo, l) + t.j * tm;
+            const int left = __builtin_amdgcn_readlane(cnt, l) - t.j * tm;
+            t.cnt = left < tm ? left : tm;
+            t.slot = many + __builtin_amdgcn_readlane(mincl, l) - __builtin_amdgcn_readlane(several, l);
+            return t;
+        }
+        run += __builtin_amdgcn_readlane(incl, 63);
+        many += __builtin_amdgcn_readlane(mincl, 63);
+    }
+    return Tile{-1, 0, 0, 0, 0, 0};
+}
+
+// The row of position p, -1 if the plan names none.
+__device__ __forceinline__ int64_t row_of(const AdaptPlan &plan, int p) {
+    const int row = plan.order ? plan.order[p] : p;
+    return row >= 0 && row < plan.M ? row : -1;
+}
+
+// ---------------------------------------------------------------- shrink --
+// One workgroup: 64 rows x all r over one split of K, wave w every fourth run
+// of 32 columns. X goes from global memory into the A operand as it lies: lane
+// (q, c) holds columns 8 q .. 8 q + 7 of row c, a full 128-byte line per row
+// (f32), so X needs no LDS and is read once.
+template <typename TX, typename TW, int RT, bool TRANS>
+__global__ __launch_bounds__(256) void adapt_shrink_kernel(AdaptShrink a) {
+    __shared__ float red[TM][RT * 16 + 1];
+    const Tile tile = find_tile(a.plan, a.plan.E, TM, blockIdx.x);
+    if (tile.e < 0) return;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int q = lane >> 4, c = lane & 15;
+    const int nt = (tile.cnt + 15) >> 4;
+    const TW *W = reinterpret_cast<const TW *>(a.W) + (int64_t)tile.e * a.r * a.K;
+    const TX *x[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        // rows past the tile, or not named by the plan, repeat one; not stored
+        const int p = t * 16 + c < tile.cnt ? t * 16 + c : tile.cnt - 1;
+        const int64_t row = row_of(a.plan, tile.p0 + p);
+        x[t] = reinterpret_cast<const TX *>(a.X) + (row < 0 ? 0 : row) * a.K;
+    }
+    vf4 acc[4][RT];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int n = 0; n < RT; ++n) acc[t][n] = vf4{0.f, 0.f, 0.f, 0.f};
+    const int units = a.K / 128;
+    const int u0 = (int)((int64_t)units * blockIdx.y / a.splits), u1 = (int)((int64_t)units * (blockIdx.y + 1) / a.splits);
+    for (int u = u0; u < u1; ++u) {
+        const int k0 = u * 128 + w * 32 + q * 8;
+        vf4 xv[4][2], wv[RT][2];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            if (t < nt) {
+                xv[t][0] = load4(x[t] + k0);
+                xv[t][1] = load4(x[t] + k0 + 4);
+            }
+#pragma unroll
+        for (int n = 0; n < RT; ++n) {
+            const int rank = n * 16 + c;
+            wv[n][0] = wv[n][1] = vf4{0.f, 0.f, 0.f, 0.f};
+            if (rank < a.r) {
+                if (TRANS) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) wv[n][j >> 2][j & 3] = (float)W[(int64_t)(k0 + j) * a.r + rank];
+                } else {
+                    wv[n][0] = load4(W + (int64_t)rank * a.K + k0);
+                    wv[n][1] = load4(W + (int64_t)rank * a.K + k0 + 4);
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            if (t < nt)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int n = 0; n < RT; ++n)
+                        acc[t][n] = mfma4(xv[t][j >> 2][j & 3], wv[n][j >> 2][j & 3], acc[t][n]);
+    }
+    // the waves' sums, in wave order
+    for (int v = 0; v < 4; ++v) {
+        if (w == v) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int n = 0; n < RT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float *at = &red[t * 16 + 4 * q + i][n * 16 + c];
+                        *at = v == 0 ? acc[t][n][i] : *at + acc[t][n][i];
+                    }
+        }
+        __syncthreads();
+    }
+    float *part = a.part + ((int64_t)blockIdx.y * a.plan.M + tile.p0) * a.r;
+    for (int i = threadIdx.x; i < tile.cnt * a.r; i += 256) part[i] = red[i / a.r][i % a.r];
+}
+
+// ---------------------------------------------------------------- expand --
+// One workgroup: 64 rows x a range of columns, wave w every fourth run of 32.
+// S stays in registers as the B operand for the whole range; the weights are
+// the A operand, so that lane (q, c) ends with eight consecutive columns of
+// row c: out is read into the accumulator and written back a whole line per
+// row, and never passes through LDS.
+template <typename TX, typename TW, int RT, bool TRANS>
+__global__ __launch_bounds__(256) void adapt_expand_kernel(AdaptExpand a, int chunks) {
+    __shared__ float S[TM][RT * 16 + 4];
+    const Tile tile = find_tile(a.plan, a.plan.E + 1, TM, blockIdx.x);
+    if (tile.e < 0) return;
+    const bool none = tile.e == a.plan.E;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int q = lane >> 4, c = lane & 15;
+    const int nt = (tile.cnt + 15) >> 4;
+    const float scale = a.scale && !none ? a.scale[tile.e] : 1.f;
+    for (int i = threadIdx.x; i < TM * RT * 16; i += 256) {
+        const int m = i / (RT * 16), k = i % (RT * 16);
+        float sum = 0.f;
+        if (m < tile.cnt && k < a.r) {
+            if (!none)
+                for (int sp = 0; sp < a.splits; ++sp)
+                    sum += a.part[((int64_t)sp * a.plan.M + tile.p0 + m) * a.r + k];
+            if (blockIdx.y == 0) {
+                const int64_t row = row_of(a.plan, tile.p0 + m);
+                if (a.s_row && row >= 0) a.s_row[row * a.r + k] = sum;
+                if (a.s_pos) a.s_pos[(int64_t)(tile.p0 + m) * a.r + k] = scale * sum;
+            }
+        }
+        S[m][k] = scale * sum;
+    }
+    if (a.out == nullptr || (none && a.acc)) return;
+    __syncthreads();
+    TX *out[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int64_t row = t * 16 + c < tile.cnt ? row_of(a.plan, tile.p0 + t * 16 + c) : -1;
+        out[t] = row < 0 ? nullptr : reinterpret_cast<TX *>(a.out) + row * a.N;
+    }
+    vf4 s[4][RT];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int n = 0; n < RT; ++n) s[t][n] = *reinterpret_cast<const vf4 *>(&S[t * 16 + c][n * 16 + q * 4]);
+    const TW *W = reinterpret_cast<const TW *>(a.W) + (int64_t)(none ? 0 : tile.e) * a.r * a.N;
+    const int units = a.N / 128;
+    const int u0 = (int)((int64_t)units * blockIdx.y / chunks), u1 = (int)((int64_t)units * (blockIdx.y + 1) / chunks);
+    for (int u = u0; u < u1; ++u) {
+        const int o0 = u * 128 + w * 32;
+        vf4 acc[4][2];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            acc[t][0] = acc[t][1] = vf4{0.f, 0.f, 0.f, 0.f};
+            if (a.acc && out[t]) {
+                acc[t][0] = load4(out[t] + o0 + q * 8);
+                acc[t][1] = load4(out[t] + o0 + q * 8 + 4);
+            }
+        }
+        if (!none) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                // row c = 4 q' + i of the A operand stands for column 8 q' + 4 h + i
+                const int o = o0 + 8 * (c >> 2) + 4 * h + (c & 3);
+#pragma unroll
+                for (int n = 0; n < RT; ++n) {
+                    vf4 wv = {0.f, 0.f, 0.f, 0.f};
+                    const int k = n * 16 + q * 4;  // r is a multiple of 8
+                    if (k < a.r) {
+                        if (TRANS) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) wv[j] = (float)W[(int64_t)(k + j) * a.N + o];
+                        } else {
+                            wv = load4(W + (int64_t)o * a.r + k);
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        if (t < nt)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) acc[t][h] = mfma4(wv[j], s[t][n][j], acc[t][h]);
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            if (out[t]) {
+                store4(out[t] + o0 + q * 8, acc[t][0]);
+                store4(out[t] + o0 + q * 8 + 4, acc[t][1]);
+            }
+    }
+}
+
+// -------------------------------------------------------------- gradients --
+// One workgroup: a range of one adapter's rows x 256 columns, wave w 64 of
+// them. Four rows a step: lane (q, c) loads columns 4 c .. 4 c + 3 of row q,
+// whose component u belongs to tile u of the output, so X again goes straight
+// into an operand. Which side X takes follows the gradient's layout, so that
+// each lane ends with consecutive elements of it.
+template <typename TX, int RT, bool TRANS>
+__global__ __launch_bounds__(256) void adapt_grad_kernel(AdaptGrad a) {
+    const Tile tile = find_tile(a.plan, a.plan.E, a.range, blockIdx.x);
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int q = lane >> 4, c = lane & 15;
+    const int n0 = blockIdx.y * 256 + w * 64;
+    if (tile.e < 0 || n0 >= a.N) return;
+    const TX *X = reinterpret_cast<const TX *>(a.X) + n0 + 4 * c;
+    vf4 acc[4][RT];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int n = 0; n < RT; ++n) acc[u][n] = vf4{0.f, 0.f, 0.f, 0.f};
+    for (int m0 = 0; m0 < tile.cnt; m0 += 4) {
+        const int p = tile.p0 + m0 + q;
+        const int64_t row = m0 + q < tile.cnt ? row_of(a.plan, p) : -1;
+        vf4 xv = {0.f, 0.f, 0.f, 0.f};
+        float tv[RT];
+        if (row >= 0) xv = load4(X + row * a.N);
+#pragma unroll
+        for (int n = 0; n < RT; ++n) {
+            const int k = n * 16 + c;
+            tv[n] = row >= 0 && k < a.r ? a.thin[(a.thin_by_row ? row : (int64_t)p) * a.r + k] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int n = 0; n < RT; ++n)
+                acc[u][n] = TRANS ? mfma4(tv[n], xv[u], acc[u][n]) : mfma4(xv[u], tv[n], acc[u][n]);
+    }
+    const int64_t size = (int64_t)a.r * a.N;
+    const bool alone = tile.of == 1;
+    if (!alone && tile.slot + tile.j >= a.slots) return;  // only for offsets out of order
+    float *g = alone ? a.grad + tile.e * size : a.part + (tile.slot + tile.j) * size;
+    const bool add = alone && a.acc;
+    const float scale = a.scale ? a.scale[tile.e] : 1.f;
+    if (TRANS) {
+        // D[rank 4 q + i][column 4 c + u]
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int n = 0; n < RT; ++n) {
+                const int k = n * 16 + 4 * q;
+                if (k >= a.r) continue;
+                float *at = g + (int64_t)(n0 + 4 * c + u) * a.r + k;
+                const vf4 v = scale * acc[u][n];
+                store4(at, add ? load4(at) + v : v);
+            }
+    } else {
+        // D[column 4 (4 q + i) + u][rank c]
+#pragma unroll
+        for (int n = 0; n < RT; ++n) {
+            const int k = n * 16 + c;
+            if (k >= a.r) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float *at = g + (int64_t)k * a.N + n0 + 16 * q + 4 * i;
+                const vf4 v = scale * vf4{acc[0][n][i], acc[1][n][i], acc[2][n][i], acc[3][n][i]};
+                store4(at, add ? load4(at) + v : v);
+            }
+        }
+    }
+}
+
+// The partials of an adapter of several ranges, added in range order; zeros
+// for an adapter without rows.
+__global__ __launch_bounds__(256) void adapt_reduce_kernel(AdaptGrad a) {
+    const int e = blockIdx.y;
+    int lo = a.plan.offsets[e], hi = a.plan.offsets[e + 1];
+    lo = lo < 0 ? 0 : lo > a.plan.M ? a.plan.M : lo;
+    hi = hi > a.plan.M ? a.plan.M : hi;
+    if (hi - lo > 0 && hi - lo <= a.range) return;  // written by its only range
+    if (hi - lo <= 0 && a.acc) return;
+    const int64_t size = (int64_t)a.r * a.N;
+    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    int slot = 0, of = 0;
+    if (hi - lo > 0) {
+        // partials of the adapters before: every wave sums for itself
+        const int lane = threadIdx.x & 63;
+        for (int base = 0; base < e; base += 64) {
+            int several = 0;
+            if (base + lane < e) {
+                int l = a.plan.offsets[base + lane], h = a.plan.offsets[base + lane + 1];
+                l = l < 0 ? 0 : l > a.plan.M ? a.plan.M : l;
+                h = h > a.plan.M ? a.plan.M : h;
+                if (h - l > a.range) several = (h - l) / a.range + ((h - l) % a.range ? 1 : 0);
+            }
+            for (int o = 32; o > 0; o /= 2) several += __shfl_xor(several, o);
+            slot += several;
+        }
+        of = (hi - lo) / a.range + ((hi - lo) % a.range ? 1 : 0);
+        if (slot + of > a.slots) return;
+    }
+    if (at >= size) return;
+    float *g = a.grad + e * size + at;
+    vf4 sum = a.acc ? load4(g) : vf4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < of; ++j) sum += load4(a.part + (int64_t)(slot + j) * size + at);
+    store4(g, sum);
+}
+
+// Workgroups that keep the chip busy: a few per CU.
+constexpr int64_t FILL = 1024;
+
+template <typename TX, typename TW, int RT>
+hipError_t shrink_t(const AdaptShrink &a, bool trans, hipStream_t s) {
+    const dim3 grid((unsigned)adapt_tiles(a.plan.M, a.plan.E, TM), (unsigned)a.splits);
+    if (trans)
+        hipLaunchKernelGGL((adapt_shrink_kernel<TX, TW, RT, true>), grid, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((adapt_shrink_kernel<TX, TW, RT, false>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+template <typename TX, typename TW, int RT>
+hipError_t expand_t(const AdaptExpand &a, bool trans, hipStream_t s) {
+    const int64_t tiles = adapt_tiles(a.plan.M, a.plan.E, TM), units = a.N / 128;
+    int64_t chunks = (FILL + tiles - 1) / tiles;
+    chunks = a.out == nullptr ? 1 : chunks > units ? units : chunks;
+    const dim3 grid((unsigned)tiles, (unsigned)chunks);
+    if (trans)
+        hipLaunchKernelGGL((adapt_expand_kernel<TX, TW, RT, true>), grid, dim3(256), 0, s, a, (int)chunks);
+    else
+        hipLaunchKernelGGL((adapt_expand_kernel<TX, TW, RT, false>), grid, dim3(256), 0, s, a, (int)chunks);
+    return hipGetLastError();
+}
+
+template <typename TX, int RT>
+hipError_t grad_t(const AdaptGrad &a, bool trans, hipStream_t s) {
+    const dim3 grid((unsigned)adapt_tiles(a.plan.M, a.plan.E, a.range), (unsigned)((a.N + 255) / 256));
+    if (trans)
+        hipLaunchKernelGGL((adapt_grad_kernel<TX, RT, true>), grid, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((adapt_grad_kernel<TX, RT, false>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+// Calls f<TX, TW, RT> for the call's types and rank.
+#define BLR_BY_RANK(r, F, TX, TW, ...)                                                          \
+    ((r) <= 16   ? F<TX, TW, 1>(__VA_ARGS__)                                                     \
+     : (r) <= 32 ? F<TX, TW, 2>(__VA_ARGS__)                                                     \
+     : (r) <= 64 ? F<TX, TW, 4>(__VA_ARGS__)                                                     \
+                 : F<TX, TW, 8>(__VA_ARGS__))
+#define BLR_BY_TYPES(a, F, ...)                                                                  \
+    ((a).act == 1   ? BLR_BY_RANK((a).r, F, _Float16, _Float16, __VA_ARGS__)                     \
+     : (a).act == 2 ? BLR_BY_RANK((a).r, F, __bf16, __bf16, __VA_ARGS__)                         \
+     : (a).wt == 1  ? BLR_BY_RANK((a).r, F, float, _Float16, __VA_ARGS__)                        \
+     : (a).wt == 2  ? BLR_BY_RANK((a).r, F, float, __bf16, __VA_ARGS__)                          \
+                    : BLR_BY_RANK((a).r, F, float, float, __VA_ARGS__))
+
+template <typename TX>
+hipError_t grad_by_rank(const AdaptGrad &a, bool trans, hipStream_t s) {
+    return a.r <= 16   ? grad_t<TX, 1>(a, trans, s)
+           : a.r <= 32 ? grad_t<TX, 2>(a, trans, s)
+           : a.r <= 64 ? grad_t<TX, 4>(a, trans, s)
+                       : grad_t<TX, 8>(a, trans, s);
+}
+
+}  // namespace
+
+int64_t adapt_tiles(int64_t M, int64_t E, int64_t tm) {
+    const int64_t groups = E + 1 < M ? E + 1 : M;  // that have rows
+    const int64_t tiles = M / tm + groups;
+    return tiles < M ? tiles : M;
+}
+
+int adapt_splits(int64_t M, int64_t E, int64_t K) {
+    const int64_t tiles = adapt_tiles(M, E, TM), units = K / 128;
+    int64_t sp = (FILL / 2 + tiles - 1) / tiles;
+    sp = sp > units ? units : sp;
+    return (int)(sp > ADAPT_MAX_SPLITS ? ADAPT_MAX_SPLITS : sp);
+}
+
+int64_t adapt_range(int64_t M, int64_t N, int64_t r) {
+    const int64_t cols = (N + 255) / 256;
+    int64_t range = M * cols / (FILL / 2);
+    const int64_t least = 8 * r > 256 ? 8 * r : 256;  // a partial costs as much as 2 r rows
+    range = range < least ? least : range;
+    range = range < M ? range : M;
+    return (range + 63) / 64 * 64;
+}
+
+int64_t adapt_range_slots(int64_t M, int64_t E, int64_t range) {
+    if (M <= range) return 0;
+    const int64_t twice = 2 * M / range, all = M / range + E;
+    return twice < all ? twice : all;
+}
+
+hipError_t launch_adapt_shrink(const AdaptShrink &a, bool trans, hipStream_t s) {
+    prof_begin(trans ? K_ADAPT_DS : K_ADAPT_DOWN, s);
+    hipError_t e = BLR_BY_TYPES(a, shrink_t, a, trans, s);
+    prof_end(s);
+    return e;
+}
+
+hipError_t launch_adapt_expand(const AdaptExpand &a, bool trans, hipStream_t s) {
+    prof_begin(trans ? K_ADAPT_DX : K_ADAPT_UP, s);
+    hipError_t e = BLR_BY_TYPES(a, expand_t, a, trans, s);
+    prof_end(s);
+    return e;
+}
+
+hipError_t launch_adapt_grad(const AdaptGrad &a, bool trans, hipStream_t s) {
+    prof_begin(K_ADAPT_GRAD, s);
+    hipError_t e = a.act == 0   ? grad_by_rank<float>(a, trans, s)
+                   : a.act == 1 ? grad_by_rank<_Float16>(a, trans, s)
+                                : grad_by_rank<__bf16>(a, trans, s);
+    prof_end(s);
+    if (e != hipSuccess) return e;
+    const int64_t blocks = ((int64_t)a.r * a.N / 4 + 255) / 256;
+    prof_begin(K_ADAPT_REDUCE, s);
+    hipLaunchKernelGGL(adapt_reduce_kernel, dim3((unsigned)blocks, (unsigned)a.plan.E), dim3(256), 0, s, a);
+    e = hipGetLastError();
+    prof_end(s);
+    return e;
+}
+
+}  // namespace blr

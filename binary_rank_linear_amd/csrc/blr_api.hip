@@ -167,6 +167,7 @@ const char *blr_status_string(int status) {
         case BLR_ERR_DEVICE: return "the current device is not gfx950";
         case BLR_ERR_HIP: return "HIP runtime error";
         case BLR_ERR_ALIGN: return "a pointer is not 16-byte aligned";
+        case BLR_ERR_DTYPE: return "element type (or pair of types) not supported by this call";
         case BLR_ERR_SCRATCH: return "sizes need more than the allocation-free forward's scratch (r * d_in / 8 bytes)";
     }
     return "unknown status";
@@ -561,6 +562,288 @@ int blr_sumsq(const float *a, int64_t n, float *partials, int nparts, void *stre
     int st = current_device_ok();
     if (st != BLR_OK) return st;
     BLR_TRY(launch_sumsq(a, n, partials, nparts, (hipStream_t)stream));
+    return BLR_OK;
+}
+
+// --------------------------------------------------------------- routing --
+namespace {
+constexpr int64_t MAX_POSITIONS = ((int64_t)1 << 31) - 65536;  // int32 positions, with room for a grid's tail
+
+bool dtype_ok(int t) { return t == BLR_F32 || t == BLR_F16 || t == BLR_BF16; }
+
+bool route_shape_ok(int64_t pairs, int64_t experts) {
+    return pairs >= 1 && pairs < MAX_POSITIONS && experts >= 1 && experts <= ROUTE_MAX_EXPERTS;
+}
+
+// Checks that the three row calls share; T k is formed only once k is known to be small.
+int route_rows_check(int64_t T, int64_t k, int64_t experts, int64_t d, int dtype, const void *a,
+                     const int32_t *offsets, const int32_t *slot, const void *out) {
+    if (!a || !offsets || !slot || !out) return BLR_ERR_NULL;
+    if (!dtype_ok(dtype)) return BLR_ERR_DTYPE;
+    if (T < 1 || T >= MAX_POSITIONS || k < 1 || k > 1024 || !route_shape_ok(T * k, experts)) return BLR_ERR_SHAPE;
+    if (d < 8 || d % 8 || d > ((int64_t)1 << 20)) return BLR_ERR_SHAPE;
+    if (!aligned16(a) || !aligned16(out) || !aligned4(offsets) || !aligned4(slot)) return BLR_ERR_ALIGN;
+    return BLR_OK;
+}
+}  // namespace
+
+size_t blr_route_workspace_bytes(int64_t pairs, int64_t experts) {
+    if (!route_shape_ok(pairs, experts)) return 0;
+    return up((size_t)(route_ranges(pairs, nullptr) * (experts + 1)) * 4);
+}
+
+int blr_route_sort(int64_t pairs, int64_t experts, const int32_t *ids, int32_t *offsets, int32_t *order,
+                   int32_t *slot, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!ids || !offsets || !order || !slot) return BLR_ERR_NULL;
+    if (!route_shape_ok(pairs, experts)) return BLR_ERR_SHAPE;
+    if (workspace == nullptr || workspace_bytes < blr_route_workspace_bytes(pairs, experts)) return BLR_ERR_WORKSPACE;
+    if (!aligned4(ids) || !aligned4(offsets) || !aligned4(order) || !aligned4(slot) || !aligned16(workspace))
+        return BLR_ERR_ALIGN;
+    int st = current_device_ok();
+    if (st != BLR_OK) return st;
+    int64_t per = 0;
+    RouteSortArgs a = {};
+    a.ranges = (int)route_ranges(pairs, &per);
+    a.per_range = (int)per;
+    a.ids = ids;
+    a.offsets = offsets;
+    a.order = order;
+    a.slot = slot;
+    a.counts = (uint32_t *)workspace;
+    a.pairs = (int)pairs;
+    a.experts = (int)experts;
+    BLR_TRY(launch_route_sort(a, (hipStream_t)stream));
+    return BLR_OK;
+}
+
+int blr_route_gather(int64_t T, int64_t k, int64_t experts, int64_t d, int dtype, const void *x,
+                     const int32_t *offsets, const int32_t *slot, void *rows, void *stream) {
+    int st = route_rows_check(T, k, experts, d, dtype, x, offsets, slot, rows);
+    if (st == BLR_OK) st = current_device_ok();
+    if (st != BLR_OK) return st;
+    RouteRows a = {};
+    a.placed = offsets + experts;
+    a.slot = slot;
+    a.a = x;
+    a.out = rows;
+    a.T = T;
+    a.d = d;
+    a.k = (int)k;
+    a.dtype = dtype;
+    BLR_TRY(launch_route_gather(a, (hipStream_t)stream));
+    return BLR_OK;
+}
+
+int blr_route_combine(int64_t T, int64_t k, int64_t experts, int64_t d, int dtype, const void *z,
+                      const int32_t *offsets, const int32_t *slot, const float *weights, void *y, int accumulate_y,
+                      void *stream) {
+    int st = route_rows_check(T, k, experts, d, dtype, z, offsets, slot, y);
+    if (st != BLR_OK) return st;
+    if (!aligned4(weights)) return BLR_ERR_ALIGN;
+    st = current_device_ok();
+    if (st != BLR_OK) return st;
+    RouteRows a = {};
+    a.placed = offsets + experts;
+    a.slot = slot;
+    a.weights = weights;
+    a.a = z;
+    a.out = y;
+    a.T = T;
+    a.d = d;
+    a.k = (int)k;
+    a.dtype = dtype;
+    a.acc = accumulate_y ? 1 : 0;
+    BLR_TRY(launch_route_combine(a, (hipStream_t)stream));
+    return BLR_OK;
+}
+
+int blr_route_combine_backward(int64_t T, int64_t k, int64_t experts, int64_t d, int dtype, const void *dy,
+                               const void *z, const int32_t *offsets, const int32_t *slot, const float *weights,
+                               void *dz, float *dw, void *stream) {
+    if (dw && !z) return BLR_ERR_NULL;
+    int st = route_rows_check(T, k, experts, d, dtype, dy, offsets, slot, dz);
+    if (st != BLR_OK) return st;
+    if (!aligned16(z) || !aligned4(weights) || !aligned4(dw)) return BLR_ERR_ALIGN;
+    st = current_device_ok();
+    if (st != BLR_OK) return st;
+    RouteRows a = {};
+    a.placed = offsets + experts;
+    a.slot = slot;
+    a.weights = weights;
+    a.a = dy;
+    a.z = z;
+    a.out = dz;
+    a.dw = dw;
+    a.T = T;
+    a.d = d;
+    a.k = (int)k;
+    a.dtype = dtype;
+    BLR_TRY(launch_route_combine_backward(a, (hipStream_t)stream));
+    return BLR_OK;
+}
+
+// -------------------------------------------------------------- adapters --
+namespace {
+bool adapt_shape_ok(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t E) {
+    const int64_t D = (int64_t)1 << 20;
+    return M >= 1 && M < MAX_POSITIONS && d_in >= 128 && d_in <= D && d_in % 128 == 0 && d_out >= 128 && d_out <= D &&
+           d_out % 128 == 0 && r >= 8 && r <= ADAPT_MAX_RANK && r % 8 == 0 && E >= 1 && E <= ROUTE_MAX_EXPERTS;
+}
+
+// Workspace: the splits' partials of s or ds (f32 [splits][M][r]), then ds by
+// position (f32 [M][r]), then the ranges' partials of one gradient.
+struct AdaptLayout {
+    size_t ds, grad, total;
+    int64_t range_in, range_out, slots_in, slots_out;
+};
+
+AdaptLayout adapt_layout(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t E) {
+    AdaptLayout L;
+    const int si = adapt_splits(M, E, d_in), so = adapt_splits(M, E, d_out);
+    size_t off = up((size_t)(si > so ? si : so) * M * r * 4);
+    L.ds = off;
+    off += up((size_t)M * r * 4);
+    L.grad = off;
+    L.range_in = adapt_range(M, d_in, r);
+    L.range_out = adapt_range(M, d_out, r);
+    L.slots_in = adapt_range_slots(M, E, L.range_in);
+    L.slots_out = adapt_range_slots(M, E, L.range_out);
+    const int64_t gi = L.slots_in * r * d_in, go = L.slots_out * r * d_out;
+    off += up((size_t)(gi > go ? gi : go) * 4);
+    L.total = off;
+    return L;
+}
+
+// Checks that both calls share.
+int adapt_check(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t E, int act, int wt, const void *down,
+                const void *up_, const int32_t *offsets, const int32_t *order, const float *scale,
+                const void *workspace, size_t workspace_bytes, size_t *need) {
+    if (!down || !up_ || !offsets) return BLR_ERR_NULL;
+    if (!dtype_ok(act) || !dtype_ok(wt) || (act != BLR_F32 && wt != act)) return BLR_ERR_DTYPE;
+    if (!adapt_shape_ok(M, d_in, d_out, r, E)) return BLR_ERR_SHAPE;
+    *need = adapt_layout(M, d_in, d_out, r, E).total;
+    if (workspace == nullptr || workspace_bytes < *need) return BLR_ERR_WORKSPACE;
+    if (!aligned16(down) || !aligned16(up_) || !aligned4(offsets) || !aligned4(order) || !aligned4(scale) ||
+        !aligned16(workspace))
+        return BLR_ERR_ALIGN;
+    return BLR_OK;
+}
+}  // namespace
+
+size_t blr_adapters_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t adapters) {
+    if (!adapt_shape_ok(M, d_in, d_out, r, adapters)) return 0;
+    return adapt_layout(M, d_in, d_out, r, adapters).total;
+}
+
+int blr_adapters_forward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t adapters, int act, int wt,
+                         const void *x, const void *down, const void *up, const int32_t *offsets,
+                         const int32_t *order, const float *scale, void *y, int accumulate_y, float *tape_s,
+                         void *workspace, size_t workspace_bytes, void *stream) {
+    if (!x || !y) return BLR_ERR_NULL;
+    size_t need = 0;
+    int st = adapt_check(M, d_in, d_out, r, adapters, act, wt, down, up, offsets, order, scale, workspace,
+                         workspace_bytes, &need);
+    if (st != BLR_OK) return st;
+    if (!aligned16(x) || !aligned16(y) || !aligned16(tape_s)) return BLR_ERR_ALIGN;
+    st = current_device_ok();
+    if (st != BLR_OK) return st;
+    hipStream_t s = (hipStream_t)stream;
+    AdaptShrink sh = {};
+    sh.plan = {offsets, order, (int)M, (int)adapters};
+    sh.X = x;
+    sh.W = down;
+    sh.part = (float *)workspace;
+    sh.K = (int)d_in;
+    sh.r = (int)r;
+    sh.splits = adapt_splits(M, adapters, d_in);
+    sh.act = act;
+    sh.wt = wt;
+    BLR_TRY(launch_adapt_shrink(sh, false, s));
+    AdaptExpand ex = {};
+    ex.plan = sh.plan;
+    ex.part = sh.part;
+    ex.scale = scale;
+    ex.W = up;
+    ex.out = y;
+    ex.s_row = tape_s;
+    ex.N = (int)d_out;
+    ex.r = (int)r;
+    ex.splits = sh.splits;
+    ex.act = act;
+    ex.wt = wt;
+    ex.acc = accumulate_y ? 1 : 0;
+    BLR_TRY(launch_adapt_expand(ex, false, s));
+    return BLR_OK;
+}
+
+int blr_adapters_backward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t adapters, int act, int wt,
+                          const void *x, const void *dy, const void *down, const void *up, const int32_t *offsets,
+                          const int32_t *order, const float *scale, const float *tape_s, float *grad_down,
+                          float *grad_up, int accumulate_grads, void *dx, int accumulate_dx, void *workspace,
+                          size_t workspace_bytes, void *stream) {
+    if (!dy || (grad_down == nullptr) != (grad_up == nullptr) || (!grad_down && !dx)) return BLR_ERR_NULL;
+    if (grad_down && (!x || !tape_s)) return BLR_ERR_NULL;
+    size_t need = 0;
+    int st = adapt_check(M, d_in, d_out, r, adapters, act, wt, down, up, offsets, order, scale, workspace,
+                         workspace_bytes, &need);
+    if (st != BLR_OK) return st;
+    const void *arrays[] = {x, dy, tape_s, grad_down, grad_up, dx};
+    for (const void *p : arrays)
+        if (!aligned16(p)) return BLR_ERR_ALIGN;
+    st = current_device_ok();
+    if (st != BLR_OK) return st;
+    hipStream_t s = (hipStream_t)stream;
+    const AdaptLayout L = adapt_layout(M, d_in, d_out, r, adapters);
+    char *ws = (char *)workspace;
+    // ds = c dy B: the contraction over d_out, then its splits' sum with dx
+    AdaptShrink sh = {};
+    sh.plan = {offsets, order, (int)M, (int)adapters};
+    sh.X = dy;
+    sh.W = up;
+    sh.part = (float *)ws;
+    sh.K = (int)d_out;
+    sh.r = (int)r;
+    sh.splits = adapt_splits(M, adapters, d_out);
+    sh.act = act;
+    sh.wt = wt;
+    BLR_TRY(launch_adapt_shrink(sh, true, s));
+    AdaptExpand ex = {};
+    ex.plan = sh.plan;
+    ex.part = sh.part;
+    ex.scale = scale;
+    ex.W = down;
+    ex.out = dx;
+    ex.s_pos = (float *)(ws + L.ds);
+    ex.N = (int)d_in;
+    ex.r = (int)r;
+    ex.splits = sh.splits;
+    ex.act = act;
+    ex.wt = wt;
+    ex.acc = accumulate_dx ? 1 : 0;
+    BLR_TRY(launch_adapt_expand(ex, true, s));
+    if (!grad_down) return BLR_OK;
+    AdaptGrad g = {};
+    g.plan = sh.plan;
+    g.part = (float *)(ws + L.grad);
+    g.r = (int)r;
+    g.act = act;
+    g.acc = accumulate_grads ? 1 : 0;
+    g.X = x;
+    g.thin = ex.s_pos;  // holds the factor already
+    g.grad = grad_down;
+    g.N = (int)d_in;
+    g.range = (int)L.range_in;
+    g.slots = L.slots_in;
+    BLR_TRY(launch_adapt_grad(g, false, s));
+    g.X = dy;
+    g.thin = tape_s;
+    g.thin_by_row = 1;
+    g.scale = scale;
+    g.grad = grad_up;
+    g.N = (int)d_out;
+    g.range = (int)L.range_out;
+    g.slots = L.slots_out;
+    BLR_TRY(launch_adapt_grad(g, true, s));
     return BLR_OK;
 }
 

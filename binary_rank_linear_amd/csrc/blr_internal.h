@@ -34,6 +34,17 @@ enum KernelId {
     K_SUMSQ,      // sum-of-squares partials (finite check)
     K_GEMM_PLANE, // dense frozen f16 linear
     K_SIGNS_REDUCE, // sign gradients: the token ranges' partials summed in order
+    K_ROUTE_COUNT,  // routing: pairs per expert of each range of pairs
+    K_ROUTE_PLACE,  // routing: order, slot and offsets
+    K_ROUTE_GATHER, // rows laid out by expert
+    K_ROUTE_COMBINE, // experts' rows weighted and summed back
+    K_ROUTE_COMBINE_BWD, // gradients of the experts' rows and of the weights
+    K_ADAPT_DOWN,   // adapters: partials of s = x A^T
+    K_ADAPT_UP,     // adapters: y (+)= c s B^T
+    K_ADAPT_DS,     // adapters: partials of ds = c dy B
+    K_ADAPT_DX,     // adapters: dx (+)= ds A
+    K_ADAPT_GRAD,   // adapters: gradients of A and B over ranges of rows
+    K_ADAPT_REDUCE, // adapters: the ranges' partials summed in order
     K_COUNT
 };
 const char *kernel_name(int id);
@@ -173,6 +184,93 @@ hipError_t launch_gemm(GemmKind kind, const GemmArgs &a, hipStream_t s);
 int gemm_tile_rows(GemmKind kind);
 hipError_t launch_colsum(const float *A, const float *B, int64_t M, int N, float *partial, hipStream_t s);
 hipError_t launch_finish(FinishJobs jobs, hipStream_t s);
+
+// ---------------------------------------------------------------- routing --
+// Most experts a sort takes (its counters lie in LDS, one table per wave).
+constexpr int ROUTE_MAX_EXPERTS = 1024;
+// Ranges of pairs of the sort: how many, and pairs per range (a multiple of
+// 64). One range is placed by a single launch.
+int64_t route_ranges(int64_t pairs, int64_t *per_range);
+struct RouteSortArgs {
+    const int32_t *ids;  // [pairs]
+    int32_t *offsets;    // [experts + 1]
+    int32_t *order, *slot;
+    uint32_t *counts;    // [ranges][experts + 1], used when ranges > 1
+    int pairs, experts, per_range, ranges;
+};
+hipError_t launch_route_sort(const RouteSortArgs &a, hipStream_t s);
+
+// Rows of d elements; row pointers 16-byte aligned, d a multiple of 8.
+struct RouteRows {
+    const int32_t *placed;  // &offsets[experts]: pairs that have an expert
+    const int32_t *slot;    // [T][k]
+    const float *weights;   // [T][k] or null (all one)
+    const void *a;          // gather: x; combine: z; backward: dy
+    const void *z;          // backward: z (null when dw is)
+    void *out;              // gather: rows; combine: y; backward: dz
+    float *dw;              // backward: [T][k] or null
+    int64_t T, d;
+    int k, dtype, acc;
+};
+hipError_t launch_route_gather(const RouteRows &a, hipStream_t s);
+hipError_t launch_route_combine(const RouteRows &a, hipStream_t s);
+hipError_t launch_route_combine_backward(const RouteRows &a, hipStream_t s);
+
+// --------------------------------------------------------------- adapters --
+// Rows per tile of the adapter contractions, and the limits of a call.
+constexpr int ADAPT_TM = 64;
+constexpr int ADAPT_MAX_RANK = 128;
+constexpr int ADAPT_MAX_SPLITS = 32;
+// Rows grouped by adapter: position p of the plan belongs to adapter e when
+// offsets[e] <= p < offsets[e + 1], and holds row order[p] (p itself when
+// order is null). Positions from offsets[E] on have no adapter.
+struct AdaptPlan {
+    const int32_t *offsets;
+    const int32_t *order;
+    int M, E;
+};
+// part[split][p][r] = sum over the split's columns of X[row(p)][k] W_e[.][k]
+// with W_e = W + e r K: [r][K], or [K][r] when trans.
+struct AdaptShrink {
+    AdaptPlan plan;
+    const void *X, *W;
+    float *part;
+    int K, r, splits, act, wt;
+};
+// out[row(p)][n] (+)= sum_k S[p][k] W_e[n][k], S[p] = scale_e sum over splits
+// of part[.][p]; W_e: [N][r], or [r][N] when trans. S goes to s_row by row,
+// unscaled, and to s_pos by position, scaled (either may be null).
+struct AdaptExpand {
+    AdaptPlan plan;
+    const float *part;
+    const float *scale;
+    const void *W;
+    void *out;  // null: only s_row / s_pos
+    float *s_row, *s_pos;
+    int N, r, splits, act, wt, acc;
+};
+// G_e (+)= scale_e sum over the adapter's rows of thin[.][k] X[row][n]: laid
+// out [r][N], or [N][r] when trans. thin is by position, or by row when
+// thin_by_row. Ranges of `range` rows; an adapter of several ranges leaves
+// partials in part[slot], which the reduction adds in range order.
+struct AdaptGrad {
+    AdaptPlan plan;
+    const void *X;
+    const float *thin;
+    const float *scale;  // null: no factor
+    float *grad, *part;
+    int N, r, act, acc, range, thin_by_row;
+    int64_t slots;  // partials that `part` has room for
+};
+hipError_t launch_adapt_shrink(const AdaptShrink &a, bool trans, hipStream_t s);
+hipError_t launch_adapt_expand(const AdaptExpand &a, bool trans, hipStream_t s);
+hipError_t launch_adapt_grad(const AdaptGrad &a, bool trans, hipStream_t s);
+// Tiles of tm positions that M positions in at most E + 1 groups can need.
+int64_t adapt_tiles(int64_t M, int64_t E, int64_t tm);
+int adapt_splits(int64_t M, int64_t E, int64_t K);
+int64_t adapt_range(int64_t M, int64_t N, int64_t r);
+// Partials of ranges that a gradient over M rows can leave.
+int64_t adapt_range_slots(int64_t M, int64_t E, int64_t range);
 
 // Profiling hooks around each launch (no-ops unless enabled).
 void prof_begin(int id, hipStream_t s);

@@ -2098,6 +2098,17 @@ const char *kernel_name(int id) {
         case K_SUMSQ: return "sumsq";
         case K_GEMM_PLANE: return "gemm_plane_linear";
         case K_SIGNS_REDUCE: return "sign_grads_reduce";
+        case K_ROUTE_COUNT: return "route_count";
+        case K_ROUTE_PLACE: return "route_place";
+        case K_ROUTE_GATHER: return "route_gather";
+        case K_ROUTE_COMBINE: return "route_combine";
+        case K_ROUTE_COMBINE_BWD: return "route_combine_backward";
+        case K_ADAPT_DOWN: return "adapters_down";
+        case K_ADAPT_UP: return "adapters_up";
+        case K_ADAPT_DS: return "adapters_ds";
+        case K_ADAPT_DX: return "adapters_dx";
+        case K_ADAPT_GRAD: return "adapters_grad";
+        case K_ADAPT_REDUCE: return "adapters_grad_reduce";
     }
     return "?";
 }

@@ -59,7 +59,8 @@ typedef enum {
     BLR_ERR_DEVICE = -5,    /* current device is not gfx950 */
     BLR_ERR_HIP = -6,       /* the HIP runtime reported an error */
     BLR_ERR_ALIGN = -7,     /* a pointer is not 16-byte aligned */
-    BLR_ERR_SCRATCH = -8    /* sizes exceed the allocation-free forward's scratch */
+    BLR_ERR_SCRATCH = -8,   /* sizes exceed the allocation-free forward's scratch */
+    BLR_ERR_DTYPE = -9      /* an element type, or a pair of them, that the call does not take */
 } blr_status;
 
 /* Human-readable text of a status code (static storage). */
@@ -217,6 +218,90 @@ int blr_plane_linear(int64_t M, int64_t n, int64_t k, const float *x, const uint
  * be 16-byte aligned, partials 4-byte aligned.
  */
 int blr_sumsq(const float *a, int64_t n, float *partials, int nparts, void *stream);
+
+/* Element types of the routing and adapter calls below. */
+typedef enum { BLR_F32 = 0, BLR_F16 = 1, BLR_BF16 = 2 } blr_dtype;
+
+/*
+ * Token routing. A token makes k choices among E experts (adapters, layers);
+ * pair p = t k + j is its j-th. The sort lays the pairs out by expert:
+ *   ids [pairs] int32: a value outside [0, E) means no expert
+ *   order [pairs] int32: order[i] is the pair at position i. Pairs are sorted
+ *     by expert, in their own order within one, those without an expert last
+ *   slot [pairs] int32: the inverse, slot[order[i]] = i
+ *   offsets [E + 1] int32: expert e has positions offsets[e] ..
+ *     offsets[e + 1] - 1; offsets[E] pairs have an expert ("are placed")
+ * 1 <= pairs < 2^31 - 65536, 1 <= E <= 1024. All three outputs are written
+ * whole, and are the same on every run. Pointers 4-byte aligned, the
+ * workspace (blr_route_workspace_bytes, 0 for invalid sizes) 16-byte.
+ */
+size_t blr_route_workspace_bytes(int64_t pairs, int64_t experts);
+int blr_route_sort(int64_t pairs, int64_t experts, const int32_t *ids, int32_t *offsets, int32_t *order,
+                   int32_t *slot, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Rows by expert and back, by the sort's offsets and slot (pairs = T k). Rows
+ * have d elements of dtype, d a multiple of 8 (whole 16-byte vectors), with
+ * row arrays 16-byte aligned; 1 <= k <= 1024; weights and dw are f32 [T][k].
+ *   gather:   rows [T k][d]: rows[slot[t k + j]] = x[t]; zero where the pair
+ *             is not placed. Its gradient is the combine without weights.
+ *   combine:  y [T][d] (+)= sum over the placed pairs of token t, in order of
+ *             j, of w[t][j] z[slot[t k + j]] (weights NULL: w = 1), summed in
+ *             f32 and rounded once. accumulate_y = 0 overwrites (zero for a
+ *             token without a placed pair), 1 adds, as in blr_forward.
+ *   backward: dz [T k][d]: dz[slot[t k + j]] = w[t][j] dy[t], zero where not
+ *             placed; dw[t][j] = dy[t] . z[slot[t k + j]], zero where not
+ *             placed (dw NULL: not formed, and z may be NULL).
+ * A pair that is not placed contributes nothing: neither its row of z nor its
+ * weight is read. A slot outside [0, T k) is skipped.
+ */
+int blr_route_gather(int64_t T, int64_t k, int64_t experts, int64_t d, int dtype, const void *x,
+                     const int32_t *offsets, const int32_t *slot, void *rows, void *stream);
+int blr_route_combine(int64_t T, int64_t k, int64_t experts, int64_t d, int dtype, const void *z,
+                      const int32_t *offsets, const int32_t *slot, const float *weights, void *y, int accumulate_y,
+                      void *stream);
+int blr_route_combine_backward(int64_t T, int64_t k, int64_t experts, int64_t d, int dtype, const void *dy,
+                               const void *z, const int32_t *offsets, const int32_t *slot, const float *weights,
+                               void *dz, float *dw, void *stream);
+
+/*
+ * Low-rank adapters of many requests at once, beside a projection all of them
+ * share (blr_forward or blr_plane_linear writes y, this call adds to it). Row
+ * t with adapter e, A_e = down[e], B_e = up[e], c_e = scale[e]:
+ *   forward   s = x A_e^T        y (+)= c_e s B_e^T
+ *   backward  ds = c_e dy B_e    dx (+)= ds A_e
+ *             grad_down[e] (+)= sum_t ds^T x    grad_up[e] (+)= c_e sum_t dy^T s
+ * with the sums over the rows of adapter e.
+ *   down [E][r][d_in], up [E][d_out][r] of type wt; x, y, dy, dx of type act;
+ *     act = BLR_F32 with any wt, or wt = act. scale f32 [E] or NULL (all 1).
+ *   offsets [E + 1], order [M]: the plan that blr_route_sort makes of the
+ *     rows' adapter ids; order NULL: the rows lie by adapter already (those of
+ *     blr_route_gather). One plan serves every layer of a model. Offsets that
+ *     do not ascend and rows outside [0, M) cannot lead outside the arrays.
+ *   Rows without an adapter: y and dx are zero, or unchanged when adding.
+ *     Adapters without rows: their gradients are zero, or unchanged.
+ *   tape_s f32 [M][r]: s by row (zero without an adapter), which the backward
+ *     reads; NULL in the forward keeps none.
+ *   grad_down, grad_up: f32, layouts of down and up, both or neither (NULL:
+ *     not formed; then x and tape_s may be NULL). dx may be NULL when they are
+ *     not. accumulate_grads = 0 overwrites, 1 adds.
+ * d_in, d_out multiples of 128 up to 2^20, r a multiple of 8 up to 128 (pad
+ * shorter adapters with zero rank rows and columns), 1 <= M < 2^31 - 65536,
+ * 1 <= E <= 1024. Every product and sum is f32 (16-bit operands are exact in
+ * it); outputs of 16 bits are rounded once. Results are the same on every run.
+ * Arrays 16-byte aligned, offsets and order 4-byte. Workspace:
+ * blr_adapters_workspace_bytes, for both calls; 0 for invalid sizes.
+ */
+size_t blr_adapters_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t adapters);
+int blr_adapters_forward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t adapters, int act, int wt,
+                         const void *x, const void *down, const void *up, const int32_t *offsets,
+                         const int32_t *order, const float *scale, void *y, int accumulate_y, float *tape_s,
+                         void *workspace, size_t workspace_bytes, void *stream);
+int blr_adapters_backward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t adapters, int act, int wt,
+                          const void *x, const void *dy, const void *down, const void *up, const int32_t *offsets,
+                          const int32_t *order, const float *scale, const float *tape_s, float *grad_down,
+                          float *grad_up, int accumulate_grads, void *dx, int accumulate_dx, void *workspace,
+                          size_t workspace_bytes, void *stream);
 
 /*
  * Per-kernel timing with HIP events (the role of the page's trainer
