@@ -387,24 +387,66 @@ def blr_plane_linear(x, plane, scale: float = 1.0, *, y=None, stream=None):
     return y
 
 
-def _wide():
-    """The element types of rows and adapters; their places are their numbers
-    in the C ABI."""
+_dtypes = None
+
+
+def _types():
+    """(f32, i32, wide, bytes): dtype tuples for the checks below. `wide` are
+    the element types of rows and adapters; their places are their numbers in
+    the C ABI."""
+    global _dtypes
+    if _dtypes is None:
+        import torch
+        _dtypes = ((torch.float32,), (torch.int32,), (torch.float32, torch.float16, torch.bfloat16), (torch.uint8,))
+    return _dtypes
+
+
+def _at(t, name, dtypes, shape, dev):
+    """Address of t, a contiguous tensor of this shape on GPU number dev. The
+    checks are _need's, in the order that costs least when all is well."""
+    try:
+        if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, dtypes, shape)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+
+
+def _new(shape, dtype, dev, stream):
+    """Memory for a call on `stream` (None: the current one): the allocator
+    hands out and takes back a tensor in the order of the stream it was made
+    on, so it is made on the one that the kernels run on."""
     import torch
-    return (torch.float32, torch.float16, torch.bfloat16)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
 
 
-def _apart(outputs, others):
-    """No output shares memory with another argument."""
-    spans = [(n, t.data_ptr(), t.numel() * t.element_size()) for n, t in others if t is not None]
-    for n, t in outputs:
-        if t is None:
-            continue
-        at, size = t.data_ptr(), t.numel() * t.element_size()
-        for m, b, bs in spans:
-            if at < b + bs and b < at + size:
-                raise ValueError(f"{n} shares memory with {m}")
-        spans.append((n, at, size))
+def _out(t, name, dtype, shape, dev, stream):
+    """(t, its address), t allocated when it is None."""
+    if t is None:
+        t = _new(shape, dtype, dev, stream)
+        return t, t.data_ptr()
+    return t, _at(t, name, (dtype,), shape, dev)
+
+
+def _ws(ws, need, name, dev, stream):
+    """(ws, (its address, its bytes)), `need` bytes allocated when it is None."""
+    u8 = _types()[3]
+    if ws is None:
+        if need == 0:
+            raise BlrError(-2, name)
+        ws = _new(need, u8[0], dev, stream)
+        return ws, (ws.data_ptr(), need)
+    _need(ws, "ws", u8)
+    return ws, (_at(ws, "ws", u8, ws.shape, dev), ws.numel())
+
+
+def _on(stream, dev):
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
 
 
 def _launch(name, dev, stream, *args):
@@ -412,22 +454,21 @@ def _launch(name, dev, stream, *args):
     unless one is given."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    handle = ctypes.c_void_p(stream.cuda_stream)
-    fn = getattr(load(), name)
-    if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, handle), name)
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        handle = stream.cuda_stream
+    fn = getattr(_lib or load(), name)
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, handle), name)
+            status = fn(*args, handle)
+    if status != 0:
+        raise BlrError(status, name)
 
 
-def _same_device(dev, tensors):
-    for n, t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{n} is on {t.device}, expected {dev}")
+# pairs that a sort places in one launch, without a workspace
+ROUTE_ONE_LAUNCH = 8192
 
 
 def workspace_route(pairs: int, experts: int, device=None):
@@ -443,57 +484,57 @@ def blr_route_sort(ids, experts: int, *, offsets=None, order=None, slot=None, ws
     [0, experts) means none. Returns (offsets [experts + 1], order [T k], slot
     in the shape of ids): the plan that the gather, the combine and the
     adapters take."""
-    import torch
-    i32 = (torch.int32,)
+    i32 = _types()[1]
     _need(ids, "ids", i32)
     if ids.dim() not in (1, 2):
         raise ValueError(f"ids has shape {tuple(ids.shape)}, expected [T] or [T][k]")
-    dev, n = ids.device, ids.numel()
-    new = lambda shape: torch.empty(shape, dtype=torch.int32, device=dev)  # noqa: E731
-    offsets = new(experts + 1) if offsets is None else _need(offsets, "offsets", i32, (experts + 1,))
-    order = new(n) if order is None else _need(order, "order", i32, (n,))
-    slot = new(ids.shape) if slot is None else _need(slot, "slot", i32, ids.shape)
-    ws = workspace_route(n, experts, dev) if ws is None else _need(ws, "ws", (torch.uint8,))
-    out = [("offsets", offsets), ("order", order), ("slot", slot), ("ws", ws)]
-    _same_device(dev, out)
-    _apart(out, [("ids", ids)])
-    _launch("blr_route_sort", dev, stream, n, experts, _ptr(ids), _ptr(offsets), _ptr(order), _ptr(slot), _ptr(ws),
-            ws.numel())
+    dev, n = ids.get_device(), ids.numel()
+    _on(stream, dev)
+    if not 1 <= experts <= 1024 or n < 1:
+        raise BlrError(-2, "blr_route_sort")
+    work = (None, 0)
+    if ws is not None or n > ROUTE_ONE_LAUNCH:
+        ws, work = _ws(ws, load().blr_route_workspace_bytes(n, experts), "blr_route_workspace_bytes", dev, stream)
+    offsets, at_offsets = _out(offsets, "offsets", i32[0], (experts + 1,), dev, stream)
+    order, at_order = _out(order, "order", i32[0], (n,), dev, stream)
+    slot, at_slot = _out(slot, "slot", i32[0], ids.shape, dev, stream)
+    _launch("blr_route_sort", dev, stream, n, experts, ids.data_ptr(), at_offsets, at_order, at_slot, *work)
     return offsets, order, slot
 
 
-def _route_shapes(offsets, slot):
-    import torch
-    _need(offsets, "offsets", (torch.int32,))
-    _need(slot, "slot", (torch.int32,))
+def _route_plan(offsets, slot, dev):
+    """(T, k, experts, the two addresses)."""
+    i32 = _types()[1]
+    _need(offsets, "offsets", i32)
+    _need(slot, "slot", i32)
     if offsets.dim() != 1 or offsets.numel() < 2:
         raise ValueError(f"offsets has shape {tuple(offsets.shape)}, expected [experts + 1]")
-    if slot.dim() not in (1, 2):
-        raise ValueError(f"slot has shape {tuple(slot.shape)}, expected [T] or [T][k]")
-    return slot.shape[0], (slot.shape[1] if slot.dim() == 2 else 1), offsets.numel() - 1
+    shape = slot.shape
+    if len(shape) not in (1, 2):
+        raise ValueError(f"slot has shape {tuple(shape)}, expected [T] or [T][k]")
+    return (shape[0], shape[1] if len(shape) == 2 else 1, offsets.numel() - 1,
+            _at(offsets, "offsets", i32, offsets.shape, dev), _at(slot, "slot", i32, shape, dev))
 
 
-def _rows(t, name, n):
-    """Width of t, rows [n][d] of one of the wide types."""
-    _need(t, name, _wide())
-    if t.dim() != 2 or t.shape[0] != n:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({n}, d)")
-    return t.shape[1]
+def _rows(t, name, stream):
+    """(number of t's element type, width, GPU) of rows t, where stream is too."""
+    wide = _types()[2]
+    _need(t, name, wide)
+    if t.dim() != 2:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [rows][d]")
+    _on(stream, t.get_device())
+    return wide.index(t.dtype), t.shape[1], t.get_device()
 
 
 def blr_route_gather(x, offsets, slot, *, rows=None, stream=None):
     """Rows by expert: rows[slot[t][j]] = x[t], zero where the pair is not
     placed. Returns rows [T k][d]. Its gradient is blr_route_combine without
     weights."""
-    import torch
-    T, k, E = _route_shapes(offsets, slot)
-    d = _rows(x, "x", T)
-    rows = torch.empty((T * k, d), dtype=x.dtype, device=x.device) if rows is None else \
-        _need(rows, "rows", (x.dtype,), (T * k, d))
-    ins = [("x", x), ("offsets", offsets), ("slot", slot)]
-    _same_device(x.device, ins + [("rows", rows)])
-    _apart([("rows", rows)], ins)
-    _launch("blr_route_gather", x.device, stream, T, k, E, d, _wide().index(x.dtype), _ptr(x), _ptr(offsets), _ptr(slot), _ptr(rows))
+    code, d, dev = _rows(x, "x", stream)
+    T, k, E, at_offsets, at_slot = _route_plan(offsets, slot, dev)
+    at_x = _at(x, "x", (x.dtype,), (T, d), dev)
+    rows, at_rows = _out(rows, "rows", x.dtype, (T * k, d), dev, stream)
+    _launch("blr_route_gather", dev, stream, T, k, E, d, code, at_x, at_offsets, at_slot, at_rows)
     return rows
 
 
@@ -501,19 +542,15 @@ def blr_route_combine(z, offsets, slot, weights=None, *, y=None, accumulate_y=Fa
     """Experts' rows back into tokens: y[t] (+)= sum_j w[t][j] z[slot[t][j]]
     over the placed pairs; weights [T][k] f32, or None for ones. y is
     overwritten unless accumulate_y. Returns y [T][d]."""
-    import torch
-    T, k, E = _route_shapes(offsets, slot)
-    d = _rows(z, "z", T * k)
-    if weights is not None:
-        _need(weights, "weights", (torch.float32,), slot.shape)
+    code, d, dev = _rows(z, "z", stream)
+    T, k, E, at_offsets, at_slot = _route_plan(offsets, slot, dev)
+    at_z = _at(z, "z", (z.dtype,), (T * k, d), dev)
+    at_weights = None if weights is None else _at(weights, "weights", _types()[0], slot.shape, dev)
     if y is None and accumulate_y:
         raise ValueError("accumulate_y needs y")
-    y = torch.empty((T, d), dtype=z.dtype, device=z.device) if y is None else _need(y, "y", (z.dtype,), (T, d))
-    ins = [("z", z), ("offsets", offsets), ("slot", slot), ("weights", weights)]
-    _same_device(z.device, ins + [("y", y)])
-    _apart([("y", y)], ins)
-    _launch("blr_route_combine", z.device, stream, T, k, E, d, _wide().index(z.dtype), _ptr(z), _ptr(offsets), _ptr(slot),
-            _ptr(weights), _ptr(y), int(bool(accumulate_y)))
+    y, at_y = _out(y, "y", z.dtype, (T, d), dev, stream)
+    _launch("blr_route_combine", dev, stream, T, k, E, d, code, at_z, at_offsets, at_slot, at_weights, at_y,
+            1 if accumulate_y else 0)
     return y
 
 
@@ -522,25 +559,21 @@ def blr_route_combine_backward(dy, z, offsets, slot, weights=None, *, dz=None, d
     weights, dw[t][j] = dy[t] . z[slot[t][j]], both zero where the pair is not
     placed. Returns (dz [T k][d], dw [T][k]), dw None without weights (z may
     then be None)."""
-    import torch
-    T, k, E = _route_shapes(offsets, slot)
-    d = _rows(dy, "dy", T)
+    f32 = _types()[0]
+    code, d, dev = _rows(dy, "dy", stream)
+    T, k, E, at_offsets, at_slot = _route_plan(offsets, slot, dev)
+    at_dy = _at(dy, "dy", (dy.dtype,), (T, d), dev)
+    at_weights = at_dw = at_z = None
     if weights is not None:
-        _need(weights, "weights", (torch.float32,), slot.shape)
-        dw = torch.empty(slot.shape, dtype=torch.float32, device=dy.device) if dw is None else \
-            _need(dw, "dw", (torch.float32,), slot.shape)
+        at_weights = _at(weights, "weights", f32, slot.shape, dev)
+        dw, at_dw = _out(dw, "dw", f32[0], slot.shape, dev, stream)
     elif dw is not None:
         raise ValueError("dw needs weights")
     if z is not None or dw is not None:
-        _need(z, "z", (dy.dtype,), (T * k, d))
-    dz = torch.empty((T * k, d), dtype=dy.dtype, device=dy.device) if dz is None else \
-        _need(dz, "dz", (dy.dtype,), (T * k, d))
-    ins = [("dy", dy), ("z", z), ("offsets", offsets), ("slot", slot), ("weights", weights)]
-    out = [("dz", dz), ("dw", dw)]
-    _same_device(dy.device, ins + out)
-    _apart(out, ins)
-    _launch("blr_route_combine_backward", dy.device, stream, T, k, E, d, _wide().index(dy.dtype),
-            _ptr(dy), _ptr(z), _ptr(offsets), _ptr(slot), _ptr(weights), _ptr(dz), _ptr(dw))
+        at_z = _at(z, "z", (dy.dtype,), (T * k, d), dev)
+    dz, at_dz = _out(dz, "dz", dy.dtype, (T * k, d), dev, stream)
+    _launch("blr_route_combine_backward", dev, stream, T, k, E, d, code, at_dy, at_z, at_offsets, at_slot, at_weights,
+            at_dz, at_dw)
     return dz, dw
 
 
@@ -552,26 +585,24 @@ def workspace_adapters(M: int, d_in: int, d_out: int, r: int, adapters: int, dev
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
-def _adapters_shapes(first, name, down, up, offsets, order, scale):
-    """Checks what both adapter calls share; `first` is x or dy. Returns
-    (M, d_in, d_out, r, E, act, wt)."""
-    import torch
-    wide = _wide()
-    _need(first, name, wide)
+def _adapters(rows, name, down, up, offsets, order, scale, ws, stream):
+    """Checks that both adapter calls share; `rows` is x or dy. Returns
+    (sizes and types, addresses of down .. scale, ws, its (address, bytes),
+    GPU)."""
+    f32, i32, wide, _ = _types()
+    act, _, dev = _rows(rows, name, stream)
     _need(down, "down", wide)
     _need(up, "up", (down.dtype,))
-    if first.dim() != 2 or down.dim() != 3 or up.dim() != 3:
-        raise ValueError(f"{name}, down and up are [M][d], [E][r][d_in] and [E][d_out][r]")
+    if down.dim() != 3 or up.dim() != 3:
+        raise ValueError("down and up are [E][r][d_in] and [E][d_out][r]")
     E, r, d_in = down.shape
-    d_out = up.shape[1]
-    _need(up, "up", (down.dtype,), (E, d_out, r))
-    M = first.shape[0]
-    _need(offsets, "offsets", (torch.int32,), (E + 1,))
-    if order is not None:
-        _need(order, "order", (torch.int32,), (M,))
-    if scale is not None:
-        _need(scale, "scale", (torch.float32,), (E,))
-    return M, d_in, d_out, r, E, wide.index(first.dtype), wide.index(down.dtype)
+    M, d_out = rows.shape[0], up.shape[1]
+    at = (_at(down, "down", wide, (E, r, d_in), dev), _at(up, "up", wide, (E, d_out, r), dev),
+          _at(offsets, "offsets", i32, (E + 1,), dev), None if order is None else _at(order, "order", i32, (M,), dev),
+          None if scale is None else _at(scale, "scale", f32, (E,), dev))
+    need = load().blr_adapters_workspace_bytes(M, d_in, d_out, r, E) if ws is None else 0
+    ws, work = _ws(ws, need, "blr_adapters_workspace_bytes", dev, stream)
+    return (M, d_in, d_out, r, E, act, wide.index(down.dtype)), at, ws, work, dev
 
 
 def blr_adapters_forward(x, down, up, offsets, order=None, scale=None, *, y=None, accumulate_y=False, tape_s=None,
@@ -583,25 +614,16 @@ def blr_adapters_forward(x, down, up, offsets, order=None, scale=None, *, y=None
     adapter already. Beside a shared projection give its result as y with
     accumulate_y. The tape x down[e]^T [M][r], which the backward reads, is
     kept when tape_s is given or keep_tape is set. Returns (y, tape_s)."""
-    import torch
-    M, d_in, d_out, r, E, act, wt = _adapters_shapes(x, "x", down, up, offsets, order, scale)
-    _need(x, "x", (x.dtype,), (M, d_in))
-    dev = x.device
     if y is None and accumulate_y:
         raise ValueError("accumulate_y needs y")
-    y = torch.empty((M, d_out), dtype=x.dtype, device=dev) if y is None else _need(y, "y", (x.dtype,), (M, d_out))
-    if tape_s is not None:
-        _need(tape_s, "tape_s", (torch.float32,), (M, r))
-    elif keep_tape:
-        tape_s = torch.empty((M, r), dtype=torch.float32, device=dev)
-    ws = workspace_adapters(M, d_in, d_out, r, E, dev) if ws is None else _need(ws, "ws", (torch.uint8,))
-    ins = [("x", x), ("down", down), ("up", up), ("offsets", offsets), ("order", order), ("scale", scale)]
-    out = [("y", y), ("tape_s", tape_s), ("ws", ws)]
-    _same_device(dev, ins + out)
-    _apart(out, ins)
-    _launch("blr_adapters_forward", dev, stream, M, d_in, d_out, r, E, act, wt, _ptr(x), _ptr(down), _ptr(up),
-            _ptr(offsets), _ptr(order), _ptr(scale), _ptr(y), int(bool(accumulate_y)), _ptr(tape_s), _ptr(ws),
-            ws.numel())
+    sizes, at, ws, work, dev = _adapters(x, "x", down, up, offsets, order, scale, ws, stream)
+    M, d_in, d_out, r = sizes[:4]
+    at_x = _at(x, "x", (x.dtype,), (M, d_in), dev)
+    y, at_y = _out(y, "y", x.dtype, (M, d_out), dev, stream)
+    at_tape = None
+    if keep_tape or tape_s is not None:
+        tape_s, at_tape = _out(tape_s, "tape_s", _types()[0][0], (M, r), dev, stream)
+    _launch("blr_adapters_forward", dev, stream, *sizes, at_x, *at, at_y, 1 if accumulate_y else 0, at_tape, *work)
     return y, tape_s
 
 
@@ -614,38 +636,26 @@ def blr_adapters_backward(x, dy, down, up, offsets, order=None, scale=None, tape
     need_dx=False the gradients alone. Outputs not given are allocated;
     overwritten unless accumulate_grads / accumulate_dx. Returns (grad_down,
     grad_up, dx), None for what was not formed."""
-    import torch
-    M, d_in, d_out, r, E, act, wt = _adapters_shapes(dy, "dy", down, up, offsets, order, scale)
-    f32 = (torch.float32,)
-    _need(dy, "dy", (dy.dtype,), (M, d_out))
-    dev = dy.device
-    if x is not None or grads:
-        _need(x, "x", (dy.dtype,), (M, d_in))
-    if tape_s is not None or grads:
-        _need(tape_s, "tape_s", f32, (M, r))
     if (accumulate_grads and (grad_down is None or grad_up is None)) or (accumulate_dx and dx is None):
         raise ValueError("what is accumulated into has to be given")
-    if grads:
-        grad_down = torch.empty((E, r, d_in), dtype=torch.float32, device=dev) if grad_down is None else \
-            _need(grad_down, "grad_down", f32, (E, r, d_in))
-        grad_up = torch.empty((E, d_out, r), dtype=torch.float32, device=dev) if grad_up is None else \
-            _need(grad_up, "grad_up", f32, (E, d_out, r))
-    elif grad_down is not None or grad_up is not None:
+    if not grads and (grad_down is not None or grad_up is not None):
         raise ValueError("grad_down and grad_up are given, but grads is False")
-    if need_dx:
-        dx = torch.empty((M, d_in), dtype=dy.dtype, device=dev) if dx is None else \
-            _need(dx, "dx", (dy.dtype,), (M, d_in))
-    elif dx is not None:
+    if not need_dx and dx is not None:
         raise ValueError("dx is given, but need_dx is False")
-    ws = workspace_adapters(M, d_in, d_out, r, E, dev) if ws is None else _need(ws, "ws", (torch.uint8,))
-    ins = [("x", x), ("dy", dy), ("down", down), ("up", up), ("offsets", offsets), ("order", order),
-           ("scale", scale), ("tape_s", tape_s)]
-    out = [("grad_down", grad_down), ("grad_up", grad_up), ("dx", dx), ("ws", ws)]
-    _same_device(dev, ins + out)
-    _apart(out, ins)
-    _launch("blr_adapters_backward", dev, stream, M, d_in, d_out, r, E, act, wt, _ptr(x), _ptr(dy), _ptr(down),
-            _ptr(up), _ptr(offsets), _ptr(order), _ptr(scale), _ptr(tape_s), _ptr(grad_down), _ptr(grad_up),
-            int(bool(accumulate_grads)), _ptr(dx), int(bool(accumulate_dx)), _ptr(ws), ws.numel())
+    sizes, at, ws, work, dev = _adapters(dy, "dy", down, up, offsets, order, scale, ws, stream)
+    M, d_in, d_out, r, E = sizes[:5]
+    f32 = _types()[0]
+    at_dy = _at(dy, "dy", (dy.dtype,), (M, d_out), dev)
+    at_x = _at(x, "x", (dy.dtype,), (M, d_in), dev) if grads or x is not None else None
+    at_tape = _at(tape_s, "tape_s", f32, (M, r), dev) if grads or tape_s is not None else None
+    at_down = at_up = at_dx = None
+    if grads:
+        grad_down, at_down = _out(grad_down, "grad_down", f32[0], (E, r, d_in), dev, stream)
+        grad_up, at_up = _out(grad_up, "grad_up", f32[0], (E, d_out, r), dev, stream)
+    if need_dx:
+        dx, at_dx = _out(dx, "dx", dy.dtype, (M, d_in), dev, stream)
+    _launch("blr_adapters_backward", dev, stream, *sizes, at_x, at_dy, *at, at_tape, at_down, at_up,
+            1 if accumulate_grads else 0, at_dx, 1 if accumulate_dx else 0, *work)
     return grad_down, grad_up, dx
 
 

@@ -7,13 +7,18 @@
 //
 // Rows are taken by the plan of the sort (blr_route.hip): a workgroup has a
 // tile of rows of one adapter, found from offsets by every wave for itself.
-// All products run on the f32 matrix instruction: operands of 16 bits are
-// exact in f32, and s, ds and the gradients keep 32 bits throughout.
+// The rank is small, so every contraction is bound by its rows' bytes; the
+// kernels read them from memory straight into matrix operands, once.
 //
-// v_mfma_f32_16x16x4_f32, D += A B: lane l = 16 q + c gives A[c][q] and
-// B[q][c], and holds D[4 q + i][c], i < 4. Which column of a product a k index
-// stands for is free as long as A and B agree; the loads below use that to
-// read four consecutive elements per lane.
+// Rows of f32 run on v_mfma_f32_16x16x4_f32 (D += A B: lane l = 16 q + c gives
+// A[c][q] and B[q][c], and holds D[4 q + i][c], i < 4), with 16-bit adapters
+// widened, which is exact. Rows of 16 bits run on the 16x16x32 instructions
+// (lane gives eight k: A[c][8 q + j], B[8 q + j][c]; D as above), whose
+// products are exact and whose sums are f32; s and ds, which are f32, enter
+// them as two or three 16-bit terms, so that their 16 or 24 leading bits take
+// part (see where they are made). Which column of a product a k index stands
+// for is free as long as A and B agree: the loads use that to read 16
+// consecutive bytes per lane.
 #include "blr_internal.h"
 #include "blr_vec.h"
 
@@ -87,13 +92,104 @@ __device__ __forceinline__ int64_t row_of(const AdaptPlan &plan, int p) {
     return row >= 0 && row < plan.M ? row : -1;
 }
 
+// Matrix instructions on 16-bit operands.
+__device__ __forceinline__ vf4 mfma8(vh8 a, vh8 b, vf4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ vf4 mfma8(vb8 a, vb8 b, vf4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+
 // ---------------------------------------------------------------- shrink --
-// One workgroup: 64 rows x all r over one split of K, wave w every fourth run
-// of 32 columns. X goes from global memory into the A operand as it lies: lane
-// (q, c) holds columns 8 q .. 8 q + 7 of row c, a full 128-byte line per row
-// (f32), so X needs no LDS and is read once.
+// What a lane holds of one step: 128 bytes of each of four rows, over the four
+// lanes q, and the weights of the same columns. Rows of f32: 32 columns, lane
+// q the columns 8 q .. 8 q + 7. Rows of 16 bits: 64, lane q 8 q .. and
+// 32 + 8 q ..
+template <typename TX, typename TW, int RT, bool TRANS>
+struct ShrinkStep {
+    static constexpr int COLS = 32;
+    vf4 x[4][2], w[RT][2];
+
+    __device__ void load(const TX *const *row, int nt, const TW *W, int r, int K, int k0, int q, int c) {
+        k0 += q * 8;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            if (t < nt) {
+                x[t][0] = load4(row[t] + k0);
+                x[t][1] = load4(row[t] + k0 + 4);
+            }
+#pragma unroll
+        for (int n = 0; n < RT; ++n) {
+            const int rank = n * 16 + c;
+            w[n][0] = w[n][1] = vf4{0.f, 0.f, 0.f, 0.f};
+            if (rank < r) {
+                if (TRANS) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) w[n][j >> 2][j & 3] = (float)W[(int64_t)(k0 + j) * r + rank];
+                } else {
+                    w[n][0] = load4(W + (int64_t)rank * K + k0);
+                    w[n][1] = load4(W + (int64_t)rank * K + k0 + 4);
+                }
+            }
+        }
+    }
+    __device__ void multiply(vf4 (&acc)[4][RT], int nt) const {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            if (t < nt)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int n = 0; n < RT; ++n) acc[t][n] = mfma4(x[t][j >> 2][j & 3], w[n][j >> 2][j & 3], acc[t][n]);
+    }
+};
+
+template <typename T, int RT, bool TRANS>
+struct ShrinkStep16 {
+    static constexpr int COLS = 64;
+    typedef typename Vec<T>::v V;
+    V x[4][2], w[RT][2];
+
+    __device__ void load(const T *const *row, int nt, const T *W, int r, int K, int k0, int q, int c) {
+        k0 += q * 8;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            if (t < nt) {
+                x[t][0] = *reinterpret_cast<const V *>(row[t] + k0);
+                x[t][1] = *reinterpret_cast<const V *>(row[t] + k0 + 32);
+            }
+#pragma unroll
+        for (int n = 0; n < RT; ++n) {
+            const int rank = n * 16 + c;
+            w[n][0] = w[n][1] = (V)(T)0;
+            if (rank < r) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (TRANS) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) w[n][h][j] = W[(int64_t)(k0 + 32 * h + j) * r + rank];
+                    } else {
+                        w[n][h] = *reinterpret_cast<const V *>(W + (int64_t)rank * K + k0 + 32 * h);
+                    }
+            }
+        }
+    }
+    __device__ void multiply(vf4 (&acc)[4][RT], int nt) const {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            if (t < nt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int n = 0; n < RT; ++n) acc[t][n] = mfma8(x[t][h], w[n][h], acc[t][n]);
+    }
+};
+template <int RT, bool TRANS>
+struct ShrinkStep<_Float16, _Float16, RT, TRANS> : ShrinkStep16<_Float16, RT, TRANS> {};
+template <int RT, bool TRANS>
+struct ShrinkStep<__bf16, __bf16, RT, TRANS> : ShrinkStep16<__bf16, RT, TRANS> {};
+
+// One workgroup: 64 rows x all r over one split of K, wave w every fourth
+// step. The next step's loads are in flight while one is multiplied.
 template <typename TX, typename TW, int RT, bool TRANS>
 __global__ __launch_bounds__(256) void adapt_shrink_kernel(AdaptShrink a) {
+    typedef ShrinkStep<TX, TW, RT, TRANS> Step;
     __shared__ float red[TM][RT * 16 + 1];
     const Tile tile = find_tile(a.plan, a.plan.E, TM, blockIdx.x);
     if (tile.e < 0) return;
@@ -114,39 +210,16 @@ __global__ __launch_bounds__(256) void adapt_shrink_kernel(AdaptShrink a) {
     for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int n = 0; n < RT; ++n) acc[t][n] = vf4{0.f, 0.f, 0.f, 0.f};
-    const int units = a.K / 128;
-    const int u0 = (int)((int64_t)units * blockIdx.y / a.splits), u1 = (int)((int64_t)units * (blockIdx.y + 1) / a.splits);
-    for (int u = u0; u < u1; ++u) {
-        const int k0 = u * 128 + w * 32 + q * 8;
-        vf4 xv[4][2], wv[RT][2];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (t < nt) {
-                xv[t][0] = load4(x[t] + k0);
-                xv[t][1] = load4(x[t] + k0 + 4);
-            }
-#pragma unroll
-        for (int n = 0; n < RT; ++n) {
-            const int rank = n * 16 + c;
-            wv[n][0] = wv[n][1] = vf4{0.f, 0.f, 0.f, 0.f};
-            if (rank < a.r) {
-                if (TRANS) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) wv[n][j >> 2][j & 3] = (float)W[(int64_t)(k0 + j) * a.r + rank];
-                } else {
-                    wv[n][0] = load4(W + (int64_t)rank * a.K + k0);
-                    wv[n][1] = load4(W + (int64_t)rank * a.K + k0 + 4);
-                }
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (t < nt)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-#pragma unroll
-                    for (int n = 0; n < RT; ++n)
-                        acc[t][n] = mfma4(xv[t][j >> 2][j & 3], wv[n][j >> 2][j & 3], acc[t][n]);
+    const int64_t steps = a.K / Step::COLS;
+    const int end = (int)(steps * (blockIdx.y + 1) / a.splits);
+    int at = (int)(steps * blockIdx.y / a.splits) + w;
+    Step one, two;
+    if (at < end) one.load(x, nt, W, a.r, a.K, at * Step::COLS, q, c);
+    for (; at < end; at += 8) {
+        if (at + 4 < end) two.load(x, nt, W, a.r, a.K, (at + 4) * Step::COLS, q, c);
+        one.multiply(acc, nt);
+        if (at + 8 < end) one.load(x, nt, W, a.r, a.K, (at + 8) * Step::COLS, q, c);
+        if (at + 4 < end) two.multiply(acc, nt);
     }
     // the waves' sums, in wave order
     for (int v = 0; v < 4; ++v) {
@@ -157,8 +230,8 @@ __global__ __launch_bounds__(256) void adapt_shrink_kernel(AdaptShrink a) {
                 for (int n = 0; n < RT; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        float *at = &red[t * 16 + 4 * q + i][n * 16 + c];
-                        *at = v == 0 ? acc[t][n][i] : *at + acc[t][n][i];
+                        float *to = &red[t * 16 + 4 * q + i][n * 16 + c];
+                        *to = v == 0 ? acc[t][n][i] : *to + acc[t][n][i];
                     }
         }
         __syncthreads();
@@ -168,14 +241,202 @@ __global__ __launch_bounds__(256) void adapt_shrink_kernel(AdaptShrink a) {
 }
 
 // ---------------------------------------------------------------- expand --
-// One workgroup: 64 rows x a range of columns, wave w every fourth run of 32.
-// S stays in registers as the B operand for the whole range; the weights are
-// the A operand, so that lane (q, c) ends with eight consecutive columns of
-// row c: out is read into the accumulator and written back a whole line per
-// row, and never passes through LDS.
+// s as the B operand of four tiles of 16 rows, kept for all columns, and one
+// step of columns: the weights are the A operand, with row c = 4 q' + i of
+// tile h standing for column 4 H q' + 4 h + i, so that lane (q, c) ends with
+// the 4 H consecutive columns from 4 H q of row c: out is read and written in
+// whole lines and never passes through LDS.
+//
+// Rows of f32: two tiles, 32 columns a step.
+template <typename TX, typename TW, int RT, bool TRANS>
+struct ExpandStep {
+    static constexpr int H = 2;
+    struct S {
+        vf4 v[4][RT];
+        __device__ void load(const float (*tile)[RT * 16 + 4], const float *, int q, int c) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int n = 0; n < RT; ++n)
+                    v[t][n] = *reinterpret_cast<const vf4 *>(&tile[t * 16 + c][n * 16 + q * 4]);
+        }
+    };
+    vf4 w[H][RT], y[4][H];
+
+    __device__ void load_out(TX *const *out, int o0, int q) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                y[t][h] = vf4{0.f, 0.f, 0.f, 0.f};
+                if (out[t]) y[t][h] = load4(out[t] + o0 + q * 8 + 4 * h);
+            }
+    }
+    __device__ void load_weights(const TW *W, int r, int N, int o0, int q, int c) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const int o = o0 + 8 * (c >> 2) + 4 * h + (c & 3);
+#pragma unroll
+            for (int n = 0; n < RT; ++n) {
+                const int k = n * 16 + q * 4;  // r is a multiple of 8
+                w[h][n] = vf4{0.f, 0.f, 0.f, 0.f};
+                if (k < r) {
+                    if (TRANS) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) w[h][n][j] = (float)W[(int64_t)(k + j) * N + o];
+                    } else {
+                        w[h][n] = load4(W + (int64_t)o * r + k);
+                    }
+                }
+            }
+        }
+    }
+    __device__ void multiply_store(const S &s, TX *const *out, int nt, bool acc, int o0, int q) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            if (t < nt) {
+                vf4 d[H];
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    d[h] = acc ? y[t][h] : vf4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int n = 0; n < RT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) d[h] = mfma4(w[h][n][j], s.v[t][n][j], d[h]);
+                }
+                if (out[t]) {
+#pragma unroll
+                    for (int h = 0; h < H; ++h) store4(out[t] + o0 + q * 8 + 4 * h, d[h]);
+                }
+            }
+    }
+};
+
+// A term of s and what it leaves; nothing where s is not finite, so that an
+// infinity stays one.
+template <typename T>
+__device__ __forceinline__ T take_term(float &v) {
+    const T t = (T)v;
+    const float left = v - (float)t;
+    v = __builtin_isfinite(left) ? left : 0.f;
+    return t;
+}
+
+// Rows of 16 bits: four tiles, 64 columns a step. out is rounded to 16 bits,
+// so two terms of s (16 leading bits in bf16, 22 in f16) leave an error far
+// below that rounding. f16 terms need s near one: each row enters divided by
+// the power of two at its largest element, and the result is multiplied back
+// (both exact). Up to rank 16 both terms share one instruction's 32 k.
+template <typename T, int RT, bool TRANS>
+struct ExpandStep16 {
+    static constexpr int H = 4;
+    static constexpr bool PACKED = RT == 1;
+    static constexpr int KS = (RT + 1) / 2;  // steps of 32 ranks
+    typedef typename Vec<T>::v V;
+    struct S {
+        V hi[4][KS], lo[4][KS];
+        float back[4];
+        __device__ void load(const float (*tile)[RT * 16 + 4], const float *largest, int q, int c) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int m = t * 16 + c;
+                float by = 1.f;
+                back[t] = 1.f;
+                if constexpr (sizeof(T) == 2 && !__is_same(T, __bf16)) {
+                    const float top = largest[m];
+                    if (top > 0.f && __builtin_isfinite(top)) {
+                        int e = (int)((__float_as_uint(top) >> 23) & 255) - 127;  // subnormal: -127
+                        e = e < -120 ? -120 : e > 120 ? 120 : e;
+                        by = __uint_as_float((unsigned)(127 - e) << 23);
+                        back[t] = __uint_as_float((unsigned)(127 + e) << 23);
+                    }
+                }
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk) {
+                    const int k = PACKED ? (q & 1) * 8 : kk * 32 + q * 8;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float v = by * tile[m][k + j];
+                        hi[t][kk][j] = take_term<T>(v);
+                        lo[t][kk][j] = take_term<T>(v);
+                    }
+                    if (PACKED && q >= 2) hi[t][kk] = lo[t][kk];
+                }
+            }
+        }
+    };
+    V w[H][KS], y[4][2];
+
+    __device__ void load_out(T *const *out, int o0, int q) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                y[t][h] = (V)(T)0;
+                if (out[t]) y[t][h] = *reinterpret_cast<const V *>(out[t] + o0 + q * 16 + 8 * h);
+            }
+    }
+    __device__ void load_weights(const T *W, int r, int N, int o0, int q, int c) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const int o = o0 + 16 * (c >> 2) + 4 * h + (c & 3);
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) {
+                const int k = PACKED ? (q & 1) * 8 : kk * 32 + q * 8;
+                w[h][kk] = (V)(T)0;
+                if (k < r) {
+                    if (TRANS) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) w[h][kk][j] = W[(int64_t)(k + j) * N + o];
+                    } else {
+                        w[h][kk] = *reinterpret_cast<const V *>(W + (int64_t)o * r + k);
+                    }
+                }
+            }
+        }
+    }
+    __device__ void multiply_store(const S &s, T *const *out, int nt, bool acc, int o0, int q) {
+        typedef float F __attribute__((ext_vector_type(8)));
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            if (t < nt) {
+                vf4 d[H];
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    d[h] = vf4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int kk = 0; kk < KS; ++kk) {
+                        d[h] = mfma8(w[h][kk], s.hi[t][kk], d[h]);
+                        if (!PACKED) d[h] = mfma8(w[h][kk], s.lo[t][kk], d[h]);
+                    }
+                }
+                if (out[t]) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const vf4 u = s.back[t] * d[2 * h], v = s.back[t] * d[2 * h + 1];
+                        F f = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+                        if (acc) f += __builtin_convertvector(y[t][h], F);
+                        *reinterpret_cast<V *>(out[t] + o0 + q * 16 + 8 * h) = __builtin_convertvector(f, V);
+                    }
+                }
+            }
+    }
+};
+template <int RT, bool TRANS>
+struct ExpandStep<_Float16, _Float16, RT, TRANS> : ExpandStep16<_Float16, RT, TRANS> {};
+template <int RT, bool TRANS>
+struct ExpandStep<__bf16, __bf16, RT, TRANS> : ExpandStep16<__bf16, RT, TRANS> {};
+
+// One workgroup: 64 rows x a range of columns, wave w every fourth step. The
+// prologue adds the splits' partials; the workgroups of the first range also
+// write s out. out and the weights of the next step are in flight while one is
+// multiplied.
 template <typename TX, typename TW, int RT, bool TRANS>
 __global__ __launch_bounds__(256) void adapt_expand_kernel(AdaptExpand a, int chunks) {
+    typedef ExpandStep<TX, TW, RT, TRANS> Step;
+    constexpr int COLS = 16 * Step::H;
     __shared__ float S[TM][RT * 16 + 4];
+    __shared__ float largest[TM];
     const Tile tile = find_tile(a.plan, a.plan.E + 1, TM, blockIdx.x);
     if (tile.e < 0) return;
     const bool none = tile.e == a.plan.E;
@@ -183,79 +444,55 @@ __global__ __launch_bounds__(256) void adapt_expand_kernel(AdaptExpand a, int ch
     const int q = lane >> 4, c = lane & 15;
     const int nt = (tile.cnt + 15) >> 4;
     const float scale = a.scale && !none ? a.scale[tile.e] : 1.f;
-    for (int i = threadIdx.x; i < TM * RT * 16; i += 256) {
+    for (int i = threadIdx.x; i < nt * 16 * RT * 16; i += 256) {
         const int m = i / (RT * 16), k = i % (RT * 16);
         float sum = 0.f;
-        if (m < tile.cnt && k < a.r) {
-            if (!none)
-                for (int sp = 0; sp < a.splits; ++sp)
-                    sum += a.part[((int64_t)sp * a.plan.M + tile.p0 + m) * a.r + k];
-            if (blockIdx.y == 0) {
-                const int64_t row = row_of(a.plan, tile.p0 + m);
-                if (a.s_row && row >= 0) a.s_row[row * a.r + k] = sum;
-                if (a.s_pos) a.s_pos[(int64_t)(tile.p0 + m) * a.r + k] = scale * sum;
-            }
+        if (m < tile.cnt && k < a.r && !none) {
+            const float *part = a.part + (int64_t)(tile.p0 + m) * a.r + k;
+            const int64_t next = (int64_t)a.plan.M * a.r;
+#pragma unroll 8
+            for (int sp = 0; sp < a.splits; ++sp) sum += part[sp * next];
+        }
+        if (blockIdx.y == 0 && m < tile.cnt && k < a.r) {
+            const int64_t row = row_of(a.plan, tile.p0 + m);
+            if (a.s_row && row >= 0) a.s_row[row * a.r + k] = sum;
+            if (a.s_pos) a.s_pos[(int64_t)(tile.p0 + m) * a.r + k] = scale * sum;
         }
         S[m][k] = scale * sum;
     }
     if (a.out == nullptr || (none && a.acc)) return;
     __syncthreads();
+    if (__is_same(TX, _Float16)) {
+        if (threadIdx.x < nt * 16) {
+            float top = 0.f;
+            for (int k = 0; k < RT * 16; ++k) top = fmaxf(top, fabsf(S[threadIdx.x][k]));
+            largest[threadIdx.x] = top;
+        }
+        __syncthreads();
+    }
     TX *out[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
         const int64_t row = t * 16 + c < tile.cnt ? row_of(a.plan, tile.p0 + t * 16 + c) : -1;
         out[t] = row < 0 ? nullptr : reinterpret_cast<TX *>(a.out) + row * a.N;
     }
-    vf4 s[4][RT];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int n = 0; n < RT; ++n) s[t][n] = *reinterpret_cast<const vf4 *>(&S[t * 16 + c][n * 16 + q * 4]);
+    typename Step::S s;
+    s.load(S, largest, q, c);
     const TW *W = reinterpret_cast<const TW *>(a.W) + (int64_t)(none ? 0 : tile.e) * a.r * a.N;
-    const int units = a.N / 128;
-    const int u0 = (int)((int64_t)units * blockIdx.y / chunks), u1 = (int)((int64_t)units * (blockIdx.y + 1) / chunks);
-    for (int u = u0; u < u1; ++u) {
-        const int o0 = u * 128 + w * 32;
-        vf4 acc[4][2];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            acc[t][0] = acc[t][1] = vf4{0.f, 0.f, 0.f, 0.f};
-            if (a.acc && out[t]) {
-                acc[t][0] = load4(out[t] + o0 + q * 8);
-                acc[t][1] = load4(out[t] + o0 + q * 8 + 4);
-            }
-        }
-        if (!none) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                // row c = 4 q' + i of the A operand stands for column 8 q' + 4 h + i
-                const int o = o0 + 8 * (c >> 2) + 4 * h + (c & 3);
-#pragma unroll
-                for (int n = 0; n < RT; ++n) {
-                    vf4 wv = {0.f, 0.f, 0.f, 0.f};
-                    const int k = n * 16 + q * 4;  // r is a multiple of 8
-                    if (k < a.r) {
-                        if (TRANS) {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) wv[j] = (float)W[(int64_t)(k + j) * a.N + o];
-                        } else {
-                            wv = load4(W + (int64_t)o * a.r + k);
-                        }
-                    }
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        if (t < nt)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) acc[t][h] = mfma4(wv[j], s[t][n][j], acc[t][h]);
-                }
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (out[t]) {
-                store4(out[t] + o0 + q * 8, acc[t][0]);
-                store4(out[t] + o0 + q * 8 + 4, acc[t][1]);
-            }
+    const int64_t steps = a.N / COLS;
+    const int end = (int)(steps * (blockIdx.y + 1) / chunks);
+    int at = (int)(steps * blockIdx.y / chunks) + w;
+    Step one, two;
+    auto load = [&](Step &st, int step) {
+        if (a.acc) st.load_out(out, step * COLS, q);
+        st.load_weights(W, none ? 0 : a.r, a.N, step * COLS, q, c);
+    };
+    if (at < end) load(one, at);
+    for (; at < end; at += 8) {
+        if (at + 4 < end) load(two, at + 4);
+        one.multiply_store(s, out, nt, a.acc, at * COLS, q);
+        if (at + 8 < end) load(one, at + 8);
+        if (at + 4 < end) two.multiply_store(s, out, nt, a.acc, (at + 4) * COLS, q);
     }
 }
 
@@ -431,7 +668,7 @@ int64_t adapt_tiles(int64_t M, int64_t E, int64_t tm) {
 }
 
 int adapt_splits(int64_t M, int64_t E, int64_t K) {
-    const int64_t tiles = adapt_tiles(M, E, TM), units = K / 128;
+    const int64_t tiles = adapt_tiles(M, E, TM), units = K / 128;  // a split has a step for each wave in f32
     int64_t sp = (FILL / 2 + tiles - 1) / tiles;
     sp = sp > units ? units : sp;
     return (int)(sp > ADAPT_MAX_SPLITS ? ADAPT_MAX_SPLITS : sp);

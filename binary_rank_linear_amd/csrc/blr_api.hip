@@ -168,6 +168,7 @@ const char *blr_status_string(int status) {
         case BLR_ERR_HIP: return "HIP runtime error";
         case BLR_ERR_ALIGN: return "a pointer is not 16-byte aligned";
         case BLR_ERR_DTYPE: return "element type (or pair of types) not supported by this call";
+        case BLR_ERR_OVERLAP: return "an output shares memory with another argument";
         case BLR_ERR_SCRATCH: return "sizes need more than the allocation-free forward's scratch (r * d_in / 8 bytes)";
     }
     return "unknown status";
@@ -569,6 +570,28 @@ int blr_sumsq(const float *a, int64_t n, float *partials, int nparts, void *stre
 namespace {
 constexpr int64_t MAX_POSITIONS = ((int64_t)1 << 31) - 65536;  // int32 positions, with room for a grid's tail
 
+// An argument's memory; an output must be apart from every other argument.
+struct Span {
+    const void *p;
+    size_t bytes;
+    bool out;
+};
+
+bool apart(const Span *s, int n) {
+    for (int i = 0; i < n; ++i) {
+        if (!s[i].out || !s[i].p) continue;
+        const uintptr_t lo = (uintptr_t)s[i].p, hi = lo + s[i].bytes;
+        for (int j = 0; j < n; ++j) {
+            if (j == i || !s[j].p) continue;
+            const uintptr_t l = (uintptr_t)s[j].p;
+            if (l < hi && lo < l + s[j].bytes) return false;
+        }
+    }
+    return true;
+}
+
+size_t size_of(int dtype) { return dtype == BLR_F32 ? 4 : 2; }
+
 bool dtype_ok(int t) { return t == BLR_F32 || t == BLR_F16 || t == BLR_BF16; }
 
 bool route_shape_ok(int64_t pairs, int64_t experts) {
@@ -596,14 +619,20 @@ int blr_route_sort(int64_t pairs, int64_t experts, const int32_t *ids, int32_t *
                    int32_t *slot, void *workspace, size_t workspace_bytes, void *stream) {
     if (!ids || !offsets || !order || !slot) return BLR_ERR_NULL;
     if (!route_shape_ok(pairs, experts)) return BLR_ERR_SHAPE;
-    if (workspace == nullptr || workspace_bytes < blr_route_workspace_bytes(pairs, experts)) return BLR_ERR_WORKSPACE;
+    int64_t per = 0;
+    const int64_t ranges = route_ranges(pairs, &per);
+    const size_t need = ranges > 1 ? blr_route_workspace_bytes(pairs, experts) : 0;
+    if (workspace_bytes < need || (need && workspace == nullptr)) return BLR_ERR_WORKSPACE;
     if (!aligned4(ids) || !aligned4(offsets) || !aligned4(order) || !aligned4(slot) || !aligned16(workspace))
         return BLR_ERR_ALIGN;
+    const size_t list = (size_t)pairs * 4;
+    const Span spans[] = {{ids, list, false}, {offsets, (size_t)(experts + 1) * 4, true}, {order, list, true},
+                          {slot, list, true}, {need ? workspace : nullptr, need, true}};
+    if (!apart(spans, 5)) return BLR_ERR_OVERLAP;
     int st = current_device_ok();
     if (st != BLR_OK) return st;
-    int64_t per = 0;
     RouteSortArgs a = {};
-    a.ranges = (int)route_ranges(pairs, &per);
+    a.ranges = (int)ranges;
     a.per_range = (int)per;
     a.ids = ids;
     a.offsets = offsets;
@@ -619,7 +648,12 @@ int blr_route_sort(int64_t pairs, int64_t experts, const int32_t *ids, int32_t *
 int blr_route_gather(int64_t T, int64_t k, int64_t experts, int64_t d, int dtype, const void *x,
                      const int32_t *offsets, const int32_t *slot, void *rows, void *stream) {
     int st = route_rows_check(T, k, experts, d, dtype, x, offsets, slot, rows);
-    if (st == BLR_OK) st = current_device_ok();
+    if (st != BLR_OK) return st;
+    const size_t row = (size_t)d * size_of(dtype), list = (size_t)(T * k) * 4;
+    const Span spans[] = {{x, T * row, false}, {offsets, (size_t)(experts + 1) * 4, false}, {slot, list, false},
+                          {rows, T * k * row, true}};
+    if (!apart(spans, 4)) return BLR_ERR_OVERLAP;
+    st = current_device_ok();
     if (st != BLR_OK) return st;
     RouteRows a = {};
     a.placed = offsets + experts;
@@ -640,6 +674,10 @@ int blr_route_combine(int64_t T, int64_t k, int64_t experts, int64_t d, int dtyp
     int st = route_rows_check(T, k, experts, d, dtype, z, offsets, slot, y);
     if (st != BLR_OK) return st;
     if (!aligned4(weights)) return BLR_ERR_ALIGN;
+    const size_t row = (size_t)d * size_of(dtype), list = (size_t)(T * k) * 4;
+    const Span spans[] = {{z, T * k * row, false}, {offsets, (size_t)(experts + 1) * 4, false}, {slot, list, false},
+                          {weights, list, false}, {y, T * row, true}};
+    if (!apart(spans, 5)) return BLR_ERR_OVERLAP;
     st = current_device_ok();
     if (st != BLR_OK) return st;
     RouteRows a = {};
@@ -664,6 +702,10 @@ int blr_route_combine_backward(int64_t T, int64_t k, int64_t experts, int64_t d,
     int st = route_rows_check(T, k, experts, d, dtype, dy, offsets, slot, dz);
     if (st != BLR_OK) return st;
     if (!aligned16(z) || !aligned4(weights) || !aligned4(dw)) return BLR_ERR_ALIGN;
+    const size_t row = (size_t)d * size_of(dtype), list = (size_t)(T * k) * 4;
+    const Span spans[] = {{dy, T * row, false}, {z, T * k * row, false}, {offsets, (size_t)(experts + 1) * 4, false},
+                          {slot, list, false}, {weights, list, false}, {dz, T * k * row, true}, {dw, list, true}};
+    if (!apart(spans, 7)) return BLR_ERR_OVERLAP;
     st = current_device_ok();
     if (st != BLR_OK) return st;
     RouteRows a = {};
@@ -745,6 +787,12 @@ int blr_adapters_forward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int6
                          workspace_bytes, &need);
     if (st != BLR_OK) return st;
     if (!aligned16(x) || !aligned16(y) || !aligned16(tape_s)) return BLR_ERR_ALIGN;
+    const size_t a = size_of(act), w = (size_t)adapters * r * size_of(wt);
+    const Span spans[] = {{x, M * d_in * a, false}, {down, w * d_in, false}, {up, w * d_out, false},
+                          {offsets, (size_t)(adapters + 1) * 4, false}, {order, (size_t)M * 4, false},
+                          {scale, (size_t)adapters * 4, false}, {y, M * d_out * a, true},
+                          {tape_s, (size_t)M * r * 4, true}, {workspace, need, true}};
+    if (!apart(spans, 9)) return BLR_ERR_OVERLAP;
     st = current_device_ok();
     if (st != BLR_OK) return st;
     hipStream_t s = (hipStream_t)stream;
@@ -790,6 +838,13 @@ int blr_adapters_backward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int
     const void *arrays[] = {x, dy, tape_s, grad_down, grad_up, dx};
     for (const void *p : arrays)
         if (!aligned16(p)) return BLR_ERR_ALIGN;
+    const size_t a = size_of(act), w = (size_t)adapters * r;
+    const Span spans[] = {{x, M * d_in * a, false}, {dy, M * d_out * a, false}, {down, w * d_in * size_of(wt), false},
+                          {up, w * d_out * size_of(wt), false}, {offsets, (size_t)(adapters + 1) * 4, false},
+                          {order, (size_t)M * 4, false}, {scale, (size_t)adapters * 4, false},
+                          {tape_s, (size_t)M * r * 4, false}, {grad_down, w * d_in * 4, true},
+                          {grad_up, w * d_out * 4, true}, {dx, M * d_in * a, true}, {workspace, need, true}};
+    if (!apart(spans, 12)) return BLR_ERR_OVERLAP;
     st = current_device_ok();
     if (st != BLR_OK) return st;
     hipStream_t s = (hipStream_t)stream;

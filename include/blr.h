@@ -60,7 +60,8 @@ typedef enum {
     BLR_ERR_HIP = -6,       /* the HIP runtime reported an error */
     BLR_ERR_ALIGN = -7,     /* a pointer is not 16-byte aligned */
     BLR_ERR_SCRATCH = -8,   /* sizes exceed the allocation-free forward's scratch */
-    BLR_ERR_DTYPE = -9      /* an element type, or a pair of them, that the call does not take */
+    BLR_ERR_DTYPE = -9,     /* an element type, or a pair of them, that the call does not take */
+    BLR_ERR_OVERLAP = -10   /* an output shares memory with another argument (routing and adapter calls) */
 } blr_status;
 
 /* Human-readable text of a status code (static storage). */
@@ -233,7 +234,8 @@ typedef enum { BLR_F32 = 0, BLR_F16 = 1, BLR_BF16 = 2 } blr_dtype;
  *     offsets[e + 1] - 1; offsets[E] pairs have an expert ("are placed")
  * 1 <= pairs < 2^31 - 65536, 1 <= E <= 1024. All three outputs are written
  * whole, and are the same on every run. Pointers 4-byte aligned, the
- * workspace (blr_route_workspace_bytes, 0 for invalid sizes) 16-byte.
+ * workspace (blr_route_workspace_bytes, 0 for invalid sizes) 16-byte; up to
+ * 8192 pairs need none (NULL).
  */
 size_t blr_route_workspace_bytes(int64_t pairs, int64_t experts);
 int blr_route_sort(int64_t pairs, int64_t experts, const int32_t *ids, int32_t *offsets, int32_t *order,

@@ -405,15 +405,15 @@ def test_binding_refuses(dev):
     for bad in [lambda: fwd(x[:, :64], down, up, o), lambda: fwd(x, down, up[:2], o), lambda: fwd(x, down, up, o[:2]),
                 lambda: fwd(x, down, up, o, order[:4]), lambda: fwd(x, down, up, o, order, c[:1]),
                 lambda: fwd(x, down, up, o, accumulate_y=True), lambda: fwd(x[0], down, up, o),
-                lambda: fwd(x, down, up, o, y=x), lambda: fwd(dy, up, up, o), lambda: fwd(x.cpu(), down, up, o),
+                lambda: fwd(dy, up, up, o), lambda: fwd(x.cpu(), down, up, o),
                 lambda: fwd(torch.zeros((128, 8), device=dev).t(), down, up, o),
-                lambda: bwd(x, dy, down, up, o, order, c, tape, dx=x),
                 lambda: bwd(x, dy, down, up, o, order, c, tape, accumulate_grads=True),
                 lambda: bwd(x, dy, down, up, o, order, c, tape, grads=False, grad_down=torch.zeros_like(down)),
                 lambda: bwd(x, dy, down, up, o, order, c, tape, need_dx=False, dx=torch.zeros_like(x))]:
         with pytest.raises(ValueError):
             bad()
-    for bad in [lambda: fwd(x.half(), down, up, o), lambda: fwd(x.half(), down.bfloat16(), up.bfloat16(), o),
+    for bad in [lambda: bwd(x, dy, down, up, o, order, c, tape, dx=x),
+                lambda: fwd(x.half(), down, up, o), lambda: fwd(x.half(), down.bfloat16(), up.bfloat16(), o),
                 lambda: fwd(x, down[:, :4].contiguous(), up[:, :, :4].contiguous(), o),
                 lambda: fwd(x, down, up, o, ws=torch.empty(64, dtype=torch.uint8, device=dev)),
                 lambda: bwd(x, dy, down, up, o, order, c, tape, grads=False, need_dx=False)]:

@@ -227,10 +227,10 @@ def test_binding_refuses(dev):
         blr.blr_route_sort(ids[:0], 4)
     with pytest.raises(ValueError):
         blr.blr_route_sort(ids.t(), 4)
-    with pytest.raises(ValueError):
+    with pytest.raises(blr.BlrError):
         blr.blr_route_sort(ids, 4, slot=ids)
     with pytest.raises(blr.BlrError):
-        blr.blr_route_sort(ids, 4, ws=torch.empty(16, dtype=torch.uint8, device=dev))
+        blr.blr_route_sort(ids.repeat(2000, 1), 4, ws=torch.empty(16, dtype=torch.uint8, device=dev))
     offsets, order, slot = blr.blr_route_sort(ids, 4)
     x = torch.zeros((4, 64), device=dev)
     with pytest.raises(TypeError):
@@ -244,7 +244,7 @@ def test_binding_refuses(dev):
     z = torch.zeros((8, 64), device=dev)
     with pytest.raises(ValueError):
         blr.blr_route_combine(z, offsets, slot, accumulate_y=True)
-    with pytest.raises(ValueError):
+    with pytest.raises(blr.BlrError):
         blr.blr_route_combine(z, offsets, slot, y=z[:4])
     with pytest.raises(TypeError):
         blr.blr_route_combine(z, offsets, slot, torch.zeros((4, 2), dtype=torch.float16, device=dev))
