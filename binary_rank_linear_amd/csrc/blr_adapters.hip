@@ -96,219 +96,224 @@ __device__ __forceinline__ int64_t row_of(const AdaptPlan &plan, int p) {
 __device__ __forceinline__ vf4 mfma8(vh8 a, vh8 b, vf4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 __device__ __forceinline__ vf4 mfma8(vb8 a, vb8 b, vf4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
 
+// Walks a wave's n steps with two register sets (DEEP): the next step's loads
+// are in flight while one is used. The walk has no branch around a load (a
+// wave's last extra load repeats its last step), or every wait would be for
+// all; the barriers keep the compiler from moving the loads behind the
+// products. Ranks over 64 leave no room for a second set.
+template <typename Step, bool DEEP, typename Load, typename Use>
+__device__ __forceinline__ void walk(int n, Load load, Use use) {
+    if (n <= 0) return;
+    if constexpr (!DEEP) {
+        for (int i = 0; i < n; ++i) {
+            Step st;
+            load(st, i);
+            use(st, i);
+        }
+    } else {
+        Step one, two;
+        load(one, 0);
+        int i = 0;
+        for (; i + 2 <= n; i += 2) {
+            load(two, i + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            use(one, i);
+            __builtin_amdgcn_sched_barrier(0);
+            load(one, i + 2 < n ? i + 2 : n - 1);
+            __builtin_amdgcn_sched_barrier(0);
+            use(two, i + 1);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (i < n) use(one, i);
+    }
+}
+
 // ---------------------------------------------------------------- shrink --
-// What a lane holds of one step: 128 bytes of each of four rows, over the four
-// lanes q, and the weights of the same columns. Rows of f32: 32 columns, lane
-// q the columns 8 q .. 8 q + 7. Rows of 16 bits: 64, lane q 8 q .. and
-// 32 + 8 q ..
-template <typename TX, typename TW, int RT, bool TRANS>
+// What a lane holds of one step: 128 bytes of each of NT x 16 rows, over the
+// four lanes q, and the weights of the same columns. Rows of f32: 32 columns,
+// lane q the columns 4 q .. 4 q + 3 and 16 + 4 q .. Rows of 16 bits: 64, lane
+// q 8 q .. 8 q + 7 and 32 + 8 q ..
+template <typename TX, typename TW, int RT, int NT>
 struct ShrinkStep {
     static constexpr int COLS = 32;
-    vf4 x[4][2], w[RT][2];
+    vf4 x[NT][2], w[RT][2];
 
-    __device__ void load(const TX *const *row, int nt, const TW *W, int r, int K, int k0, int q, int c) {
-        k0 += q * 8;
+    __device__ __forceinline__ void load(const TX *const *row, const TW *W, int r, int K, int k0, int q, int c) {
+        k0 += q * 4;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (t < nt) {
-                x[t][0] = load4(row[t] + k0);
-                x[t][1] = load4(row[t] + k0 + 4);
-            }
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) x[t][h] = load4(row[t] + k0 + 16 * h);
 #pragma unroll
         for (int n = 0; n < RT; ++n) {
-            const int rank = n * 16 + c;
-            w[n][0] = w[n][1] = vf4{0.f, 0.f, 0.f, 0.f};
-            if (rank < r) {
-                if (TRANS) {
+            const int rank = n * 16 + c < r ? n * 16 + c : r - 1;  // columns past r of the product are not stored
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) w[n][j >> 2][j & 3] = (float)W[(int64_t)(k0 + j) * r + rank];
-                } else {
-                    w[n][0] = load4(W + (int64_t)rank * K + k0);
-                    w[n][1] = load4(W + (int64_t)rank * K + k0 + 4);
-                }
-            }
+            for (int h = 0; h < 2; ++h) w[n][h] = load4(W + (int64_t)rank * K + k0 + 16 * h);
         }
     }
-    __device__ void multiply(vf4 (&acc)[4][RT], int nt) const {
+    __device__ __forceinline__ void multiply(vf4 (&acc)[NT][RT]) const {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (t < nt)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int n = 0; n < RT; ++n) acc[t][n] = mfma4(x[t][j >> 2][j & 3], w[n][j >> 2][j & 3], acc[t][n]);
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int n = 0; n < RT; ++n) acc[t][n] = mfma4(x[t][h][j], w[n][h][j], acc[t][n]);
     }
 };
 
-template <typename T, int RT, bool TRANS>
+template <typename T, int RT, int NT>
 struct ShrinkStep16 {
     static constexpr int COLS = 64;
     typedef typename Vec<T>::v V;
-    V x[4][2], w[RT][2];
+    V x[NT][2], w[RT][2];
 
-    __device__ void load(const T *const *row, int nt, const T *W, int r, int K, int k0, int q, int c) {
+    __device__ __forceinline__ void load(const T *const *row, const T *W, int r, int K, int k0, int q, int c) {
         k0 += q * 8;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (t < nt) {
-                x[t][0] = *reinterpret_cast<const V *>(row[t] + k0);
-                x[t][1] = *reinterpret_cast<const V *>(row[t] + k0 + 32);
-            }
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) x[t][h] = *reinterpret_cast<const V *>(row[t] + k0 + 32 * h);
 #pragma unroll
         for (int n = 0; n < RT; ++n) {
-            const int rank = n * 16 + c;
-            w[n][0] = w[n][1] = (V)(T)0;
-            if (rank < r) {
+            const int rank = n * 16 + c < r ? n * 16 + c : r - 1;
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (TRANS) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) w[n][h][j] = W[(int64_t)(k0 + 32 * h + j) * r + rank];
-                    } else {
-                        w[n][h] = *reinterpret_cast<const V *>(W + (int64_t)rank * K + k0 + 32 * h);
-                    }
-            }
+            for (int h = 0; h < 2; ++h) w[n][h] = *reinterpret_cast<const V *>(W + (int64_t)rank * K + k0 + 32 * h);
         }
     }
-    __device__ void multiply(vf4 (&acc)[4][RT], int nt) const {
+    __device__ __forceinline__ void multiply(vf4 (&acc)[NT][RT]) const {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (t < nt)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int n = 0; n < RT; ++n) acc[t][n] = mfma8(x[t][h], w[n][h], acc[t][n]);
+                for (int n = 0; n < RT; ++n) acc[t][n] = mfma8(x[t][h], w[n][h], acc[t][n]);
     }
 };
-template <int RT, bool TRANS>
-struct ShrinkStep<_Float16, _Float16, RT, TRANS> : ShrinkStep16<_Float16, RT, TRANS> {};
-template <int RT, bool TRANS>
-struct ShrinkStep<__bf16, __bf16, RT, TRANS> : ShrinkStep16<__bf16, RT, TRANS> {};
+template <int RT, int NT>
+struct ShrinkStep<_Float16, _Float16, RT, NT> : ShrinkStep16<_Float16, RT, NT> {};
+template <int RT, int NT>
+struct ShrinkStep<__bf16, __bf16, RT, NT> : ShrinkStep16<__bf16, RT, NT> {};
 
-// One workgroup: 64 rows x all r over one split of K, wave w every fourth
-// step. The next step's loads are in flight while one is multiplied.
-template <typename TX, typename TW, int RT, bool TRANS>
-__global__ __launch_bounds__(256) void adapt_shrink_kernel(AdaptShrink a) {
-    typedef ShrinkStep<TX, TW, RT, TRANS> Step;
-    __shared__ float red[TM][RT * 16 + 1];
-    const Tile tile = find_tile(a.plan, a.plan.E, TM, blockIdx.x);
-    if (tile.e < 0) return;
+// A wave's steps (every fourth of [from, to)) over NT x 16 rows of the tile,
+// then the four waves' sums, in wave order, into red.
+template <typename TX, typename TW, int RT, int NT>
+__device__ void shrink_tile(const AdaptShrink &a, const Tile &tile, int from, int to, float (*red)[RT * 16 + 1]) {
+    typedef ShrinkStep<TX, TW, RT, NT> Step;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int q = lane >> 4, c = lane & 15;
-    const int nt = (tile.cnt + 15) >> 4;
     const TW *W = reinterpret_cast<const TW *>(a.W) + (int64_t)tile.e * a.r * a.K;
-    const TX *x[4];
+    const TX *x[NT];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int t = 0; t < NT; ++t) {
         // rows past the tile, or not named by the plan, repeat one; not stored
         const int p = t * 16 + c < tile.cnt ? t * 16 + c : tile.cnt - 1;
         const int64_t row = row_of(a.plan, tile.p0 + p);
         x[t] = reinterpret_cast<const TX *>(a.X) + (row < 0 ? 0 : row) * a.K;
     }
-    vf4 acc[4][RT];
+    vf4 acc[NT][RT];
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int n = 0; n < RT; ++n) acc[t][n] = vf4{0.f, 0.f, 0.f, 0.f};
-    const int64_t steps = a.K / Step::COLS;
-    const int end = (int)(steps * (blockIdx.y + 1) / a.splits);
-    int at = (int)(steps * blockIdx.y / a.splits) + w;
-    Step one, two;
-    if (at < end) one.load(x, nt, W, a.r, a.K, at * Step::COLS, q, c);
-    for (; at < end; at += 8) {
-        if (at + 4 < end) two.load(x, nt, W, a.r, a.K, (at + 4) * Step::COLS, q, c);
-        one.multiply(acc, nt);
-        if (at + 8 < end) one.load(x, nt, W, a.r, a.K, (at + 8) * Step::COLS, q, c);
-        if (at + 4 < end) two.multiply(acc, nt);
-    }
-    // the waves' sums, in wave order
+    const int first = from + w;
+    walk<Step, RT <= 4>((to - first + 3) / 4,
+               [&](Step &s, int i) { s.load(x, W, a.r, a.K, (first + 4 * i) * Step::COLS, q, c); },
+               [&](const Step &s, int) { s.multiply(acc); });
     for (int v = 0; v < 4; ++v) {
         if (w == v) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int n = 0; n < RT; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        float *to = &red[t * 16 + 4 * q + i][n * 16 + c];
-                        *to = v == 0 ? acc[t][n][i] : *to + acc[t][n][i];
+                        float *at = &red[t * 16 + 4 * q + i][n * 16 + c];
+                        *at = v == 0 ? acc[t][n][i] : *at + acc[t][n][i];
                     }
         }
         __syncthreads();
     }
+}
+
+// One workgroup: 64 rows x all r over one split of K.
+template <typename TX, typename TW, int RT>
+__global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_shrink_kernel(AdaptShrink a) {
+    __shared__ float red[TM][RT * 16 + 1];
+    const Tile tile = find_tile(a.plan, a.plan.E, TM, blockIdx.x);
+    if (tile.e < 0) return;
+    const int64_t steps = a.K / ShrinkStep<TX, TW, RT, 1>::COLS;
+    const int from = (int)(steps * blockIdx.y / a.splits), to = (int)(steps * (blockIdx.y + 1) / a.splits);
+    if (tile.cnt <= 16)
+        shrink_tile<TX, TW, RT, 1>(a, tile, from, to, red);
+    else
+        shrink_tile<TX, TW, RT, 4>(a, tile, from, to, red);
     float *part = a.part + ((int64_t)blockIdx.y * a.plan.M + tile.p0) * a.r;
     for (int i = threadIdx.x; i < tile.cnt * a.r; i += 256) part[i] = red[i / a.r][i % a.r];
 }
 
 // ---------------------------------------------------------------- expand --
-// s as the B operand of four tiles of 16 rows, kept for all columns, and one
-// step of columns: the weights are the A operand, with row c = 4 q' + i of
-// tile h standing for column 4 H q' + 4 h + i, so that lane (q, c) ends with
-// the 4 H consecutive columns from 4 H q of row c: out is read and written in
-// whole lines and never passes through LDS.
+// s as the B operand of NT tiles of 16 rows, kept for all columns, and one
+// step of columns: the weights are the A operand, its rows placed on columns
+// so that lane (q, c) ends with 16 consecutive bytes of row c, next to those
+// of the lanes q: out is read and written in whole lines and never passes
+// through LDS. row[t] is a row to read (repeated past the tile's end), out[t]
+// the row to write or null.
 //
-// Rows of f32: two tiles, 32 columns a step.
-template <typename TX, typename TW, int RT, bool TRANS>
+// Rows of f32: two tiles of 16 columns a step, tile h at 16 h.
+template <typename TX, typename TW, int RT, int NT>
 struct ExpandStep {
-    static constexpr int H = 2;
+    static constexpr int COLS = 32;
     struct S {
-        vf4 v[4][RT];
-        __device__ void load(const float (*tile)[RT * 16 + 4], const float *, int q, int c) {
+        vf4 v[NT][RT];
+        __device__ __forceinline__ void load(const float (*tile)[RT * 16 + 4], const float *, int q, int c) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int n = 0; n < RT; ++n)
                     v[t][n] = *reinterpret_cast<const vf4 *>(&tile[t * 16 + c][n * 16 + q * 4]);
         }
     };
-    vf4 w[H][RT], y[4][H];
+    vf4 w[2][RT], y[NT][2];
 
-    __device__ void load_out(TX *const *out, int o0, int q) {
+    template <bool ACC>
+    __device__ __forceinline__ void load(TX *const *row, const TW *W, int r, int N, int o0, int q, int c) {
+        if (ACC) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-                y[t][h] = vf4{0.f, 0.f, 0.f, 0.f};
-                if (out[t]) y[t][h] = load4(out[t] + o0 + q * 8 + 4 * h);
-            }
-    }
-    __device__ void load_weights(const TW *W, int r, int N, int o0, int q, int c) {
+                for (int h = 0; h < 2; ++h) y[t][h] = load4(row[t] + o0 + 16 * h + 4 * q);
+        }
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-            const int o = o0 + 8 * (c >> 2) + 4 * h + (c & 3);
+        for (int h = 0; h < 2; ++h) {
+            const int o = o0 + 16 * h + c;
 #pragma unroll
             for (int n = 0; n < RT; ++n) {
-                const int k = n * 16 + q * 4;  // r is a multiple of 8
-                w[h][n] = vf4{0.f, 0.f, 0.f, 0.f};
-                if (k < r) {
-                    if (TRANS) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) w[h][n][j] = (float)W[(int64_t)(k + j) * N + o];
-                    } else {
-                        w[h][n] = load4(W + (int64_t)o * r + k);
-                    }
-                }
+                const int k = n * 16 + q * 4, kc = k < r ? k : 0;  // r is a multiple of 8
+                w[h][n] = load4(W + (int64_t)o * r + kc);
+                if (k >= r) w[h][n] = vf4{0.f, 0.f, 0.f, 0.f};
             }
         }
     }
-    __device__ void multiply_store(const S &s, TX *const *out, int nt, bool acc, int o0, int q) {
+    template <bool ACC, bool FULL>
+    __device__ __forceinline__ void multiply_store(const S &s, TX *const *out, int o0, int q) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (t < nt) {
-                vf4 d[H];
+        for (int t = 0; t < NT; ++t) {
+            vf4 d[2];
 #pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    d[h] = acc ? y[t][h] : vf4{0.f, 0.f, 0.f, 0.f};
+            for (int h = 0; h < 2; ++h) d[h] = ACC ? y[t][h] : vf4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int n = 0; n < RT; ++n)
+            for (int n = 0; n < RT; ++n)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) d[h] = mfma4(w[h][n][j], s.v[t][n][j], d[h]);
-                }
-                if (out[t]) {
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int h = 0; h < H; ++h) store4(out[t] + o0 + q * 8 + 4 * h, d[h]);
-                }
+                    for (int h = 0; h < 2; ++h) d[h] = mfma4(w[h][n][j], s.v[t][n][j], d[h]);
+            if (FULL || out[t]) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) store4(out[t] + o0 + 16 * h + 4 * q, d[h]);
             }
+        }
     }
 };
 
@@ -322,27 +327,28 @@ __device__ __forceinline__ T take_term(float &v) {
     return t;
 }
 
-// Rows of 16 bits: four tiles, 64 columns a step. out is rounded to 16 bits,
-// so two terms of s (16 leading bits in bf16, 22 in f16) leave an error far
-// below that rounding. f16 terms need s near one: each row enters divided by
-// the power of two at its largest element, and the result is multiplied back
-// (both exact). Up to rank 16 both terms share one instruction's 32 k.
-template <typename T, int RT, bool TRANS>
+// Rows of 16 bits: four tiles, 64 columns a step; column i of row 4 q' of tile
+// 2 g + h is 32 g + 8 q' + 4 h + i. out is rounded to 16 bits, so two terms of
+// s (16 leading bits in bf16, 22 in f16) leave an error far below that
+// rounding. f16 terms need s near one: each row enters divided by the power of
+// two at its largest element, and the result is multiplied back (both exact).
+// Up to rank 16 both terms share one instruction's 32 k.
+template <typename T, int RT, int NT>
 struct ExpandStep16 {
-    static constexpr int H = 4;
+    static constexpr int COLS = 64;
     static constexpr bool PACKED = RT == 1;
     static constexpr int KS = (RT + 1) / 2;  // steps of 32 ranks
     typedef typename Vec<T>::v V;
     struct S {
-        V hi[4][KS], lo[4][KS];
-        float back[4];
-        __device__ void load(const float (*tile)[RT * 16 + 4], const float *largest, int q, int c) {
+        V hi[NT][KS], lo[NT][KS];
+        float back[NT];
+        __device__ __forceinline__ void load(const float (*tile)[RT * 16 + 4], const float *largest, int q, int c) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
+            for (int t = 0; t < NT; ++t) {
                 const int m = t * 16 + c;
                 float by = 1.f;
                 back[t] = 1.f;
-                if constexpr (sizeof(T) == 2 && !__is_same(T, __bf16)) {
+                if constexpr (__is_same(T, _Float16)) {
                     const float top = largest[m];
                     if (top > 0.f && __builtin_isfinite(top)) {
                         int e = (int)((__float_as_uint(top) >> 23) & 255) - 127;  // subnormal: -127
@@ -365,86 +371,106 @@ struct ExpandStep16 {
             }
         }
     };
-    V w[H][KS], y[4][2];
+    V w[4][KS], y[NT][2];
 
-    __device__ void load_out(T *const *out, int o0, int q) {
+    template <bool ACC>
+    __device__ __forceinline__ void load(T *const *row, const T *W, int r, int N, int o0, int q, int c) {
+        if (ACC) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                y[t][h] = (V)(T)0;
-                if (out[t]) y[t][h] = *reinterpret_cast<const V *>(out[t] + o0 + q * 16 + 8 * h);
-            }
-    }
-    __device__ void load_weights(const T *W, int r, int N, int o0, int q, int c) {
+                for (int g = 0; g < 2; ++g) y[t][g] = *reinterpret_cast<const V *>(row[t] + o0 + 32 * g + 8 * q);
+        }
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-            const int o = o0 + 16 * (c >> 2) + 4 * h + (c & 3);
+        for (int h = 0; h < 4; ++h) {
+            const int o = o0 + 32 * (h >> 1) + 8 * (c >> 2) + 4 * (h & 1) + (c & 3);
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
-                const int k = PACKED ? (q & 1) * 8 : kk * 32 + q * 8;
-                w[h][kk] = (V)(T)0;
-                if (k < r) {
-                    if (TRANS) {
+                const int k = PACKED ? (q & 1) * 8 : kk * 32 + q * 8, kc = k < r ? k : 0;
+                w[h][kk] = *reinterpret_cast<const V *>(W + (int64_t)o * r + kc);
+                if (k >= r) w[h][kk] = (V)(T)0;
+            }
+        }
+    }
+    template <bool ACC, bool FULL>
+    __device__ __forceinline__ void multiply_store(const S &s, T *const *out, int o0, int q) {
+        typedef float F __attribute__((ext_vector_type(8)));
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) w[h][kk][j] = W[(int64_t)(k + j) * N + o];
-                    } else {
-                        w[h][kk] = *reinterpret_cast<const V *>(W + (int64_t)o * r + k);
-                    }
+        for (int t = 0; t < NT; ++t) {
+            vf4 d[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) d[h] = vf4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) d[h] = mfma8(w[h][kk], s.hi[t][kk], d[h]);
+                if (!PACKED) {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) d[h] = mfma8(w[h][kk], s.lo[t][kk], d[h]);
+                }
+            }
+            if (FULL || out[t]) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const vf4 u = s.back[t] * d[2 * g], v = s.back[t] * d[2 * g + 1];
+                    F f = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+                    if (ACC) f += __builtin_convertvector(y[t][g], F);
+                    *reinterpret_cast<V *>(out[t] + o0 + 32 * g + 8 * q) = __builtin_convertvector(f, V);
                 }
             }
         }
     }
-    __device__ void multiply_store(const S &s, T *const *out, int nt, bool acc, int o0, int q) {
-        typedef float F __attribute__((ext_vector_type(8)));
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (t < nt) {
-                vf4 d[H];
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    d[h] = vf4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int kk = 0; kk < KS; ++kk) {
-                        d[h] = mfma8(w[h][kk], s.hi[t][kk], d[h]);
-                        if (!PACKED) d[h] = mfma8(w[h][kk], s.lo[t][kk], d[h]);
-                    }
-                }
-                if (out[t]) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const vf4 u = s.back[t] * d[2 * h], v = s.back[t] * d[2 * h + 1];
-                        F f = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
-                        if (acc) f += __builtin_convertvector(y[t][h], F);
-                        *reinterpret_cast<V *>(out[t] + o0 + q * 16 + 8 * h) = __builtin_convertvector(f, V);
-                    }
-                }
-            }
-    }
 };
-template <int RT, bool TRANS>
-struct ExpandStep<_Float16, _Float16, RT, TRANS> : ExpandStep16<_Float16, RT, TRANS> {};
-template <int RT, bool TRANS>
-struct ExpandStep<__bf16, __bf16, RT, TRANS> : ExpandStep16<__bf16, RT, TRANS> {};
+template <int RT, int NT>
+struct ExpandStep<_Float16, _Float16, RT, NT> : ExpandStep16<_Float16, RT, NT> {};
+template <int RT, int NT>
+struct ExpandStep<__bf16, __bf16, RT, NT> : ExpandStep16<__bf16, RT, NT> {};
 
-// One workgroup: 64 rows x a range of columns, wave w every fourth step. The
-// prologue adds the splits' partials; the workgroups of the first range also
-// write s out. out and the weights of the next step are in flight while one is
-// multiplied.
-template <typename TX, typename TW, int RT, bool TRANS>
-__global__ __launch_bounds__(256) void adapt_expand_kernel(AdaptExpand a, int chunks) {
-    typedef ExpandStep<TX, TW, RT, TRANS> Step;
-    constexpr int COLS = 16 * Step::H;
+// A wave's steps (every fourth of [from, to)) over NT x 16 rows. FULL: every
+// row of the tile is written.
+template <typename TX, typename TW, int RT, int NT, bool ACC, bool FULL>
+__device__ void expand_tile(const AdaptExpand &a, const Tile &tile, int r, int from, int to,
+                            const float (*S)[RT * 16 + 4], const float *largest) {
+    typedef ExpandStep<TX, TW, RT, NT> Step;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int q = lane >> 4, c = lane & 15;
+    TX *row[NT], *out[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const bool in = t * 16 + c < tile.cnt;
+        const int64_t at = row_of(a.plan, tile.p0 + (in ? t * 16 + c : tile.cnt - 1));
+        row[t] = reinterpret_cast<TX *>(a.out) + (at < 0 ? 0 : at) * a.N;
+        out[t] = in && at >= 0 ? row[t] : nullptr;
+    }
+    typename Step::S s;
+    s.load(S, largest, q, c);
+    const TW *W = reinterpret_cast<const TW *>(a.W) + (int64_t)(r ? tile.e : 0) * a.r * a.N;
+    const int first = from + w;
+    walk<Step, RT <= 4>((to - first + 3) / 4,
+               [&](Step &st, int i) { st.template load<ACC>(row, W, r, a.N, (first + 4 * i) * Step::COLS, q, c); },
+               [&](Step &st, int i) {
+                   st.template multiply_store<ACC, FULL>(s, FULL ? row : out, (first + 4 * i) * Step::COLS, q);
+               });
+}
+
+// One workgroup: 64 rows x a range of columns. The prologue adds the splits'
+// partials; the workgroups of the first range also write s out.
+template <typename TX, typename TW, int RT, bool ACC>
+__global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_expand_kernel(AdaptExpand a, int chunks) {
     __shared__ float S[TM][RT * 16 + 4];
     __shared__ float largest[TM];
+    __shared__ int named;
     const Tile tile = find_tile(a.plan, a.plan.E + 1, TM, blockIdx.x);
     if (tile.e < 0) return;
     const bool none = tile.e == a.plan.E;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int q = lane >> 4, c = lane & 15;
-    const int nt = (tile.cnt + 15) >> 4;
     const float scale = a.scale && !none ? a.scale[tile.e] : 1.f;
-    for (int i = threadIdx.x; i < nt * 16 * RT * 16; i += 256) {
+    if (threadIdx.x < TM) {  // one wave
+        const bool ok = threadIdx.x < tile.cnt && row_of(a.plan, tile.p0 + threadIdx.x) >= 0;
+        if (__ballot(ok) == ~0ull && threadIdx.x == 0) named = 1;
+        if (__ballot(ok) != ~0ull && threadIdx.x == 0) named = 0;
+    }
+    const int rows = tile.cnt <= 16 ? 16 : TM;
+    for (int i = threadIdx.x; i < rows * RT * 16; i += 256) {
         const int m = i / (RT * 16), k = i % (RT * 16);
         float sum = 0.f;
         if (m < tile.cnt && k < a.r && !none) {
@@ -460,39 +486,60 @@ __global__ __launch_bounds__(256) void adapt_expand_kernel(AdaptExpand a, int ch
         }
         S[m][k] = scale * sum;
     }
-    if (a.out == nullptr || (none && a.acc)) return;
+    if (a.out == nullptr || (none && ACC)) return;
     __syncthreads();
     if (__is_same(TX, _Float16)) {
-        if (threadIdx.x < nt * 16) {
+        if (threadIdx.x < rows) {
             float top = 0.f;
             for (int k = 0; k < RT * 16; ++k) top = fmaxf(top, fabsf(S[threadIdx.x][k]));
             largest[threadIdx.x] = top;
         }
         __syncthreads();
     }
-    TX *out[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const int64_t row = t * 16 + c < tile.cnt ? row_of(a.plan, tile.p0 + t * 16 + c) : -1;
-        out[t] = row < 0 ? nullptr : reinterpret_cast<TX *>(a.out) + row * a.N;
+    const int64_t steps = a.N / ExpandStep<TX, TW, RT, 1>::COLS;
+    const int from = (int)(steps * blockIdx.y / chunks), to = (int)(steps * (blockIdx.y + 1) / chunks);
+    const int r = none ? 0 : a.r;
+    if (tile.cnt <= 16)
+        expand_tile<TX, TW, RT, 1, ACC, false>(a, tile, r, from, to, S, largest);
+    else if (named)
+        expand_tile<TX, TW, RT, 4, ACC, true>(a, tile, r, from, to, S, largest);
+    else
+        expand_tile<TX, TW, RT, 4, ACC, false>(a, tile, r, from, to, S, largest);
+}
+
+// ------------------------------------------------------------- transpose --
+// The backward contracts over the other side of A and B than the forward, so
+// it lays their transposes out first: then every operand above and below is
+// read 16 consecutive bytes a lane. Adapters without rows are left out. One
+// workgroup: 64 x 64 elements through LDS.
+template <typename T>
+__global__ __launch_bounds__(256) void adapt_transpose_kernel(AdaptTranspose a) {
+    constexpr int n = 16 / sizeof(T);
+    typedef T V __attribute__((ext_vector_type(n)));
+    __shared__ T tile[64][64 + n];
+    const int e = blockIdx.y;
+    if (a.offsets[e + 1] <= a.offsets[e]) return;
+    const int job = (int)blockIdx.x >= a.tiles[0];
+    const int b = blockIdx.x - (job ? a.tiles[0] : 0);
+    const int R = a.rows[job], C = a.cols[job], across = (C + 63) / 64;
+    const int r0 = b / across * 64, c0 = b % across * 64;
+    const T *src = reinterpret_cast<const T *>(a.src[job]) + (int64_t)e * R * C;
+    T *dst = reinterpret_cast<T *>(a.dst[job]) + (int64_t)e * R * C;
+    constexpr int per = 64 / n;  // vectors of a tile's row
+    for (int i = threadIdx.x; i < 64 * per; i += 256) {
+        const int r = i / per, c = i % per * n;
+        if (r0 + r < R && c0 + c < C)  // R and C are multiples of 8
+            *reinterpret_cast<V *>(&tile[r][c]) = *reinterpret_cast<const V *>(src + (int64_t)(r0 + r) * C + c0 + c);
     }
-    typename Step::S s;
-    s.load(S, largest, q, c);
-    const TW *W = reinterpret_cast<const TW *>(a.W) + (int64_t)(none ? 0 : tile.e) * a.r * a.N;
-    const int64_t steps = a.N / COLS;
-    const int end = (int)(steps * (blockIdx.y + 1) / chunks);
-    int at = (int)(steps * blockIdx.y / chunks) + w;
-    Step one, two;
-    auto load = [&](Step &st, int step) {
-        if (a.acc) st.load_out(out, step * COLS, q);
-        st.load_weights(W, none ? 0 : a.r, a.N, step * COLS, q, c);
-    };
-    if (at < end) load(one, at);
-    for (; at < end; at += 8) {
-        if (at + 4 < end) load(two, at + 4);
-        one.multiply_store(s, out, nt, a.acc, at * COLS, q);
-        if (at + 8 < end) load(one, at + 8);
-        if (at + 4 < end) two.multiply_store(s, out, nt, a.acc, (at + 4) * COLS, q);
+    __syncthreads();
+    for (int i = threadIdx.x; i < 64 * per; i += 256) {
+        const int c = i / per, r = i % per * n;
+        if (r0 + r < R && c0 + c < C) {
+            V v;
+#pragma unroll
+            for (int j = 0; j < n; ++j) v[j] = tile[r + j][c];
+            *reinterpret_cast<V *>(dst + (int64_t)(c0 + c) * R + r0 + r) = v;
+        }
     }
 }
 
@@ -606,22 +653,19 @@ __global__ __launch_bounds__(256) void adapt_reduce_kernel(AdaptGrad a) {
 constexpr int64_t FILL = 1024;
 
 template <typename TX, typename TW, int RT>
-hipError_t shrink_t(const AdaptShrink &a, bool trans, hipStream_t s) {
+hipError_t shrink_t(const AdaptShrink &a, hipStream_t s) {
     const dim3 grid((unsigned)adapt_tiles(a.plan.M, a.plan.E, TM), (unsigned)a.splits);
-    if (trans)
-        hipLaunchKernelGGL((adapt_shrink_kernel<TX, TW, RT, true>), grid, dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL((adapt_shrink_kernel<TX, TW, RT, false>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((adapt_shrink_kernel<TX, TW, RT>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
 template <typename TX, typename TW, int RT>
-hipError_t expand_t(const AdaptExpand &a, bool trans, hipStream_t s) {
+hipError_t expand_t(const AdaptExpand &a, hipStream_t s) {
     const int64_t tiles = adapt_tiles(a.plan.M, a.plan.E, TM), units = a.N / 128;
     int64_t chunks = (FILL + tiles - 1) / tiles;
     chunks = a.out == nullptr ? 1 : chunks > units ? units : chunks;
     const dim3 grid((unsigned)tiles, (unsigned)chunks);
-    if (trans)
+    if (a.acc)
         hipLaunchKernelGGL((adapt_expand_kernel<TX, TW, RT, true>), grid, dim3(256), 0, s, a, (int)chunks);
     else
         hipLaunchKernelGGL((adapt_expand_kernel<TX, TW, RT, false>), grid, dim3(256), 0, s, a, (int)chunks);
@@ -689,16 +733,29 @@ int64_t adapt_range_slots(int64_t M, int64_t E, int64_t range) {
     return twice < all ? twice : all;
 }
 
-hipError_t launch_adapt_shrink(const AdaptShrink &a, bool trans, hipStream_t s) {
-    prof_begin(trans ? K_ADAPT_DS : K_ADAPT_DOWN, s);
-    hipError_t e = BLR_BY_TYPES(a, shrink_t, a, trans, s);
+hipError_t launch_adapt_transpose(AdaptTranspose a, int wt, hipStream_t s) {
+    for (int j = 0; j < 2; ++j) a.tiles[j] = (a.rows[j] + 63) / 64 * ((a.cols[j] + 63) / 64);
+    const dim3 grid((unsigned)(a.tiles[0] + a.tiles[1]), (unsigned)a.E);
+    prof_begin(K_ADAPT_TRANSPOSE, s);
+    if (wt == 0)
+        hipLaunchKernelGGL((adapt_transpose_kernel<uint32_t>), grid, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((adapt_transpose_kernel<uint16_t>), grid, dim3(256), 0, s, a);
+    hipError_t e = hipGetLastError();
     prof_end(s);
     return e;
 }
 
-hipError_t launch_adapt_expand(const AdaptExpand &a, bool trans, hipStream_t s) {
-    prof_begin(trans ? K_ADAPT_DX : K_ADAPT_UP, s);
-    hipError_t e = BLR_BY_TYPES(a, expand_t, a, trans, s);
+hipError_t launch_adapt_shrink(const AdaptShrink &a, int id, hipStream_t s) {
+    prof_begin(id, s);
+    hipError_t e = BLR_BY_TYPES(a, shrink_t, a, s);
+    prof_end(s);
+    return e;
+}
+
+hipError_t launch_adapt_expand(const AdaptExpand &a, int id, hipStream_t s) {
+    prof_begin(id, s);
+    hipError_t e = BLR_BY_TYPES(a, expand_t, a, s);
     prof_end(s);
     return e;
 }

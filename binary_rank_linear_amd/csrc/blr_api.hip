@@ -732,17 +732,23 @@ bool adapt_shape_ok(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t E
            d_out % 128 == 0 && r >= 8 && r <= ADAPT_MAX_RANK && r % 8 == 0 && E >= 1 && E <= ROUTE_MAX_EXPERTS;
 }
 
-// Workspace: the splits' partials of s or ds (f32 [splits][M][r]), then ds by
-// position (f32 [M][r]), then the ranges' partials of one gradient.
+// Workspace: the splits' partials of s or ds (f32 [splits][M][r]), then for
+// the backward the transposes of down and up, ds by position (f32 [M][r]) and
+// the ranges' partials of one gradient.
 struct AdaptLayout {
-    size_t ds, grad, total;
+    size_t down_t, up_t, ds, grad, total;
     int64_t range_in, range_out, slots_in, slots_out;
 };
 
-AdaptLayout adapt_layout(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t E) {
+AdaptLayout adapt_layout(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t E, int wt = BLR_F32) {
     AdaptLayout L;
     const int si = adapt_splits(M, E, d_in), so = adapt_splits(M, E, d_out);
     size_t off = up((size_t)(si > so ? si : so) * M * r * 4);
+    const size_t w = (size_t)E * r * size_of(wt);
+    L.down_t = off;
+    off += up(w * d_in);
+    L.up_t = off;
+    off += up(w * d_out);
     L.ds = off;
     off += up((size_t)M * r * 4);
     L.grad = off;
@@ -763,7 +769,7 @@ int adapt_check(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t E, in
     if (!down || !up_ || !offsets) return BLR_ERR_NULL;
     if (!dtype_ok(act) || !dtype_ok(wt) || (act != BLR_F32 && wt != act)) return BLR_ERR_DTYPE;
     if (!adapt_shape_ok(M, d_in, d_out, r, E)) return BLR_ERR_SHAPE;
-    *need = adapt_layout(M, d_in, d_out, r, E).total;
+    *need = adapt_layout(M, d_in, d_out, r, E).total;  // whatever wt is
     if (workspace == nullptr || workspace_bytes < *need) return BLR_ERR_WORKSPACE;
     if (!aligned16(down) || !aligned16(up_) || !aligned4(offsets) || !aligned4(order) || !aligned4(scale) ||
         !aligned16(workspace))
@@ -806,7 +812,7 @@ int blr_adapters_forward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int6
     sh.splits = adapt_splits(M, adapters, d_in);
     sh.act = act;
     sh.wt = wt;
-    BLR_TRY(launch_adapt_shrink(sh, false, s));
+    BLR_TRY(launch_adapt_shrink(sh, K_ADAPT_DOWN, s));
     AdaptExpand ex = {};
     ex.plan = sh.plan;
     ex.part = sh.part;
@@ -820,7 +826,7 @@ int blr_adapters_forward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int6
     ex.act = act;
     ex.wt = wt;
     ex.acc = accumulate_y ? 1 : 0;
-    BLR_TRY(launch_adapt_expand(ex, false, s));
+    BLR_TRY(launch_adapt_expand(ex, K_ADAPT_UP, s));
     return BLR_OK;
 }
 
@@ -850,23 +856,35 @@ int blr_adapters_backward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int
     hipStream_t s = (hipStream_t)stream;
     const AdaptLayout L = adapt_layout(M, d_in, d_out, r, adapters);
     char *ws = (char *)workspace;
+    AdaptTranspose tr = {};
+    tr.offsets = offsets;
+    tr.E = (int)adapters;
+    tr.src[0] = down;
+    tr.dst[0] = ws + L.down_t;
+    tr.rows[0] = (int)r;
+    tr.cols[0] = (int)d_in;
+    tr.src[1] = up;
+    tr.dst[1] = ws + L.up_t;
+    tr.rows[1] = (int)d_out;
+    tr.cols[1] = (int)r;
+    BLR_TRY(launch_adapt_transpose(tr, wt, s));
     // ds = c dy B: the contraction over d_out, then its splits' sum with dx
     AdaptShrink sh = {};
     sh.plan = {offsets, order, (int)M, (int)adapters};
     sh.X = dy;
-    sh.W = up;
+    sh.W = tr.dst[1];
     sh.part = (float *)ws;
     sh.K = (int)d_out;
     sh.r = (int)r;
     sh.splits = adapt_splits(M, adapters, d_out);
     sh.act = act;
     sh.wt = wt;
-    BLR_TRY(launch_adapt_shrink(sh, true, s));
+    BLR_TRY(launch_adapt_shrink(sh, K_ADAPT_DS, s));
     AdaptExpand ex = {};
     ex.plan = sh.plan;
     ex.part = sh.part;
     ex.scale = scale;
-    ex.W = down;
+    ex.W = tr.dst[0];
     ex.out = dx;
     ex.s_pos = (float *)(ws + L.ds);
     ex.N = (int)d_in;
@@ -875,7 +893,7 @@ int blr_adapters_backward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int
     ex.act = act;
     ex.wt = wt;
     ex.acc = accumulate_dx ? 1 : 0;
-    BLR_TRY(launch_adapt_expand(ex, true, s));
+    BLR_TRY(launch_adapt_expand(ex, K_ADAPT_DX, s));
     if (!grad_down) return BLR_OK;
     AdaptGrad g = {};
     g.plan = sh.plan;

@@ -41,6 +41,7 @@ enum KernelId {
     K_ROUTE_COMBINE_BWD, // gradients of the experts' rows and of the weights
     K_ADAPT_DOWN,   // adapters: partials of s = x A^T
     K_ADAPT_UP,     // adapters: y (+)= c s B^T
+    K_ADAPT_TRANSPOSE, // adapters: A^T and B^T for the backward
     K_ADAPT_DS,     // adapters: partials of ds = c dy B
     K_ADAPT_DX,     // adapters: dx (+)= ds A
     K_ADAPT_GRAD,   // adapters: gradients of A and B over ranges of rows
@@ -230,7 +231,7 @@ struct AdaptPlan {
     int M, E;
 };
 // part[split][p][r] = sum over the split's columns of X[row(p)][k] W_e[.][k]
-// with W_e = W + e r K: [r][K], or [K][r] when trans.
+// with W_e = W + e r K, [r][K].
 struct AdaptShrink {
     AdaptPlan plan;
     const void *X, *W;
@@ -238,7 +239,7 @@ struct AdaptShrink {
     int K, r, splits, act, wt;
 };
 // out[row(p)][n] (+)= sum_k S[p][k] W_e[n][k], S[p] = scale_e sum over splits
-// of part[.][p]; W_e: [N][r], or [r][N] when trans. S goes to s_row by row,
+// of part[.][p]; W_e: [N][r]. S goes to s_row by row,
 // unscaled, and to s_pos by position, scaled (either may be null).
 struct AdaptExpand {
     AdaptPlan plan;
@@ -262,8 +263,20 @@ struct AdaptGrad {
     int N, r, act, acc, range, thin_by_row;
     int64_t slots;  // partials that `part` has room for
 };
-hipError_t launch_adapt_shrink(const AdaptShrink &a, bool trans, hipStream_t s);
-hipError_t launch_adapt_expand(const AdaptExpand &a, bool trans, hipStream_t s);
+// dst_e [cols][rows] = the transpose of src_e [rows][cols], for the adapters
+// that have rows; two tables in one launch.
+struct AdaptTranspose {
+    const int32_t *offsets;
+    int E;
+    const void *src[2];
+    void *dst[2];
+    int rows[2], cols[2];
+    int tiles[2];  // filled by the launcher
+};
+hipError_t launch_adapt_transpose(AdaptTranspose a, int wt, hipStream_t s);
+// id: the kernel kind that the launch is timed as.
+hipError_t launch_adapt_shrink(const AdaptShrink &a, int id, hipStream_t s);
+hipError_t launch_adapt_expand(const AdaptExpand &a, int id, hipStream_t s);
 hipError_t launch_adapt_grad(const AdaptGrad &a, bool trans, hipStream_t s);
 // Tiles of tm positions that M positions in at most E + 1 groups can need.
 int64_t adapt_tiles(int64_t M, int64_t E, int64_t tm);

@@ -169,9 +169,9 @@ def test_accepted_sizes_reach_the_device():
                                              (30000, 5120, 17408, 64, 16), (100000, 128, 1 << 20, 128, 1024)])
 def test_adapter_workspace_stays_in_proportion(M, d_in, d_out, r, E):
     """The gradients' partials stay below the activations that the call reads,
-    and the splits' below 34 copies of s."""
+    the splits' below 34 copies of s, and the transposes take the adapters once."""
     n = blr.load().blr_adapters_workspace_bytes(M, d_in, d_out, r, E)
-    assert 0 < n <= 34 * 4 * M * r + 4 * M * max(d_in, d_out) + 4096
+    assert 0 < n <= 34 * 4 * M * r + 4 * M * max(d_in, d_out) + 4 * E * r * (d_in + d_out) + 4096
 
 
 def test_binding_refuses():
