@@ -19,6 +19,8 @@
 // part (see where they are made). Which column of a product a k index stands
 // for is free as long as A and B agree: the loads use that to read 16
 // consecutive bytes per lane.
+#include <type_traits>
+
 #include "blr_internal.h"
 #include "blr_vec.h"
 
@@ -32,6 +34,16 @@ __device__ __forceinline__ vf4 mfma4(float a, float b, vf4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
+// The wave's number in its workgroup, in a scalar register.
+__device__ __forceinline__ int wave() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
+
+// base + bytes: where base is the same in all lanes, the address needs one
+// 32-bit register per lane.
+template <typename T>
+__device__ __forceinline__ const T *ahead(const T *base, unsigned bytes) {
+    return reinterpret_cast<const T *>(reinterpret_cast<const char *>(base) + bytes);
+}
+
 // A tile of one group of the plan; group E is the rows without an adapter.
 struct Tile {
     int e;      // -1: the grid has more tiles than the plan
@@ -39,13 +51,14 @@ struct Tile {
     int cnt;    // positions
     int j, of;  // this tile is the j-th of the group's `of`
     int slot;   // tiles of earlier groups that have several
+    int panel;  // tiles of 64 positions of earlier groups
 };
 
 // Tile b of tiles of tm positions over groups 0 .. groups-1 (wave-uniform).
 // Offsets out of order or out of range cannot lead outside [0, M).
 __device__ Tile find_tile(const AdaptPlan &plan, int groups, int tm, int b) {
     const int lane = threadIdx.x & 63;
-    int run = 0, many = 0;
+    int run = 0, many = 0, panels = 0;
     for (int base = 0; base < groups; base += 64) {
         const int e = base + lane;
         int lo = 0, cnt = 0;
@@ -58,13 +71,15 @@ __device__ Tile find_tile(const AdaptPlan &plan, int groups, int tm, int b) {
         }
         const int nt = cnt / tm + (cnt % tm ? 1 : 0);
         const int several = nt > 1 ? nt : 0;
-        int incl = nt, mincl = several;
+        const int np = cnt / TM + (cnt % TM ? 1 : 0);
+        int incl = nt, mincl = several, pincl = np;
 #pragma unroll
         for (int o = 1; o < 64; o *= 2) {
-            const int u = __shfl_up(incl, o), v = __shfl_up(mincl, o);
+            const int u = __shfl_up(incl, o), v = __shfl_up(mincl, o), z = __shfl_up(pincl, o);
             if (lane >= o) {
                 incl += u;
                 mincl += v;
+                pincl += z;
             }
         }
         const uint64_t past = __ballot(run + incl > b);
@@ -78,12 +93,14 @@ __device__ Tile find_tile(const AdaptPlan &plan, int groups, int tm, int b) {
             const int left = __builtin_amdgcn_readlane(cnt, l) - t.j * tm;
             t.cnt = left < tm ? left : tm;
             t.slot = many + __builtin_amdgcn_readlane(mincl, l) - __builtin_amdgcn_readlane(several, l);
+            t.panel = panels + __builtin_amdgcn_readlane(pincl, l) - __builtin_amdgcn_readlane(np, l);
             return t;
         }
         run += __builtin_amdgcn_readlane(incl, 63);
         many += __builtin_amdgcn_readlane(mincl, 63);
+        panels += __builtin_amdgcn_readlane(pincl, 63);
     }
-    return Tile{-1, 0, 0, 0, 0, 0};
+    return Tile{-1, 0, 0, 0, 0, 0, 0};
 }
 
 // The row of position p, -1 if the plan names none.
@@ -136,19 +153,21 @@ __device__ __forceinline__ void walk(int n, Load load, Use use) {
 template <typename TX, typename TW, int RT, int NT>
 struct ShrinkStep {
     static constexpr int COLS = 32;
-    vf4 x[NT][2], w[RT][2];
+    vf4 x[NT][2];
+    typename Vec<TW>::v4 w[RT][2];  // widened where they are used, or the wait for them would stand here
 
     __device__ __forceinline__ void load(const TX *const *row, const TW *W, int r, int K, int k0, int q, int c) {
-        k0 += q * 4;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) x[t][h] = load4(row[t] + k0 + 16 * h);
+            for (int h = 0; h < 2; ++h) x[t][h] = load4(row[t] + k0 + 16 * h + 4 * q);
 #pragma unroll
         for (int n = 0; n < RT; ++n) {
             const int rank = n * 16 + c < r ? n * 16 + c : r - 1;  // columns past r of the product are not stored
 #pragma unroll
-            for (int h = 0; h < 2; ++h) w[n][h] = load4(W + (int64_t)rank * K + k0 + 16 * h);
+            for (int h = 0; h < 2; ++h)
+                w[n][h] = *reinterpret_cast<const typename Vec<TW>::v4 *>(
+                    ahead(W + k0 + 16 * h, (unsigned)(rank * K + 4 * q) * (unsigned)sizeof(TW)));
         }
     }
     __device__ __forceinline__ void multiply(vf4 (&acc)[NT][RT]) const {
@@ -159,7 +178,7 @@ struct ShrinkStep {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int n = 0; n < RT; ++n) acc[t][n] = mfma4(x[t][h][j], w[n][h][j], acc[t][n]);
+                    for (int n = 0; n < RT; ++n) acc[t][n] = mfma4(x[t][h][j], (float)w[n][h][j], acc[t][n]);
     }
 };
 
@@ -170,16 +189,17 @@ struct ShrinkStep16 {
     V x[NT][2], w[RT][2];
 
     __device__ __forceinline__ void load(const T *const *row, const T *W, int r, int K, int k0, int q, int c) {
-        k0 += q * 8;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) x[t][h] = *reinterpret_cast<const V *>(row[t] + k0 + 32 * h);
+            for (int h = 0; h < 2; ++h) x[t][h] = *reinterpret_cast<const V *>(row[t] + k0 + 32 * h + 8 * q);
 #pragma unroll
         for (int n = 0; n < RT; ++n) {
             const int rank = n * 16 + c < r ? n * 16 + c : r - 1;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) w[n][h] = *reinterpret_cast<const V *>(W + (int64_t)rank * K + k0 + 32 * h);
+            for (int h = 0; h < 2; ++h)
+                w[n][h] = *reinterpret_cast<const V *>(
+                    ahead(W + k0 + 32 * h, (unsigned)(rank * K + 8 * q) * (unsigned)sizeof(T)));
         }
     }
     __device__ __forceinline__ void multiply(vf4 (&acc)[NT][RT]) const {
@@ -201,7 +221,7 @@ struct ShrinkStep<__bf16, __bf16, RT, NT> : ShrinkStep16<__bf16, RT, NT> {};
 template <typename TX, typename TW, int RT, int NT>
 __device__ void shrink_tile(const AdaptShrink &a, const Tile &tile, int from, int to, float (*red)[RT * 16 + 1]) {
     typedef ShrinkStep<TX, TW, RT, NT> Step;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, w = wave();
     const int q = lane >> 4, c = lane & 15;
     const TW *W = reinterpret_cast<const TW *>(a.W) + (int64_t)tile.e * a.r * a.K;
     const TX *x[NT];
@@ -237,19 +257,21 @@ __device__ void shrink_tile(const AdaptShrink &a, const Tile &tile, int from, in
     }
 }
 
-// One workgroup: 64 rows x all r over one split of K.
+// One workgroup: 64 rows x all r over one split of K, the splits of a tile next
+// to each other (the grid is one-dimensional: its other dimensions are short).
 template <typename TX, typename TW, int RT>
 __global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_shrink_kernel(AdaptShrink a) {
     __shared__ float red[TM][RT * 16 + 1];
-    const Tile tile = find_tile(a.plan, a.plan.E, TM, blockIdx.x);
+    const int split = blockIdx.x % a.splits;
+    const Tile tile = find_tile(a.plan, a.plan.E, TM, blockIdx.x / a.splits);
     if (tile.e < 0) return;
     const int64_t steps = a.K / ShrinkStep<TX, TW, RT, 1>::COLS;
-    const int from = (int)(steps * blockIdx.y / a.splits), to = (int)(steps * (blockIdx.y + 1) / a.splits);
+    const int from = (int)(steps * split / a.splits), to = (int)(steps * (split + 1) / a.splits);
     if (tile.cnt <= 16)
         shrink_tile<TX, TW, RT, 1>(a, tile, from, to, red);
     else
         shrink_tile<TX, TW, RT, 4>(a, tile, from, to, red);
-    float *part = a.part + ((int64_t)blockIdx.y * a.plan.M + tile.p0) * a.r;
+    float *part = a.part + ((int64_t)split * a.plan.M + tile.p0) * a.r;
     for (int i = threadIdx.x; i < tile.cnt * a.r; i += 256) part[i] = red[i / a.r][i % a.r];
 }
 
@@ -275,7 +297,8 @@ struct ExpandStep {
                     v[t][n] = *reinterpret_cast<const vf4 *>(&tile[t * 16 + c][n * 16 + q * 4]);
         }
     };
-    vf4 w[2][RT], y[NT][2];
+    typename Vec<TW>::v4 w[2][RT];
+    vf4 y[NT][2];
 
     template <bool ACC>
     __device__ __forceinline__ void load(TX *const *row, const TW *W, int r, int N, int o0, int q, int c) {
@@ -287,17 +310,24 @@ struct ExpandStep {
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int o = o0 + 16 * h + c;
 #pragma unroll
             for (int n = 0; n < RT; ++n) {
                 const int k = n * 16 + q * 4, kc = k < r ? k : 0;  // r is a multiple of 8
-                w[h][n] = load4(W + (int64_t)o * r + kc);
-                if (k >= r) w[h][n] = vf4{0.f, 0.f, 0.f, 0.f};
+                w[h][n] = *reinterpret_cast<const typename Vec<TW>::v4 *>(
+                    ahead(W + (int64_t)(o0 + 16 * h) * r, (unsigned)(c * r + kc) * (unsigned)sizeof(TW)));
             }
         }
     }
     template <bool ACC, bool FULL>
-    __device__ __forceinline__ void multiply_store(const S &s, TX *const *out, int o0, int q) {
+    __device__ __forceinline__ void multiply_store(const S &s, TX *const *out, int r, int o0, int q) {
+        vf4 v[2][RT];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int n = 0; n < RT; ++n) {
+                v[h][n] = __builtin_convertvector(w[h][n], vf4);
+                if (n * 16 + q * 4 >= r) v[h][n] = vf4{0.f, 0.f, 0.f, 0.f};  // s is zero there
+            }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             vf4 d[2];
@@ -308,7 +338,7 @@ struct ExpandStep {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) d[h] = mfma4(w[h][n][j], s.v[t][n][j], d[h]);
+                    for (int h = 0; h < 2; ++h) d[h] = mfma4(v[h][n][j], s.v[t][n][j], d[h]);
             if (FULL || out[t]) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) store4(out[t] + o0 + 16 * h + 4 * q, d[h]);
@@ -383,18 +413,24 @@ struct ExpandStep16 {
         }
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-            const int o = o0 + 32 * (h >> 1) + 8 * (c >> 2) + 4 * (h & 1) + (c & 3);
+            const int o = 8 * (c >> 2) + (c & 3);
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
                 const int k = PACKED ? (q & 1) * 8 : kk * 32 + q * 8, kc = k < r ? k : 0;
-                w[h][kk] = *reinterpret_cast<const V *>(W + (int64_t)o * r + kc);
-                if (k >= r) w[h][kk] = (V)(T)0;
+                w[h][kk] = *reinterpret_cast<const V *>(ahead(W + (int64_t)(o0 + 32 * (h >> 1) + 4 * (h & 1)) * r,
+                                                              (unsigned)(o * r + kc) * (unsigned)sizeof(T)));
             }
         }
     }
     template <bool ACC, bool FULL>
-    __device__ __forceinline__ void multiply_store(const S &s, T *const *out, int o0, int q) {
+    __device__ __forceinline__ void multiply_store(const S &s, T *const *out, int r, int o0, int q) {
         typedef float F __attribute__((ext_vector_type(8)));
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk)
+            if ((PACKED ? (q & 1) * 8 : kk * 32 + q * 8) >= r) {  // s is zero there
+#pragma unroll
+                for (int h = 0; h < 4; ++h) w[h][kk] = (V)(T)0;
+            }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             vf4 d[4];
@@ -432,7 +468,7 @@ template <typename TX, typename TW, int RT, int NT, bool ACC, bool FULL>
 __device__ void expand_tile(const AdaptExpand &a, const Tile &tile, int r, int from, int to,
                             const float (*S)[RT * 16 + 4], const float *largest) {
     typedef ExpandStep<TX, TW, RT, NT> Step;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, w = wave();
     const int q = lane >> 4, c = lane & 15;
     TX *row[NT], *out[NT];
 #pragma unroll
@@ -449,18 +485,20 @@ __device__ void expand_tile(const AdaptExpand &a, const Tile &tile, int r, int f
     walk<Step, RT <= 4>((to - first + 3) / 4,
                [&](Step &st, int i) { st.template load<ACC>(row, W, r, a.N, (first + 4 * i) * Step::COLS, q, c); },
                [&](Step &st, int i) {
-                   st.template multiply_store<ACC, FULL>(s, FULL ? row : out, (first + 4 * i) * Step::COLS, q);
+                   st.template multiply_store<ACC, FULL>(s, FULL ? row : out, r, (first + 4 * i) * Step::COLS, q);
                });
 }
 
 // One workgroup: 64 rows x a range of columns. The prologue adds the splits'
 // partials; the workgroups of the first range also write s out.
+// Two workgroups share a CU where their registers allow it without spills.
 template <typename TX, typename TW, int RT, bool ACC>
-__global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_expand_kernel(AdaptExpand a, int chunks) {
+__global__ __launch_bounds__(256, RT <= (__is_same(TX, _Float16) && ACC ? 2 : 4) ? 2 : 1) void adapt_expand_kernel(AdaptExpand a, int chunks) {
     __shared__ float S[TM][RT * 16 + 4];
     __shared__ float largest[TM];
     __shared__ int named;
-    const Tile tile = find_tile(a.plan, a.plan.E + 1, TM, blockIdx.x);
+    const int chunk = blockIdx.x % chunks;
+    const Tile tile = find_tile(a.plan, a.plan.E + 1, TM, blockIdx.x / chunks);
     if (tile.e < 0) return;
     const bool none = tile.e == a.plan.E;
     const float scale = a.scale && !none ? a.scale[tile.e] : 1.f;
@@ -479,14 +517,13 @@ __global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_expand_kernel(Adap
 #pragma unroll 8
             for (int sp = 0; sp < a.splits; ++sp) sum += part[sp * next];
         }
-        if (blockIdx.y == 0 && m < tile.cnt && k < a.r) {
+        if (chunk == 0 && m < tile.cnt && k < a.r) {
             const int64_t row = row_of(a.plan, tile.p0 + m);
             if (a.s_row && row >= 0) a.s_row[row * a.r + k] = sum;
-            if (a.s_pos) a.s_pos[(int64_t)(tile.p0 + m) * a.r + k] = scale * sum;
         }
         S[m][k] = scale * sum;
     }
-    if (a.out == nullptr || (none && ACC)) return;
+    if (none && ACC) return;
     __syncthreads();
     if (__is_same(TX, _Float16)) {
         if (threadIdx.x < rows) {
@@ -497,7 +534,7 @@ __global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_expand_kernel(Adap
         __syncthreads();
     }
     const int64_t steps = a.N / ExpandStep<TX, TW, RT, 1>::COLS;
-    const int from = (int)(steps * blockIdx.y / chunks), to = (int)(steps * (blockIdx.y + 1) / chunks);
+    const int from = (int)(steps * chunk / chunks), to = (int)(steps * (chunk + 1) / chunks);
     const int r = none ? 0 : a.r;
     if (tile.cnt <= 16)
         expand_tile<TX, TW, RT, 1, ACC, false>(a, tile, r, from, to, S, largest);
@@ -543,109 +580,255 @@ __global__ __launch_bounds__(256) void adapt_transpose_kernel(AdaptTranspose a) 
     }
 }
 
+// ------------------------------------------------------------------ thin --
+// One workgroup: a tile's panel of ds (blockIdx.y = 0) or of the tape.
+template <typename TX, int RT>
+__global__ __launch_bounds__(256) void adapt_thin_kernel(AdaptThin a) {
+    __shared__ float S[TM][RT * 16 + 1];
+    const Tile tile = find_tile(a.plan, a.plan.E, TM, blockIdx.x);
+    if (tile.e < 0) return;
+    const float scale = a.scale ? a.scale[tile.e] : 1.f;
+    const int64_t next = (int64_t)a.plan.M * a.r;
+    for (int i = threadIdx.x; i < TM * RT * 16; i += 256) {
+        const int m = i / (RT * 16), k = i % (RT * 16);
+        float v = 0.f;
+        if (m < tile.cnt && k < a.r) {
+            if (blockIdx.y == 0) {
+                const float *part = a.part + (int64_t)(tile.p0 + m) * a.r + k;
+#pragma unroll 8
+                for (int sp = 0; sp < a.splits; ++sp) v += part[sp * next];
+                v *= scale;
+                a.ds[(int64_t)(tile.p0 + m) * a.r + k] = v;
+            } else {
+                const int64_t row = row_of(a.plan, tile.p0 + m);
+                if (row >= 0) v = a.tape[row * a.r + k];
+            }
+        }
+        S[m][k] = v;
+    }
+    if (a.tape == nullptr) return;
+    __syncthreads();
+    const int64_t panel = (int64_t)blockIdx.x * RT * 16 * TM;
+    if constexpr (sizeof(TX) == 4) {
+        float *to = reinterpret_cast<float *>(a.panel[blockIdx.y]) + panel;
+        for (int i = threadIdx.x; i < RT * 16 * 16; i += 256) {
+            const int k = i >> 4, t = (i & 15) * 4;
+            store4(to + k * TM + t, vf4{S[t][k], S[t + 1][k], S[t + 2][k], S[t + 3][k]});
+        }
+    } else {
+        __bf16 *to = reinterpret_cast<__bf16 *>(a.panel[blockIdx.y]) + 3 * panel;
+        for (int i = threadIdx.x; i < RT * 16 * 8; i += 256) {
+            const int k = i >> 3, t = (i & 7) * 8;
+            vb8 term[3];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float v = S[t + j][k];
+#pragma unroll
+                for (int h = 0; h < 3; ++h) term[h][j] = take_term<__bf16>(v);
+            }
+#pragma unroll
+            for (int h = 0; h < 3; ++h) *reinterpret_cast<vb8 *>(to + (h * RT * 16 + k) * TM + t) = term[h];
+        }
+    }
+}
+
 // -------------------------------------------------------------- gradients --
+// Rows past a range's end: zeros, so that they add nothing whatever a real row
+// holds. A wave reads up to 64 columns of a row.
+__device__ float zero_row[64];  // never written; not const, or its loads would not be global ones
+
+// X as the A operand, straight from its rows: lane (q, c) loads columns
+// 4 c .. 4 c + 3, component u belonging to tile u of the output (so that row m
+// of tile u stands for column 4 m + u), of the rows q of the step's k indices;
+// the thin operand's panel gives B[k][rank]. D then holds
+// G[column 4 (4 q + i) + u][rank c].
+//
+// Rows of f32: 16 a step, k index 4 q + j.
+template <typename TX, int RT>
+struct GradStep {
+    static constexpr int ROWS = 16;
+    vf4 x[4], t[RT];
+
+    __device__ __forceinline__ void load(const TX *X, int N, const int *row, const float *panel, int m, int q, int c) {
+        const int4 at = *reinterpret_cast<const int4 *>(row + m + 4 * q);
+        const int r[4] = {at.x, at.y, at.z, at.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            x[j] = load4((r[j] < 0 ? reinterpret_cast<const TX *>(zero_row) : X + (int64_t)r[j] * N) + 4 * c);
+        const float *p = panel + (int64_t)(m / TM) * RT * 16 * TM + m % TM;
+#pragma unroll
+        for (int n = 0; n < RT; ++n) t[n] = load4(ahead(p + n * 16 * TM, (unsigned)(c * TM + 4 * q) * 4u));
+    }
+    __device__ __forceinline__ void multiply(vf4 (&acc)[4][RT]) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int n = 0; n < RT; ++n) acc[u][n] = mfma4(x[j][u], t[n][j], acc[u][n]);
+    }
+};
+
+// Rows of 16 bits: 32 a step, k index 8 q + j, on the bf16 instruction. The
+// gradients are f32, so the thin operand takes part with 24 leading bits, in
+// three bf16 terms; an f16 element of X is exactly two (11 bits in 8 + 3), and
+// the product of its second with the third term, 2^-25 of the whole at most,
+// is left out. bf16 has f32's range, so no term needs a scale.
+template <typename T, int RT>
+struct GradStep16 {
+    static constexpr int ROWS = 32;
+    uint2 x[8];  // four elements
+    vb8 t[3][RT];
+
+    __device__ __forceinline__ void load(const T *X, int N, const int *row, const __bf16 *panel, int m, int q, int c) {
+        const int4 a = *reinterpret_cast<const int4 *>(row + m + 8 * q);
+        const int4 b = *reinterpret_cast<const int4 *>(row + m + 8 * q + 4);
+        const int r[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            x[j] = *reinterpret_cast<const uint2 *>(
+                (r[j] < 0 ? reinterpret_cast<const T *>(zero_row) : X + (int64_t)r[j] * N) + 4 * c);
+        const __bf16 *p = panel + (int64_t)(m / TM) * 3 * RT * 16 * TM + m % TM;
+#pragma unroll
+        for (int h = 0; h < 3; ++h)
+#pragma unroll
+            for (int n = 0; n < RT; ++n)
+                t[h][n] = *reinterpret_cast<const vb8 *>(
+                    ahead(p + (h * RT + n) * 16 * TM, (unsigned)(c * TM + 8 * q) * 2u));
+    }
+    __device__ __forceinline__ void multiply(vf4 (&acc)[4][RT]) const {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            vb8 hi, lo;
+            if constexpr (__is_same(T, __bf16)) {
+                uint32_t pair[4];  // element u of two rows
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    pair[j] = __builtin_amdgcn_perm(u < 2 ? x[2 * j + 1].x : x[2 * j + 1].y,
+                                                    u < 2 ? x[2 * j].x : x[2 * j].y, u & 1 ? 0x07060302u : 0x05040100u);
+                hi = __builtin_bit_cast(vb8, make_uint4(pair[0], pair[1], pair[2], pair[3]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float v = (float)__builtin_bit_cast(vh4, x[j])[u];
+                    hi[j] = take_term<__bf16>(v);
+                    lo[j] = take_term<__bf16>(v);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 3; ++h)
+#pragma unroll
+                for (int n = 0; n < RT; ++n) acc[u][n] = mfma8(hi, t[h][n], acc[u][n]);
+            if constexpr (!__is_same(T, __bf16)) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int n = 0; n < RT; ++n) acc[u][n] = mfma8(lo, t[h][n], acc[u][n]);
+            }
+        }
+    }
+};
+template <int RT>
+struct GradStep<_Float16, RT> : GradStep16<_Float16, RT> {};
+template <int RT>
+struct GradStep<__bf16, RT> : GradStep16<__bf16, RT> {};
+
 // One workgroup: a range of one adapter's rows x 256 columns, wave w 64 of
-// them. Four rows a step: lane (q, c) loads columns 4 c .. 4 c + 3 of row q,
-// whose component u belongs to tile u of the output, so X again goes straight
-// into an operand. Which side X takes follows the gradient's layout, so that
-// each lane ends with consecutive elements of it.
-template <typename TX, int RT, bool TRANS>
-__global__ __launch_bounds__(256) void adapt_grad_kernel(AdaptGrad a) {
-    const Tile tile = find_tile(a.plan, a.plan.E, a.range, blockIdx.x);
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+// them.
+template <typename TX, int RT>
+__global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_grad_kernel(AdaptGrad a) {
+    typedef GradStep<TX, RT> Step;
+    typedef typename std::conditional<sizeof(TX) == 4, float, __bf16>::type P;
+    __shared__ __align__(16) int row[ADAPT_MAX_RANGE];
+    const int which = (int)blockIdx.x >= a.blocks;
+    const AdaptGradJob &job = a.job[which];
+    const int N = job.N, across = (N + 255) / 256;
+    const int b = blockIdx.x - (which ? a.blocks : 0);
+    const Tile tile = find_tile(a.plan, a.plan.E, job.range, b / across);
+    if (tile.e < 0) return;
+    const int first = tile.panel + tile.j * (job.range / TM);
+    // only offsets out of order can count more panels or partials than there are
+    if (first + (tile.cnt + TM - 1) / TM > a.panels || (tile.of > 1 && tile.slot + tile.j >= job.slots)) return;
+    const int steps = (tile.cnt + Step::ROWS - 1) / Step::ROWS;
+    for (int i = threadIdx.x; i < steps * Step::ROWS; i += 256)
+        row[i] = i < tile.cnt ? (int)row_of(a.plan, tile.p0 + i) : -1;
+    __syncthreads();
+    const int lane = threadIdx.x & 63, w = wave();
     const int q = lane >> 4, c = lane & 15;
-    const int n0 = blockIdx.y * 256 + w * 64;
-    if (tile.e < 0 || n0 >= a.N) return;
-    const TX *X = reinterpret_cast<const TX *>(a.X) + n0 + 4 * c;
+    const int n0 = b % across * 256 + w * 64;
+    if (n0 >= N) return;
+    const TX *X = reinterpret_cast<const TX *>(job.X) + n0;
+    const P *panel =
+        reinterpret_cast<const P *>(job.panel) + (int64_t)first * (sizeof(TX) == 4 ? 1 : 3) * RT * 16 * TM;
     vf4 acc[4][RT];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
         for (int n = 0; n < RT; ++n) acc[u][n] = vf4{0.f, 0.f, 0.f, 0.f};
-    for (int m0 = 0; m0 < tile.cnt; m0 += 4) {
-        const int p = tile.p0 + m0 + q;
-        const int64_t row = m0 + q < tile.cnt ? row_of(a.plan, p) : -1;
-        vf4 xv = {0.f, 0.f, 0.f, 0.f};
-        float tv[RT];
-        if (row >= 0) xv = load4(X + row * a.N);
-#pragma unroll
-        for (int n = 0; n < RT; ++n) {
-            const int k = n * 16 + c;
-            tv[n] = row >= 0 && k < a.r ? a.thin[(a.thin_by_row ? row : (int64_t)p) * a.r + k] : 0.f;
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int n = 0; n < RT; ++n)
-                acc[u][n] = TRANS ? mfma4(tv[n], xv[u], acc[u][n]) : mfma4(xv[u], tv[n], acc[u][n]);
-    }
-    const int64_t size = (int64_t)a.r * a.N;
+    walk<Step, RT <= 4>(steps, [&](Step &s, int i) { s.load(X, N, row, panel, i * Step::ROWS, q, c); },
+                        [&](const Step &s, int) { s.multiply(acc); });
+    const int64_t size = (int64_t)a.r * N;
     const bool alone = tile.of == 1;
-    if (!alone && tile.slot + tile.j >= a.slots) return;  // only for offsets out of order
-    float *g = alone ? a.grad + tile.e * size : a.part + (tile.slot + tile.j) * size;
+    float *g = alone ? job.grad + tile.e * size : job.part + (tile.slot + tile.j) * size;
     const bool add = alone && a.acc;
-    const float scale = a.scale ? a.scale[tile.e] : 1.f;
-    if (TRANS) {
-        // D[rank 4 q + i][column 4 c + u]
+    const float scale = job.scale ? job.scale[tile.e] : 1.f;
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+    for (int n = 0; n < RT; ++n) {
+        const int k = n * 16 + c;
+        if (k >= a.r) continue;
 #pragma unroll
-            for (int n = 0; n < RT; ++n) {
-                const int k = n * 16 + 4 * q;
-                if (k >= a.r) continue;
-                float *at = g + (int64_t)(n0 + 4 * c + u) * a.r + k;
-                const vf4 v = scale * acc[u][n];
+        for (int i = 0; i < 4; ++i) {
+            const vf4 v = scale * vf4{acc[0][n][i], acc[1][n][i], acc[2][n][i], acc[3][n][i]};
+            const int col = n0 + 16 * q + 4 * i;
+            if (which == 0) {
+                float *at = g + (int64_t)k * N + col;
                 store4(at, add ? load4(at) + v : v);
-            }
-    } else {
-        // D[column 4 (4 q + i) + u][rank c]
+            } else {
+                float *at = g + (int64_t)col * a.r + k;
 #pragma unroll
-        for (int n = 0; n < RT; ++n) {
-            const int k = n * 16 + c;
-            if (k >= a.r) continue;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float *at = g + (int64_t)k * a.N + n0 + 16 * q + 4 * i;
-                const vf4 v = scale * vf4{acc[0][n][i], acc[1][n][i], acc[2][n][i], acc[3][n][i]};
-                store4(at, add ? load4(at) + v : v);
+                for (int u = 0; u < 4; ++u) at[u * a.r] = add ? at[u * a.r] + v[u] : v[u];
             }
         }
     }
 }
 
 // The partials of an adapter of several ranges, added in range order; zeros
-// for an adapter without rows.
+// for an adapter without rows. blockIdx.z: the gradient.
 __global__ __launch_bounds__(256) void adapt_reduce_kernel(AdaptGrad a) {
+    const AdaptGradJob &job = a.job[blockIdx.z];
     const int e = blockIdx.y;
-    int lo = a.plan.offsets[e], hi = a.plan.offsets[e + 1];
-    lo = lo < 0 ? 0 : lo > a.plan.M ? a.plan.M : lo;
-    hi = hi > a.plan.M ? a.plan.M : hi;
-    if (hi - lo > 0 && hi - lo <= a.range) return;  // written by its only range
-    if (hi - lo <= 0 && a.acc) return;
-    const int64_t size = (int64_t)a.r * a.N;
+    const int64_t size = (int64_t)a.r * job.N;
     const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if ((int64_t)blockIdx.x * 1024 >= size) return;
+    auto rows = [&](int f) {
+        int lo = a.plan.offsets[f], hi = a.plan.offsets[f + 1];
+        lo = lo < 0 ? 0 : lo > a.plan.M ? a.plan.M : lo;
+        hi = hi > a.plan.M ? a.plan.M : hi;
+        return hi > lo ? hi - lo : 0;
+    };
+    const int cnt = rows(e);
+    if (cnt > 0 ? cnt <= job.range : a.acc) return;  // written by its only range, or nothing to add
     int slot = 0, of = 0;
-    if (hi - lo > 0) {
+    if (cnt > 0) {
         // partials of the adapters before: every wave sums for itself
         const int lane = threadIdx.x & 63;
         for (int base = 0; base < e; base += 64) {
             int several = 0;
             if (base + lane < e) {
-                int l = a.plan.offsets[base + lane], h = a.plan.offsets[base + lane + 1];
-                l = l < 0 ? 0 : l > a.plan.M ? a.plan.M : l;
-                h = h > a.plan.M ? a.plan.M : h;
-                if (h - l > a.range) several = (h - l) / a.range + ((h - l) % a.range ? 1 : 0);
+                const int n = rows(base + lane);
+                if (n > job.range) several = n / job.range + (n % job.range ? 1 : 0);
             }
             for (int o = 32; o > 0; o /= 2) several += __shfl_xor(several, o);
             slot += several;
         }
-        of = (hi - lo) / a.range + ((hi - lo) % a.range ? 1 : 0);
-        if (slot + of > a.slots) return;
+        of = cnt / job.range + (cnt % job.range ? 1 : 0);
+        if (slot + of > job.slots) return;
     }
     if (at >= size) return;
-    float *g = a.grad + e * size + at;
+    float *g = job.grad + e * size + at;
     vf4 sum = a.acc ? load4(g) : vf4{0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < of; ++j) sum += load4(a.part + (int64_t)(slot + j) * size + at);
+#pragma unroll 4
+    for (int j = 0; j < of; ++j) sum += load4(job.part + (int64_t)(slot + j) * size + at);
     store4(g, sum);
 }
 
@@ -654,7 +837,7 @@ constexpr int64_t FILL = 1024;
 
 template <typename TX, typename TW, int RT>
 hipError_t shrink_t(const AdaptShrink &a, hipStream_t s) {
-    const dim3 grid((unsigned)adapt_tiles(a.plan.M, a.plan.E, TM), (unsigned)a.splits);
+    const dim3 grid((unsigned)(a.splits * adapt_tiles(a.plan.M, a.plan.E, TM)));
     hipLaunchKernelGGL((adapt_shrink_kernel<TX, TW, RT>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
@@ -663,8 +846,9 @@ template <typename TX, typename TW, int RT>
 hipError_t expand_t(const AdaptExpand &a, hipStream_t s) {
     const int64_t tiles = adapt_tiles(a.plan.M, a.plan.E, TM), units = a.N / 128;
     int64_t chunks = (FILL + tiles - 1) / tiles;
-    chunks = a.out == nullptr ? 1 : chunks > units ? units : chunks;
-    const dim3 grid((unsigned)tiles, (unsigned)chunks);
+    chunks = chunks > units ? units : chunks;
+    if (chunks > 8) chunks = chunks / 8 * 8;
+    const dim3 grid((unsigned)(chunks * tiles));
     if (a.acc)
         hipLaunchKernelGGL((adapt_expand_kernel<TX, TW, RT, true>), grid, dim3(256), 0, s, a, (int)chunks);
     else
@@ -673,12 +857,19 @@ hipError_t expand_t(const AdaptExpand &a, hipStream_t s) {
 }
 
 template <typename TX, int RT>
-hipError_t grad_t(const AdaptGrad &a, bool trans, hipStream_t s) {
-    const dim3 grid((unsigned)adapt_tiles(a.plan.M, a.plan.E, a.range), (unsigned)((a.N + 255) / 256));
-    if (trans)
-        hipLaunchKernelGGL((adapt_grad_kernel<TX, RT, true>), grid, dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL((adapt_grad_kernel<TX, RT, false>), grid, dim3(256), 0, s, a);
+hipError_t thin_t(const AdaptThin &a, hipStream_t s) {
+    const dim3 grid((unsigned)adapt_tiles(a.plan.M, a.plan.E, TM), a.tape ? 2 : 1);
+    hipLaunchKernelGGL((adapt_thin_kernel<TX, RT>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+template <typename TX, int RT>
+hipError_t grad_t(AdaptGrad a, hipStream_t s) {
+    int64_t blocks[2];
+    for (int j = 0; j < 2; ++j)
+        blocks[j] = adapt_tiles(a.plan.M, a.plan.E, a.job[j].range) * ((a.job[j].N + 255) / 256);
+    a.blocks = (int)blocks[0];
+    hipLaunchKernelGGL((adapt_grad_kernel<TX, RT>), dim3((unsigned)(blocks[0] + blocks[1])), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -695,13 +886,15 @@ hipError_t grad_t(const AdaptGrad &a, bool trans, hipStream_t s) {
      : (a).wt == 2  ? BLR_BY_RANK((a).r, F, float, __bf16, __VA_ARGS__)                          \
                     : BLR_BY_RANK((a).r, F, float, float, __VA_ARGS__))
 
-template <typename TX>
-hipError_t grad_by_rank(const AdaptGrad &a, bool trans, hipStream_t s) {
-    return a.r <= 16   ? grad_t<TX, 1>(a, trans, s)
-           : a.r <= 32 ? grad_t<TX, 2>(a, trans, s)
-           : a.r <= 64 ? grad_t<TX, 4>(a, trans, s)
-                       : grad_t<TX, 8>(a, trans, s);
-}
+#define BLR_BY_ROWS(a, F, ...)                                                                   \
+    ((a).act == 0   ? BLR_BY_RANK1((a).r, F, float, __VA_ARGS__)                                 \
+     : (a).act == 1 ? BLR_BY_RANK1((a).r, F, _Float16, __VA_ARGS__)                              \
+                    : BLR_BY_RANK1((a).r, F, __bf16, __VA_ARGS__))
+#define BLR_BY_RANK1(r, F, TX, ...)                                                              \
+    ((r) <= 16   ? F<TX, 1>(__VA_ARGS__)                                                         \
+     : (r) <= 32 ? F<TX, 2>(__VA_ARGS__)                                                         \
+     : (r) <= 64 ? F<TX, 4>(__VA_ARGS__)                                                         \
+                 : F<TX, 8>(__VA_ARGS__))
 
 }  // namespace
 
@@ -723,6 +916,7 @@ int64_t adapt_range(int64_t M, int64_t N, int64_t r) {
     int64_t range = M * cols / (FILL / 2);
     const int64_t least = 8 * r > 256 ? 8 * r : 256;  // a partial costs as much as 2 r rows
     range = range < least ? least : range;
+    range = range < ADAPT_MAX_RANGE ? range : ADAPT_MAX_RANGE;
     range = range < M ? range : M;
     return (range + 63) / 64 * 64;
 }
@@ -760,16 +954,22 @@ hipError_t launch_adapt_expand(const AdaptExpand &a, int id, hipStream_t s) {
     return e;
 }
 
-hipError_t launch_adapt_grad(const AdaptGrad &a, bool trans, hipStream_t s) {
+hipError_t launch_adapt_thin(const AdaptThin &a, hipStream_t s) {
+    prof_begin(K_ADAPT_THIN, s);
+    hipError_t e = BLR_BY_ROWS(a, thin_t, a, s);
+    prof_end(s);
+    return e;
+}
+
+hipError_t launch_adapt_grad(const AdaptGrad &a, hipStream_t s) {
     prof_begin(K_ADAPT_GRAD, s);
-    hipError_t e = a.act == 0   ? grad_by_rank<float>(a, trans, s)
-                   : a.act == 1 ? grad_by_rank<_Float16>(a, trans, s)
-                                : grad_by_rank<__bf16>(a, trans, s);
+    hipError_t e = BLR_BY_ROWS(a, grad_t, a, s);
     prof_end(s);
     if (e != hipSuccess) return e;
-    const int64_t blocks = ((int64_t)a.r * a.N / 4 + 255) / 256;
+    const int N = a.job[0].N > a.job[1].N ? a.job[0].N : a.job[1].N;
+    const int64_t blocks = ((int64_t)a.r * N / 4 + 255) / 256;
     prof_begin(K_ADAPT_REDUCE, s);
-    hipLaunchKernelGGL(adapt_reduce_kernel, dim3((unsigned)blocks, (unsigned)a.plan.E), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(adapt_reduce_kernel, dim3((unsigned)blocks, (unsigned)a.plan.E, 2), dim3(256), 0, s, a);
     e = hipGetLastError();
     prof_end(s);
     return e;

@@ -733,31 +733,35 @@ bool adapt_shape_ok(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t E
 }
 
 // Workspace: the splits' partials of s or ds (f32 [splits][M][r]), then for
-// the backward the transposes of down and up, ds by position (f32 [M][r]) and
-// the ranges' partials of one gradient.
+// the backward the transposes of down and up, ds by position (f32 [M][r]), the
+// panels of ds and of the tape and the ranges' partials of both gradients.
 struct AdaptLayout {
-    size_t down_t, up_t, ds, grad, total;
+    size_t down_t, up_t, ds, panel[2], part[2], total;
     int64_t range_in, range_out, slots_in, slots_out;
 };
 
-AdaptLayout adapt_layout(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t E, int wt = BLR_F32) {
+AdaptLayout adapt_layout(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t E) {
     AdaptLayout L;
     const int si = adapt_splits(M, E, d_in), so = adapt_splits(M, E, d_out);
     size_t off = up((size_t)(si > so ? si : so) * M * r * 4);
-    const size_t w = (size_t)E * r * size_of(wt);
-    L.down_t = off;
-    off += up(w * d_in);
-    L.up_t = off;
-    off += up(w * d_out);
-    L.ds = off;
-    off += up((size_t)M * r * 4);
-    L.grad = off;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += up(bytes);
+        return at;
+    };
+    // sized for the widest types, so that one workspace serves them all
+    L.down_t = take((size_t)E * r * d_in * 4);
+    L.up_t = take((size_t)E * r * d_out * 4);
+    L.ds = take((size_t)M * r * 4);
+    const size_t panels = (size_t)adapt_tiles(M, E, ADAPT_TM) * adapt_panel_bytes(r, BLR_BF16);
+    L.panel[0] = take(panels);
+    L.panel[1] = take(panels);
     L.range_in = adapt_range(M, d_in, r);
     L.range_out = adapt_range(M, d_out, r);
     L.slots_in = adapt_range_slots(M, E, L.range_in);
     L.slots_out = adapt_range_slots(M, E, L.range_out);
-    const int64_t gi = L.slots_in * r * d_in, go = L.slots_out * r * d_out;
-    off += up((size_t)(gi > go ? gi : go) * 4);
+    L.part[0] = take((size_t)L.slots_in * r * d_in * 4);
+    L.part[1] = take((size_t)L.slots_out * r * d_out * 4);
     L.total = off;
     return L;
 }
@@ -880,43 +884,42 @@ int blr_adapters_backward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int
     sh.act = act;
     sh.wt = wt;
     BLR_TRY(launch_adapt_shrink(sh, K_ADAPT_DS, s));
-    AdaptExpand ex = {};
-    ex.plan = sh.plan;
-    ex.part = sh.part;
-    ex.scale = scale;
-    ex.W = tr.dst[0];
-    ex.out = dx;
-    ex.s_pos = (float *)(ws + L.ds);
-    ex.N = (int)d_in;
-    ex.r = (int)r;
-    ex.splits = sh.splits;
-    ex.act = act;
-    ex.wt = wt;
-    ex.acc = accumulate_dx ? 1 : 0;
-    BLR_TRY(launch_adapt_expand(ex, K_ADAPT_DX, s));
+    AdaptThin th = {};
+    th.plan = sh.plan;
+    th.part = sh.part;
+    th.scale = scale;
+    th.tape = grad_down ? tape_s : nullptr;
+    th.ds = (float *)(ws + L.ds);
+    th.panel[0] = ws + L.panel[0];
+    th.panel[1] = ws + L.panel[1];
+    th.r = (int)r;
+    th.splits = sh.splits;
+    th.act = act;
+    BLR_TRY(launch_adapt_thin(th, s));
+    if (dx) {
+        AdaptExpand ex = {};
+        ex.plan = sh.plan;
+        ex.part = th.ds;  // holds the factor already
+        ex.W = tr.dst[0];
+        ex.out = dx;
+        ex.N = (int)d_in;
+        ex.r = (int)r;
+        ex.splits = 1;
+        ex.act = act;
+        ex.wt = wt;
+        ex.acc = accumulate_dx ? 1 : 0;
+        BLR_TRY(launch_adapt_expand(ex, K_ADAPT_DX, s));
+    }
     if (!grad_down) return BLR_OK;
-    AdaptGrad g = {};
-    g.plan = sh.plan;
-    g.part = (float *)(ws + L.grad);
-    g.r = (int)r;
-    g.act = act;
-    g.acc = accumulate_grads ? 1 : 0;
-    g.X = x;
-    g.thin = ex.s_pos;  // holds the factor already
-    g.grad = grad_down;
-    g.N = (int)d_in;
-    g.range = (int)L.range_in;
-    g.slots = L.slots_in;
-    BLR_TRY(launch_adapt_grad(g, false, s));
-    g.X = dy;
-    g.thin = tape_s;
-    g.thin_by_row = 1;
-    g.scale = scale;
-    g.grad = grad_up;
-    g.N = (int)d_out;
-    g.range = (int)L.range_out;
-    g.slots = L.slots_out;
-    BLR_TRY(launch_adapt_grad(g, true, s));
+    AdaptGrad gr = {};
+    gr.plan = sh.plan;
+    gr.r = (int)r;
+    gr.act = act;
+    gr.acc = accumulate_grads ? 1 : 0;
+    gr.panels = adapt_tiles(M, adapters, ADAPT_TM);
+    gr.job[0] = {x, th.panel[0], nullptr, grad_down, (float *)(ws + L.part[0]), (int)d_in, (int)L.range_in, L.slots_in};
+    gr.job[1] = {dy, th.panel[1], scale, grad_up, (float *)(ws + L.part[1]), (int)d_out, (int)L.range_out, L.slots_out};
+    BLR_TRY(launch_adapt_grad(gr, s));
     return BLR_OK;
 }
 

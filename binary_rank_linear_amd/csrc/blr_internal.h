@@ -44,6 +44,7 @@ enum KernelId {
     K_ADAPT_TRANSPOSE, // adapters: A^T and B^T for the backward
     K_ADAPT_DS,     // adapters: partials of ds = c dy B
     K_ADAPT_DX,     // adapters: dx (+)= ds A
+    K_ADAPT_THIN,   // adapters: ds, and ds and s as the gradients' operands
     K_ADAPT_GRAD,   // adapters: gradients of A and B over ranges of rows
     K_ADAPT_REDUCE, // adapters: the ranges' partials summed in order
     K_COUNT
@@ -239,29 +240,49 @@ struct AdaptShrink {
     int K, r, splits, act, wt;
 };
 // out[row(p)][n] (+)= sum_k S[p][k] W_e[n][k], S[p] = scale_e sum over splits
-// of part[.][p]; W_e: [N][r]. S goes to s_row by row,
-// unscaled, and to s_pos by position, scaled (either may be null).
+// of part[.][p]; W_e: [N][r]. S goes to s_row by row, unscaled (unless null).
 struct AdaptExpand {
     AdaptPlan plan;
     const float *part;
     const float *scale;
     const void *W;
-    void *out;  // null: only s_row / s_pos
-    float *s_row, *s_pos;
+    void *out;
+    float *s_row;
     int N, r, splits, act, wt, acc;
 };
-// G_e (+)= scale_e sum over the adapter's rows of thin[.][k] X[row][n]: laid
-// out [r][N], or [N][r] when trans. thin is by position, or by row when
-// thin_by_row. Ranges of `range` rows; an adapter of several ranges leaves
-// partials in part[slot], which the reduction adds in range order.
-struct AdaptGrad {
+// The gradients' thin operands, once per call: ds [p][r] = scale_e sum over
+// splits of part[.][p], and both ds and the tape s (by row) as panels: of each
+// tile of 64 positions, its ranks (rounded up to 16, 32, 64 or 128: r16) by 64
+// positions, zero past the tile's end. For rows of f32 a panel is f32
+// [r16][64]; for rows of 16 bits three bf16 terms [3][r16][64].
+struct AdaptThin {
     AdaptPlan plan;
+    const float *part, *scale, *tape;  // tape null: ds alone, no panels
+    float *ds;
+    void *panel[2];                    // of ds and of the tape
+    int r, splits, act;
+};
+constexpr int64_t adapt_r16(int64_t r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
+constexpr int64_t adapt_panel_bytes(int64_t r, int act) { return adapt_r16(r) * 64 * (act == 0 ? 4 : 6); }
+// Two gradients in one launch, G_e (+)= scale_e sum over the adapter's rows of
+// thin[.][k] X[row][n]: job 0 laid out [r][N], job 1 [N][r]. Ranges of `range`
+// positions; an adapter of several ranges leaves partials in part[slot], which
+// the reduction adds in range order.
+constexpr int ADAPT_MAX_RANGE = 4096;  // its rows' numbers lie in LDS
+struct AdaptGradJob {
     const void *X;
-    const float *thin;
+    const void *panel;
     const float *scale;  // null: no factor
     float *grad, *part;
-    int N, r, act, acc, range, thin_by_row;
+    int N, range;
     int64_t slots;  // partials that `part` has room for
+};
+struct AdaptGrad {
+    AdaptPlan plan;
+    AdaptGradJob job[2];
+    int r, act, acc;
+    int64_t panels;  // that exist
+    int blocks;      // of job 0; filled by the launcher
 };
 // dst_e [cols][rows] = the transpose of src_e [rows][cols], for the adapters
 // that have rows; two tables in one launch.
@@ -277,7 +298,8 @@ hipError_t launch_adapt_transpose(AdaptTranspose a, int wt, hipStream_t s);
 // id: the kernel kind that the launch is timed as.
 hipError_t launch_adapt_shrink(const AdaptShrink &a, int id, hipStream_t s);
 hipError_t launch_adapt_expand(const AdaptExpand &a, int id, hipStream_t s);
-hipError_t launch_adapt_grad(const AdaptGrad &a, bool trans, hipStream_t s);
+hipError_t launch_adapt_thin(const AdaptThin &a, hipStream_t s);
+hipError_t launch_adapt_grad(const AdaptGrad &a, hipStream_t s);
 // Tiles of tm positions that M positions in at most E + 1 groups can need.
 int64_t adapt_tiles(int64_t M, int64_t E, int64_t tm);
 int adapt_splits(int64_t M, int64_t E, int64_t K);

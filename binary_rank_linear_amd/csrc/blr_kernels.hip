@@ -2108,6 +2108,7 @@ const char *kernel_name(int id) {
         case K_ADAPT_TRANSPOSE: return "adapters_transpose";
         case K_ADAPT_DS: return "adapters_ds";
         case K_ADAPT_DX: return "adapters_dx";
+        case K_ADAPT_THIN: return "adapters_thin";
         case K_ADAPT_GRAD: return "adapters_grad";
         case K_ADAPT_REDUCE: return "adapters_grad_reduce";
     }

@@ -135,6 +135,13 @@ __global__ __launch_bounds__(SORT_THREADS) void route_place_kernel(RouteSortArgs
     }
 }
 
+// Workgroups along the tokens; the kernels step on by the grid past it.
+constexpr int64_t TOKEN_BLOCKS = (int64_t)1 << 22;
+unsigned token_blocks(int64_t T, int64_t per) {
+    const int64_t n = (T + per - 1) / per;
+    return (unsigned)(n < TOKEN_BLOCKS ? n : TOKEN_BLOCKS);
+}
+
 // Threads of a workgroup over a row: tx (a power of two) take its vectors, the
 // 256 / tx others further tokens.
 int row_threads(int64_t nv) {
@@ -144,16 +151,17 @@ int row_threads(int64_t nv) {
 }
 
 __global__ __launch_bounds__(256) void route_gather_kernel(RouteRows a, int64_t nv) {
-    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int64_t c = (int64_t)blockIdx.y * blockDim.x + threadIdx.x;
-    if (t >= a.T || c >= nv) return;
+    if (c >= nv) return;
     const int placed = *a.placed;
     const int64_t pairs = a.T * a.k;
-    const vf4 v = reinterpret_cast<const vf4 *>(a.a)[t * nv + c];
-    for (int j = 0; j < a.k; ++j) {
-        const int at = a.slot[t * a.k + j];
-        if (at < 0 || at >= pairs) continue;
-        reinterpret_cast<vf4 *>(a.out)[at * nv + c] = at < placed ? v : vf4{0.f, 0.f, 0.f, 0.f};
+    for (int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; t < a.T; t += (int64_t)gridDim.x * blockDim.y) {
+        const vf4 v = reinterpret_cast<const vf4 *>(a.a)[t * nv + c];
+        for (int j = 0; j < a.k; ++j) {
+            const int at = a.slot[t * a.k + j];
+            if (at < 0 || at >= pairs) continue;
+            reinterpret_cast<vf4 *>(a.out)[at * nv + c] = at < placed ? v : vf4{0.f, 0.f, 0.f, 0.f};
+        }
     }
 }
 
@@ -162,22 +170,23 @@ __global__ __launch_bounds__(256) void route_combine_kernel(RouteRows a, int64_t
     constexpr int n = Vec<T>::n;
     typedef typename Vec<T>::v V;
     typedef float F __attribute__((ext_vector_type(n)));
-    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int64_t c = (int64_t)blockIdx.y * blockDim.x + threadIdx.x;
-    if (t >= a.T || c >= nv) return;
+    if (c >= nv) return;
     const int64_t pairs = a.T * a.k;
     const int64_t placed = *a.placed < pairs ? *a.placed : pairs;
     const V *z = reinterpret_cast<const V *>(a.a);
-    V *y = reinterpret_cast<V *>(a.out) + t * nv + c;
-    F sum = a.acc ? __builtin_convertvector(*y, F) : (F)(0.f);
+    for (int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; t < a.T; t += (int64_t)gridDim.x * blockDim.y) {
+        V *y = reinterpret_cast<V *>(a.out) + t * nv + c;
+        F sum = a.acc ? __builtin_convertvector(*y, F) : (F)(0.f);
 #pragma unroll 4
-    for (int j = 0; j < a.k; ++j) {
-        const int at = a.slot[t * a.k + j];
-        if (at < 0 || at >= placed) continue;  // nothing of its row or weight is read
-        const float w = a.weights ? a.weights[t * a.k + j] : 1.f;
-        sum += w * __builtin_convertvector(z[at * nv + c], F);
+        for (int j = 0; j < a.k; ++j) {
+            const int at = a.slot[t * a.k + j];
+            if (at < 0 || at >= placed) continue;  // nothing of its row or weight is read
+            const float w = a.weights ? a.weights[t * a.k + j] : 1.f;
+            sum += w * __builtin_convertvector(z[at * nv + c], F);
+        }
+        *y = __builtin_convertvector(sum, V);
     }
-    *y = __builtin_convertvector(sum, V);
 }
 
 // W waves walk a token's row together (W = 1: four tokens a workgroup). Four
@@ -190,57 +199,59 @@ __global__ __launch_bounds__(256) void route_combine_backward_kernel(RouteRows a
     typedef float F __attribute__((ext_vector_type(n)));
     __shared__ float part[4][4];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t t = W == 1 ? (int64_t)blockIdx.x * 4 + w : (int64_t)blockIdx.x;
-    if (t >= a.T) return;  // W = 1: no barrier follows; W = 4: never
     const int64_t pairs = a.T * a.k;
     const int64_t placed = *a.placed < pairs ? *a.placed : pairs;
-    const V *dy = reinterpret_cast<const V *>(a.a) + t * nv;
     const V *z = reinterpret_cast<const V *>(a.z);
     V *dz = reinterpret_cast<V *>(a.out);
-    for (int j0 = 0; j0 < a.k; j0 += 4) {
-        int at[4];
-        float wt[4], dot[4];
+    // W = 4: every wave takes the same tokens, so all meet at the barriers
+    for (int64_t t = W == 1 ? (int64_t)blockIdx.x * 4 + w : (int64_t)blockIdx.x; t < a.T;
+         t += (int64_t)gridDim.x * (4 / W)) {
+        const V *dy = reinterpret_cast<const V *>(a.a) + t * nv;
+        for (int j0 = 0; j0 < a.k; j0 += 4) {
+            int at[4];
+            float wt[4], dot[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool in = j0 + j < a.k;
-            at[j] = in ? a.slot[t * a.k + j0 + j] : -1;
-            if (at[j] >= pairs) at[j] = -1;
-            wt[j] = at[j] >= 0 && at[j] < placed && a.weights ? a.weights[t * a.k + j0 + j] : 1.f;
-            dot[j] = 0.f;
-        }
-        for (int64_t c = W == 1 ? lane : (int64_t)threadIdx.x; c < nv; c += 64 * W) {
-            const F g = __builtin_convertvector(dy[c], F);
+            for (int j = 0; j < 4; ++j) {
+                const bool in = j0 + j < a.k;
+                at[j] = in ? a.slot[t * a.k + j0 + j] : -1;
+                if (at[j] >= pairs) at[j] = -1;
+                wt[j] = at[j] >= 0 && at[j] < placed && a.weights ? a.weights[t * a.k + j0 + j] : 1.f;
+                dot[j] = 0.f;
+            }
+            for (int64_t c = W == 1 ? lane : (int64_t)threadIdx.x; c < nv; c += 64 * W) {
+                const F g = __builtin_convertvector(dy[c], F);
+                if (a.dw) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (at[j] >= 0 && at[j] < placed) {
+                            const F v = g * __builtin_convertvector(z[at[j] * nv + c], F);
+#pragma unroll
+                            for (int q = 0; q < n; ++q) dot[j] += v[q];
+                        }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (at[j] >= 0)
+                        dz[at[j] * nv + c] = at[j] < placed ? __builtin_convertvector(wt[j] * g, V) : (V)(T)0;
+            }
             if (a.dw) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (at[j] >= 0 && at[j] < placed) {
-                        const F v = g * __builtin_convertvector(z[at[j] * nv + c], F);
+                    for (int o = 32; o > 0; o /= 2) dot[j] += __shfl_xor(dot[j], o);
+                if (W == 1) {
+                    if (lane < 4 && j0 + lane < a.k)
+                        a.dw[t * a.k + j0 + lane] = lane == 0 ? dot[0] : lane == 1 ? dot[1] : lane == 2 ? dot[2] : dot[3];
+                } else {
+                    __syncthreads();  // the last four's sums have been read
+                    if (lane == 0) {
 #pragma unroll
-                        for (int q = 0; q < n; ++q) dot[j] += v[q];
+                        for (int j = 0; j < 4; ++j) part[w][j] = dot[j];
                     }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (at[j] >= 0)
-                    dz[at[j] * nv + c] = at[j] < placed ? __builtin_convertvector(wt[j] * g, V) : (V)(T)0;
-        }
-        if (a.dw) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                for (int o = 32; o > 0; o /= 2) dot[j] += __shfl_xor(dot[j], o);
-            if (W == 1) {
-                if (lane < 4 && j0 + lane < a.k)
-                    a.dw[t * a.k + j0 + lane] = lane == 0 ? dot[0] : lane == 1 ? dot[1] : lane == 2 ? dot[2] : dot[3];
-            } else {
-                __syncthreads();  // the last four's sums have been read
-                if (lane == 0) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) part[w][j] = dot[j];
+                    __syncthreads();
+                    const int j = threadIdx.x;
+                    if (j < 4 && j0 + j < a.k)
+                        a.dw[t * a.k + j0 + j] = ((part[0][j] + part[1][j]) + part[2][j]) + part[3][j];
                 }
-                __syncthreads();
-                const int j = threadIdx.x;
-                if (j < 4 && j0 + j < a.k)
-                    a.dw[t * a.k + j0 + j] = ((part[0][j] + part[1][j]) + part[2][j]) + part[3][j];
             }
         }
     }
@@ -250,7 +261,7 @@ template <typename T>
 hipError_t combine_t(const RouteRows &a, hipStream_t s) {
     const int64_t nv = a.d / Vec<T>::n;
     const int tx = row_threads(nv);
-    const dim3 block(tx, 256 / tx), grid((unsigned)((a.T + block.y - 1) / block.y), (unsigned)((nv + tx - 1) / tx));
+    const dim3 block(tx, 256 / tx), grid(token_blocks(a.T, block.y), (unsigned)((nv + tx - 1) / tx));
     hipLaunchKernelGGL((route_combine_kernel<T>), grid, block, 0, s, a, nv);
     return hipGetLastError();
 }
@@ -260,10 +271,9 @@ hipError_t combine_backward_t(const RouteRows &a, hipStream_t s) {
     const int64_t nv = a.d / Vec<T>::n;
     // rows of up to 256 vectors: a wave each, no barrier; longer ones: four
     if (nv <= 256)
-        hipLaunchKernelGGL((route_combine_backward_kernel<T, 1>), dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, s, a,
-                           nv);
+        hipLaunchKernelGGL((route_combine_backward_kernel<T, 1>), dim3(token_blocks(a.T, 4)), dim3(256), 0, s, a, nv);
     else
-        hipLaunchKernelGGL((route_combine_backward_kernel<T, 4>), dim3((unsigned)a.T), dim3(256), 0, s, a, nv);
+        hipLaunchKernelGGL((route_combine_backward_kernel<T, 4>), dim3(token_blocks(a.T, 1)), dim3(256), 0, s, a, nv);
     return hipGetLastError();
 }
 
@@ -296,7 +306,7 @@ hipError_t launch_route_sort(const RouteSortArgs &a, hipStream_t s) {
 hipError_t launch_route_gather(const RouteRows &a, hipStream_t s) {
     const int64_t nv = a.d * (a.dtype == 0 ? 4 : 2) / 16;
     const int tx = row_threads(nv);
-    const dim3 block(tx, 256 / tx), grid((unsigned)((a.T + block.y - 1) / block.y), (unsigned)((nv + tx - 1) / tx));
+    const dim3 block(tx, 256 / tx), grid(token_blocks(a.T, block.y), (unsigned)((nv + tx - 1) / tx));
     prof_begin(K_ROUTE_GATHER, s);
     hipLaunchKernelGGL(route_gather_kernel, grid, block, 0, s, a, nv);
     hipError_t e = hipGetLastError();

@@ -169,9 +169,11 @@ def test_accepted_sizes_reach_the_device():
                                              (30000, 5120, 17408, 64, 16), (100000, 128, 1 << 20, 128, 1024)])
 def test_adapter_workspace_stays_in_proportion(M, d_in, d_out, r, E):
     """The gradients' partials stay below the activations that the call reads,
-    the splits' below 34 copies of s, and the transposes take the adapters once."""
+    the splits' below 34 copies of s, the transposes take the adapters once, and
+    the panels six bytes for each of at most 16 more ranks and E tiles."""
     n = blr.load().blr_adapters_workspace_bytes(M, d_in, d_out, r, E)
-    assert 0 < n <= 34 * 4 * M * r + 4 * M * max(d_in, d_out) + 4 * E * r * (d_in + d_out) + 4096
+    assert 0 < n <= 34 * 4 * M * r + 4 * M * (d_in + d_out) + 4 * E * r * (d_in + d_out) \
+        + 2 * 6 * 2 * r * (M + 64 * min(E + 1, M)) + 4096
 
 
 def test_binding_refuses():
