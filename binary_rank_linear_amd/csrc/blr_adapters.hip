@@ -29,6 +29,7 @@ namespace blr {
 namespace {
 
 constexpr int TM = ADAPT_TM;
+typedef uint32_t vu4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ vf4 mfma4(float a, float b, vf4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
@@ -257,20 +258,168 @@ __device__ void shrink_tile(const AdaptShrink &a, const Tile &tile, int from, in
     }
 }
 
+// The same for tiles of up to 64 rows, by way of LDS. A load instruction takes
+// the vector cache one cycle for every four lanes if those lie together in
+// memory, and one for every lane if not: lanes laid out for the matrix operand
+// (each another row) cost four times the cycles, and that, not HBM, bounds the
+// loads above. So eight lanes read 128 bytes of a row, and a wave turns its
+// step of X and of the weights round through 16-byte slots of its own (slot
+// h of row m stands at h ^ (m & 7), which spreads both sides over the banks);
+// no barrier, since no other wave reads them.
+template <typename TX, typename TW, int RT>
+struct ShrinkLds {
+    static constexpr int COLS = 128 / sizeof(TX);
+    static constexpr int X_BYTES = 64 * 128;
+    static constexpr int W_ROW = COLS * sizeof(TW);  // 128, or 64 for 16-bit weights beside f32 rows
+    static constexpr int W_BYTES = RT * 16 * W_ROW;
+    static constexpr int W_LOADS = W_BYTES / 1024;
+    static constexpr int BYTES = X_BYTES + W_BYTES;
+    vu4 x[8], w[W_LOADS];
+
+    __device__ __forceinline__ void load(const TX *const *row, const TW *W, const unsigned *rank, int k0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const vu4 *>(row[i] + k0);
+#pragma unroll
+        for (int i = 0; i < W_LOADS; ++i) w[i] = *reinterpret_cast<const vu4 *>(ahead(W + k0, rank[i]));
+    }
+    __device__ __forceinline__ void stage(char *lds, int lane) const {
+        const int m = lane >> 3, h = (lane & 7) ^ (m & 7);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *reinterpret_cast<vu4 *>(lds + (8 * i + m) * 128 + h * 16) = x[i];
+        lds += X_BYTES;
+        if constexpr (W_ROW == 128) {
+#pragma unroll
+            for (int i = 0; i < W_LOADS; ++i) *reinterpret_cast<vu4 *>(lds + (8 * i + m) * 128 + h * 16) = w[i];
+        } else {
+            const int n = lane >> 2, g = (lane & 3) ^ ((n >> 1) & 3);
+#pragma unroll
+            for (int i = 0; i < W_LOADS; ++i) *reinterpret_cast<vu4 *>(lds + (16 * i + n) * 64 + g * 16) = w[i];
+        }
+    }
+    // One tile of 16 rows against all ranks, half h of the step's columns.
+    static __device__ __forceinline__ void multiply(const char *lds, vf4 (&acc)[4][RT], int q, int c) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int at = ((4 * h + q) ^ (c & 7)) * 16;
+            if constexpr (sizeof(TX) == 4) {
+                vf4 wv[RT];
+#pragma unroll
+                for (int n = 0; n < RT; ++n) {
+                    const char *p = lds + X_BYTES + (16 * n + c) * W_ROW;
+                    if constexpr (W_ROW == 128)
+                        wv[n] = *reinterpret_cast<const vf4 *>(p + at);
+                    else
+                        wv[n] = load4(reinterpret_cast<const TW *>(p + ((2 * h + (q >> 1)) ^ ((c >> 1) & 3)) * 16) +
+                                      4 * (q & 1));
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const vf4 xv = *reinterpret_cast<const vf4 *>(lds + (16 * t + c) * 128 + at);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int n = 0; n < RT; ++n) acc[t][n] = mfma4(xv[j], wv[n][j], acc[t][n]);
+                }
+            } else {
+                typedef typename Vec<TX>::v V;
+                V wv[RT];
+#pragma unroll
+                for (int n = 0; n < RT; ++n)
+                    wv[n] = *reinterpret_cast<const V *>(lds + X_BYTES + (16 * n + c) * 128 + at);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const V xv = *reinterpret_cast<const V *>(lds + (16 * t + c) * 128 + at);
+#pragma unroll
+                    for (int n = 0; n < RT; ++n) acc[t][n] = mfma8(xv, wv[n], acc[t][n]);
+                }
+            }
+        }
+    }
+};
+
+// Orders a wave's own writes and reads of LDS (they execute in order; this
+// keeps the compiler from moving one past the other).
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+template <typename TX, typename TW, int RT>
+__device__ void shrink_tile_lds(const AdaptShrink &a, const Tile &tile, int from, int to, char *lds,
+                                float (*red)[RT * 16 + 1]) {
+    typedef ShrinkLds<TX, TW, RT> Step;
+    const int lane = threadIdx.x & 63, w = wave();
+    const int q = lane >> 4, c = lane & 15;
+    const TW *W = reinterpret_cast<const TW *>(a.W) + (int64_t)tile.e * a.r * a.K;
+    const TX *x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        // rows past the tile, or not named by the plan, repeat one; not stored
+        const int m = 8 * i + (lane >> 3);
+        const int64_t row = row_of(a.plan, tile.p0 + (m < tile.cnt ? m : tile.cnt - 1));
+        x[i] = reinterpret_cast<const TX *>(a.X) + (row < 0 ? 0 : row) * a.K + (lane & 7) * (16 / sizeof(TX));
+    }
+    unsigned rank[Step::W_LOADS];
+#pragma unroll
+    for (int i = 0; i < Step::W_LOADS; ++i) {
+        const int per = Step::W_ROW / 16;  // lanes of a rank's columns
+        const int n = i * (64 / per) + lane / per;  // columns past r of the product are not stored
+        rank[i] = (unsigned)((n < a.r ? n : a.r - 1) * a.K) * (unsigned)sizeof(TW) + (lane % per) * 16;
+    }
+    vf4 acc[4][RT];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int n = 0; n < RT; ++n) acc[t][n] = vf4{0.f, 0.f, 0.f, 0.f};
+    char *mine = lds + w * Step::BYTES;
+    const int first = from + w, n = (to - first + 3) / 4;
+    if (n > 0) {
+        Step st;
+        st.load(x, W, rank, first * Step::COLS);
+        for (int i = 0; i < n; ++i) {
+            st.stage(mine, lane);
+            wave_lds_fence();
+            st.load(x, W, rank, (first + 4 * (i + 1 < n ? i + 1 : i)) * Step::COLS);  // no branch: see walk
+            __builtin_amdgcn_sched_barrier(0);
+            Step::multiply(mine, acc, q, c);
+            wave_lds_fence();
+        }
+    }
+    __syncthreads();  // red lies in the same memory
+    for (int v = 0; v < 4; ++v) {
+        if (w == v) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int n = 0; n < RT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float *at = &red[t * 16 + 4 * q + i][n * 16 + c];
+                        *at = v == 0 ? acc[t][n][i] : *at + acc[t][n][i];
+                    }
+        }
+        __syncthreads();
+    }
+}
+
 // One workgroup: 64 rows x all r over one split of K, the splits of a tile next
 // to each other (the grid is one-dimensional: its other dimensions are short).
 template <typename TX, typename TW, int RT>
 __global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_shrink_kernel(AdaptShrink a) {
-    __shared__ float red[TM][RT * 16 + 1];
+    typedef ShrinkLds<TX, TW, RT> Lds;
+    __shared__ __align__(16) char lds[4 * Lds::BYTES];
+    float(*red)[RT * 16 + 1] = reinterpret_cast<float(*)[RT * 16 + 1]>(lds);
+    static_assert(sizeof(float) * TM * (RT * 16 + 1) <= sizeof(lds), "the sums fit");
     const int split = blockIdx.x % a.splits;
     const Tile tile = find_tile(a.plan, a.plan.E, TM, blockIdx.x / a.splits);
     if (tile.e < 0) return;
-    const int64_t steps = a.K / ShrinkStep<TX, TW, RT, 1>::COLS;
+    const int64_t steps = a.K / Lds::COLS;
     const int from = (int)(steps * split / a.splits), to = (int)(steps * (split + 1) / a.splits);
     if (tile.cnt <= 16)
         shrink_tile<TX, TW, RT, 1>(a, tile, from, to, red);
     else
-        shrink_tile<TX, TW, RT, 4>(a, tile, from, to, red);
+        shrink_tile_lds<TX, TW, RT>(a, tile, from, to, lds, red);
     float *part = a.part + ((int64_t)split * a.plan.M + tile.p0) * a.r;
     for (int i = threadIdx.x; i < tile.cnt * a.r; i += 256) part[i] = red[i / a.r][i % a.r];
 }
@@ -301,7 +450,7 @@ struct ExpandStep {
     vf4 y[NT][2];
 
     template <bool ACC>
-    __device__ __forceinline__ void load(TX *const *row, const TW *W, int r, int N, int o0, int q, int c) {
+    __device__ __forceinline__ void load(TX *const *row, const TW *W, int r, int o0, int q, int c) {
         if (ACC) {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -318,7 +467,7 @@ struct ExpandStep {
             }
         }
     }
-    template <bool ACC, bool FULL>
+    template <bool ACC>
     __device__ __forceinline__ void multiply_store(const S &s, TX *const *out, int r, int o0, int q) {
         vf4 v[2][RT];
 #pragma unroll
@@ -339,7 +488,7 @@ struct ExpandStep {
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) d[h] = mfma4(v[h][n][j], s.v[t][n][j], d[h]);
-            if (FULL || out[t]) {
+            if (out[t]) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) store4(out[t] + o0 + 16 * h + 4 * q, d[h]);
             }
@@ -355,6 +504,15 @@ __device__ __forceinline__ T take_term(float &v) {
     const float left = v - (float)t;
     v = __builtin_isfinite(left) ? left : 0.f;
     return t;
+}
+
+// The power of two at the largest element of a row of s, or its inverse; 1
+// where that is zero or not finite.
+__device__ __forceinline__ float power_of(float top, bool itself) {
+    if (!(top > 0.f) || !__builtin_isfinite(top)) return 1.f;
+    int e = (int)((__float_as_uint(top) >> 23) & 255) - 127;  // subnormal: -127
+    e = e < -120 ? -120 : e > 120 ? 120 : e;
+    return __uint_as_float((unsigned)(127 + (itself ? e : -e)) << 23);
 }
 
 // Rows of 16 bits: four tiles, 64 columns a step; column i of row 4 q' of tile
@@ -379,13 +537,8 @@ struct ExpandStep16 {
                 float by = 1.f;
                 back[t] = 1.f;
                 if constexpr (__is_same(T, _Float16)) {
-                    const float top = largest[m];
-                    if (top > 0.f && __builtin_isfinite(top)) {
-                        int e = (int)((__float_as_uint(top) >> 23) & 255) - 127;  // subnormal: -127
-                        e = e < -120 ? -120 : e > 120 ? 120 : e;
-                        by = __uint_as_float((unsigned)(127 - e) << 23);
-                        back[t] = __uint_as_float((unsigned)(127 + e) << 23);
-                    }
+                    by = power_of(largest[m], false);
+                    back[t] = power_of(largest[m], true);
                 }
 #pragma unroll
                 for (int kk = 0; kk < KS; ++kk) {
@@ -404,7 +557,7 @@ struct ExpandStep16 {
     V w[4][KS], y[NT][2];
 
     template <bool ACC>
-    __device__ __forceinline__ void load(T *const *row, const T *W, int r, int N, int o0, int q, int c) {
+    __device__ __forceinline__ void load(T *const *row, const T *W, int r, int o0, int q, int c) {
         if (ACC) {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -422,7 +575,7 @@ struct ExpandStep16 {
             }
         }
     }
-    template <bool ACC, bool FULL>
+    template <bool ACC>
     __device__ __forceinline__ void multiply_store(const S &s, T *const *out, int r, int o0, int q) {
         typedef float F __attribute__((ext_vector_type(8)));
 #pragma unroll
@@ -445,7 +598,7 @@ struct ExpandStep16 {
                     for (int h = 0; h < 4; ++h) d[h] = mfma8(w[h][kk], s.lo[t][kk], d[h]);
                 }
             }
-            if (FULL || out[t]) {
+            if (out[t]) {
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     const vf4 u = s.back[t] * d[2 * g], v = s.back[t] * d[2 * g + 1];
@@ -462,11 +615,10 @@ struct ExpandStep<_Float16, _Float16, RT, NT> : ExpandStep16<_Float16, RT, NT> {
 template <int RT, int NT>
 struct ExpandStep<__bf16, __bf16, RT, NT> : ExpandStep16<__bf16, RT, NT> {};
 
-// A wave's steps (every fourth of [from, to)) over NT x 16 rows. FULL: every
-// row of the tile is written.
-template <typename TX, typename TW, int RT, int NT, bool ACC, bool FULL>
-__device__ void expand_tile(const AdaptExpand &a, const Tile &tile, int r, int from, int to,
-                            const float (*S)[RT * 16 + 4], const float *largest) {
+// A wave's steps (every fourth of [from, to)) over NT x 16 rows.
+template <typename TX, typename TW, int RT, int NT, bool ACC>
+__device__ void expand_tile(const AdaptExpand &a, const Tile &tile, int from, int to, const float (*S)[RT * 16 + 4],
+                            const float *largest) {
     typedef ExpandStep<TX, TW, RT, NT> Step;
     const int lane = threadIdx.x & 63, w = wave();
     const int q = lane >> 4, c = lane & 15;
@@ -480,21 +632,191 @@ __device__ void expand_tile(const AdaptExpand &a, const Tile &tile, int r, int f
     }
     typename Step::S s;
     s.load(S, largest, q, c);
-    const TW *W = reinterpret_cast<const TW *>(a.W) + (int64_t)(r ? tile.e : 0) * a.r * a.N;
+    const TW *W = reinterpret_cast<const TW *>(a.W) + (int64_t)tile.e * a.r * a.N;
     const int first = from + w;
     walk<Step, RT <= 4>((to - first + 3) / 4,
-               [&](Step &st, int i) { st.template load<ACC>(row, W, r, a.N, (first + 4 * i) * Step::COLS, q, c); },
+               [&](Step &st, int i) { st.template load<ACC>(row, W, a.r, (first + 4 * i) * Step::COLS, q, c); },
                [&](Step &st, int i) {
-                   st.template multiply_store<ACC, FULL>(s, FULL ? row : out, r, (first + 4 * i) * Step::COLS, q);
+                   st.template multiply_store<ACC>(s, out, a.r, (first + 4 * i) * Step::COLS, q);
                });
+}
+
+// The same for tiles of up to 64 rows, each wave its 16 of them, by way of
+// LDS: the lanes of a load or store have to lie together in memory (see the
+// shrink), so here the rows are the A operand and the columns the B operand,
+// with column c of tile h standing for column 16 / size * c + h of the step:
+// lane (q, c) ends with 16 consecutive bytes of each of rows 4 q .. 4 q + 3,
+// 256 bytes of a row in 16 lanes. The step's weights, which lie together, are
+// brought into operand order through LDS once for the four waves, in two
+// buffers, one barrier a step.
+//
+// Operand slots of 16 bytes: [tile h][group of ranks][lane].
+template <typename TX, typename TW, int RT>
+struct ExpandLds {
+    static constexpr bool WIDE = sizeof(TX) == 4;  // f32 rows: 4 ranks a slot, else 8
+    static constexpr int H = 16 / sizeof(TX);      // tiles of a step, and elements of 16 bytes of a row
+    static constexpr int COLS = 16 * H;
+    static constexpr bool PACKED = !WIDE && RT == 1;  // both terms of s in one instruction
+    static constexpr int KS = WIDE ? RT : (RT + 1) / 2;
+    static constexpr int SLOTS = H * KS * 64;
+    typedef typename Vec<TX>::v V;
+    typedef typename std::conditional<WIDE, typename Vec<TW>::v4, vu4>::type Piece;  // a slot's ranks, as they lie
+    static constexpr int RANKS = WIDE ? 4 : 8;
+    static constexpr int PIECES = (COLS * RT * 16 / RANKS + 255) / 256;  // a thread's, at most
+
+    // Thread i's pieces of the step: piece p holds ranks RANKS (p % per) ..
+    // of column p / per, p = i + 256 j.
+    static __device__ __forceinline__ void load(Piece (&w)[PIECES], const TW *W, int r, int o0) {
+        const int total = COLS * r / RANKS;
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j) {
+            const int p = threadIdx.x + 256 * j;
+            w[j] = *reinterpret_cast<const Piece *>(
+                ahead(W + (int64_t)o0 * r, (unsigned)(p < total ? p : 0) * (unsigned)(RANKS * sizeof(TW))));
+        }
+    }
+    // Where they go, -1: nowhere.
+    static __device__ __forceinline__ void places(int (&at)[PIECES], int r) {
+        const int per = r / RANKS;
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j) {
+            const int p = threadIdx.x + 256 * j, o = p / per, k = p % per;
+            const int h = o % H, c = o / H;
+            at[j] = o < COLS ? ((h * KS + k / 4) * 64 + (k % 4) * 16 + c) : -1;
+        }
+    }
+    static __device__ __forceinline__ void stage(vu4 *lds, const Piece (&w)[PIECES], const int (&at)[PIECES]) {
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j)
+            if (at[j] >= 0) {
+                if constexpr (WIDE)
+                    *reinterpret_cast<vf4 *>(lds + at[j]) = __builtin_convertvector(w[j], vf4);
+                else {
+                    lds[at[j]] = w[j];
+                    if (PACKED) lds[at[j] + 32] = w[j];  // lanes q + 2: the second term's
+                }
+            }
+    }
+};
+
+// FULL: every row of the tile is written.
+template <typename TX, typename TW, int RT, bool ACC, bool FULL>
+__device__ void expand_tile_lds(const AdaptExpand &a, const Tile &tile, int from, int to, const float (*S)[RT * 16 + 4],
+                                const float *largest, vu4 *lds) {
+    typedef ExpandLds<TX, TW, RT> L;
+    typedef typename L::V V;
+    typedef float F __attribute__((ext_vector_type(L::H)));
+    const int lane = threadIdx.x & 63, w = wave();
+    const int q = lane >> 4, c = lane & 15;
+    TX *row[4];
+    bool in[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int m = 16 * w + 4 * q + i;
+        const int64_t at = row_of(a.plan, tile.p0 + (m < tile.cnt ? m : tile.cnt - 1));
+        row[i] = reinterpret_cast<TX *>(a.out) + (at < 0 ? 0 : at) * a.N + L::H * c;
+        in[i] = m < tile.cnt && at >= 0;
+    }
+    // s of row c as the A operand: f32, or two terms
+    const int m = 16 * w + c;
+    vf4 s[RT];
+    V hi[L::KS], lo[L::KS];
+    float back[4] = {1.f, 1.f, 1.f, 1.f};
+    if constexpr (L::WIDE) {
+#pragma unroll
+        for (int n = 0; n < RT; ++n) s[n] = *reinterpret_cast<const vf4 *>(&S[m][n * 16 + q * 4]);
+    } else {
+        float by = 1.f;
+        if constexpr (__is_same(TX, _Float16)) {
+            by = power_of(largest[m], false);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) back[i] = power_of(largest[16 * w + 4 * q + i], true);
+        }
+#pragma unroll
+        for (int kk = 0; kk < L::KS; ++kk) {
+            const int k = L::PACKED ? (q & 1) * 8 : kk * 32 + q * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float v = by * S[m][k + j];
+                hi[kk][j] = take_term<TX>(v);
+                lo[kk][j] = take_term<TX>(v);
+            }
+            if (L::PACKED && q >= 2) hi[kk] = lo[kk];
+        }
+    }
+    __syncthreads();  // S lies in the same memory as the weights
+    for (int i = threadIdx.x; i < 2 * L::SLOTS; i += 256) lds[i] = vu4{0, 0, 0, 0};  // ranks past r stay zero
+    __syncthreads();
+    const TW *W = reinterpret_cast<const TW *>(a.W) + (int64_t)tile.e * a.r * a.N;
+    typename L::Piece piece[L::PIECES];
+    int place[L::PIECES];
+    L::places(place, a.r);
+    V next[4];
+    auto load = [&](int step) {
+        L::load(piece, W, a.r, step * L::COLS);
+        if (ACC) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) next[i] = *reinterpret_cast<const V *>(row[i] + step * L::COLS);
+        }
+    };
+    load(from);
+    for (int step = from; step < to; ++step) {
+        vu4 *buf = lds + ((step - from) & 1) * L::SLOTS;
+        L::stage(buf, piece, place);
+        V old[4];
+        if (ACC) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) old[i] = next[i];
+        }
+        __syncthreads();
+        load(step + 1 < to ? step + 1 : step);  // no branch: see walk
+        __builtin_amdgcn_sched_barrier(0);
+        vf4 d[L::H];
+#pragma unroll
+        for (int h = 0; h < L::H; ++h) {
+            d[h] = vf4{0.f, 0.f, 0.f, 0.f};
+            if constexpr (L::WIDE && ACC) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[h][i] = old[i][h];
+            }
+        }
+#pragma unroll
+        for (int kk = 0; kk < L::KS; ++kk)
+#pragma unroll
+            for (int h = 0; h < L::H; ++h) {
+                const vu4 slot = buf[(h * L::KS + kk) * 64 + lane];
+                if constexpr (L::WIDE) {
+                    const vf4 v = __builtin_bit_cast(vf4, slot);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) d[h] = mfma4(s[kk][j], v[j], d[h]);
+                } else {
+                    const V v = __builtin_bit_cast(V, slot);
+                    d[h] = mfma8(hi[kk], v, d[h]);
+                    if (!L::PACKED) d[h] = mfma8(lo[kk], v, d[h]);
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            F f;
+#pragma unroll
+            for (int h = 0; h < L::H; ++h) f[h] = d[h][i];
+            if constexpr (!L::WIDE) {
+                f *= back[i];
+                if (ACC) f += __builtin_convertvector(old[i], F);
+            }
+            if (FULL || in[i]) *reinterpret_cast<V *>(row[i] + step * L::COLS) = __builtin_convertvector(f, V);
+        }
+    }
 }
 
 // One workgroup: 64 rows x a range of columns. The prologue adds the splits'
 // partials; the workgroups of the first range also write s out.
-// Two workgroups share a CU where their registers allow it without spills.
 template <typename TX, typename TW, int RT, bool ACC>
-__global__ __launch_bounds__(256, RT <= (__is_same(TX, _Float16) && ACC ? 2 : 4) ? 2 : 1) void adapt_expand_kernel(AdaptExpand a, int chunks) {
-    __shared__ float S[TM][RT * 16 + 4];
+__global__ __launch_bounds__(256) void adapt_expand_kernel(AdaptExpand a, int chunks) {
+    typedef ExpandLds<TX, TW, RT> Lds;
+    constexpr int S_BYTES = sizeof(float) * TM * (RT * 16 + 4), W_BYTES = 2 * 16 * Lds::SLOTS;
+    __shared__ __align__(16) char lds[S_BYTES > W_BYTES ? S_BYTES : W_BYTES];
+    float(*S)[RT * 16 + 4] = reinterpret_cast<float(*)[RT * 16 + 4]>(lds);
     __shared__ float largest[TM];
     __shared__ int named;
     const int chunk = blockIdx.x % chunks;
@@ -504,8 +826,8 @@ __global__ __launch_bounds__(256, RT <= (__is_same(TX, _Float16) && ACC ? 2 : 4)
     const float scale = a.scale && !none ? a.scale[tile.e] : 1.f;
     if (threadIdx.x < TM) {  // one wave
         const bool ok = threadIdx.x < tile.cnt && row_of(a.plan, tile.p0 + threadIdx.x) >= 0;
+        if (threadIdx.x == 0) named = 0;
         if (__ballot(ok) == ~0ull && threadIdx.x == 0) named = 1;
-        if (__ballot(ok) != ~0ull && threadIdx.x == 0) named = 0;
     }
     const int rows = tile.cnt <= 16 ? 16 : TM;
     for (int i = threadIdx.x; i < rows * RT * 16; i += 256) {
@@ -525,6 +847,17 @@ __global__ __launch_bounds__(256, RT <= (__is_same(TX, _Float16) && ACC ? 2 : 4)
     }
     if (none && ACC) return;
     __syncthreads();
+    if (none) {
+        // rows without an adapter: zeros
+        const int64_t n16 = (int64_t)a.N * sizeof(TX) / 16, lo = n16 * chunk / chunks, hi = n16 * (chunk + 1) / chunks;
+        for (int m = 0; m < tile.cnt; ++m) {
+            const int64_t row = row_of(a.plan, tile.p0 + m);
+            if (row < 0) continue;
+            vu4 *out = reinterpret_cast<vu4 *>(reinterpret_cast<TX *>(a.out) + row * a.N);
+            for (int64_t i = lo + threadIdx.x; i < hi; i += 256) out[i] = vu4{0, 0, 0, 0};
+        }
+        return;
+    }
     if (__is_same(TX, _Float16)) {
         if (threadIdx.x < rows) {
             float top = 0.f;
@@ -533,15 +866,18 @@ __global__ __launch_bounds__(256, RT <= (__is_same(TX, _Float16) && ACC ? 2 : 4)
         }
         __syncthreads();
     }
-    const int64_t steps = a.N / ExpandStep<TX, TW, RT, 1>::COLS;
+    if (tile.cnt <= 16) {
+        const int64_t steps = a.N / ExpandStep<TX, TW, RT, 1>::COLS;
+        const int from = (int)(steps * chunk / chunks), to = (int)(steps * (chunk + 1) / chunks);
+        expand_tile<TX, TW, RT, 1, ACC>(a, tile, from, to, S, largest);
+        return;
+    }
+    const int64_t steps = a.N / Lds::COLS;
     const int from = (int)(steps * chunk / chunks), to = (int)(steps * (chunk + 1) / chunks);
-    const int r = none ? 0 : a.r;
-    if (tile.cnt <= 16)
-        expand_tile<TX, TW, RT, 1, ACC, false>(a, tile, r, from, to, S, largest);
-    else if (named)
-        expand_tile<TX, TW, RT, 4, ACC, true>(a, tile, r, from, to, S, largest);
+    if (named)
+        expand_tile_lds<TX, TW, RT, ACC, true>(a, tile, from, to, S, largest, reinterpret_cast<vu4 *>(lds));
     else
-        expand_tile<TX, TW, RT, 4, ACC, false>(a, tile, r, from, to, S, largest);
+        expand_tile_lds<TX, TW, RT, ACC, false>(a, tile, from, to, S, largest, reinterpret_cast<vu4 *>(lds));
 }
 
 // ------------------------------------------------------------- transpose --
@@ -610,15 +946,19 @@ __global__ __launch_bounds__(256) void adapt_thin_kernel(AdaptThin a) {
     __syncthreads();
     const int64_t panel = (int64_t)blockIdx.x * RT * 16 * TM;
     if constexpr (sizeof(TX) == 4) {
+        // [16 rows][16 ranks][lane][4]
         float *to = reinterpret_cast<float *>(a.panel[blockIdx.y]) + panel;
-        for (int i = threadIdx.x; i < RT * 16 * 16; i += 256) {
-            const int k = i >> 4, t = (i & 15) * 4;
-            store4(to + k * TM + t, vf4{S[t][k], S[t + 1][k], S[t + 2][k], S[t + 3][k]});
+        for (int i = threadIdx.x; i < 4 * RT * 64; i += 256) {
+            const int lane = i & 63, n = (i >> 6) % RT, step = (i >> 6) / RT;
+            const int k = n * 16 + (lane & 15), t = step * 16 + (lane >> 4) * 4;
+            store4(to + i * 4, vf4{S[t][k], S[t + 1][k], S[t + 2][k], S[t + 3][k]});
         }
     } else {
+        // [32 rows][term][16 ranks][lane][8]
         __bf16 *to = reinterpret_cast<__bf16 *>(a.panel[blockIdx.y]) + 3 * panel;
-        for (int i = threadIdx.x; i < RT * 16 * 8; i += 256) {
-            const int k = i >> 3, t = (i & 7) * 8;
+        for (int i = threadIdx.x; i < 2 * RT * 64; i += 256) {
+            const int lane = i & 63, n = (i >> 6) % RT, step = (i >> 6) / RT;
+            const int k = n * 16 + (lane & 15), t = step * 32 + (lane >> 4) * 8;
             vb8 term[3];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -627,7 +967,8 @@ __global__ __launch_bounds__(256) void adapt_thin_kernel(AdaptThin a) {
                 for (int h = 0; h < 3; ++h) term[h][j] = take_term<__bf16>(v);
             }
 #pragma unroll
-            for (int h = 0; h < 3; ++h) *reinterpret_cast<vb8 *>(to + (h * RT * 16 + k) * TM + t) = term[h];
+            for (int h = 0; h < 3; ++h)
+                *reinterpret_cast<vb8 *>(to + (((step * 3 + h) * RT + n) * 64 + lane) * 8) = term[h];
         }
     }
 }
@@ -655,9 +996,9 @@ struct GradStep {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             x[j] = load4((r[j] < 0 ? reinterpret_cast<const TX *>(zero_row) : X + (int64_t)r[j] * N) + 4 * c);
-        const float *p = panel + (int64_t)(m / TM) * RT * 16 * TM + m % TM;
+        const float *p = panel + (int64_t)(m / ROWS) * RT * 256;
 #pragma unroll
-        for (int n = 0; n < RT; ++n) t[n] = load4(ahead(p + n * 16 * TM, (unsigned)(c * TM + 4 * q) * 4u));
+        for (int n = 0; n < RT; ++n) t[n] = load4(ahead(p + n * 256, (unsigned)(q * 16 + c) * 16u));
     }
     __device__ __forceinline__ void multiply(vf4 (&acc)[4][RT]) const {
 #pragma unroll
@@ -688,13 +1029,13 @@ struct GradStep16 {
         for (int j = 0; j < 8; ++j)
             x[j] = *reinterpret_cast<const uint2 *>(
                 (r[j] < 0 ? reinterpret_cast<const T *>(zero_row) : X + (int64_t)r[j] * N) + 4 * c);
-        const __bf16 *p = panel + (int64_t)(m / TM) * 3 * RT * 16 * TM + m % TM;
+        const __bf16 *p = panel + (int64_t)(m / ROWS) * 3 * RT * 512;
 #pragma unroll
         for (int h = 0; h < 3; ++h)
 #pragma unroll
             for (int n = 0; n < RT; ++n)
                 t[h][n] = *reinterpret_cast<const vb8 *>(
-                    ahead(p + (h * RT + n) * 16 * TM, (unsigned)(c * TM + 8 * q) * 2u));
+                    ahead(p + (h * RT + n) * 512, (unsigned)(q * 16 + c) * 16u));
     }
     __device__ __forceinline__ void multiply(vf4 (&acc)[4][RT]) const {
 #pragma unroll

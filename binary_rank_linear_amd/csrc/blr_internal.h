@@ -253,8 +253,8 @@ struct AdaptExpand {
 // The gradients' thin operands, once per call: ds [p][r] = scale_e sum over
 // splits of part[.][p], and both ds and the tape s (by row) as panels: of each
 // tile of 64 positions, its ranks (rounded up to 16, 32, 64 or 128: r16) by 64
-// positions, zero past the tile's end. For rows of f32 a panel is f32
-// [r16][64]; for rows of 16 bits three bf16 terms [3][r16][64].
+// positions, zero past the tile's end, in the order of the matrix operand; f32
+// for rows of f32, three bf16 terms for rows of 16 bits.
 struct AdaptThin {
     AdaptPlan plan;
     const float *part, *scale, *tape;  // tape null: ds alone, no panels
