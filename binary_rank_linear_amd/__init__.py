@@ -391,13 +391,13 @@ _dtypes = None
 
 
 def _types():
-    """(f32, i32, wide, bytes): dtype tuples for the checks below. `wide` are
-    the element types of rows and adapters; their places are their numbers in
-    the C ABI."""
+    """(f32, i32, wide, bytes, codes): dtype tuples for the checks below, and
+    the numbers in the C ABI of `wide`, the element types of rows and adapters."""
     global _dtypes
     if _dtypes is None:
         import torch
-        _dtypes = ((torch.float32,), (torch.int32,), (torch.float32, torch.float16, torch.bfloat16), (torch.uint8,))
+        wide = (torch.float32, torch.float16, torch.bfloat16)
+        _dtypes = ((torch.float32,), (torch.int32,), wide, (torch.uint8,), {t: i for i, t in enumerate(wide)})
     return _dtypes
 
 
@@ -405,12 +405,23 @@ def _at(t, name, dtypes, shape, dev):
     """Address of t, a contiguous tensor of this shape on GPU number dev. The
     checks are _need's, in the order that costs least when all is well."""
     try:
-        if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == dev >= 0:
             return t.data_ptr()
     except AttributeError:
         pass
     _need(t, name, dtypes, shape)
     raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+
+
+def _shape(t, name, dims):
+    """t's shape, of `dims` dimensions."""
+    try:
+        shape = t.shape
+        if len(shape) == dims:
+            return shape
+    except (AttributeError, TypeError):
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    raise ValueError(f"{name} has shape {tuple(shape)}, expected {dims} dimensions")
 
 
 def _new(shape, dtype, dev, stream):
@@ -419,9 +430,9 @@ def _new(shape, dtype, dev, stream):
     on, so it is made on the one that the kernels run on."""
     import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
 
 
 def _out(t, name, dtype, shape, dev, stream):
@@ -440,13 +451,21 @@ def _ws(ws, need, name, dev, stream):
             raise BlrError(-2, name)
         ws = _new(need, u8[0], dev, stream)
         return ws, (ws.data_ptr(), need)
-    _need(ws, "ws", u8)
-    return ws, (_at(ws, "ws", u8, ws.shape, dev), ws.numel())
+    shape = _shape(ws, "ws", 1)
+    return ws, (_at(ws, "ws", u8, shape, dev), shape[0])
 
 
-def _on(stream, dev):
+def _device(t, name, dtypes, stream):
+    """The GPU that t is on, and stream too."""
+    try:
+        dev = t.get_device()
+    except AttributeError:
+        dev = -1
+    if dev < 0:
+        _need(t, name, dtypes)
     if stream is not None and stream.device.index != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+    return dev
 
 
 def _launch(name, dev, stream, *args):
@@ -485,11 +504,11 @@ def blr_route_sort(ids, experts: int, *, offsets=None, order=None, slot=None, ws
     in the shape of ids): the plan that the gather, the combine and the
     adapters take."""
     i32 = _types()[1]
-    _need(ids, "ids", i32)
-    if ids.dim() not in (1, 2):
-        raise ValueError(f"ids has shape {tuple(ids.shape)}, expected [T] or [T][k]")
-    dev, n = ids.get_device(), ids.numel()
-    _on(stream, dev)
+    dev = _device(ids, "ids", i32, stream)
+    shape = ids.shape
+    if len(shape) not in (1, 2):
+        raise ValueError(f"ids has shape {tuple(shape)}, expected [T] or [T][k]")
+    at_ids, n = _at(ids, "ids", i32, shape, dev), ids.numel()
     if not 1 <= experts <= 1024 or n < 1:
         raise BlrError(-2, "blr_route_sort")
     work = (None, 0)
@@ -497,40 +516,38 @@ def blr_route_sort(ids, experts: int, *, offsets=None, order=None, slot=None, ws
         ws, work = _ws(ws, load().blr_route_workspace_bytes(n, experts), "blr_route_workspace_bytes", dev, stream)
     offsets, at_offsets = _out(offsets, "offsets", i32[0], (experts + 1,), dev, stream)
     order, at_order = _out(order, "order", i32[0], (n,), dev, stream)
-    slot, at_slot = _out(slot, "slot", i32[0], ids.shape, dev, stream)
-    _launch("blr_route_sort", dev, stream, n, experts, ids.data_ptr(), at_offsets, at_order, at_slot, *work)
+    slot, at_slot = _out(slot, "slot", i32[0], shape, dev, stream)
+    _launch("blr_route_sort", dev, stream, n, experts, at_ids, at_offsets, at_order, at_slot, *work)
     return offsets, order, slot
 
 
 def _route_plan(offsets, slot, dev):
     """(T, k, experts, the two addresses)."""
     i32 = _types()[1]
-    _need(offsets, "offsets", i32)
-    _need(slot, "slot", i32)
-    if offsets.dim() != 1 or offsets.numel() < 2:
-        raise ValueError(f"offsets has shape {tuple(offsets.shape)}, expected [experts + 1]")
-    shape = slot.shape
-    if len(shape) not in (1, 2):
-        raise ValueError(f"slot has shape {tuple(shape)}, expected [T] or [T][k]")
-    return (shape[0], shape[1] if len(shape) == 2 else 1, offsets.numel() - 1,
-            _at(offsets, "offsets", i32, offsets.shape, dev), _at(slot, "slot", i32, shape, dev))
+    ends = _shape(offsets, "offsets", 1)
+    if ends[0] < 2:
+        raise ValueError(f"offsets has shape {tuple(ends)}, expected [experts + 1]")
+    shape = _shape(slot, "slot", 1 if getattr(slot, "ndim", 2) == 1 else 2)
+    return (shape[0], shape[1] if len(shape) == 2 else 1, ends[0] - 1, _at(offsets, "offsets", i32, ends, dev),
+            _at(slot, "slot", i32, shape, dev))
 
 
 def _rows(t, name, stream):
-    """(number of t's element type, width, GPU) of rows t, where stream is too."""
-    wide = _types()[2]
-    _need(t, name, wide)
-    if t.dim() != 2:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [rows][d]")
-    _on(stream, t.get_device())
-    return wide.index(t.dtype), t.shape[1], t.get_device()
+    """(number of t's element type, rows, width, GPU) of rows t, where stream
+    is too."""
+    _, _, wide, _, codes = _types()
+    dev = _device(t, name, wide, stream)
+    rows, width = _shape(t, name, 2)
+    if t.dtype not in codes:
+        _need(t, name, wide)
+    return codes[t.dtype], rows, width, dev
 
 
 def blr_route_gather(x, offsets, slot, *, rows=None, stream=None):
     """Rows by expert: rows[slot[t][j]] = x[t], zero where the pair is not
     placed. Returns rows [T k][d]. Its gradient is blr_route_combine without
     weights."""
-    code, d, dev = _rows(x, "x", stream)
+    code, _, d, dev = _rows(x, "x", stream)
     T, k, E, at_offsets, at_slot = _route_plan(offsets, slot, dev)
     at_x = _at(x, "x", (x.dtype,), (T, d), dev)
     rows, at_rows = _out(rows, "rows", x.dtype, (T * k, d), dev, stream)
@@ -542,7 +559,7 @@ def blr_route_combine(z, offsets, slot, weights=None, *, y=None, accumulate_y=Fa
     """Experts' rows back into tokens: y[t] (+)= sum_j w[t][j] z[slot[t][j]]
     over the placed pairs; weights [T][k] f32, or None for ones. y is
     overwritten unless accumulate_y. Returns y [T][d]."""
-    code, d, dev = _rows(z, "z", stream)
+    code, _, d, dev = _rows(z, "z", stream)
     T, k, E, at_offsets, at_slot = _route_plan(offsets, slot, dev)
     at_z = _at(z, "z", (z.dtype,), (T * k, d), dev)
     at_weights = None if weights is None else _at(weights, "weights", _types()[0], slot.shape, dev)
@@ -560,7 +577,7 @@ def blr_route_combine_backward(dy, z, offsets, slot, weights=None, *, dz=None, d
     placed. Returns (dz [T k][d], dw [T][k]), dw None without weights (z may
     then be None)."""
     f32 = _types()[0]
-    code, d, dev = _rows(dy, "dy", stream)
+    code, _, d, dev = _rows(dy, "dy", stream)
     T, k, E, at_offsets, at_slot = _route_plan(offsets, slot, dev)
     at_dy = _at(dy, "dy", (dy.dtype,), (T, d), dev)
     at_weights = at_dw = at_z = None
@@ -589,20 +606,16 @@ def _adapters(rows, name, down, up, offsets, order, scale, ws, stream):
     """Checks that both adapter calls share; `rows` is x or dy. Returns
     (sizes and types, addresses of down .. scale, ws, its (address, bytes),
     GPU)."""
-    f32, i32, wide, _ = _types()
-    act, _, dev = _rows(rows, name, stream)
-    _need(down, "down", wide)
-    _need(up, "up", (down.dtype,))
-    if down.dim() != 3 or up.dim() != 3:
-        raise ValueError("down and up are [E][r][d_in] and [E][d_out][r]")
-    E, r, d_in = down.shape
-    M, d_out = rows.shape[0], up.shape[1]
-    at = (_at(down, "down", wide, (E, r, d_in), dev), _at(up, "up", wide, (E, d_out, r), dev),
+    f32, i32, wide, _, codes = _types()
+    act, M, _, dev = _rows(rows, name, stream)
+    E, r, d_in = _shape(down, "down", 3)
+    d_out = _shape(up, "up", 3)[1]
+    at = (_at(down, "down", wide, (E, r, d_in), dev), _at(up, "up", (down.dtype,), (E, d_out, r), dev),
           _at(offsets, "offsets", i32, (E + 1,), dev), None if order is None else _at(order, "order", i32, (M,), dev),
           None if scale is None else _at(scale, "scale", f32, (E,), dev))
     need = load().blr_adapters_workspace_bytes(M, d_in, d_out, r, E) if ws is None else 0
     ws, work = _ws(ws, need, "blr_adapters_workspace_bytes", dev, stream)
-    return (M, d_in, d_out, r, E, act, wide.index(down.dtype)), at, ws, work, dev
+    return (M, d_in, d_out, r, E, act, codes[down.dtype]), at, ws, work, dev
 
 
 def blr_adapters_forward(x, down, up, offsets, order=None, scale=None, *, y=None, accumulate_y=False, tape_s=None,
