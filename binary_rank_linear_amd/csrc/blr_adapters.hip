@@ -424,6 +424,49 @@ __global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_shrink_kernel(Adap
     for (int i = threadIdx.x; i < tile.cnt * a.r; i += 256) part[i] = red[i / a.r][i % a.r];
 }
 
+// A term of s and what it leaves; nothing where s is not finite, so that an
+// infinity stays one.
+template <typename T>
+__device__ __forceinline__ T take_term(float &v) {
+    const T t = (T)v;
+    const float left = v - (float)t;
+    v = __builtin_isfinite(left) ? left : 0.f;
+    return t;
+}
+
+// ------------------------------------------------------------------ thin --
+// A tile's ds or s, S[64][.] with zeros past the tile's end, as the gradients'
+// panel: in the order of the matrix operand, a slot of 16 bytes a lane. f32
+// for rows of f32: [16 rows][16 ranks][lane][4]. For rows of 16 bits three
+// bf16 terms: [32 rows][term][16 ranks][lane][8].
+template <typename TX, int RT, int STRIDE>
+__device__ void write_panel(void *panels, int64_t tile, const float (*S)[STRIDE]) {
+    if constexpr (sizeof(TX) == 4) {
+        float *to = reinterpret_cast<float *>(panels) + tile * RT * 16 * TM;
+        for (int i = threadIdx.x; i < 4 * RT * 64; i += 256) {
+            const int lane = i & 63, n = (i >> 6) % RT, step = (i >> 6) / RT;
+            const int k = n * 16 + (lane & 15), t = step * 16 + (lane >> 4) * 4;
+            store4(to + i * 4, vf4{S[t][k], S[t + 1][k], S[t + 2][k], S[t + 3][k]});
+        }
+    } else {
+        __bf16 *to = reinterpret_cast<__bf16 *>(panels) + 3 * tile * RT * 16 * TM;
+        for (int i = threadIdx.x; i < 2 * RT * 64; i += 256) {
+            const int lane = i & 63, n = (i >> 6) % RT, step = (i >> 6) / RT;
+            const int k = n * 16 + (lane & 15), t = step * 32 + (lane >> 4) * 8;
+            vb8 term[3];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float v = S[t + j][k];
+#pragma unroll
+                for (int h = 0; h < 3; ++h) term[h][j] = take_term<__bf16>(v);
+            }
+#pragma unroll
+            for (int h = 0; h < 3; ++h)
+                *reinterpret_cast<vb8 *>(to + (((step * 3 + h) * RT + n) * 64 + lane) * 8) = term[h];
+        }
+    }
+}
+
 // ---------------------------------------------------------------- expand --
 // s as the B operand of NT tiles of 16 rows, kept for all columns, and one
 // step of columns: the weights are the A operand, its rows placed on columns
@@ -495,16 +538,6 @@ struct ExpandStep {
         }
     }
 };
-
-// A term of s and what it leaves; nothing where s is not finite, so that an
-// infinity stays one.
-template <typename T>
-__device__ __forceinline__ T take_term(float &v) {
-    const T t = (T)v;
-    const float left = v - (float)t;
-    v = __builtin_isfinite(left) ? left : 0.f;
-    return t;
-}
 
 // The power of two at the largest element of a row of s, or its inverse; 1
 // where that is zero or not finite.
@@ -810,7 +843,8 @@ __device__ void expand_tile_lds(const AdaptExpand &a, const Tile &tile, int from
 }
 
 // One workgroup: 64 rows x a range of columns. The prologue adds the splits'
-// partials; the workgroups of the first range also write s out.
+// partials; the workgroups of the first range also write s out. One more
+// workgroup a tile writes its panel.
 template <typename TX, typename TW, int RT, bool ACC>
 __global__ __launch_bounds__(256) void adapt_expand_kernel(AdaptExpand a, int chunks) {
     typedef ExpandLds<TX, TW, RT> Lds;
@@ -819,8 +853,8 @@ __global__ __launch_bounds__(256) void adapt_expand_kernel(AdaptExpand a, int ch
     float(*S)[RT * 16 + 4] = reinterpret_cast<float(*)[RT * 16 + 4]>(lds);
     __shared__ float largest[TM];
     __shared__ int named;
-    const int chunk = blockIdx.x % chunks;
-    const Tile tile = find_tile(a.plan, a.plan.E + 1, TM, blockIdx.x / chunks);
+    const int across = chunks + (a.panel ? 1 : 0), chunk = blockIdx.x % across, tile_index = blockIdx.x / across;
+    const Tile tile = find_tile(a.plan, a.plan.E + 1, TM, tile_index);
     if (tile.e < 0) return;
     const bool none = tile.e == a.plan.E;
     const float scale = a.scale && !none ? a.scale[tile.e] : 1.f;
@@ -829,24 +863,32 @@ __global__ __launch_bounds__(256) void adapt_expand_kernel(AdaptExpand a, int ch
         if (threadIdx.x == 0) named = 0;
         if (__ballot(ok) == ~0ull && threadIdx.x == 0) named = 1;
     }
-    const int rows = tile.cnt <= 16 ? 16 : TM;
-    for (int i = threadIdx.x; i < rows * RT * 16; i += 256) {
-        const int m = i / (RT * 16), k = i % (RT * 16);
-        float sum = 0.f;
-        if (m < tile.cnt && k < a.r && !none) {
-            const float *part = a.part + (int64_t)(tile.p0 + m) * a.r + k;
-            const int64_t next = (int64_t)a.plan.M * a.r;
+    const bool panel = chunk == chunks;  // the workgroup that writes the panel
+    if (panel && none) return;
+    const int rows = tile.cnt <= 16 && !panel ? 16 : TM;
+    for (int i = threadIdx.x; i < rows * RT * 4; i += 256) {
+        const int m = i / (RT * 4), k = i % (RT * 4) * 4;
+        vf4 sum = {0.f, 0.f, 0.f, 0.f};
+        if (m < tile.cnt && k < a.r) {  // r is a multiple of 8
+            if (!none) {
+                const float *part = a.part + (int64_t)(tile.p0 + m) * a.r + k;
+                const int64_t next = (int64_t)a.plan.M * a.r;
 #pragma unroll 8
-            for (int sp = 0; sp < a.splits; ++sp) sum += part[sp * next];
+                for (int sp = 0; sp < a.splits; ++sp) sum += load4(part + sp * next);
+            }
+            if (chunk == 0 && a.s_row) {
+                const int64_t row = row_of(a.plan, tile.p0 + m);
+                if (row >= 0) store4(a.s_row + row * a.r + k, sum);
+            }
         }
-        if (chunk == 0 && m < tile.cnt && k < a.r) {
-            const int64_t row = row_of(a.plan, tile.p0 + m);
-            if (a.s_row && row >= 0) a.s_row[row * a.r + k] = sum;
-        }
-        S[m][k] = scale * sum;
+        *reinterpret_cast<vf4 *>(&S[m][k]) = scale * sum;
     }
     if (none && ACC) return;
     __syncthreads();
+    if (panel) {
+        write_panel<TX, RT>(a.panel, tile_index, S);
+        return;
+    }
     if (none) {
         // rows without an adapter: zeros
         const int64_t n16 = (int64_t)a.N * sizeof(TX) / 16, lo = n16 * chunk / chunks, hi = n16 * (chunk + 1) / chunks;
@@ -880,20 +922,17 @@ __global__ __launch_bounds__(256) void adapt_expand_kernel(AdaptExpand a, int ch
         expand_tile_lds<TX, TW, RT, ACC, false>(a, tile, from, to, S, largest, reinterpret_cast<vu4 *>(lds));
 }
 
-// ------------------------------------------------------------- transpose --
-// The backward contracts over the other side of A and B than the forward, so
-// it lays their transposes out first: then every operand above and below is
-// read 16 consecutive bytes a lane. Adapters without rows are left out. One
-// workgroup: 64 x 64 elements through LDS.
+// --------------------------------------------------------------- prepare --
+// The backward's first launch; each workgroup does one of three things.
+//
+// Transpose: the backward contracts over the other side of A and B than the
+// forward, so both are laid out transposed, 64 x 64 elements at a time through
+// LDS; then every weight is read 16 consecutive bytes a lane, as in the
+// forward. Adapters without rows are left out.
 template <typename T>
-__global__ __launch_bounds__(256) void adapt_transpose_kernel(AdaptTranspose a) {
+__device__ void transpose_tile(const AdaptPrepare &a, int job, int e, int b, T (*tile)[64 + 16 / sizeof(T)]) {
     constexpr int n = 16 / sizeof(T);
     typedef T V __attribute__((ext_vector_type(n)));
-    __shared__ T tile[64][64 + n];
-    const int e = blockIdx.y;
-    if (a.offsets[e + 1] <= a.offsets[e]) return;
-    const int job = (int)blockIdx.x >= a.tiles[0];
-    const int b = blockIdx.x - (job ? a.tiles[0] : 0);
     const int R = a.rows[job], C = a.cols[job], across = (C + 63) / 64;
     const int r0 = b / across * 64, c0 = b % across * 64;
     const T *src = reinterpret_cast<const T *>(a.src[job]) + (int64_t)e * R * C;
@@ -916,8 +955,55 @@ __global__ __launch_bounds__(256) void adapt_transpose_kernel(AdaptTranspose a) 
     }
 }
 
-// ------------------------------------------------------------------ thin --
-// One workgroup: a tile's panel of ds (blockIdx.y = 0) or of the tape.
+// Workgroups of 64 KB of an adapter's two gradients: zeros, where it has no rows.
+constexpr int ZERO_FLOATS = 16384;
+
+template <typename TX, typename TW, int RT>
+__global__ __launch_bounds__(256) void adapt_prepare_kernel(AdaptPrepare a) {
+    typedef typename std::conditional<sizeof(TW) == 4, uint32_t, uint16_t>::type T;
+    constexpr int T_BYTES = 64 * (64 * sizeof(T) + 16), S_BYTES = sizeof(float) * TM * (RT * 16 + 1);
+    __shared__ __align__(16) char lds[T_BYTES > S_BYTES ? T_BYTES : S_BYTES];
+    int b = blockIdx.x;
+    if (b < a.panels) {
+        // the tape's panel
+        float(*S)[RT * 16 + 1] = reinterpret_cast<float(*)[RT * 16 + 1]>(lds);
+        const Tile tile = find_tile(a.plan, a.plan.E, TM, b);
+        if (tile.e < 0) return;
+        for (int i = threadIdx.x; i < TM * RT * 16; i += 256) {
+            const int m = i / (RT * 16), k = i % (RT * 16);
+            float v = 0.f;
+            if (m < tile.cnt && k < a.r) {
+                const int64_t row = row_of(a.plan, tile.p0 + m);
+                if (row >= 0) v = a.tape[row * a.r + k];
+            }
+            S[m][k] = v;
+        }
+        __syncthreads();
+        write_panel<TX, RT>(a.panel, b, S);
+        return;
+    }
+    b -= a.panels;
+    const int per = a.tiles[0] + a.tiles[1] + a.zeros, e = b / per;
+    b %= per;
+    const bool empty = a.plan.offsets[e + 1] <= a.plan.offsets[e];
+    if (b >= a.tiles[0] + a.tiles[1]) {
+        if (!empty) return;
+        int64_t at = (int64_t)(b - a.tiles[0] - a.tiles[1]) * ZERO_FLOATS + threadIdx.x * 4;
+        const int64_t size[2] = {(int64_t)a.rows[0] * a.cols[0], (int64_t)a.rows[1] * a.cols[1]};
+        for (int i = 0; i < ZERO_FLOATS / 1024; ++i, at += 1024) {
+            if (at < size[0])
+                store4(a.grad[0] + e * size[0] + at, vf4{0.f, 0.f, 0.f, 0.f});
+            else if (at < size[0] + size[1])
+                store4(a.grad[1] + e * size[1] + at - size[0], vf4{0.f, 0.f, 0.f, 0.f});
+        }
+        return;
+    }
+    if (empty) return;
+    const int job = b >= a.tiles[0];
+    transpose_tile<T>(a, job, e, b - (job ? a.tiles[0] : 0), reinterpret_cast<T(*)[64 + 16 / sizeof(T)]>(lds));
+}
+
+// The panel of ds where no dx is formed, whose kernel writes it otherwise.
 template <typename TX, int RT>
 __global__ __launch_bounds__(256) void adapt_thin_kernel(AdaptThin a) {
     __shared__ float S[TM][RT * 16 + 1];
@@ -929,48 +1015,14 @@ __global__ __launch_bounds__(256) void adapt_thin_kernel(AdaptThin a) {
         const int m = i / (RT * 16), k = i % (RT * 16);
         float v = 0.f;
         if (m < tile.cnt && k < a.r) {
-            if (blockIdx.y == 0) {
-                const float *part = a.part + (int64_t)(tile.p0 + m) * a.r + k;
+            const float *part = a.part + (int64_t)(tile.p0 + m) * a.r + k;
 #pragma unroll 8
-                for (int sp = 0; sp < a.splits; ++sp) v += part[sp * next];
-                v *= scale;
-                a.ds[(int64_t)(tile.p0 + m) * a.r + k] = v;
-            } else {
-                const int64_t row = row_of(a.plan, tile.p0 + m);
-                if (row >= 0) v = a.tape[row * a.r + k];
-            }
+            for (int sp = 0; sp < a.splits; ++sp) v += part[sp * next];
         }
-        S[m][k] = v;
+        S[m][k] = scale * v;
     }
-    if (a.tape == nullptr) return;
     __syncthreads();
-    const int64_t panel = (int64_t)blockIdx.x * RT * 16 * TM;
-    if constexpr (sizeof(TX) == 4) {
-        // [16 rows][16 ranks][lane][4]
-        float *to = reinterpret_cast<float *>(a.panel[blockIdx.y]) + panel;
-        for (int i = threadIdx.x; i < 4 * RT * 64; i += 256) {
-            const int lane = i & 63, n = (i >> 6) % RT, step = (i >> 6) / RT;
-            const int k = n * 16 + (lane & 15), t = step * 16 + (lane >> 4) * 4;
-            store4(to + i * 4, vf4{S[t][k], S[t + 1][k], S[t + 2][k], S[t + 3][k]});
-        }
-    } else {
-        // [32 rows][term][16 ranks][lane][8]
-        __bf16 *to = reinterpret_cast<__bf16 *>(a.panel[blockIdx.y]) + 3 * panel;
-        for (int i = threadIdx.x; i < 2 * RT * 64; i += 256) {
-            const int lane = i & 63, n = (i >> 6) % RT, step = (i >> 6) / RT;
-            const int k = n * 16 + (lane & 15), t = step * 32 + (lane >> 4) * 8;
-            vb8 term[3];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float v = S[t + j][k];
-#pragma unroll
-                for (int h = 0; h < 3; ++h) term[h][j] = take_term<__bf16>(v);
-            }
-#pragma unroll
-            for (int h = 0; h < 3; ++h)
-                *reinterpret_cast<vb8 *>(to + (((step * 3 + h) * RT + n) * 64 + lane) * 8) = term[h];
-        }
-    }
+    write_panel<TX, RT>(a.panel, blockIdx.x, S);
 }
 
 // -------------------------------------------------------------- gradients --
@@ -1081,22 +1133,22 @@ __global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_grad_kernel(AdaptG
     typedef GradStep<TX, RT> Step;
     typedef typename std::conditional<sizeof(TX) == 4, float, __bf16>::type P;
     __shared__ __align__(16) int row[ADAPT_MAX_RANGE];
-    const int which = (int)blockIdx.x >= a.blocks;
+    const int per = a.across[0] + a.across[1];
+    const int col = blockIdx.x % per, which = col >= a.across[0];
     const AdaptGradJob &job = a.job[which];
-    const int N = job.N, across = (N + 255) / 256;
-    const int b = blockIdx.x - (which ? a.blocks : 0);
-    const Tile tile = find_tile(a.plan, a.plan.E, job.range, b / across);
+    const int N = job.N;
+    const Tile tile = find_tile(a.plan, a.plan.E, a.range, blockIdx.x / per);
     if (tile.e < 0) return;
-    const int first = tile.panel + tile.j * (job.range / TM);
+    const int first = tile.panel + tile.j * (a.range / TM);
     // only offsets out of order can count more panels or partials than there are
-    if (first + (tile.cnt + TM - 1) / TM > a.panels || (tile.of > 1 && tile.slot + tile.j >= job.slots)) return;
+    if (first + (tile.cnt + TM - 1) / TM > a.panels || (tile.of > 1 && tile.slot + tile.j >= a.slots)) return;
     const int steps = (tile.cnt + Step::ROWS - 1) / Step::ROWS;
     for (int i = threadIdx.x; i < steps * Step::ROWS; i += 256)
         row[i] = i < tile.cnt ? (int)row_of(a.plan, tile.p0 + i) : -1;
     __syncthreads();
     const int lane = threadIdx.x & 63, w = wave();
     const int q = lane >> 4, c = lane & 15;
-    const int n0 = b % across * 256 + w * 64;
+    const int n0 = (col - (which ? a.across[0] : 0)) * 256 + w * 64;
     if (n0 >= N) return;
     const TX *X = reinterpret_cast<const TX *>(job.X) + n0;
     const P *panel =
@@ -1120,12 +1172,12 @@ __global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_grad_kernel(AdaptG
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const vf4 v = scale * vf4{acc[0][n][i], acc[1][n][i], acc[2][n][i], acc[3][n][i]};
-            const int col = n0 + 16 * q + 4 * i;
+            const int o = n0 + 16 * q + 4 * i;
             if (which == 0) {
-                float *at = g + (int64_t)k * N + col;
+                float *at = g + (int64_t)k * N + o;
                 store4(at, add ? load4(at) + v : v);
             } else {
-                float *at = g + (int64_t)col * a.r + k;
+                float *at = g + (int64_t)o * a.r + k;
 #pragma unroll
                 for (int u = 0; u < 4; ++u) at[u * a.r] = add ? at[u * a.r] + v[u] : v[u];
             }
@@ -1133,8 +1185,8 @@ __global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_grad_kernel(AdaptG
     }
 }
 
-// The partials of an adapter of several ranges, added in range order; zeros
-// for an adapter without rows. blockIdx.z: the gradient.
+// The partials of an adapter of several ranges, added in range order.
+// blockIdx.z: the gradient.
 __global__ __launch_bounds__(256) void adapt_reduce_kernel(AdaptGrad a) {
     const AdaptGradJob &job = a.job[blockIdx.z];
     const int e = blockIdx.y;
@@ -1148,23 +1200,21 @@ __global__ __launch_bounds__(256) void adapt_reduce_kernel(AdaptGrad a) {
         return hi > lo ? hi - lo : 0;
     };
     const int cnt = rows(e);
-    if (cnt > 0 ? cnt <= job.range : a.acc) return;  // written by its only range, or nothing to add
-    int slot = 0, of = 0;
-    if (cnt > 0) {
-        // partials of the adapters before: every wave sums for itself
-        const int lane = threadIdx.x & 63;
-        for (int base = 0; base < e; base += 64) {
-            int several = 0;
-            if (base + lane < e) {
-                const int n = rows(base + lane);
-                if (n > job.range) several = n / job.range + (n % job.range ? 1 : 0);
-            }
-            for (int o = 32; o > 0; o /= 2) several += __shfl_xor(several, o);
-            slot += several;
+    if (cnt <= a.range) return;
+    // partials of the adapters before: every wave sums for itself
+    const int lane = threadIdx.x & 63;
+    int slot = 0;
+    for (int base = 0; base < e; base += 64) {
+        int several = 0;
+        if (base + lane < e) {
+            const int n = rows(base + lane);
+            if (n > a.range) several = n / a.range + (n % a.range ? 1 : 0);
         }
-        of = cnt / job.range + (cnt % job.range ? 1 : 0);
-        if (slot + of > job.slots) return;
+        for (int o = 32; o > 0; o /= 2) several += __shfl_xor(several, o);
+        slot += several;
     }
+    const int of = cnt / a.range + (cnt % a.range ? 1 : 0);
+    if (slot + of > a.slots) return;
     if (at >= size) return;
     float *g = job.grad + e * size + at;
     vf4 sum = a.acc ? load4(g) : vf4{0.f, 0.f, 0.f, 0.f};
@@ -1189,7 +1239,7 @@ hipError_t expand_t(const AdaptExpand &a, hipStream_t s) {
     int64_t chunks = (FILL + tiles - 1) / tiles;
     chunks = chunks > units ? units : chunks;
     if (chunks > 8) chunks = chunks / 8 * 8;
-    const dim3 grid((unsigned)(chunks * tiles));
+    const dim3 grid((unsigned)((chunks + (a.panel ? 1 : 0)) * tiles));
     if (a.acc)
         hipLaunchKernelGGL((adapt_expand_kernel<TX, TW, RT, true>), grid, dim3(256), 0, s, a, (int)chunks);
     else
@@ -1197,20 +1247,30 @@ hipError_t expand_t(const AdaptExpand &a, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <typename TX, typename TW, int RT>
+hipError_t prepare_t(AdaptPrepare a, hipStream_t s) {
+    for (int j = 0; j < 2; ++j) a.tiles[j] = (a.rows[j] + 63) / 64 * ((a.cols[j] + 63) / 64);
+    const int64_t floats = (int64_t)a.rows[0] * a.cols[0] + (int64_t)a.rows[1] * a.cols[1];
+    a.zeros = a.grad[0] ? (int)((floats + ZERO_FLOATS - 1) / ZERO_FLOATS) : 0;
+    a.panels = a.tape ? (int)adapt_tiles(a.plan.M, a.plan.E, TM) : 0;
+    const int64_t blocks = a.panels + (int64_t)a.plan.E * (a.tiles[0] + a.tiles[1] + a.zeros);
+    hipLaunchKernelGGL((adapt_prepare_kernel<TX, TW, RT>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
 template <typename TX, int RT>
 hipError_t thin_t(const AdaptThin &a, hipStream_t s) {
-    const dim3 grid((unsigned)adapt_tiles(a.plan.M, a.plan.E, TM), a.tape ? 2 : 1);
-    hipLaunchKernelGGL((adapt_thin_kernel<TX, RT>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((adapt_thin_kernel<TX, RT>), dim3((unsigned)adapt_tiles(a.plan.M, a.plan.E, TM)), dim3(256), 0,
+                       s, a);
     return hipGetLastError();
 }
 
 template <typename TX, int RT>
 hipError_t grad_t(AdaptGrad a, hipStream_t s) {
-    int64_t blocks[2];
-    for (int j = 0; j < 2; ++j)
-        blocks[j] = adapt_tiles(a.plan.M, a.plan.E, a.job[j].range) * ((a.job[j].N + 255) / 256);
-    a.blocks = (int)blocks[0];
-    hipLaunchKernelGGL((adapt_grad_kernel<TX, RT>), dim3((unsigned)(blocks[0] + blocks[1])), dim3(256), 0, s, a);
+    const int64_t tiles = adapt_tiles(a.plan.M, a.plan.E, a.range);
+    for (int j = 0; j < 2; ++j) a.across[j] = (a.job[j].N + 255) / 256;
+    const dim3 grid((unsigned)(tiles * (a.across[0] + a.across[1])));
+    hipLaunchKernelGGL((adapt_grad_kernel<TX, RT>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -1252,10 +1312,10 @@ int adapt_splits(int64_t M, int64_t E, int64_t K) {
     return (int)(sp > ADAPT_MAX_SPLITS ? ADAPT_MAX_SPLITS : sp);
 }
 
-int64_t adapt_range(int64_t M, int64_t N, int64_t r) {
-    const int64_t cols = (N + 255) / 256;
+int64_t adapt_range(int64_t M, int64_t d_in, int64_t d_out, int64_t r) {
+    const int64_t cols = (d_in + 255) / 256 + (d_out + 255) / 256;
     int64_t range = M * cols / (FILL / 2);
-    const int64_t least = 8 * r > 256 ? 8 * r : 256;  // a partial costs as much as 2 r rows
+    const int64_t least = 8 * r > 512 ? 8 * r : 512;  // a partial costs as much as 2 r rows
     range = range < least ? least : range;
     range = range < ADAPT_MAX_RANGE ? range : ADAPT_MAX_RANGE;
     range = range < M ? range : M;
@@ -1268,15 +1328,9 @@ int64_t adapt_range_slots(int64_t M, int64_t E, int64_t range) {
     return twice < all ? twice : all;
 }
 
-hipError_t launch_adapt_transpose(AdaptTranspose a, int wt, hipStream_t s) {
-    for (int j = 0; j < 2; ++j) a.tiles[j] = (a.rows[j] + 63) / 64 * ((a.cols[j] + 63) / 64);
-    const dim3 grid((unsigned)(a.tiles[0] + a.tiles[1]), (unsigned)a.E);
-    prof_begin(K_ADAPT_TRANSPOSE, s);
-    if (wt == 0)
-        hipLaunchKernelGGL((adapt_transpose_kernel<uint32_t>), grid, dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL((adapt_transpose_kernel<uint16_t>), grid, dim3(256), 0, s, a);
-    hipError_t e = hipGetLastError();
+hipError_t launch_adapt_prepare(const AdaptPrepare &a, hipStream_t s) {
+    prof_begin(K_ADAPT_PREPARE, s);
+    hipError_t e = BLR_BY_TYPES(a, prepare_t, a, s);
     prof_end(s);
     return e;
 }
@@ -1306,7 +1360,7 @@ hipError_t launch_adapt_grad(const AdaptGrad &a, hipStream_t s) {
     prof_begin(K_ADAPT_GRAD, s);
     hipError_t e = BLR_BY_ROWS(a, grad_t, a, s);
     prof_end(s);
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || a.slots == 0) return e;
     const int N = a.job[0].N > a.job[1].N ? a.job[0].N : a.job[1].N;
     const int64_t blocks = ((int64_t)a.r * N / 4 + 255) / 256;
     prof_begin(K_ADAPT_REDUCE, s);

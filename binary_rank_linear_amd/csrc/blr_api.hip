@@ -733,11 +733,11 @@ bool adapt_shape_ok(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t E
 }
 
 // Workspace: the splits' partials of s or ds (f32 [splits][M][r]), then for
-// the backward the transposes of down and up, ds by position (f32 [M][r]), the
-// panels of ds and of the tape and the ranges' partials of both gradients.
+// the backward the transposes of down and up, the panels of ds and of the tape
+// and the ranges' partials of both gradients.
 struct AdaptLayout {
-    size_t down_t, up_t, ds, panel[2], part[2], total;
-    int64_t range_in, range_out, slots_in, slots_out;
+    size_t down_t, up_t, panel[2], part[2], total;
+    int64_t range, slots;
 };
 
 AdaptLayout adapt_layout(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t E) {
@@ -752,16 +752,13 @@ AdaptLayout adapt_layout(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int6
     // sized for the widest types, so that one workspace serves them all
     L.down_t = take((size_t)E * r * d_in * 4);
     L.up_t = take((size_t)E * r * d_out * 4);
-    L.ds = take((size_t)M * r * 4);
     const size_t panels = (size_t)adapt_tiles(M, E, ADAPT_TM) * adapt_panel_bytes(r, BLR_BF16);
     L.panel[0] = take(panels);
     L.panel[1] = take(panels);
-    L.range_in = adapt_range(M, d_in, r);
-    L.range_out = adapt_range(M, d_out, r);
-    L.slots_in = adapt_range_slots(M, E, L.range_in);
-    L.slots_out = adapt_range_slots(M, E, L.range_out);
-    L.part[0] = take((size_t)L.slots_in * r * d_in * 4);
-    L.part[1] = take((size_t)L.slots_out * r * d_out * 4);
+    L.range = adapt_range(M, d_in, d_out, r);
+    L.slots = adapt_range_slots(M, E, L.range);
+    L.part[0] = take((size_t)L.slots * r * d_in * 4);
+    L.part[1] = take((size_t)L.slots * r * d_out * 4);
     L.total = off;
     return L;
 }
@@ -860,23 +857,29 @@ int blr_adapters_backward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int
     hipStream_t s = (hipStream_t)stream;
     const AdaptLayout L = adapt_layout(M, d_in, d_out, r, adapters);
     char *ws = (char *)workspace;
-    AdaptTranspose tr = {};
-    tr.offsets = offsets;
-    tr.E = (int)adapters;
-    tr.src[0] = down;
-    tr.dst[0] = ws + L.down_t;
-    tr.rows[0] = (int)r;
-    tr.cols[0] = (int)d_in;
-    tr.src[1] = up;
-    tr.dst[1] = ws + L.up_t;
-    tr.rows[1] = (int)d_out;
-    tr.cols[1] = (int)r;
-    BLR_TRY(launch_adapt_transpose(tr, wt, s));
+    AdaptPrepare pr = {};
+    pr.plan = {offsets, order, (int)M, (int)adapters};
+    pr.src[0] = down;
+    pr.dst[0] = ws + L.down_t;
+    pr.rows[0] = (int)r;
+    pr.cols[0] = (int)d_in;
+    pr.src[1] = up;
+    pr.dst[1] = ws + L.up_t;
+    pr.rows[1] = (int)d_out;
+    pr.cols[1] = (int)r;
+    pr.tape = grad_down ? tape_s : nullptr;
+    pr.panel = ws + L.panel[1];
+    pr.grad[0] = accumulate_grads ? nullptr : grad_down;
+    pr.grad[1] = accumulate_grads ? nullptr : grad_up;
+    pr.r = (int)r;
+    pr.act = act;
+    pr.wt = wt;
+    BLR_TRY(launch_adapt_prepare(pr, s));
     // ds = c dy B: the contraction over d_out, then its splits' sum with dx
     AdaptShrink sh = {};
-    sh.plan = {offsets, order, (int)M, (int)adapters};
+    sh.plan = pr.plan;
     sh.X = dy;
-    sh.W = tr.dst[1];
+    sh.W = pr.dst[1];
     sh.part = (float *)ws;
     sh.K = (int)d_out;
     sh.r = (int)r;
@@ -884,31 +887,25 @@ int blr_adapters_backward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int
     sh.act = act;
     sh.wt = wt;
     BLR_TRY(launch_adapt_shrink(sh, K_ADAPT_DS, s));
-    AdaptThin th = {};
-    th.plan = sh.plan;
-    th.part = sh.part;
-    th.scale = scale;
-    th.tape = grad_down ? tape_s : nullptr;
-    th.ds = (float *)(ws + L.ds);
-    th.panel[0] = ws + L.panel[0];
-    th.panel[1] = ws + L.panel[1];
-    th.r = (int)r;
-    th.splits = sh.splits;
-    th.act = act;
-    BLR_TRY(launch_adapt_thin(th, s));
+    void *ds_panel = ws + L.panel[0];
     if (dx) {
         AdaptExpand ex = {};
         ex.plan = sh.plan;
-        ex.part = th.ds;  // holds the factor already
-        ex.W = tr.dst[0];
+        ex.part = sh.part;
+        ex.scale = scale;
+        ex.W = pr.dst[0];
         ex.out = dx;
+        ex.panel = grad_down ? ds_panel : nullptr;
         ex.N = (int)d_in;
         ex.r = (int)r;
-        ex.splits = 1;
+        ex.splits = sh.splits;
         ex.act = act;
         ex.wt = wt;
         ex.acc = accumulate_dx ? 1 : 0;
         BLR_TRY(launch_adapt_expand(ex, K_ADAPT_DX, s));
+    } else {
+        AdaptThin th = {sh.plan, sh.part, scale, ds_panel, (int)r, sh.splits, act};
+        BLR_TRY(launch_adapt_thin(th, s));
     }
     if (!grad_down) return BLR_OK;
     AdaptGrad gr = {};
@@ -917,8 +914,10 @@ int blr_adapters_backward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int
     gr.act = act;
     gr.acc = accumulate_grads ? 1 : 0;
     gr.panels = adapt_tiles(M, adapters, ADAPT_TM);
-    gr.job[0] = {x, th.panel[0], nullptr, grad_down, (float *)(ws + L.part[0]), (int)d_in, (int)L.range_in, L.slots_in};
-    gr.job[1] = {dy, th.panel[1], scale, grad_up, (float *)(ws + L.part[1]), (int)d_out, (int)L.range_out, L.slots_out};
+    gr.range = (int)L.range;
+    gr.slots = L.slots;
+    gr.job[0] = {x, ds_panel, nullptr, grad_down, (float *)(ws + L.part[0]), (int)d_in};
+    gr.job[1] = {dy, pr.panel, scale, grad_up, (float *)(ws + L.part[1]), (int)d_out};
     BLR_TRY(launch_adapt_grad(gr, s));
     return BLR_OK;
 }

@@ -41,10 +41,10 @@ enum KernelId {
     K_ROUTE_COMBINE_BWD, // gradients of the experts' rows and of the weights
     K_ADAPT_DOWN,   // adapters: partials of s = x A^T
     K_ADAPT_UP,     // adapters: y (+)= c s B^T
-    K_ADAPT_TRANSPOSE, // adapters: A^T and B^T for the backward
+    K_ADAPT_PREPARE, // adapters: the backward's A^T and B^T, the tape's panel
     K_ADAPT_DS,     // adapters: partials of ds = c dy B
     K_ADAPT_DX,     // adapters: dx (+)= ds A
-    K_ADAPT_THIN,   // adapters: ds, and ds and s as the gradients' operands
+    K_ADAPT_THIN,   // adapters: ds's panel where no dx is formed
     K_ADAPT_GRAD,   // adapters: gradients of A and B over ranges of rows
     K_ADAPT_REDUCE, // adapters: the ranges' partials summed in order
     K_COUNT
@@ -240,7 +240,8 @@ struct AdaptShrink {
     int K, r, splits, act, wt;
 };
 // out[row(p)][n] (+)= sum_k S[p][k] W_e[n][k], S[p] = scale_e sum over splits
-// of part[.][p]; W_e: [N][r]. S goes to s_row by row, unscaled (unless null).
+// of part[.][p]; W_e: [N][r]. S goes to s_row by row, unscaled, and to panel
+// as panels (either may be null).
 struct AdaptExpand {
     AdaptPlan plan;
     const float *part;
@@ -248,19 +249,32 @@ struct AdaptExpand {
     const void *W;
     void *out;
     float *s_row;
+    void *panel;
     int N, r, splits, act, wt, acc;
 };
-// The gradients' thin operands, once per call: ds [p][r] = scale_e sum over
-// splits of part[.][p], and both ds and the tape s (by row) as panels: of each
+// The gradients' thin operands, ds (scaled) and the tape s, as panels: of each
 // tile of 64 positions, its ranks (rounded up to 16, 32, 64 or 128: r16) by 64
 // positions, zero past the tile's end, in the order of the matrix operand; f32
 // for rows of f32, three bf16 terms for rows of 16 bits.
-struct AdaptThin {
+struct AdaptThin {  // panels of ds alone
     AdaptPlan plan;
-    const float *part, *scale, *tape;  // tape null: ds alone, no panels
-    float *ds;
-    void *panel[2];                    // of ds and of the tape
+    const float *part, *scale;
+    void *panel;
     int r, splits, act;
+};
+// dst_e [cols][rows] = the transpose of src_e [rows][cols] for the adapters that
+// have rows, two tables; the tape's panels (tape null: none); zeros into grad_e
+// of the adapters that have none (null: not).
+struct AdaptPrepare {
+    AdaptPlan plan;
+    const void *src[2];
+    void *dst[2];
+    int rows[2], cols[2];
+    const float *tape;
+    void *panel;
+    float *grad[2];
+    int r, act, wt;
+    int tiles[2], zeros, panels;  // workgroups of each kind; filled by the launcher
 };
 constexpr int64_t adapt_r16(int64_t r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 constexpr int64_t adapt_panel_bytes(int64_t r, int act) { return adapt_r16(r) * 64 * (act == 0 ? 4 : 6); }
@@ -274,27 +288,17 @@ struct AdaptGradJob {
     const void *panel;
     const float *scale;  // null: no factor
     float *grad, *part;
-    int N, range;
-    int64_t slots;  // partials that `part` has room for
+    int N;
 };
 struct AdaptGrad {
     AdaptPlan plan;
     AdaptGradJob job[2];
-    int r, act, acc;
+    int r, act, acc, range;
     int64_t panels;  // that exist
-    int blocks;      // of job 0; filled by the launcher
+    int64_t slots;   // partials that each `part` has room for
+    int across[2];   // workgroups across each job's columns; filled by the launcher
 };
-// dst_e [cols][rows] = the transpose of src_e [rows][cols], for the adapters
-// that have rows; two tables in one launch.
-struct AdaptTranspose {
-    const int32_t *offsets;
-    int E;
-    const void *src[2];
-    void *dst[2];
-    int rows[2], cols[2];
-    int tiles[2];  // filled by the launcher
-};
-hipError_t launch_adapt_transpose(AdaptTranspose a, int wt, hipStream_t s);
+hipError_t launch_adapt_prepare(const AdaptPrepare &a, hipStream_t s);
 // id: the kernel kind that the launch is timed as.
 hipError_t launch_adapt_shrink(const AdaptShrink &a, int id, hipStream_t s);
 hipError_t launch_adapt_expand(const AdaptExpand &a, int id, hipStream_t s);
@@ -303,7 +307,7 @@ hipError_t launch_adapt_grad(const AdaptGrad &a, hipStream_t s);
 // Tiles of tm positions that M positions in at most E + 1 groups can need.
 int64_t adapt_tiles(int64_t M, int64_t E, int64_t tm);
 int adapt_splits(int64_t M, int64_t E, int64_t K);
-int64_t adapt_range(int64_t M, int64_t N, int64_t r);
+int64_t adapt_range(int64_t M, int64_t d_in, int64_t d_out, int64_t r);
 // Partials of ranges that a gradient over M rows can leave.
 int64_t adapt_range_slots(int64_t M, int64_t E, int64_t range);
 

@@ -2105,7 +2105,7 @@ const char *kernel_name(int id) {
         case K_ROUTE_COMBINE_BWD: return "route_combine_backward";
         case K_ADAPT_DOWN: return "adapters_down";
         case K_ADAPT_UP: return "adapters_up";
-        case K_ADAPT_TRANSPOSE: return "adapters_transpose";
+        case K_ADAPT_PREPARE: return "adapters_prepare";
         case K_ADAPT_DS: return "adapters_ds";
         case K_ADAPT_DX: return "adapters_dx";
         case K_ADAPT_THIN: return "adapters_thin";
