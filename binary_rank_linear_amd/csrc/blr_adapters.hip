@@ -296,42 +296,38 @@ struct ShrinkLds {
             for (int i = 0; i < W_LOADS; ++i) *reinterpret_cast<vu4 *>(lds + (16 * i + n) * 64 + g * 16) = w[i];
         }
     }
-    // One tile of 16 rows against all ranks, half h of the step's columns.
+    // All 64 rows against all ranks; all of the step's reads go out first.
     static __device__ __forceinline__ void multiply(const char *lds, vf4 (&acc)[4][RT], int q, int c) {
+        typedef typename Vec<TX>::v V;
+        V xv[2][4];
+        typename std::conditional<W_ROW == 128, V, typename Vec<TW>::v4>::type wv[2][RT];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int at = ((4 * h + q) ^ (c & 7)) * 16;
+#pragma unroll
+            for (int n = 0; n < RT; ++n) {
+                const char *p = lds + X_BYTES + (16 * n + c) * W_ROW;
+                p += W_ROW == 128 ? at : ((2 * h + (q >> 1)) ^ ((c >> 1) & 3)) * 16 + 8 * (q & 1);
+                wv[h][n] = *reinterpret_cast<decltype(&wv[0][0])>(const_cast<char *>(p));
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) xv[h][t] = *reinterpret_cast<const V *>(lds + (16 * t + c) * 128 + at);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
             if constexpr (sizeof(TX) == 4) {
-                vf4 wv[RT];
 #pragma unroll
-                for (int n = 0; n < RT; ++n) {
-                    const char *p = lds + X_BYTES + (16 * n + c) * W_ROW;
-                    if constexpr (W_ROW == 128)
-                        wv[n] = *reinterpret_cast<const vf4 *>(p + at);
-                    else
-                        wv[n] = load4(reinterpret_cast<const TW *>(p + ((2 * h + (q >> 1)) ^ ((c >> 1) & 3)) * 16) +
-                                      4 * (q & 1));
-                }
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const vf4 xv = *reinterpret_cast<const vf4 *>(lds + (16 * t + c) * 128 + at);
+                    for (int n = 0; n < RT; ++n)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int n = 0; n < RT; ++n) acc[t][n] = mfma4(xv[j], wv[n][j], acc[t][n]);
-                }
+                        for (int t = 0; t < 4; ++t) acc[t][n] = mfma4(xv[h][t][j], (float)wv[h][n][j], acc[t][n]);
             } else {
-                typedef typename Vec<TX>::v V;
-                V wv[RT];
 #pragma unroll
                 for (int n = 0; n < RT; ++n)
-                    wv[n] = *reinterpret_cast<const V *>(lds + X_BYTES + (16 * n + c) * 128 + at);
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const V xv = *reinterpret_cast<const V *>(lds + (16 * t + c) * 128 + at);
-#pragma unroll
-                    for (int n = 0; n < RT; ++n) acc[t][n] = mfma8(xv, wv[n], acc[t][n]);
-                }
+                    for (int t = 0; t < 4; ++t) acc[t][n] = mfma8(xv[h][t], wv[h][n], acc[t][n]);
             }
         }
     }
@@ -692,6 +688,7 @@ struct ExpandLds {
     static constexpr bool PACKED = !WIDE && RT == 1;  // both terms of s in one instruction
     static constexpr int KS = WIDE ? RT : (RT + 1) / 2;
     static constexpr int SLOTS = H * KS * 64;
+    static constexpr int BUFFER = SLOTS + 33;  // and the spare ones
     typedef typename Vec<TX>::v V;
     typedef typename std::conditional<WIDE, typename Vec<TW>::v4, vu4>::type Piece;  // a slot's ranks, as they lie
     static constexpr int RANKS = WIDE ? 4 : 8;
@@ -708,27 +705,27 @@ struct ExpandLds {
                 ahead(W + (int64_t)o0 * r, (unsigned)(p < total ? p : 0) * (unsigned)(RANKS * sizeof(TW))));
         }
     }
-    // Where they go, -1: nowhere.
+    // Where they go; those past the step to a spare slot, so that no branch
+    // stands before the write (its wait would be for the last step's stores).
     static __device__ __forceinline__ void places(int (&at)[PIECES], int r) {
         const int per = r / RANKS;
 #pragma unroll
         for (int j = 0; j < PIECES; ++j) {
             const int p = threadIdx.x + 256 * j, o = p / per, k = p % per;
             const int h = o % H, c = o / H;
-            at[j] = o < COLS ? ((h * KS + k / 4) * 64 + (k % 4) * 16 + c) : -1;
+            at[j] = o < COLS ? ((h * KS + k / 4) * 64 + (k % 4) * 16 + c) : SLOTS;
         }
     }
     static __device__ __forceinline__ void stage(vu4 *lds, const Piece (&w)[PIECES], const int (&at)[PIECES]) {
 #pragma unroll
-        for (int j = 0; j < PIECES; ++j)
-            if (at[j] >= 0) {
-                if constexpr (WIDE)
-                    *reinterpret_cast<vf4 *>(lds + at[j]) = __builtin_convertvector(w[j], vf4);
-                else {
-                    lds[at[j]] = w[j];
-                    if (PACKED) lds[at[j] + 32] = w[j];  // lanes q + 2: the second term's
-                }
+        for (int j = 0; j < PIECES; ++j) {
+            if constexpr (WIDE)
+                *reinterpret_cast<vf4 *>(lds + at[j]) = __builtin_convertvector(w[j], vf4);
+            else {
+                lds[at[j]] = w[j];
+                if (PACKED) lds[at[j] + 32] = w[j];  // lanes q + 2: the second term's
             }
+        }
     }
 };
 
@@ -778,7 +775,7 @@ __device__ void expand_tile_lds(const AdaptExpand &a, const Tile &tile, int from
         }
     }
     __syncthreads();  // S lies in the same memory as the weights
-    for (int i = threadIdx.x; i < 2 * L::SLOTS; i += 256) lds[i] = vu4{0, 0, 0, 0};  // ranks past r stay zero
+    for (int i = threadIdx.x; i < 2 * L::BUFFER; i += 256) lds[i] = vu4{0, 0, 0, 0};  // ranks past r stay zero
     __syncthreads();
     const TW *W = reinterpret_cast<const TW *>(a.W) + (int64_t)tile.e * a.r * a.N;
     typename L::Piece piece[L::PIECES];
@@ -792,16 +789,27 @@ __device__ void expand_tile_lds(const AdaptExpand &a, const Tile &tile, int from
             for (int i = 0; i < 4; ++i) next[i] = *reinterpret_cast<const V *>(row[i] + step * L::COLS);
         }
     };
-    load(from);
-    for (int step = from; step < to; ++step) {
-        vu4 *buf = lds + ((step - from) & 1) * L::SLOTS;
-        L::stage(buf, piece, place);
-        V old[4];
+    // What the next step needs is waited for and put in place behind this step's
+    // stores: the loads are older than they, so nothing waits for them. (At the
+    // loop's head the wait would have to hold for its first entry too.)
+    V old[4];
+    auto take = [&](int buffer) {
+        L::stage(lds + buffer * L::BUFFER, piece, place);
         if (ACC) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) old[i] = next[i];
+            for (int i = 0; i < 4; ++i) {
+                old[i] = next[i];
+                asm volatile("" : "+v"(old[i]));
+            }
         }
         __syncthreads();
+    };
+    if (from < to) {
+        load(from);
+        take(0);
+    }
+    for (int step = from; step < to; ++step) {
+        const vu4 *buf = lds + ((step - from) & 1) * L::BUFFER;
         load(step + 1 < to ? step + 1 : step);  // no branch: see walk
         __builtin_amdgcn_sched_barrier(0);
         vf4 d[L::H];
@@ -813,21 +821,32 @@ __device__ void expand_tile_lds(const AdaptExpand &a, const Tile &tile, int from
                 for (int i = 0; i < 4; ++i) d[h][i] = old[i][h];
             }
         }
+        vu4 slot[2][L::H];  // the next group's reads are in flight while one is multiplied
 #pragma unroll
-        for (int kk = 0; kk < L::KS; ++kk)
+        for (int h = 0; h < L::H; ++h) slot[0][h] = buf[h * L::KS * 64 + lane];
 #pragma unroll
-            for (int h = 0; h < L::H; ++h) {
-                const vu4 slot = buf[(h * L::KS + kk) * 64 + lane];
-                if constexpr (L::WIDE) {
-                    const vf4 v = __builtin_bit_cast(vf4, slot);
+        for (int kk = 0; kk < L::KS; ++kk) {
+            if (kk + 1 < L::KS) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) d[h] = mfma4(s[kk][j], v[j], d[h]);
-                } else {
-                    const V v = __builtin_bit_cast(V, slot);
-                    d[h] = mfma8(hi[kk], v, d[h]);
-                    if (!L::PACKED) d[h] = mfma8(lo[kk], v, d[h]);
+                for (int h = 0; h < L::H; ++h) slot[(kk + 1) & 1][h] = buf[(h * L::KS + kk + 1) * 64 + lane];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (L::WIDE) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int h = 0; h < L::H; ++h)
+                        d[h] = mfma4(s[kk][j], __builtin_bit_cast(vf4, slot[kk & 1][h])[j], d[h]);
+            } else {
+#pragma unroll
+                for (int h = 0; h < L::H; ++h) d[h] = mfma8(hi[kk], __builtin_bit_cast(V, slot[kk & 1][h]), d[h]);
+                if (!L::PACKED) {
+#pragma unroll
+                    for (int h = 0; h < L::H; ++h) d[h] = mfma8(lo[kk], __builtin_bit_cast(V, slot[kk & 1][h]), d[h]);
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             F f;
@@ -839,6 +858,8 @@ __device__ void expand_tile_lds(const AdaptExpand &a, const Tile &tile, int from
             }
             if (FULL || in[i]) *reinterpret_cast<V *>(row[i] + step * L::COLS) = __builtin_convertvector(f, V);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        take((step + 1 - from) & 1);
     }
 }
 
@@ -848,7 +869,7 @@ __device__ void expand_tile_lds(const AdaptExpand &a, const Tile &tile, int from
 template <typename TX, typename TW, int RT, bool ACC>
 __global__ __launch_bounds__(256) void adapt_expand_kernel(AdaptExpand a, int chunks) {
     typedef ExpandLds<TX, TW, RT> Lds;
-    constexpr int S_BYTES = sizeof(float) * TM * (RT * 16 + 4), W_BYTES = 2 * 16 * Lds::SLOTS;
+    constexpr int S_BYTES = sizeof(float) * TM * (RT * 16 + 4), W_BYTES = 2 * 16 * Lds::BUFFER;
     __shared__ __align__(16) char lds[S_BYTES > W_BYTES ? S_BYTES : W_BYTES];
     float(*S)[RT * 16 + 4] = reinterpret_cast<float(*)[RT * 16 + 4]>(lds);
     __shared__ float largest[TM];
@@ -1032,33 +1053,35 @@ __device__ float zero_row[64];  // never written; not const, or its loads would 
 
 // X as the A operand, straight from its rows: lane (q, c) loads columns
 // 4 c .. 4 c + 3, component u belonging to tile u of the output (so that row m
-// of tile u stands for column 4 m + u), of the rows q of the step's k indices;
-// the thin operand's panel gives B[k][rank]. D then holds
+// of tile u stands for column 4 m + u), of the rows q of the step's k indices.
+// The thin operand's panel gives B[k][rank] from LDS. D then holds
 // G[column 4 (4 q + i) + u][rank c].
 //
 // Rows of f32: 16 a step, k index 4 q + j.
 template <typename TX, int RT>
 struct GradStep {
     static constexpr int ROWS = 16;
-    vf4 x[4], t[RT];
+    static constexpr int SLOTS = RT * 64;  // of a step's panel
+    vf4 x[4];
 
-    __device__ __forceinline__ void load(const TX *X, int N, const int *row, const float *panel, int m, int q, int c) {
-        const int4 at = *reinterpret_cast<const int4 *>(row + m + 4 * q);
+    __device__ __forceinline__ void load(const TX *X, int N, const int *row, int q, int c) {
+        const int4 at = *reinterpret_cast<const int4 *>(row + 4 * q);
         const int r[4] = {at.x, at.y, at.z, at.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             x[j] = load4((r[j] < 0 ? reinterpret_cast<const TX *>(zero_row) : X + (int64_t)r[j] * N) + 4 * c);
-        const float *p = panel + (int64_t)(m / ROWS) * RT * 256;
-#pragma unroll
-        for (int n = 0; n < RT; ++n) t[n] = load4(ahead(p + n * 256, (unsigned)(q * 16 + c) * 16u));
     }
-    __device__ __forceinline__ void multiply(vf4 (&acc)[4][RT]) const {
+    __device__ __forceinline__ void multiply(const vu4 *panel, vf4 (&acc)[4][RT], int lane) const {
+        vf4 t[RT];
+#pragma unroll
+        for (int n = 0; n < RT; ++n) t[n] = __builtin_bit_cast(vf4, panel[n * 64 + lane]);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int n = 0; n < RT; ++n)
 #pragma unroll
-                for (int n = 0; n < RT; ++n) acc[u][n] = mfma4(x[j][u], t[n][j], acc[u][n]);
+                for (int u = 0; u < 4; ++u) acc[u][n] = mfma4(x[j][u], t[n][j], acc[u][n]);
     }
 };
 
@@ -1070,54 +1093,62 @@ struct GradStep {
 template <typename T, int RT>
 struct GradStep16 {
     static constexpr int ROWS = 32;
+    static constexpr int SLOTS = 3 * RT * 64;
     uint2 x[8];  // four elements
-    vb8 t[3][RT];
 
-    __device__ __forceinline__ void load(const T *X, int N, const int *row, const __bf16 *panel, int m, int q, int c) {
-        const int4 a = *reinterpret_cast<const int4 *>(row + m + 8 * q);
-        const int4 b = *reinterpret_cast<const int4 *>(row + m + 8 * q + 4);
+    __device__ __forceinline__ void load(const T *X, int N, const int *row, int q, int c) {
+        const int4 a = *reinterpret_cast<const int4 *>(row + 8 * q);
+        const int4 b = *reinterpret_cast<const int4 *>(row + 8 * q + 4);
         const int r[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             x[j] = *reinterpret_cast<const uint2 *>(
                 (r[j] < 0 ? reinterpret_cast<const T *>(zero_row) : X + (int64_t)r[j] * N) + 4 * c);
-        const __bf16 *p = panel + (int64_t)(m / ROWS) * 3 * RT * 512;
-#pragma unroll
-        for (int h = 0; h < 3; ++h)
-#pragma unroll
-            for (int n = 0; n < RT; ++n)
-                t[h][n] = *reinterpret_cast<const vb8 *>(
-                    ahead(p + (h * RT + n) * 512, (unsigned)(q * 16 + c) * 16u));
     }
-    __device__ __forceinline__ void multiply(vf4 (&acc)[4][RT]) const {
+    __device__ __forceinline__ void multiply(const vu4 *panel, vf4 (&acc)[4][RT], int lane) const {
+        vb8 hi[4], lo[4];
+        vu4 t[2][RT];  // the next term's reads are in flight while one is multiplied
+#pragma unroll
+        for (int n = 0; n < RT; ++n) t[0][n] = panel[n * 64 + lane];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            vb8 hi, lo;
             if constexpr (__is_same(T, __bf16)) {
-                uint32_t pair[4];  // element u of two rows
+                vu4 pairs;  // element u of two rows each
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    pair[j] = __builtin_amdgcn_perm(u < 2 ? x[2 * j + 1].x : x[2 * j + 1].y,
-                                                    u < 2 ? x[2 * j].x : x[2 * j].y, u & 1 ? 0x07060302u : 0x05040100u);
-                hi = __builtin_bit_cast(vb8, make_uint4(pair[0], pair[1], pair[2], pair[3]));
+                    pairs[j] = __builtin_amdgcn_perm(u < 2 ? x[2 * j + 1].x : x[2 * j + 1].y,
+                                                     u < 2 ? x[2 * j].x : x[2 * j].y, u & 1 ? 0x07060302u : 0x05040100u);
+                hi[u] = __builtin_bit_cast(vb8, pairs);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     float v = (float)__builtin_bit_cast(vh4, x[j])[u];
-                    hi[j] = take_term<__bf16>(v);
-                    lo[j] = take_term<__bf16>(v);
+                    hi[u][j] = take_term<__bf16>(v);
+                    lo[u][j] = take_term<__bf16>(v);
                 }
             }
+        }
 #pragma unroll
-            for (int h = 0; h < 3; ++h)
+        for (int h = 0; h < 3; ++h) {
+            if (h < 2) {
 #pragma unroll
-                for (int n = 0; n < RT; ++n) acc[u][n] = mfma8(hi, t[h][n], acc[u][n]);
-            if constexpr (!__is_same(T, __bf16)) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int n = 0; n < RT; ++n) acc[u][n] = mfma8(lo, t[h][n], acc[u][n]);
+                for (int n = 0; n < RT; ++n) t[(h + 1) & 1][n] = panel[((h + 1) * RT + n) * 64 + lane];
             }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int n = 0; n < RT; ++n)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) acc[u][n] = mfma8(hi[u], __builtin_bit_cast(vb8, t[h & 1][n]), acc[u][n]);
+            if constexpr (!__is_same(T, __bf16)) {
+                if (h < 2) {
+#pragma unroll
+                    for (int n = 0; n < RT; ++n)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            acc[u][n] = mfma8(lo[u], __builtin_bit_cast(vb8, t[h & 1][n]), acc[u][n]);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 };
@@ -1127,39 +1158,71 @@ template <int RT>
 struct GradStep<__bf16, RT> : GradStep16<__bf16, RT> {};
 
 // One workgroup: a range of one adapter's rows x 256 columns, wave w 64 of
-// them.
+// them. A panel of 64 rows is up to three times as many bytes as the 64
+// columns it meets, so the four waves share it through LDS (in two buffers,
+// one barrier a panel); the next panel and the next step's rows are in flight
+// while a step is multiplied.
 template <typename TX, int RT>
 __global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_grad_kernel(AdaptGrad a) {
     typedef GradStep<TX, RT> Step;
-    typedef typename std::conditional<sizeof(TX) == 4, float, __bf16>::type P;
+    constexpr int STEPS = TM / Step::ROWS, SLOTS = STEPS * Step::SLOTS, PIECES = (SLOTS + 255) / 256;
+    static_assert(STEPS % 2 == 0, "the two register sets alternate through a panel");
     __shared__ __align__(16) int row[ADAPT_MAX_RANGE];
+    __shared__ __align__(16) vu4 lds[2][SLOTS];
     const int per = a.across[0] + a.across[1];
     const int col = blockIdx.x % per, which = col >= a.across[0];
     const AdaptGradJob &job = a.job[which];
     const int N = job.N;
     const Tile tile = find_tile(a.plan, a.plan.E, a.range, blockIdx.x / per);
     if (tile.e < 0) return;
-    const int first = tile.panel + tile.j * (a.range / TM);
+    const int first = tile.panel + tile.j * (a.range / TM), panels = (tile.cnt + TM - 1) / TM;
     // only offsets out of order can count more panels or partials than there are
-    if (first + (tile.cnt + TM - 1) / TM > a.panels || (tile.of > 1 && tile.slot + tile.j >= a.slots)) return;
-    const int steps = (tile.cnt + Step::ROWS - 1) / Step::ROWS;
-    for (int i = threadIdx.x; i < steps * Step::ROWS; i += 256)
+    if (first + panels > a.panels || (tile.of > 1 && tile.slot + tile.j >= a.slots)) return;
+    for (int i = threadIdx.x; i < panels * TM; i += 256)
         row[i] = i < tile.cnt ? (int)row_of(a.plan, tile.p0 + i) : -1;
     __syncthreads();
     const int lane = threadIdx.x & 63, w = wave();
     const int q = lane >> 4, c = lane & 15;
     const int n0 = (col - (which ? a.across[0] : 0)) * 256 + w * 64;
-    if (n0 >= N) return;
-    const TX *X = reinterpret_cast<const TX *>(job.X) + n0;
-    const P *panel =
-        reinterpret_cast<const P *>(job.panel) + (int64_t)first * (sizeof(TX) == 4 ? 1 : 3) * RT * 16 * TM;
+    // waves past the last column repeat column 0, for the barriers; not stored
+    const TX *X = reinterpret_cast<const TX *>(job.X) + (n0 < N ? n0 : 0);
+    const vu4 *panel = reinterpret_cast<const vu4 *>(job.panel) + (int64_t)first * SLOTS;
     vf4 acc[4][RT];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
         for (int n = 0; n < RT; ++n) acc[u][n] = vf4{0.f, 0.f, 0.f, 0.f};
-    walk<Step, RT <= 4>(steps, [&](Step &s, int i) { s.load(X, N, row, panel, i * Step::ROWS, q, c); },
-                        [&](const Step &s, int) { s.multiply(acc); });
+    vu4 piece[PIECES];
+    auto load_panel = [&](int p) {
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j) {
+            const unsigned i = threadIdx.x + 256 * j;
+            piece[j] = *ahead(panel + (int64_t)p * SLOTS, (SLOTS % 256 == 0 || i < SLOTS ? i : 0) * 16u);
+        }
+    };
+    Step set[2];
+    load_panel(0);
+    set[0].load(X, N, row, q, c);
+    for (int p = 0; p < panels; ++p) {
+        vu4 *buf = lds[p & 1];
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j) {
+            const int i = threadIdx.x + 256 * j;
+            if (SLOTS % 256 == 0 || i < SLOTS) buf[i] = piece[j];
+        }
+        __syncthreads();
+        const bool last = p + 1 == panels;
+        load_panel(last ? p : p + 1);  // no branch: see walk
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int next = last && s + 1 == STEPS ? s : s + 1;
+            set[(s + 1) & 1].load(X, N, row + p * TM + next * Step::ROWS, q, c);
+            __builtin_amdgcn_sched_barrier(0);
+            set[s & 1].multiply(buf + s * Step::SLOTS, acc, lane);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    if (n0 >= N) return;
     const int64_t size = (int64_t)a.r * N;
     const bool alone = tile.of == 1;
     float *g = alone ? job.grad + tile.e * size : job.part + (tile.slot + tile.j) * size;
