@@ -1,1293 +1,25 @@
-// Low-rank adapters of many requests at once, for gfx950. Row t with adapter
-// e (A_e [r][d_in], B_e [d_out][r], factor c_e):
-//
-//   forward   s = x A_e^T          y (+)= c_e s B_e^T
-//   backward  ds = c_e dy B_e      dx (+)= ds A_e
-//             dA_e (+)= sum_t ds^T x      dB_e (+)= c_e sum_t dy^T s
-//
-// Rows are taken by the plan of the sort (blr_route.hip): a workgroup has a
-// tile of rows of one adapter, found from offsets by every wave for itself.
-// The rank is small, so every contraction is bound by its rows' bytes; the
-// kernels read them from memory straight into matrix operands, once.
-//
-// Rows of f32 run on v_mfma_f32_16x16x4_f32 (D += A B: lane l = 16 q + c gives
-// A[c][q] and B[q][c], and holds D[4 q + i][c], i < 4), with 16-bit adapters
-// widened, which is exact. Rows of 16 bits run on the 16x16x32 instructions
-// (lane gives eight k: A[c][8 q + j], B[8 q + j][c]; D as above), whose
-// products are exact and whose sums are f32; s and ds, which are f32, enter
-// them as two or three 16-bit terms, so that their 16 or 24 leading bits take
-// part (see where they are made). Which column of a product a k index stands
-// for is free as long as A and B agree: the loads use that to read 16
-// consecutive bytes per lane.
-#include <type_traits>
-
-#include "blr_internal.h"
-#include "blr_vec.h"
+// Low-rank adapters: launches of the contractions that the forward uses, and
+// of the backward's where no gradient of an adapter is asked for.
+#include "blr_adapters.h"
 
 namespace blr {
 
 namespace {
 
-constexpr int TM = ADAPT_TM;
-typedef uint32_t vu4 __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ vf4 mfma4(float a, float b, vf4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
-}
-
-// The wave's number in its workgroup, in a scalar register.
-__device__ __forceinline__ int wave() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
-
-// base + bytes: where base is the same in all lanes, the address needs one
-// 32-bit register per lane.
-template <typename T>
-__device__ __forceinline__ const T *ahead(const T *base, unsigned bytes) {
-    return reinterpret_cast<const T *>(reinterpret_cast<const char *>(base) + bytes);
-}
-
-// A tile of one group of the plan; group E is the rows without an adapter.
-struct Tile {
-    int e;      // -1: the grid has more tiles than the plan
-    int p0;     // first position
-    int cnt;    // positions
-    int j, of;  // this tile is the j-th of the group's `of`
-    int slot;   // tiles of earlier groups that have several
-    int panel;  // tiles of 64 positions of earlier groups
-};
-
-// Tile b of tiles of tm positions over groups 0 .. groups-1 (wave-uniform).
-// Offsets out of order or out of range cannot lead outside [0, M).
-__device__ Tile find_tile(const AdaptPlan &plan, int groups, int tm, int b) {
-    const int lane = threadIdx.x & 63;
-    int run = 0, many = 0, panels = 0;
-    for (int base = 0; base < groups; base += 64) {
-        const int e = base + lane;
-        int lo = 0, cnt = 0;
-        if (e < groups) {
-            lo = plan.offsets[e];
-            const int hi = e < plan.E ? plan.offsets[e + 1] : plan.M;
-            lo = lo < 0 ? 0 : lo > plan.M ? plan.M : lo;
-            cnt = (hi > plan.M ? plan.M : hi) - lo;
-            cnt = cnt < 0 ? 0 : cnt;
-        }
-        const int nt = cnt / tm + (cnt % tm ? 1 : 0);
-        const int several = nt > 1 ? nt : 0;
-        const int np = cnt / TM + (cnt % TM ? 1 : 0);
-        int incl = nt, mincl = several, pincl = np;
-#pragma unroll
-        for (int o = 1; o < 64; o *= 2) {
-            const int u = __shfl_up(incl, o), v = __shfl_up(mincl, o), z = __shfl_up(pincl, o);
-            if (lane >= o) {
-                incl += u;
-                mincl += v;
-                pincl += z;
-            }
-        }
-        const uint64_t past = __ballot(run + incl > b);
-        if (past) {
-            const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)past) - 1);
-            Tile t;
-            t.e = base + l;
-            t.of = __builtin_amdgcn_readlane(nt, l);
-            t.j = b - run - (__builtin_amdgcn_readlane(incl, l) - t.of);
-            t.p0 = __builtin_amdgcn_readlane(lo, l) + t.j * tm;
-            const int left = __builtin_amdgcn_readlane(cnt, l) - t.j * tm;
-            t.cnt = left < tm ? left : tm;
-            t.slot = many + __builtin_amdgcn_readlane(mincl, l) - __builtin_amdgcn_readlane(several, l);
-            t.panel = panels + __builtin_amdgcn_readlane(pincl, l) - __builtin_amdgcn_readlane(np, l);
-            return t;
-        }
-        run += __builtin_amdgcn_readlane(incl, 63);
-        many += __builtin_amdgcn_readlane(mincl, 63);
-        panels += __builtin_amdgcn_readlane(pincl, 63);
-    }
-    return Tile{-1, 0, 0, 0, 0, 0, 0};
-}
-
-// The row of position p, -1 if the plan names none.
-__device__ __forceinline__ int64_t row_of(const AdaptPlan &plan, int p) {
-    const int row = plan.order ? plan.order[p] : p;
-    return row >= 0 && row < plan.M ? row : -1;
-}
-
-// Matrix instructions on 16-bit operands.
-__device__ __forceinline__ vf4 mfma8(vh8 a, vh8 b, vf4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
-__device__ __forceinline__ vf4 mfma8(vb8 a, vb8 b, vf4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
-
-// Walks a wave's n steps with two register sets (DEEP): the next step's loads
-// are in flight while one is used. The walk has no branch around a load (a
-// wave's last extra load repeats its last step), or every wait would be for
-// all; the barriers keep the compiler from moving the loads behind the
-// products. Ranks over 64 leave no room for a second set.
-template <typename Step, bool DEEP, typename Load, typename Use>
-__device__ __forceinline__ void walk(int n, Load load, Use use) {
-    if (n <= 0) return;
-    if constexpr (!DEEP) {
-        for (int i = 0; i < n; ++i) {
-            Step st;
-            load(st, i);
-            use(st, i);
-        }
-    } else {
-        Step one, two;
-        load(one, 0);
-        int i = 0;
-        for (; i + 2 <= n; i += 2) {
-            load(two, i + 1);
-            __builtin_amdgcn_sched_barrier(0);
-            use(one, i);
-            __builtin_amdgcn_sched_barrier(0);
-            load(one, i + 2 < n ? i + 2 : n - 1);
-            __builtin_amdgcn_sched_barrier(0);
-            use(two, i + 1);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        if (i < n) use(one, i);
-    }
-}
-
-// ---------------------------------------------------------------- shrink --
-// What a lane holds of one step: 128 bytes of each of NT x 16 rows, over the
-// four lanes q, and the weights of the same columns. Rows of f32: 32 columns,
-// lane q the columns 4 q .. 4 q + 3 and 16 + 4 q .. Rows of 16 bits: 64, lane
-// q 8 q .. 8 q + 7 and 32 + 8 q ..
-template <typename TX, typename TW, int RT, int NT>
-struct ShrinkStep {
-    static constexpr int COLS = 32;
-    vf4 x[NT][2];
-    typename Vec<TW>::v4 w[RT][2];  // widened where they are used, or the wait for them would stand here
-
-    __device__ __forceinline__ void load(const TX *const *row, const TW *W, int r, int K, int k0, int q, int c) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) x[t][h] = load4(row[t] + k0 + 16 * h + 4 * q);
-#pragma unroll
-        for (int n = 0; n < RT; ++n) {
-            const int rank = n * 16 + c < r ? n * 16 + c : r - 1;  // columns past r of the product are not stored
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                w[n][h] = *reinterpret_cast<const typename Vec<TW>::v4 *>(
-                    ahead(W + k0 + 16 * h, (unsigned)(rank * K + 4 * q) * (unsigned)sizeof(TW)));
-        }
-    }
-    __device__ __forceinline__ void multiply(vf4 (&acc)[NT][RT]) const {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int n = 0; n < RT; ++n) acc[t][n] = mfma4(x[t][h][j], (float)w[n][h][j], acc[t][n]);
-    }
-};
-
-template <typename T, int RT, int NT>
-struct ShrinkStep16 {
-    static constexpr int COLS = 64;
-    typedef typename Vec<T>::v V;
-    V x[NT][2], w[RT][2];
-
-    __device__ __forceinline__ void load(const T *const *row, const T *W, int r, int K, int k0, int q, int c) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) x[t][h] = *reinterpret_cast<const V *>(row[t] + k0 + 32 * h + 8 * q);
-#pragma unroll
-        for (int n = 0; n < RT; ++n) {
-            const int rank = n * 16 + c < r ? n * 16 + c : r - 1;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                w[n][h] = *reinterpret_cast<const V *>(
-                    ahead(W + k0 + 32 * h, (unsigned)(rank * K + 8 * q) * (unsigned)sizeof(T)));
-        }
-    }
-    __device__ __forceinline__ void multiply(vf4 (&acc)[NT][RT]) const {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int n = 0; n < RT; ++n) acc[t][n] = mfma8(x[t][h], w[n][h], acc[t][n]);
-    }
-};
-template <int RT, int NT>
-struct ShrinkStep<_Float16, _Float16, RT, NT> : ShrinkStep16<_Float16, RT, NT> {};
-template <int RT, int NT>
-struct ShrinkStep<__bf16, __bf16, RT, NT> : ShrinkStep16<__bf16, RT, NT> {};
-
-// A wave's steps (every fourth of [from, to)) over NT x 16 rows of the tile,
-// then the four waves' sums, in wave order, into red.
-template <typename TX, typename TW, int RT, int NT>
-__device__ void shrink_tile(const AdaptShrink &a, const Tile &tile, int from, int to, float (*red)[RT * 16 + 1]) {
-    typedef ShrinkStep<TX, TW, RT, NT> Step;
-    const int lane = threadIdx.x & 63, w = wave();
-    const int q = lane >> 4, c = lane & 15;
-    const TW *W = reinterpret_cast<const TW *>(a.W) + (int64_t)tile.e * a.r * a.K;
-    const TX *x[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        // rows past the tile, or not named by the plan, repeat one; not stored
-        const int p = t * 16 + c < tile.cnt ? t * 16 + c : tile.cnt - 1;
-        const int64_t row = row_of(a.plan, tile.p0 + p);
-        x[t] = reinterpret_cast<const TX *>(a.X) + (row < 0 ? 0 : row) * a.K;
-    }
-    vf4 acc[NT][RT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int n = 0; n < RT; ++n) acc[t][n] = vf4{0.f, 0.f, 0.f, 0.f};
-    const int first = from + w;
-    walk<Step, RT <= 4>((to - first + 3) / 4,
-               [&](Step &s, int i) { s.load(x, W, a.r, a.K, (first + 4 * i) * Step::COLS, q, c); },
-               [&](const Step &s, int) { s.multiply(acc); });
-    for (int v = 0; v < 4; ++v) {
-        if (w == v) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int n = 0; n < RT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float *at = &red[t * 16 + 4 * q + i][n * 16 + c];
-                        *at = v == 0 ? acc[t][n][i] : *at + acc[t][n][i];
-                    }
-        }
-        __syncthreads();
-    }
-}
-
-// The same for tiles of up to 64 rows, by way of LDS. A load instruction takes
-// the vector cache one cycle for every four lanes if those lie together in
-// memory, and one for every lane if not: lanes laid out for the matrix operand
-// (each another row) cost four times the cycles, and that, not HBM, bounds the
-// loads above. So eight lanes read 128 bytes of a row, and a wave turns its
-// step of X and of the weights round through 16-byte slots of its own (slot
-// h of row m stands at h ^ (m & 7), which spreads both sides over the banks);
-// no barrier, since no other wave reads them.
-template <typename TX, typename TW, int RT>
-struct ShrinkLds {
-    static constexpr int COLS = 128 / sizeof(TX);
-    static constexpr int X_BYTES = 64 * 128;
-    static constexpr int W_ROW = COLS * sizeof(TW);  // 128, or 64 for 16-bit weights beside f32 rows
-    static constexpr int W_BYTES = RT * 16 * W_ROW;
-    static constexpr int W_LOADS = W_BYTES / 1024;
-    static constexpr int BYTES = X_BYTES + W_BYTES;
-    vu4 x[8], w[W_LOADS];
-
-    __device__ __forceinline__ void load(const TX *const *row, const TW *W, const unsigned *rank, int k0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const vu4 *>(row[i] + k0);
-#pragma unroll
-        for (int i = 0; i < W_LOADS; ++i) w[i] = *reinterpret_cast<const vu4 *>(ahead(W + k0, rank[i]));
-    }
-    __device__ __forceinline__ void stage(char *lds, int lane) const {
-        const int m = lane >> 3, h = (lane & 7) ^ (m & 7);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) *reinterpret_cast<vu4 *>(lds + (8 * i + m) * 128 + h * 16) = x[i];
-        lds += X_BYTES;
-        if constexpr (W_ROW == 128) {
-#pragma unroll
-            for (int i = 0; i < W_LOADS; ++i) *reinterpret_cast<vu4 *>(lds + (8 * i + m) * 128 + h * 16) = w[i];
-        } else {
-            const int n = lane >> 2, g = (lane & 3) ^ ((n >> 1) & 3);
-#pragma unroll
-            for (int i = 0; i < W_LOADS; ++i) *reinterpret_cast<vu4 *>(lds + (16 * i + n) * 64 + g * 16) = w[i];
-        }
-    }
-    // All 64 rows against all ranks; all of the step's reads go out first.
-    static __device__ __forceinline__ void multiply(const char *lds, vf4 (&acc)[4][RT], int q, int c) {
-        typedef typename Vec<TX>::v V;
-        V xv[2][4];
-        typename std::conditional<W_ROW == 128, V, typename Vec<TW>::v4>::type wv[2][RT];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int at = ((4 * h + q) ^ (c & 7)) * 16;
-#pragma unroll
-            for (int n = 0; n < RT; ++n) {
-                const char *p = lds + X_BYTES + (16 * n + c) * W_ROW;
-                p += W_ROW == 128 ? at : ((2 * h + (q >> 1)) ^ ((c >> 1) & 3)) * 16 + 8 * (q & 1);
-                wv[h][n] = *reinterpret_cast<decltype(&wv[0][0])>(const_cast<char *>(p));
-            }
-#pragma unroll
-            for (int t = 0; t < 4; ++t) xv[h][t] = *reinterpret_cast<const V *>(lds + (16 * t + c) * 128 + at);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if constexpr (sizeof(TX) == 4) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int n = 0; n < RT; ++n)
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) acc[t][n] = mfma4(xv[h][t][j], (float)wv[h][n][j], acc[t][n]);
-            } else {
-#pragma unroll
-                for (int n = 0; n < RT; ++n)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) acc[t][n] = mfma8(xv[h][t], wv[h][n], acc[t][n]);
-            }
-        }
-    }
-};
-
-// Orders a wave's own writes and reads of LDS (they execute in order; this
-// keeps the compiler from moving one past the other).
-__device__ __forceinline__ void wave_lds_fence() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
-template <typename TX, typename TW, int RT>
-__device__ void shrink_tile_lds(const AdaptShrink &a, const Tile &tile, int from, int to, char *lds,
-                                float (*red)[RT * 16 + 1]) {
-    typedef ShrinkLds<TX, TW, RT> Step;
-    const int lane = threadIdx.x & 63, w = wave();
-    const int q = lane >> 4, c = lane & 15;
-    const TW *W = reinterpret_cast<const TW *>(a.W) + (int64_t)tile.e * a.r * a.K;
-    const TX *x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        // rows past the tile, or not named by the plan, repeat one; not stored
-        const int m = 8 * i + (lane >> 3);
-        const int64_t row = row_of(a.plan, tile.p0 + (m < tile.cnt ? m : tile.cnt - 1));
-        x[i] = reinterpret_cast<const TX *>(a.X) + (row < 0 ? 0 : row) * a.K + (lane & 7) * (16 / sizeof(TX));
-    }
-    unsigned rank[Step::W_LOADS];
-#pragma unroll
-    for (int i = 0; i < Step::W_LOADS; ++i) {
-        const int per = Step::W_ROW / 16;  // lanes of a rank's columns
-        const int n = i * (64 / per) + lane / per;  // columns past r of the product are not stored
-        rank[i] = (unsigned)((n < a.r ? n : a.r - 1) * a.K) * (unsigned)sizeof(TW) + (lane % per) * 16;
-    }
-    vf4 acc[4][RT];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int n = 0; n < RT; ++n) acc[t][n] = vf4{0.f, 0.f, 0.f, 0.f};
-    char *mine = lds + w * Step::BYTES;
-    const int first = from + w, n = (to - first + 3) / 4;
-    if (n > 0) {
-        Step st;
-        st.load(x, W, rank, first * Step::COLS);
-        for (int i = 0; i < n; ++i) {
-            st.stage(mine, lane);
-            wave_lds_fence();
-            st.load(x, W, rank, (first + 4 * (i + 1 < n ? i + 1 : i)) * Step::COLS);  // no branch: see walk
-            __builtin_amdgcn_sched_barrier(0);
-            Step::multiply(mine, acc, q, c);
-            wave_lds_fence();
-        }
-    }
-    __syncthreads();  // red lies in the same memory
-    for (int v = 0; v < 4; ++v) {
-        if (w == v) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int n = 0; n < RT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float *at = &red[t * 16 + 4 * q + i][n * 16 + c];
-                        *at = v == 0 ? acc[t][n][i] : *at + acc[t][n][i];
-                    }
-        }
-        __syncthreads();
-    }
-}
-
-// One workgroup: 64 rows x all r over one split of K, the splits of a tile next
-// to each other (the grid is one-dimensional: its other dimensions are short).
-template <typename TX, typename TW, int RT>
-__global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_shrink_kernel(AdaptShrink a) {
-    typedef ShrinkLds<TX, TW, RT> Lds;
-    __shared__ __align__(16) char lds[4 * Lds::BYTES];
-    float(*red)[RT * 16 + 1] = reinterpret_cast<float(*)[RT * 16 + 1]>(lds);
-    static_assert(sizeof(float) * TM * (RT * 16 + 1) <= sizeof(lds), "the sums fit");
-    const int split = blockIdx.x % a.splits;
-    const Tile tile = find_tile(a.plan, a.plan.E, TM, blockIdx.x / a.splits);
-    if (tile.e < 0) return;
-    const int64_t steps = a.K / Lds::COLS;
-    const int from = (int)(steps * split / a.splits), to = (int)(steps * (split + 1) / a.splits);
-    if (tile.cnt <= 16)
-        shrink_tile<TX, TW, RT, 1>(a, tile, from, to, red);
-    else
-        shrink_tile_lds<TX, TW, RT>(a, tile, from, to, lds, red);
-    float *part = a.part + ((int64_t)split * a.plan.M + tile.p0) * a.r;
-    for (int i = threadIdx.x; i < tile.cnt * a.r; i += 256) part[i] = red[i / a.r][i % a.r];
-}
-
-// A term of s and what it leaves; nothing where s is not finite, so that an
-// infinity stays one.
-template <typename T>
-__device__ __forceinline__ T take_term(float &v) {
-    const T t = (T)v;
-    const float left = v - (float)t;
-    v = __builtin_isfinite(left) ? left : 0.f;
-    return t;
-}
-
-// ------------------------------------------------------------------ thin --
-// A tile's ds or s, S[64][.] with zeros past the tile's end, as the gradients'
-// panel: in the order of the matrix operand, a slot of 16 bytes a lane. f32
-// for rows of f32: [16 rows][16 ranks][lane][4]. For rows of 16 bits three
-// bf16 terms: [32 rows][term][16 ranks][lane][8].
-template <typename TX, int RT, int STRIDE>
-__device__ void write_panel(void *panels, int64_t tile, const float (*S)[STRIDE]) {
-    if constexpr (sizeof(TX) == 4) {
-        float *to = reinterpret_cast<float *>(panels) + tile * RT * 16 * TM;
-        for (int i = threadIdx.x; i < 4 * RT * 64; i += 256) {
-            const int lane = i & 63, n = (i >> 6) % RT, step = (i >> 6) / RT;
-            const int k = n * 16 + (lane & 15), t = step * 16 + (lane >> 4) * 4;
-            store4(to + i * 4, vf4{S[t][k], S[t + 1][k], S[t + 2][k], S[t + 3][k]});
-        }
-    } else {
-        __bf16 *to = reinterpret_cast<__bf16 *>(panels) + 3 * tile * RT * 16 * TM;
-        for (int i = threadIdx.x; i < 2 * RT * 64; i += 256) {
-            const int lane = i & 63, n = (i >> 6) % RT, step = (i >> 6) / RT;
-            const int k = n * 16 + (lane & 15), t = step * 32 + (lane >> 4) * 8;
-            vb8 term[3];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float v = S[t + j][k];
-#pragma unroll
-                for (int h = 0; h < 3; ++h) term[h][j] = take_term<__bf16>(v);
-            }
-#pragma unroll
-            for (int h = 0; h < 3; ++h)
-                *reinterpret_cast<vb8 *>(to + (((step * 3 + h) * RT + n) * 64 + lane) * 8) = term[h];
-        }
-    }
-}
-
-// ---------------------------------------------------------------- expand --
-// s as the B operand of NT tiles of 16 rows, kept for all columns, and one
-// step of columns: the weights are the A operand, its rows placed on columns
-// so that lane (q, c) ends with 16 consecutive bytes of row c, next to those
-// of the lanes q: out is read and written in whole lines and never passes
-// through LDS. row[t] is a row to read (repeated past the tile's end), out[t]
-// the row to write or null.
-//
-// Rows of f32: two tiles of 16 columns a step, tile h at 16 h.
-template <typename TX, typename TW, int RT, int NT>
-struct ExpandStep {
-    static constexpr int COLS = 32;
-    struct S {
-        vf4 v[NT][RT];
-        __device__ __forceinline__ void load(const float (*tile)[RT * 16 + 4], const float *, int q, int c) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int n = 0; n < RT; ++n)
-                    v[t][n] = *reinterpret_cast<const vf4 *>(&tile[t * 16 + c][n * 16 + q * 4]);
-        }
-    };
-    typename Vec<TW>::v4 w[2][RT];
-    vf4 y[NT][2];
-
-    template <bool ACC>
-    __device__ __forceinline__ void load(TX *const *row, const TW *W, int r, int o0, int q, int c) {
-        if (ACC) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) y[t][h] = load4(row[t] + o0 + 16 * h + 4 * q);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int n = 0; n < RT; ++n) {
-                const int k = n * 16 + q * 4, kc = k < r ? k : 0;  // r is a multiple of 8
-                w[h][n] = *reinterpret_cast<const typename Vec<TW>::v4 *>(
-                    ahead(W + (int64_t)(o0 + 16 * h) * r, (unsigned)(c * r + kc) * (unsigned)sizeof(TW)));
-            }
-        }
-    }
-    template <bool ACC>
-    __device__ __forceinline__ void multiply_store(const S &s, TX *const *out, int r, int o0, int q) {
-        vf4 v[2][RT];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int n = 0; n < RT; ++n) {
-                v[h][n] = __builtin_convertvector(w[h][n], vf4);
-                if (n * 16 + q * 4 >= r) v[h][n] = vf4{0.f, 0.f, 0.f, 0.f};  // s is zero there
-            }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            vf4 d[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) d[h] = ACC ? y[t][h] : vf4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int n = 0; n < RT; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) d[h] = mfma4(v[h][n][j], s.v[t][n][j], d[h]);
-            if (out[t]) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) store4(out[t] + o0 + 16 * h + 4 * q, d[h]);
-            }
-        }
-    }
-};
-
-// The power of two at the largest element of a row of s, or its inverse; 1
-// where that is zero or not finite.
-__device__ __forceinline__ float power_of(float top, bool itself) {
-    if (!(top > 0.f) || !__builtin_isfinite(top)) return 1.f;
-    int e = (int)((__float_as_uint(top) >> 23) & 255) - 127;  // subnormal: -127
-    e = e < -120 ? -120 : e > 120 ? 120 : e;
-    return __uint_as_float((unsigned)(127 + (itself ? e : -e)) << 23);
-}
-
-// Rows of 16 bits: four tiles, 64 columns a step; column i of row 4 q' of tile
-// 2 g + h is 32 g + 8 q' + 4 h + i. out is rounded to 16 bits, so two terms of
-// s (16 leading bits in bf16, 22 in f16) leave an error far below that
-// rounding. f16 terms need s near one: each row enters divided by the power of
-// two at its largest element, and the result is multiplied back (both exact).
-// Up to rank 16 both terms share one instruction's 32 k.
-template <typename T, int RT, int NT>
-struct ExpandStep16 {
-    static constexpr int COLS = 64;
-    static constexpr bool PACKED = RT == 1;
-    static constexpr int KS = (RT + 1) / 2;  // steps of 32 ranks
-    typedef typename Vec<T>::v V;
-    struct S {
-        V hi[NT][KS], lo[NT][KS];
-        float back[NT];
-        __device__ __forceinline__ void load(const float (*tile)[RT * 16 + 4], const float *largest, int q, int c) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int m = t * 16 + c;
-                float by = 1.f;
-                back[t] = 1.f;
-                if constexpr (__is_same(T, _Float16)) {
-                    by = power_of(largest[m], false);
-                    back[t] = power_of(largest[m], true);
-                }
-#pragma unroll
-                for (int kk = 0; kk < KS; ++kk) {
-                    const int k = PACKED ? (q & 1) * 8 : kk * 32 + q * 8;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float v = by * tile[m][k + j];
-                        hi[t][kk][j] = take_term<T>(v);
-                        lo[t][kk][j] = take_term<T>(v);
-                    }
-                    if (PACKED && q >= 2) hi[t][kk] = lo[t][kk];
-                }
-            }
-        }
-    };
-    V w[4][KS], y[NT][2];
-
-    template <bool ACC>
-    __device__ __forceinline__ void load(T *const *row, const T *W, int r, int o0, int q, int c) {
-        if (ACC) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int g = 0; g < 2; ++g) y[t][g] = *reinterpret_cast<const V *>(row[t] + o0 + 32 * g + 8 * q);
-        }
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            const int o = 8 * (c >> 2) + (c & 3);
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk) {
-                const int k = PACKED ? (q & 1) * 8 : kk * 32 + q * 8, kc = k < r ? k : 0;
-                w[h][kk] = *reinterpret_cast<const V *>(ahead(W + (int64_t)(o0 + 32 * (h >> 1) + 4 * (h & 1)) * r,
-                                                              (unsigned)(o * r + kc) * (unsigned)sizeof(T)));
-            }
-        }
-    }
-    template <bool ACC>
-    __device__ __forceinline__ void multiply_store(const S &s, T *const *out, int r, int o0, int q) {
-        typedef float F __attribute__((ext_vector_type(8)));
-#pragma unroll
-        for (int kk = 0; kk < KS; ++kk)
-            if ((PACKED ? (q & 1) * 8 : kk * 32 + q * 8) >= r) {  // s is zero there
-#pragma unroll
-                for (int h = 0; h < 4; ++h) w[h][kk] = (V)(T)0;
-            }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            vf4 d[4];
-#pragma unroll
-            for (int h = 0; h < 4; ++h) d[h] = vf4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk) {
-#pragma unroll
-                for (int h = 0; h < 4; ++h) d[h] = mfma8(w[h][kk], s.hi[t][kk], d[h]);
-                if (!PACKED) {
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) d[h] = mfma8(w[h][kk], s.lo[t][kk], d[h]);
-                }
-            }
-            if (out[t]) {
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const vf4 u = s.back[t] * d[2 * g], v = s.back[t] * d[2 * g + 1];
-                    F f = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
-                    if (ACC) f += __builtin_convertvector(y[t][g], F);
-                    *reinterpret_cast<V *>(out[t] + o0 + 32 * g + 8 * q) = __builtin_convertvector(f, V);
-                }
-            }
-        }
-    }
-};
-template <int RT, int NT>
-struct ExpandStep<_Float16, _Float16, RT, NT> : ExpandStep16<_Float16, RT, NT> {};
-template <int RT, int NT>
-struct ExpandStep<__bf16, __bf16, RT, NT> : ExpandStep16<__bf16, RT, NT> {};
-
-// A wave's steps (every fourth of [from, to)) over NT x 16 rows.
-template <typename TX, typename TW, int RT, int NT, bool ACC>
-__device__ void expand_tile(const AdaptExpand &a, const Tile &tile, int from, int to, const float (*S)[RT * 16 + 4],
-                            const float *largest) {
-    typedef ExpandStep<TX, TW, RT, NT> Step;
-    const int lane = threadIdx.x & 63, w = wave();
-    const int q = lane >> 4, c = lane & 15;
-    TX *row[NT], *out[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const bool in = t * 16 + c < tile.cnt;
-        const int64_t at = row_of(a.plan, tile.p0 + (in ? t * 16 + c : tile.cnt - 1));
-        row[t] = reinterpret_cast<TX *>(a.out) + (at < 0 ? 0 : at) * a.N;
-        out[t] = in && at >= 0 ? row[t] : nullptr;
-    }
-    typename Step::S s;
-    s.load(S, largest, q, c);
-    const TW *W = reinterpret_cast<const TW *>(a.W) + (int64_t)tile.e * a.r * a.N;
-    const int first = from + w;
-    walk<Step, RT <= 4>((to - first + 3) / 4,
-               [&](Step &st, int i) { st.template load<ACC>(row, W, a.r, (first + 4 * i) * Step::COLS, q, c); },
-               [&](Step &st, int i) {
-                   st.template multiply_store<ACC>(s, out, a.r, (first + 4 * i) * Step::COLS, q);
-               });
-}
-
-// The same for tiles of up to 64 rows, each wave its 16 of them, by way of
-// LDS: the lanes of a load or store have to lie together in memory (see the
-// shrink), so here the rows are the A operand and the columns the B operand,
-// with column c of tile h standing for column 16 / size * c + h of the step:
-// lane (q, c) ends with 16 consecutive bytes of each of rows 4 q .. 4 q + 3,
-// 256 bytes of a row in 16 lanes. The step's weights, which lie together, are
-// brought into operand order through LDS once for the four waves, in two
-// buffers, one barrier a step.
-//
-// Operand slots of 16 bytes: [tile h][group of ranks][lane].
-template <typename TX, typename TW, int RT>
-struct ExpandLds {
-    static constexpr bool WIDE = sizeof(TX) == 4;  // f32 rows: 4 ranks a slot, else 8
-    static constexpr int H = 16 / sizeof(TX);      // tiles of a step, and elements of 16 bytes of a row
-    static constexpr int COLS = 16 * H;
-    static constexpr bool PACKED = !WIDE && RT == 1;  // both terms of s in one instruction
-    static constexpr int KS = WIDE ? RT : (RT + 1) / 2;
-    static constexpr int SLOTS = H * KS * 64;
-    static constexpr int BUFFER = SLOTS + 33;  // and the spare ones
-    typedef typename Vec<TX>::v V;
-    typedef typename std::conditional<WIDE, typename Vec<TW>::v4, vu4>::type Piece;  // a slot's ranks, as they lie
-    static constexpr int RANKS = WIDE ? 4 : 8;
-    static constexpr int PIECES = (COLS * RT * 16 / RANKS + 255) / 256;  // a thread's, at most
-
-    // Thread i's pieces of the step: piece p holds ranks RANKS (p % per) ..
-    // of column p / per, p = i + 256 j.
-    static __device__ __forceinline__ void load(Piece (&w)[PIECES], const TW *W, int r, int o0) {
-        const int total = COLS * r / RANKS;
-#pragma unroll
-        for (int j = 0; j < PIECES; ++j) {
-            const int p = threadIdx.x + 256 * j;
-            w[j] = *reinterpret_cast<const Piece *>(
-                ahead(W + (int64_t)o0 * r, (unsigned)(p < total ? p : 0) * (unsigned)(RANKS * sizeof(TW))));
-        }
-    }
-    // Where they go; those past the step to a spare slot, so that no branch
-    // stands before the write (its wait would be for the last step's stores).
-    static __device__ __forceinline__ void places(int (&at)[PIECES], int r) {
-        const int per = r / RANKS;
-#pragma unroll
-        for (int j = 0; j < PIECES; ++j) {
-            const int p = threadIdx.x + 256 * j, o = p / per, k = p % per;
-            const int h = o % H, c = o / H;
-            at[j] = o < COLS ? ((h * KS + k / 4) * 64 + (k % 4) * 16 + c) : SLOTS;
-        }
-    }
-    static __device__ __forceinline__ void stage(vu4 *lds, const Piece (&w)[PIECES], const int (&at)[PIECES]) {
-#pragma unroll
-        for (int j = 0; j < PIECES; ++j) {
-            if constexpr (WIDE)
-                *reinterpret_cast<vf4 *>(lds + at[j]) = __builtin_convertvector(w[j], vf4);
-            else {
-                lds[at[j]] = w[j];
-                if (PACKED) lds[at[j] + 32] = w[j];  // lanes q + 2: the second term's
-            }
-        }
-    }
-};
-
-// FULL: every row of the tile is written.
-template <typename TX, typename TW, int RT, bool ACC, bool FULL>
-__device__ void expand_tile_lds(const AdaptExpand &a, const Tile &tile, int from, int to, const float (*S)[RT * 16 + 4],
-                                const float *largest, vu4 *lds) {
-    typedef ExpandLds<TX, TW, RT> L;
-    typedef typename L::V V;
-    typedef float F __attribute__((ext_vector_type(L::H)));
-    const int lane = threadIdx.x & 63, w = wave();
-    const int q = lane >> 4, c = lane & 15;
-    TX *row[4];
-    bool in[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int m = 16 * w + 4 * q + i;
-        const int64_t at = row_of(a.plan, tile.p0 + (m < tile.cnt ? m : tile.cnt - 1));
-        row[i] = reinterpret_cast<TX *>(a.out) + (at < 0 ? 0 : at) * a.N + L::H * c;
-        in[i] = m < tile.cnt && at >= 0;
-    }
-    // s of row c as the A operand: f32, or two terms
-    const int m = 16 * w + c;
-    vf4 s[RT];
-    V hi[L::KS], lo[L::KS];
-    float back[4] = {1.f, 1.f, 1.f, 1.f};
-    if constexpr (L::WIDE) {
-#pragma unroll
-        for (int n = 0; n < RT; ++n) s[n] = *reinterpret_cast<const vf4 *>(&S[m][n * 16 + q * 4]);
-    } else {
-        float by = 1.f;
-        if constexpr (__is_same(TX, _Float16)) {
-            by = power_of(largest[m], false);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) back[i] = power_of(largest[16 * w + 4 * q + i], true);
-        }
-#pragma unroll
-        for (int kk = 0; kk < L::KS; ++kk) {
-            const int k = L::PACKED ? (q & 1) * 8 : kk * 32 + q * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float v = by * S[m][k + j];
-                hi[kk][j] = take_term<TX>(v);
-                lo[kk][j] = take_term<TX>(v);
-            }
-            if (L::PACKED && q >= 2) hi[kk] = lo[kk];
-        }
-    }
-    __syncthreads();  // S lies in the same memory as the weights
-    for (int i = threadIdx.x; i < 2 * L::BUFFER; i += 256) lds[i] = vu4{0, 0, 0, 0};  // ranks past r stay zero
-    __syncthreads();
-    const TW *W = reinterpret_cast<const TW *>(a.W) + (int64_t)tile.e * a.r * a.N;
-    typename L::Piece piece[L::PIECES];
-    int place[L::PIECES];
-    L::places(place, a.r);
-    V next[4];
-    auto load = [&](int step) {
-        L::load(piece, W, a.r, step * L::COLS);
-        if (ACC) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) next[i] = *reinterpret_cast<const V *>(row[i] + step * L::COLS);
-        }
-    };
-    // What the next step needs is waited for and put in place behind this step's
-    // stores: the loads are older than they, so nothing waits for them. (At the
-    // loop's head the wait would have to hold for its first entry too.)
-    V old[4];
-    auto take = [&](int buffer) {
-        L::stage(lds + buffer * L::BUFFER, piece, place);
-        if (ACC) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                old[i] = next[i];
-                asm volatile("" : "+v"(old[i]));
-            }
-        }
-        __syncthreads();
-    };
-    if (from < to) {
-        load(from);
-        take(0);
-    }
-    for (int step = from; step < to; ++step) {
-        const vu4 *buf = lds + ((step - from) & 1) * L::BUFFER;
-        load(step + 1 < to ? step + 1 : step);  // no branch: see walk
-        __builtin_amdgcn_sched_barrier(0);
-        vf4 d[L::H];
-#pragma unroll
-        for (int h = 0; h < L::H; ++h) {
-            d[h] = vf4{0.f, 0.f, 0.f, 0.f};
-            if constexpr (L::WIDE && ACC) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) d[h][i] = old[i][h];
-            }
-        }
-        vu4 slot[2][L::H];  // the next group's reads are in flight while one is multiplied
-#pragma unroll
-        for (int h = 0; h < L::H; ++h) slot[0][h] = buf[h * L::KS * 64 + lane];
-#pragma unroll
-        for (int kk = 0; kk < L::KS; ++kk) {
-            if (kk + 1 < L::KS) {
-#pragma unroll
-                for (int h = 0; h < L::H; ++h) slot[(kk + 1) & 1][h] = buf[(h * L::KS + kk + 1) * 64 + lane];
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            if constexpr (L::WIDE) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int h = 0; h < L::H; ++h)
-                        d[h] = mfma4(s[kk][j], __builtin_bit_cast(vf4, slot[kk & 1][h])[j], d[h]);
-            } else {
-#pragma unroll
-                for (int h = 0; h < L::H; ++h) d[h] = mfma8(hi[kk], __builtin_bit_cast(V, slot[kk & 1][h]), d[h]);
-                if (!L::PACKED) {
-#pragma unroll
-                    for (int h = 0; h < L::H; ++h) d[h] = mfma8(lo[kk], __builtin_bit_cast(V, slot[kk & 1][h]), d[h]);
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            F f;
-#pragma unroll
-            for (int h = 0; h < L::H; ++h) f[h] = d[h][i];
-            if constexpr (!L::WIDE) {
-                f *= back[i];
-                if (ACC) f += __builtin_convertvector(old[i], F);
-            }
-            if (FULL || in[i]) *reinterpret_cast<V *>(row[i] + step * L::COLS) = __builtin_convertvector(f, V);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        take((step + 1 - from) & 1);
-    }
-}
-
-// One workgroup: 64 rows x a range of columns. The prologue adds the splits'
-// partials; the workgroups of the first range also write s out. One more
-// workgroup a tile writes its panel.
-template <typename TX, typename TW, int RT, bool ACC>
-__global__ __launch_bounds__(256) void adapt_expand_kernel(AdaptExpand a, int chunks) {
-    typedef ExpandLds<TX, TW, RT> Lds;
-    constexpr int S_BYTES = sizeof(float) * TM * (RT * 16 + 4), W_BYTES = 2 * 16 * Lds::BUFFER;
-    __shared__ __align__(16) char lds[S_BYTES > W_BYTES ? S_BYTES : W_BYTES];
-    float(*S)[RT * 16 + 4] = reinterpret_cast<float(*)[RT * 16 + 4]>(lds);
-    __shared__ float largest[TM];
-    __shared__ int named;
-    const int across = chunks + (a.panel ? 1 : 0), chunk = blockIdx.x % across, tile_index = blockIdx.x / across;
-    const Tile tile = find_tile(a.plan, a.plan.E + 1, TM, tile_index);
-    if (tile.e < 0) return;
-    const bool none = tile.e == a.plan.E;
-    const float scale = a.scale && !none ? a.scale[tile.e] : 1.f;
-    if (threadIdx.x < TM) {  // one wave
-        const bool ok = threadIdx.x < tile.cnt && row_of(a.plan, tile.p0 + threadIdx.x) >= 0;
-        if (threadIdx.x == 0) named = 0;
-        if (__ballot(ok) == ~0ull && threadIdx.x == 0) named = 1;
-    }
-    const bool panel = chunk == chunks;  // the workgroup that writes the panel
-    if (panel && none) return;
-    const int rows = tile.cnt <= 16 && !panel ? 16 : TM;
-    for (int i = threadIdx.x; i < rows * RT * 4; i += 256) {
-        const int m = i / (RT * 4), k = i % (RT * 4) * 4;
-        vf4 sum = {0.f, 0.f, 0.f, 0.f};
-        if (m < tile.cnt && k < a.r) {  // r is a multiple of 8
-            if (!none) {
-                const float *part = a.part + (int64_t)(tile.p0 + m) * a.r + k;
-                const int64_t next = (int64_t)a.plan.M * a.r;
-#pragma unroll 8
-                for (int sp = 0; sp < a.splits; ++sp) sum += load4(part + sp * next);
-            }
-            if (chunk == 0 && a.s_row) {
-                const int64_t row = row_of(a.plan, tile.p0 + m);
-                if (row >= 0) store4(a.s_row + row * a.r + k, sum);
-            }
-        }
-        *reinterpret_cast<vf4 *>(&S[m][k]) = scale * sum;
-    }
-    if (none && ACC) return;
-    __syncthreads();
-    if (panel) {
-        write_panel<TX, RT>(a.panel, tile_index, S);
-        return;
-    }
-    if (none) {
-        // rows without an adapter: zeros
-        const int64_t n16 = (int64_t)a.N * sizeof(TX) / 16, lo = n16 * chunk / chunks, hi = n16 * (chunk + 1) / chunks;
-        for (int m = 0; m < tile.cnt; ++m) {
-            const int64_t row = row_of(a.plan, tile.p0 + m);
-            if (row < 0) continue;
-            vu4 *out = reinterpret_cast<vu4 *>(reinterpret_cast<TX *>(a.out) + row * a.N);
-            for (int64_t i = lo + threadIdx.x; i < hi; i += 256) out[i] = vu4{0, 0, 0, 0};
-        }
-        return;
-    }
-    if (__is_same(TX, _Float16)) {
-        if (threadIdx.x < rows) {
-            float top = 0.f;
-            for (int k = 0; k < RT * 16; ++k) top = fmaxf(top, fabsf(S[threadIdx.x][k]));
-            largest[threadIdx.x] = top;
-        }
-        __syncthreads();
-    }
-    if (tile.cnt <= 16) {
-        const int64_t steps = a.N / ExpandStep<TX, TW, RT, 1>::COLS;
-        const int from = (int)(steps * chunk / chunks), to = (int)(steps * (chunk + 1) / chunks);
-        expand_tile<TX, TW, RT, 1, ACC>(a, tile, from, to, S, largest);
-        return;
-    }
-    const int64_t steps = a.N / Lds::COLS;
-    const int from = (int)(steps * chunk / chunks), to = (int)(steps * (chunk + 1) / chunks);
-    if (named)
-        expand_tile_lds<TX, TW, RT, ACC, true>(a, tile, from, to, S, largest, reinterpret_cast<vu4 *>(lds));
-    else
-        expand_tile_lds<TX, TW, RT, ACC, false>(a, tile, from, to, S, largest, reinterpret_cast<vu4 *>(lds));
-}
-
-// --------------------------------------------------------------- prepare --
-// The backward's first launch; each workgroup does one of three things.
-//
-// Transpose: the backward contracts over the other side of A and B than the
-// forward, so both are laid out transposed, 64 x 64 elements at a time through
-// LDS; then every weight is read 16 consecutive bytes a lane, as in the
-// forward. Adapters without rows are left out.
-template <typename T>
-__device__ void transpose_tile(const AdaptPrepare &a, int job, int e, int b, T (*tile)[64 + 16 / sizeof(T)]) {
-    constexpr int n = 16 / sizeof(T);
-    typedef T V __attribute__((ext_vector_type(n)));
-    const int R = a.rows[job], C = a.cols[job], across = (C + 63) / 64;
-    const int r0 = b / across * 64, c0 = b % across * 64;
-    const T *src = reinterpret_cast<const T *>(a.src[job]) + (int64_t)e * R * C;
-    T *dst = reinterpret_cast<T *>(a.dst[job]) + (int64_t)e * R * C;
-    constexpr int per = 64 / n;  // vectors of a tile's row
-    for (int i = threadIdx.x; i < 64 * per; i += 256) {
-        const int r = i / per, c = i % per * n;
-        if (r0 + r < R && c0 + c < C)  // R and C are multiples of 8
-            *reinterpret_cast<V *>(&tile[r][c]) = *reinterpret_cast<const V *>(src + (int64_t)(r0 + r) * C + c0 + c);
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 64 * per; i += 256) {
-        const int c = i / per, r = i % per * n;
-        if (r0 + r < R && c0 + c < C) {
-            V v;
-#pragma unroll
-            for (int j = 0; j < n; ++j) v[j] = tile[r + j][c];
-            *reinterpret_cast<V *>(dst + (int64_t)(c0 + c) * R + r0 + r) = v;
-        }
-    }
-}
-
-// Workgroups of 64 KB of an adapter's two gradients: zeros, where it has no rows.
-constexpr int ZERO_FLOATS = 16384;
-
-template <typename TX, typename TW, int RT>
-__global__ __launch_bounds__(256) void adapt_prepare_kernel(AdaptPrepare a) {
-    typedef typename std::conditional<sizeof(TW) == 4, uint32_t, uint16_t>::type T;
-    constexpr int T_BYTES = 64 * (64 * sizeof(T) + 16), S_BYTES = sizeof(float) * TM * (RT * 16 + 1);
-    __shared__ __align__(16) char lds[T_BYTES > S_BYTES ? T_BYTES : S_BYTES];
-    int b = blockIdx.x;
-    if (b < a.panels) {
-        // the tape's panel
-        float(*S)[RT * 16 + 1] = reinterpret_cast<float(*)[RT * 16 + 1]>(lds);
-        const Tile tile = find_tile(a.plan, a.plan.E, TM, b);
-        if (tile.e < 0) return;
-        for (int i = threadIdx.x; i < TM * RT * 16; i += 256) {
-            const int m = i / (RT * 16), k = i % (RT * 16);
-            float v = 0.f;
-            if (m < tile.cnt && k < a.r) {
-                const int64_t row = row_of(a.plan, tile.p0 + m);
-                if (row >= 0) v = a.tape[row * a.r + k];
-            }
-            S[m][k] = v;
-        }
-        __syncthreads();
-        write_panel<TX, RT>(a.panel, b, S);
-        return;
-    }
-    b -= a.panels;
-    const int per = a.tiles[0] + a.tiles[1] + a.zeros, e = b / per;
-    b %= per;
-    const bool empty = a.plan.offsets[e + 1] <= a.plan.offsets[e];
-    if (b >= a.tiles[0] + a.tiles[1]) {
-        if (!empty) return;
-        int64_t at = (int64_t)(b - a.tiles[0] - a.tiles[1]) * ZERO_FLOATS + threadIdx.x * 4;
-        const int64_t size[2] = {(int64_t)a.rows[0] * a.cols[0], (int64_t)a.rows[1] * a.cols[1]};
-        for (int i = 0; i < ZERO_FLOATS / 1024; ++i, at += 1024) {
-            if (at < size[0])
-                store4(a.grad[0] + e * size[0] + at, vf4{0.f, 0.f, 0.f, 0.f});
-            else if (at < size[0] + size[1])
-                store4(a.grad[1] + e * size[1] + at - size[0], vf4{0.f, 0.f, 0.f, 0.f});
-        }
-        return;
-    }
-    if (empty) return;
-    const int job = b >= a.tiles[0];
-    transpose_tile<T>(a, job, e, b - (job ? a.tiles[0] : 0), reinterpret_cast<T(*)[64 + 16 / sizeof(T)]>(lds));
-}
-
-// The panel of ds where no dx is formed, whose kernel writes it otherwise.
-template <typename TX, int RT>
-__global__ __launch_bounds__(256) void adapt_thin_kernel(AdaptThin a) {
-    __shared__ float S[TM][RT * 16 + 1];
-    const Tile tile = find_tile(a.plan, a.plan.E, TM, blockIdx.x);
-    if (tile.e < 0) return;
-    const float scale = a.scale ? a.scale[tile.e] : 1.f;
-    const int64_t next = (int64_t)a.plan.M * a.r;
-    for (int i = threadIdx.x; i < TM * RT * 16; i += 256) {
-        const int m = i / (RT * 16), k = i % (RT * 16);
-        float v = 0.f;
-        if (m < tile.cnt && k < a.r) {
-            const float *part = a.part + (int64_t)(tile.p0 + m) * a.r + k;
-#pragma unroll 8
-            for (int sp = 0; sp < a.splits; ++sp) v += part[sp * next];
-        }
-        S[m][k] = scale * v;
-    }
-    __syncthreads();
-    write_panel<TX, RT>(a.panel, blockIdx.x, S);
-}
-
-// -------------------------------------------------------------- gradients --
-// Rows past a range's end: zeros, so that they add nothing whatever a real row
-// holds. A wave reads up to 64 columns of a row.
-__device__ float zero_row[64];  // never written; not const, or its loads would not be global ones
-
-// X as the A operand, straight from its rows: lane (q, c) loads columns
-// 4 c .. 4 c + 3, component u belonging to tile u of the output (so that row m
-// of tile u stands for column 4 m + u), of the rows q of the step's k indices.
-// The thin operand's panel gives B[k][rank] from LDS. D then holds
-// G[column 4 (4 q + i) + u][rank c].
-//
-// Rows of f32: 16 a step, k index 4 q + j.
-template <typename TX, int RT>
-struct GradStep {
-    static constexpr int ROWS = 16;
-    static constexpr int SLOTS = RT * 64;  // of a step's panel
-    vf4 x[4];
-
-    __device__ __forceinline__ void load(const TX *X, int N, const int *row, int q, int c) {
-        const int4 at = *reinterpret_cast<const int4 *>(row + 4 * q);
-        const int r[4] = {at.x, at.y, at.z, at.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            x[j] = load4((r[j] < 0 ? reinterpret_cast<const TX *>(zero_row) : X + (int64_t)r[j] * N) + 4 * c);
-    }
-    __device__ __forceinline__ void multiply(const vu4 *panel, vf4 (&acc)[4][RT], int lane) const {
-        vf4 t[RT];
-#pragma unroll
-        for (int n = 0; n < RT; ++n) t[n] = __builtin_bit_cast(vf4, panel[n * 64 + lane]);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int n = 0; n < RT; ++n)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) acc[u][n] = mfma4(x[j][u], t[n][j], acc[u][n]);
-    }
-};
-
-// Rows of 16 bits: 32 a step, k index 8 q + j, on the bf16 instruction. The
-// gradients are f32, so the thin operand takes part with 24 leading bits, in
-// three bf16 terms; an f16 element of X is exactly two (11 bits in 8 + 3), and
-// the product of its second with the third term, 2^-25 of the whole at most,
-// is left out. bf16 has f32's range, so no term needs a scale.
-template <typename T, int RT>
-struct GradStep16 {
-    static constexpr int ROWS = 32;
-    static constexpr int SLOTS = 3 * RT * 64;
-    uint2 x[8];  // four elements
-
-    __device__ __forceinline__ void load(const T *X, int N, const int *row, int q, int c) {
-        const int4 a = *reinterpret_cast<const int4 *>(row + 8 * q);
-        const int4 b = *reinterpret_cast<const int4 *>(row + 8 * q + 4);
-        const int r[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            x[j] = *reinterpret_cast<const uint2 *>(
-                (r[j] < 0 ? reinterpret_cast<const T *>(zero_row) : X + (int64_t)r[j] * N) + 4 * c);
-    }
-    __device__ __forceinline__ void multiply(const vu4 *panel, vf4 (&acc)[4][RT], int lane) const {
-        vb8 hi[4], lo[4];
-        vu4 t[2][RT];  // the next term's reads are in flight while one is multiplied
-#pragma unroll
-        for (int n = 0; n < RT; ++n) t[0][n] = panel[n * 64 + lane];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if constexpr (__is_same(T, __bf16)) {
-                vu4 pairs;  // element u of two rows each
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    pairs[j] = __builtin_amdgcn_perm(u < 2 ? x[2 * j + 1].x : x[2 * j + 1].y,
-                                                     u < 2 ? x[2 * j].x : x[2 * j].y, u & 1 ? 0x07060302u : 0x05040100u);
-                hi[u] = __builtin_bit_cast(vb8, pairs);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float v = (float)__builtin_bit_cast(vh4, x[j])[u];
-                    hi[u][j] = take_term<__bf16>(v);
-                    lo[u][j] = take_term<__bf16>(v);
-                }
-            }
-        }
-#pragma unroll
-        for (int h = 0; h < 3; ++h) {
-            if (h < 2) {
-#pragma unroll
-                for (int n = 0; n < RT; ++n) t[(h + 1) & 1][n] = panel[((h + 1) * RT + n) * 64 + lane];
-            }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int n = 0; n < RT; ++n)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) acc[u][n] = mfma8(hi[u], __builtin_bit_cast(vb8, t[h & 1][n]), acc[u][n]);
-            if constexpr (!__is_same(T, __bf16)) {
-                if (h < 2) {
-#pragma unroll
-                    for (int n = 0; n < RT; ++n)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            acc[u][n] = mfma8(lo[u], __builtin_bit_cast(vb8, t[h & 1][n]), acc[u][n]);
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    }
-};
-template <int RT>
-struct GradStep<_Float16, RT> : GradStep16<_Float16, RT> {};
-template <int RT>
-struct GradStep<__bf16, RT> : GradStep16<__bf16, RT> {};
-
-// One workgroup: a range of one adapter's rows x 256 columns, wave w 64 of
-// them. A panel of 64 rows is up to three times as many bytes as the 64
-// columns it meets, so the four waves share it through LDS (in two buffers,
-// one barrier a panel); the next panel and the next step's rows are in flight
-// while a step is multiplied.
-template <typename TX, int RT>
-__global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_grad_kernel(AdaptGrad a) {
-    typedef GradStep<TX, RT> Step;
-    constexpr int STEPS = TM / Step::ROWS, SLOTS = STEPS * Step::SLOTS, PIECES = (SLOTS + 255) / 256;
-    static_assert(STEPS % 2 == 0, "the two register sets alternate through a panel");
-    __shared__ __align__(16) int row[ADAPT_MAX_RANGE];
-    __shared__ __align__(16) vu4 lds[2][SLOTS];
-    const int per = a.across[0] + a.across[1];
-    const int col = blockIdx.x % per, which = col >= a.across[0];
-    const AdaptGradJob &job = a.job[which];
-    const int N = job.N;
-    const Tile tile = find_tile(a.plan, a.plan.E, a.range, blockIdx.x / per);
-    if (tile.e < 0) return;
-    const int first = tile.panel + tile.j * (a.range / TM), panels = (tile.cnt + TM - 1) / TM;
-    // only offsets out of order can count more panels or partials than there are
-    if (first + panels > a.panels || (tile.of > 1 && tile.slot + tile.j >= a.slots)) return;
-    for (int i = threadIdx.x; i < panels * TM; i += 256)
-        row[i] = i < tile.cnt ? (int)row_of(a.plan, tile.p0 + i) : -1;
-    __syncthreads();
-    const int lane = threadIdx.x & 63, w = wave();
-    const int q = lane >> 4, c = lane & 15;
-    const int n0 = (col - (which ? a.across[0] : 0)) * 256 + w * 64;
-    // waves past the last column repeat column 0, for the barriers; not stored
-    const TX *X = reinterpret_cast<const TX *>(job.X) + (n0 < N ? n0 : 0);
-    const vu4 *panel = reinterpret_cast<const vu4 *>(job.panel) + (int64_t)first * SLOTS;
-    vf4 acc[4][RT];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int n = 0; n < RT; ++n) acc[u][n] = vf4{0.f, 0.f, 0.f, 0.f};
-    vu4 piece[PIECES];
-    auto load_panel = [&](int p) {
-#pragma unroll
-        for (int j = 0; j < PIECES; ++j) {
-            const unsigned i = threadIdx.x + 256 * j;
-            piece[j] = *ahead(panel + (int64_t)p * SLOTS, (SLOTS % 256 == 0 || i < SLOTS ? i : 0) * 16u);
-        }
-    };
-    Step set[2];
-    load_panel(0);
-    set[0].load(X, N, row, q, c);
-    for (int p = 0; p < panels; ++p) {
-        vu4 *buf = lds[p & 1];
-#pragma unroll
-        for (int j = 0; j < PIECES; ++j) {
-            const int i = threadIdx.x + 256 * j;
-            if (SLOTS % 256 == 0 || i < SLOTS) buf[i] = piece[j];
-        }
-        __syncthreads();
-        const bool last = p + 1 == panels;
-        load_panel(last ? p : p + 1);  // no branch: see walk
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int next = last && s + 1 == STEPS ? s : s + 1;
-            set[(s + 1) & 1].load(X, N, row + p * TM + next * Step::ROWS, q, c);
-            __builtin_amdgcn_sched_barrier(0);
-            set[s & 1].multiply(buf + s * Step::SLOTS, acc, lane);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    }
-    if (n0 >= N) return;
-    const int64_t size = (int64_t)a.r * N;
-    const bool alone = tile.of == 1;
-    float *g = alone ? job.grad + tile.e * size : job.part + (tile.slot + tile.j) * size;
-    const bool add = alone && a.acc;
-    const float scale = job.scale ? job.scale[tile.e] : 1.f;
-#pragma unroll
-    for (int n = 0; n < RT; ++n) {
-        const int k = n * 16 + c;
-        if (k >= a.r) continue;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const vf4 v = scale * vf4{acc[0][n][i], acc[1][n][i], acc[2][n][i], acc[3][n][i]};
-            const int o = n0 + 16 * q + 4 * i;
-            if (which == 0) {
-                float *at = g + (int64_t)k * N + o;
-                store4(at, add ? load4(at) + v : v);
-            } else {
-                float *at = g + (int64_t)o * a.r + k;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) at[u * a.r] = add ? at[u * a.r] + v[u] : v[u];
-            }
-        }
-    }
-}
-
-// The partials of an adapter of several ranges, added in range order.
-// blockIdx.z: the gradient.
-__global__ __launch_bounds__(256) void adapt_reduce_kernel(AdaptGrad a) {
-    const AdaptGradJob &job = a.job[blockIdx.z];
-    const int e = blockIdx.y;
-    const int64_t size = (int64_t)a.r * job.N;
-    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if ((int64_t)blockIdx.x * 1024 >= size) return;
-    auto rows = [&](int f) {
-        int lo = a.plan.offsets[f], hi = a.plan.offsets[f + 1];
-        lo = lo < 0 ? 0 : lo > a.plan.M ? a.plan.M : lo;
-        hi = hi > a.plan.M ? a.plan.M : hi;
-        return hi > lo ? hi - lo : 0;
-    };
-    const int cnt = rows(e);
-    if (cnt <= a.range) return;
-    // partials of the adapters before: every wave sums for itself
-    const int lane = threadIdx.x & 63;
-    int slot = 0;
-    for (int base = 0; base < e; base += 64) {
-        int several = 0;
-        if (base + lane < e) {
-            const int n = rows(base + lane);
-            if (n > a.range) several = n / a.range + (n % a.range ? 1 : 0);
-        }
-        for (int o = 32; o > 0; o /= 2) several += __shfl_xor(several, o);
-        slot += several;
-    }
-    const int of = cnt / a.range + (cnt % a.range ? 1 : 0);
-    if (slot + of > a.slots) return;
-    if (at >= size) return;
-    float *g = job.grad + e * size + at;
-    vf4 sum = a.acc ? load4(g) : vf4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int j = 0; j < of; ++j) sum += load4(job.part + (int64_t)(slot + j) * size + at);
-    store4(g, sum);
-}
-
 // Workgroups that keep the chip busy: a few per CU.
 constexpr int64_t FILL = 1024;
+
+template <typename TX, typename TW, int RT>
+__global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_shrink_kernel(AdaptShrink a) {
+    __shared__ __align__(16) char lds[ShrinkBlock<TX, TW, RT>::BYTES];
+    ShrinkBlock<TX, TW, RT>::run(a, blockIdx.x, lds);
+}
+
+template <typename TX, typename TW, int RT, bool ACC>
+__global__ __launch_bounds__(256) void adapt_expand_kernel(AdaptExpand a, int chunks) {
+    __shared__ __align__(16) char lds[ExpandBlock<TX, TW, RT, ACC>::BYTES];
+    ExpandBlock<TX, TW, RT, ACC>::run(a, chunks, blockIdx.x, lds);
+}
 
 template <typename TX, typename TW, int RT>
 hipError_t shrink_t(const AdaptShrink &a, hipStream_t s) {
@@ -1298,67 +30,14 @@ hipError_t shrink_t(const AdaptShrink &a, hipStream_t s) {
 
 template <typename TX, typename TW, int RT>
 hipError_t expand_t(const AdaptExpand &a, hipStream_t s) {
-    const int64_t tiles = adapt_tiles(a.plan.M, a.plan.E, TM), units = a.N / 128;
-    int64_t chunks = (FILL + tiles - 1) / tiles;
-    chunks = chunks > units ? units : chunks;
-    if (chunks > 8) chunks = chunks / 8 * 8;
-    const dim3 grid((unsigned)((chunks + (a.panel ? 1 : 0)) * tiles));
+    const int64_t chunks = adapt_chunks(a.plan.M, a.plan.E, a.N);
+    const dim3 grid((unsigned)(chunks * adapt_tiles(a.plan.M, a.plan.E, TM)));
     if (a.acc)
         hipLaunchKernelGGL((adapt_expand_kernel<TX, TW, RT, true>), grid, dim3(256), 0, s, a, (int)chunks);
     else
         hipLaunchKernelGGL((adapt_expand_kernel<TX, TW, RT, false>), grid, dim3(256), 0, s, a, (int)chunks);
     return hipGetLastError();
 }
-
-template <typename TX, typename TW, int RT>
-hipError_t prepare_t(AdaptPrepare a, hipStream_t s) {
-    for (int j = 0; j < 2; ++j) a.tiles[j] = (a.rows[j] + 63) / 64 * ((a.cols[j] + 63) / 64);
-    const int64_t floats = (int64_t)a.rows[0] * a.cols[0] + (int64_t)a.rows[1] * a.cols[1];
-    a.zeros = a.grad[0] ? (int)((floats + ZERO_FLOATS - 1) / ZERO_FLOATS) : 0;
-    a.panels = a.tape ? (int)adapt_tiles(a.plan.M, a.plan.E, TM) : 0;
-    const int64_t blocks = a.panels + (int64_t)a.plan.E * (a.tiles[0] + a.tiles[1] + a.zeros);
-    hipLaunchKernelGGL((adapt_prepare_kernel<TX, TW, RT>), dim3((unsigned)blocks), dim3(256), 0, s, a);
-    return hipGetLastError();
-}
-
-template <typename TX, int RT>
-hipError_t thin_t(const AdaptThin &a, hipStream_t s) {
-    hipLaunchKernelGGL((adapt_thin_kernel<TX, RT>), dim3((unsigned)adapt_tiles(a.plan.M, a.plan.E, TM)), dim3(256), 0,
-                       s, a);
-    return hipGetLastError();
-}
-
-template <typename TX, int RT>
-hipError_t grad_t(AdaptGrad a, hipStream_t s) {
-    const int64_t tiles = adapt_tiles(a.plan.M, a.plan.E, a.range);
-    for (int j = 0; j < 2; ++j) a.across[j] = (a.job[j].N + 255) / 256;
-    const dim3 grid((unsigned)(tiles * (a.across[0] + a.across[1])));
-    hipLaunchKernelGGL((adapt_grad_kernel<TX, RT>), grid, dim3(256), 0, s, a);
-    return hipGetLastError();
-}
-
-// Calls f<TX, TW, RT> for the call's types and rank.
-#define BLR_BY_RANK(r, F, TX, TW, ...)                                                          \
-    ((r) <= 16   ? F<TX, TW, 1>(__VA_ARGS__)                                                     \
-     : (r) <= 32 ? F<TX, TW, 2>(__VA_ARGS__)                                                     \
-     : (r) <= 64 ? F<TX, TW, 4>(__VA_ARGS__)                                                     \
-                 : F<TX, TW, 8>(__VA_ARGS__))
-#define BLR_BY_TYPES(a, F, ...)                                                                  \
-    ((a).act == 1   ? BLR_BY_RANK((a).r, F, _Float16, _Float16, __VA_ARGS__)                     \
-     : (a).act == 2 ? BLR_BY_RANK((a).r, F, __bf16, __bf16, __VA_ARGS__)                         \
-     : (a).wt == 1  ? BLR_BY_RANK((a).r, F, float, _Float16, __VA_ARGS__)                        \
-     : (a).wt == 2  ? BLR_BY_RANK((a).r, F, float, __bf16, __VA_ARGS__)                          \
-                    : BLR_BY_RANK((a).r, F, float, float, __VA_ARGS__))
-
-#define BLR_BY_ROWS(a, F, ...)                                                                   \
-    ((a).act == 0   ? BLR_BY_RANK1((a).r, F, float, __VA_ARGS__)                                 \
-     : (a).act == 1 ? BLR_BY_RANK1((a).r, F, _Float16, __VA_ARGS__)                              \
-                    : BLR_BY_RANK1((a).r, F, __bf16, __VA_ARGS__))
-#define BLR_BY_RANK1(r, F, TX, ...)                                                              \
-    ((r) <= 16   ? F<TX, 1>(__VA_ARGS__)                                                         \
-     : (r) <= 32 ? F<TX, 2>(__VA_ARGS__)                                                         \
-     : (r) <= 64 ? F<TX, 4>(__VA_ARGS__)                                                         \
-                 : F<TX, 8>(__VA_ARGS__))
 
 }  // namespace
 
@@ -1373,6 +52,13 @@ int adapt_splits(int64_t M, int64_t E, int64_t K) {
     int64_t sp = (FILL / 2 + tiles - 1) / tiles;
     sp = sp > units ? units : sp;
     return (int)(sp > ADAPT_MAX_SPLITS ? ADAPT_MAX_SPLITS : sp);
+}
+
+int64_t adapt_chunks(int64_t M, int64_t E, int64_t N) {
+    const int64_t tiles = adapt_tiles(M, E, TM), units = N / 128;
+    int64_t chunks = (FILL + tiles - 1) / tiles;
+    chunks = chunks > units ? units : chunks;
+    return chunks > 8 ? chunks / 8 * 8 : chunks;  // a range of columns then stays on one XCD
 }
 
 int64_t adapt_range(int64_t M, int64_t d_in, int64_t d_out, int64_t r) {
@@ -1391,13 +77,6 @@ int64_t adapt_range_slots(int64_t M, int64_t E, int64_t range) {
     return twice < all ? twice : all;
 }
 
-hipError_t launch_adapt_prepare(const AdaptPrepare &a, hipStream_t s) {
-    prof_begin(K_ADAPT_PREPARE, s);
-    hipError_t e = BLR_BY_TYPES(a, prepare_t, a, s);
-    prof_end(s);
-    return e;
-}
-
 hipError_t launch_adapt_shrink(const AdaptShrink &a, int id, hipStream_t s) {
     prof_begin(id, s);
     hipError_t e = BLR_BY_TYPES(a, shrink_t, a, s);
@@ -1408,27 +87,6 @@ hipError_t launch_adapt_shrink(const AdaptShrink &a, int id, hipStream_t s) {
 hipError_t launch_adapt_expand(const AdaptExpand &a, int id, hipStream_t s) {
     prof_begin(id, s);
     hipError_t e = BLR_BY_TYPES(a, expand_t, a, s);
-    prof_end(s);
-    return e;
-}
-
-hipError_t launch_adapt_thin(const AdaptThin &a, hipStream_t s) {
-    prof_begin(K_ADAPT_THIN, s);
-    hipError_t e = BLR_BY_ROWS(a, thin_t, a, s);
-    prof_end(s);
-    return e;
-}
-
-hipError_t launch_adapt_grad(const AdaptGrad &a, hipStream_t s) {
-    prof_begin(K_ADAPT_GRAD, s);
-    hipError_t e = BLR_BY_ROWS(a, grad_t, a, s);
-    prof_end(s);
-    if (e != hipSuccess || a.slots == 0) return e;
-    const int N = a.job[0].N > a.job[1].N ? a.job[0].N : a.job[1].N;
-    const int64_t blocks = ((int64_t)a.r * N / 4 + 255) / 256;
-    prof_begin(K_ADAPT_REDUCE, s);
-    hipLaunchKernelGGL(adapt_reduce_kernel, dim3((unsigned)blocks, (unsigned)a.plan.E, 2), dim3(256), 0, s, a);
-    e = hipGetLastError();
     prof_end(s);
     return e;
 }

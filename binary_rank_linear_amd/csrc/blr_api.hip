@@ -813,7 +813,6 @@ int blr_adapters_forward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int6
     sh.splits = adapt_splits(M, adapters, d_in);
     sh.act = act;
     sh.wt = wt;
-    BLR_TRY(launch_adapt_shrink(sh, K_ADAPT_DOWN, s));
     AdaptExpand ex = {};
     ex.plan = sh.plan;
     ex.part = sh.part;
@@ -827,6 +826,7 @@ int blr_adapters_forward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int6
     ex.act = act;
     ex.wt = wt;
     ex.acc = accumulate_y ? 1 : 0;
+    BLR_TRY(launch_adapt_shrink(sh, K_ADAPT_DOWN, s));
     BLR_TRY(launch_adapt_expand(ex, K_ADAPT_UP, s));
     return BLR_OK;
 }
@@ -886,28 +886,23 @@ int blr_adapters_backward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int
     sh.splits = adapt_splits(M, adapters, d_out);
     sh.act = act;
     sh.wt = wt;
-    BLR_TRY(launch_adapt_shrink(sh, K_ADAPT_DS, s));
-    void *ds_panel = ws + L.panel[0];
-    if (dx) {
-        AdaptExpand ex = {};
-        ex.plan = sh.plan;
-        ex.part = sh.part;
-        ex.scale = scale;
-        ex.W = pr.dst[0];
-        ex.out = dx;
-        ex.panel = grad_down ? ds_panel : nullptr;
-        ex.N = (int)d_in;
-        ex.r = (int)r;
-        ex.splits = sh.splits;
-        ex.act = act;
-        ex.wt = wt;
-        ex.acc = accumulate_dx ? 1 : 0;
+    AdaptExpand ex = {};
+    ex.plan = sh.plan;
+    ex.part = sh.part;
+    ex.scale = scale;
+    ex.W = pr.dst[0];
+    ex.out = dx;
+    ex.N = (int)d_in;
+    ex.r = (int)r;
+    ex.splits = sh.splits;
+    ex.act = act;
+    ex.wt = wt;
+    ex.acc = accumulate_dx ? 1 : 0;
+    if (!grad_down) {
+        BLR_TRY(launch_adapt_shrink(sh, K_ADAPT_DS, s));
         BLR_TRY(launch_adapt_expand(ex, K_ADAPT_DX, s));
-    } else {
-        AdaptThin th = {sh.plan, sh.part, scale, ds_panel, (int)r, sh.splits, act};
-        BLR_TRY(launch_adapt_thin(th, s));
+        return BLR_OK;
     }
-    if (!grad_down) return BLR_OK;
     AdaptGrad gr = {};
     gr.plan = sh.plan;
     gr.r = (int)r;
@@ -916,9 +911,14 @@ int blr_adapters_backward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int
     gr.panels = adapt_tiles(M, adapters, ADAPT_TM);
     gr.range = (int)L.range;
     gr.slots = L.slots;
+    void *ds_panel = ws + L.panel[0];
     gr.job[0] = {x, ds_panel, nullptr, grad_down, (float *)(ws + L.part[0]), (int)d_in};
     gr.job[1] = {dy, pr.panel, scale, grad_up, (float *)(ws + L.part[1]), (int)d_out};
-    BLR_TRY(launch_adapt_grad(gr, s));
+    BLR_TRY(launch_adapt_dy(sh, gr, s));
+    AdaptThin th = {sh.plan, sh.part, scale, ds_panel, (int)r, sh.splits, act};
+    BLR_TRY(launch_adapt_thin(th, s));
+    BLR_TRY(launch_adapt_dx(ex, gr, s));
+    if (L.slots > 0) BLR_TRY(launch_adapt_reduce(gr, s));  // otherwise no adapter can have several ranges
     return BLR_OK;
 }
 

@@ -44,8 +44,9 @@ enum KernelId {
     K_ADAPT_PREPARE, // adapters: the backward's A^T and B^T, the tape's panel
     K_ADAPT_DS,     // adapters: partials of ds = c dy B
     K_ADAPT_DX,     // adapters: dx (+)= ds A
-    K_ADAPT_THIN,   // adapters: ds's panel where no dx is formed
-    K_ADAPT_GRAD,   // adapters: gradients of A and B over ranges of rows
+    K_ADAPT_DY,     // adapters: partials of ds, and the gradient of B
+    K_ADAPT_THIN,   // adapters: ds as the gradient's operand
+    K_ADAPT_DX_GRAD, // adapters: dx, and the gradient of A
     K_ADAPT_REDUCE, // adapters: the ranges' partials summed in order
     K_COUNT
 };
@@ -240,8 +241,7 @@ struct AdaptShrink {
     int K, r, splits, act, wt;
 };
 // out[row(p)][n] (+)= sum_k S[p][k] W_e[n][k], S[p] = scale_e sum over splits
-// of part[.][p]; W_e: [N][r]. S goes to s_row by row, unscaled, and to panel
-// as panels (either may be null).
+// of part[.][p]; W_e: [N][r]. S goes to s_row by row, unscaled (unless null).
 struct AdaptExpand {
     AdaptPlan plan;
     const float *part;
@@ -249,7 +249,6 @@ struct AdaptExpand {
     const void *W;
     void *out;
     float *s_row;
-    void *panel;
     int N, r, splits, act, wt, acc;
 };
 // The gradients' thin operands, ds (scaled) and the tape s, as panels: of each
@@ -278,7 +277,7 @@ struct AdaptPrepare {
 };
 constexpr int64_t adapt_r16(int64_t r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 constexpr int64_t adapt_panel_bytes(int64_t r, int act) { return adapt_r16(r) * 64 * (act == 0 ? 4 : 6); }
-// Two gradients in one launch, G_e (+)= scale_e sum over the adapter's rows of
+// The two gradients, G_e (+)= scale_e sum over the adapter's rows of
 // thin[.][k] X[row][n]: job 0 laid out [r][N], job 1 [N][r]. Ranges of `range`
 // positions; an adapter of several ranges leaves partials in part[slot], which
 // the reduction adds in range order.
@@ -296,14 +295,17 @@ struct AdaptGrad {
     int r, act, acc, range;
     int64_t panels;  // that exist
     int64_t slots;   // partials that each `part` has room for
-    int across[2];   // workgroups across each job's columns; filled by the launcher
 };
 hipError_t launch_adapt_prepare(const AdaptPrepare &a, hipStream_t s);
 // id: the kernel kind that the launch is timed as.
 hipError_t launch_adapt_shrink(const AdaptShrink &a, int id, hipStream_t s);
 hipError_t launch_adapt_expand(const AdaptExpand &a, int id, hipStream_t s);
+hipError_t launch_adapt_dy(const AdaptShrink &sh, const AdaptGrad &gr, hipStream_t s);  // ds, and job 1
 hipError_t launch_adapt_thin(const AdaptThin &a, hipStream_t s);
-hipError_t launch_adapt_grad(const AdaptGrad &a, hipStream_t s);
+hipError_t launch_adapt_dx(const AdaptExpand &ex, const AdaptGrad &gr, hipStream_t s);  // dx (out null: not), and job 0
+hipError_t launch_adapt_reduce(const AdaptGrad &a, hipStream_t s);
+// Ranges of columns of the expand, per tile.
+int64_t adapt_chunks(int64_t M, int64_t E, int64_t N);
 // Tiles of tm positions that M positions in at most E + 1 groups can need.
 int64_t adapt_tiles(int64_t M, int64_t E, int64_t tm);
 int adapt_splits(int64_t M, int64_t E, int64_t K);

@@ -2109,7 +2109,8 @@ const char *kernel_name(int id) {
         case K_ADAPT_DS: return "adapters_ds";
         case K_ADAPT_DX: return "adapters_dx";
         case K_ADAPT_THIN: return "adapters_thin";
-        case K_ADAPT_GRAD: return "adapters_grad";
+        case K_ADAPT_DY: return "adapters_ds_grad_up";
+        case K_ADAPT_DX_GRAD: return "adapters_dx_grad_down";
         case K_ADAPT_REDUCE: return "adapters_grad_reduce";
     }
     return "?";
