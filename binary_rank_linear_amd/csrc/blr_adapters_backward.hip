@@ -51,45 +51,47 @@ __global__ __launch_bounds__(256) void adapt_prepare_kernel(AdaptPrepare a) {
     typedef typename std::conditional<sizeof(TW) == 4, uint32_t, uint16_t>::type T;
     constexpr int T_BYTES = 64 * (64 * sizeof(T) + 16), S_BYTES = sizeof(float) * TM * (RT * 16 + 1);
     __shared__ __align__(16) char lds[T_BYTES > S_BYTES ? T_BYTES : S_BYTES];
-    int b = blockIdx.x;
-    if (b < a.panels) {
-        // the tape's panel
-        float(*S)[RT * 16 + 1] = reinterpret_cast<float(*)[RT * 16 + 1]>(lds);
-        const Tile tile = find_tile<false>(a.plan, a.plan.E, TM, b);
-        if (tile.e < 0) return;
-        for (int i = threadIdx.x; i < TM * RT * 4; i += 256) {
-            const int m = i / (RT * 4), k = i % (RT * 4) * 4;
-            vf4 v = {0.f, 0.f, 0.f, 0.f};
-            if (m < tile.cnt && k < a.r) {  // r is a multiple of 8
-                const int64_t row = row_of(a.plan, tile.p0 + m);
-                if (row >= 0) v = load4(a.tape + row * a.r + k);
-            }
+    const int transposes = a.tiles[0] + a.tiles[1], per = transposes + a.zeros;
+    const int64_t all = a.panels + (int64_t)a.plan.E * per;
+    // the conditions below are the same in the whole workgroup
+    for (int64_t b = blockIdx.x; b < all; b += gridDim.x, __syncthreads()) {
+        if (b < a.panels) {
+            // the tape's panel
+            float(*S)[RT * 16 + 1] = reinterpret_cast<float(*)[RT * 16 + 1]>(lds);
+            const Tile tile = find_tile<false>(a.plan, a.plan.E, TM, (int)b);
+            if (tile.e < 0) continue;
+            for (int i = threadIdx.x; i < TM * RT * 4; i += 256) {
+                const int m = i / (RT * 4), k = i % (RT * 4) * 4;
+                vf4 v = {0.f, 0.f, 0.f, 0.f};
+                if (m < tile.cnt && k < a.r) {  // r is a multiple of 8
+                    const int64_t row = row_of(a.plan, tile.p0 + m);
+                    if (row >= 0) v = load4(a.tape + row * a.r + k);
+                }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) S[m][k + j] = v[j];
+                for (int j = 0; j < 4; ++j) S[m][k + j] = v[j];
+            }
+            __syncthreads();
+            write_panel<TX, RT>(a.panel, b, S);
+            continue;
         }
-        __syncthreads();
-        write_panel<TX, RT>(a.panel, b, S);
-        return;
-    }
-    b -= a.panels;
-    const int per = a.tiles[0] + a.tiles[1] + a.zeros, e = b / per;
-    b %= per;
-    const bool empty = a.plan.offsets[e + 1] <= a.plan.offsets[e];
-    if (b >= a.tiles[0] + a.tiles[1]) {
-        if (!empty) return;
-        int64_t at = (int64_t)(b - a.tiles[0] - a.tiles[1]) * ZERO_FLOATS + threadIdx.x * 4;
-        const int64_t size[2] = {(int64_t)a.rows[0] * a.cols[0], (int64_t)a.rows[1] * a.cols[1]};
-        for (int i = 0; i < ZERO_FLOATS / 1024; ++i, at += 1024) {
-            if (at < size[0])
-                store4(a.grad[0] + e * size[0] + at, vf4{0.f, 0.f, 0.f, 0.f});
-            else if (at < size[0] + size[1])
-                store4(a.grad[1] + e * size[1] + at - size[0], vf4{0.f, 0.f, 0.f, 0.f});
+        const int e = (int)((b - a.panels) / per), t = (int)((b - a.panels) % per);
+        const bool empty = a.plan.offsets[e + 1] <= a.plan.offsets[e];
+        if (t < transposes) {
+            const int job = t >= a.tiles[0];
+            if (!empty)
+                transpose_tile<T>(a, job, e, t - (job ? a.tiles[0] : 0),
+                                  reinterpret_cast<T(*)[64 + 16 / sizeof(T)]>(lds));
+        } else if (empty) {
+            int64_t at = (int64_t)(t - transposes) * ZERO_FLOATS + threadIdx.x * 4;
+            const int64_t size[2] = {(int64_t)a.rows[0] * a.cols[0], (int64_t)a.rows[1] * a.cols[1]};
+            for (int i = 0; i < ZERO_FLOATS / 1024; ++i, at += 1024) {
+                if (at < size[0])
+                    store4(a.grad[0] + e * size[0] + at, vf4{0.f, 0.f, 0.f, 0.f});
+                else if (at < size[0] + size[1])
+                    store4(a.grad[1] + e * size[1] + at - size[0], vf4{0.f, 0.f, 0.f, 0.f});
+            }
         }
-        return;
     }
-    if (empty) return;
-    const int job = b >= a.tiles[0];
-    transpose_tile<T>(a, job, e, b - (job ? a.tiles[0] : 0), reinterpret_cast<T(*)[64 + 16 / sizeof(T)]>(lds));
 }
 
 // The panel of ds, from the splits' partials.
@@ -135,9 +137,13 @@ __global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_dy_kernel(AdaptShr
         GradBlock<TX, RT>::run(gr, 1, b, lds);
 }
 
+// Two workgroups to a CU where that needs no spill.
+template <typename TX, int RT, bool ACC>
+constexpr int dx_per_cu = RT <= (__is_same(TX, _Float16) && ACC ? 2 : 4) ? 2 : 1;
+
 template <typename TX, typename TW, int RT, bool ACC>
-__global__ __launch_bounds__(256, RT <= (__is_same(TX, _Float16) && ACC ? 2 : 4) ? 2 : 1) void adapt_dx_kernel(AdaptExpand ex, AdaptGrad gr, int chunks,
-                                                                         int expands, int grads) {
+__global__ __launch_bounds__(256, (dx_per_cu<TX, RT, ACC>)) void adapt_dx_kernel(AdaptExpand ex, AdaptGrad gr,
+                                                                                int chunks, int expands, int grads) {
     constexpr int A = ExpandBlock<TX, TW, RT, ACC>::BYTES, B = GradBlock<TX, RT>::BYTES;
     __shared__ __align__(16) char lds[A > B ? A : B];
     int b;
@@ -191,7 +197,8 @@ hipError_t prepare_t(AdaptPrepare a, hipStream_t s) {
     const int64_t floats = (int64_t)a.rows[0] * a.cols[0] + (int64_t)a.rows[1] * a.cols[1];
     a.zeros = a.grad[0] ? (int)((floats + ZERO_FLOATS - 1) / ZERO_FLOATS) : 0;
     a.panels = a.tape ? (int)adapt_tiles(a.plan.M, a.plan.E, TM) : 0;
-    const int64_t blocks = a.panels + (int64_t)a.plan.E * (a.tiles[0] + a.tiles[1] + a.zeros);
+    int64_t blocks = a.panels + (int64_t)a.plan.E * (a.tiles[0] + a.tiles[1] + a.zeros);
+    if (blocks > ((int64_t)1 << 22)) blocks = (int64_t)1 << 22;  // the kernel steps on by the grid
     hipLaunchKernelGGL((adapt_prepare_kernel<TX, TW, RT>), dim3((unsigned)blocks), dim3(256), 0, s, a);
     return hipGetLastError();
 }

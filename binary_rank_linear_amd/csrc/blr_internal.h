@@ -273,7 +273,7 @@ struct AdaptPrepare {
     void *panel;
     float *grad[2];
     int r, act, wt;
-    int tiles[2], zeros, panels;  // workgroups of each kind; filled by the launcher
+    int tiles[2], zeros, panels;  // pieces of each kind of work; filled by the launcher
 };
 constexpr int64_t adapt_r16(int64_t r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 constexpr int64_t adapt_panel_bytes(int64_t r, int act) { return adapt_r16(r) * 64 * (act == 0 ? 4 : 6); }

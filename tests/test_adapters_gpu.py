@@ -270,6 +270,56 @@ def test_rows_past_32_bit_offsets(dev):
 
 
 @pytest.mark.gpu
+def test_long_ranges(dev):
+    """Rows enough for several ranges of the greatest length (4096) in the
+    gradients; their sums against 64 bits on the GPU, in runs of columns."""
+    import torch
+    say("adapters gradients of 9000 rows of 131072")
+    M, d_in, d_out, r = 9000, 128, 131072, 8
+    torch.manual_seed(1)
+    ids = torch.zeros(M, dtype=torch.int32, device=dev)
+    ids[::9] = -1
+    offsets, order, _ = blr.blr_route_sort(ids, 1)
+    x = torch.randn((M, d_in), device=dev).to(torch.bfloat16)
+    dy = torch.randn((M, d_out), device=dev).to(torch.bfloat16)
+    down = torch.randn((1, r, d_in), device=dev).to(torch.bfloat16)
+    up = (torch.randn((1, d_out, r), device=dev) / 256).to(torch.bfloat16)
+    tape = torch.randn((M, r), device=dev)
+    gd, gu, dx = blr.blr_adapters_backward(x, dy, down, up, offsets, order, None, tape)
+    on = ids >= 0
+    s, ds = tape[on].double(), torch.zeros((int(on.sum()), r), dtype=torch.float64, device=dev)
+    dm = torch.zeros_like(ds)
+    for c in range(0, d_out, 16384):
+        part, w = dy[on, c:c + 16384].double(), up[0, c:c + 16384].double()
+        ref.within(host(gu[0, c:c + 16384].double()), host(part.T @ s), host(part.abs().T @ s.abs()), M)
+        ds += part @ w
+        dm += part.abs() @ w.abs()
+    xs = x[on].double()
+    ref.within(num(gd[0]), host(ds.T @ xs), host(dm.T @ xs.abs()), d_out + M)
+    ref.within(num(dx[on]), host(ds @ down[0].double()), host(dm @ down[0].double().abs()), d_out + r, "bfloat16")
+    assert not dx[~on].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cnt", [1, 15, 16, 17, 63, 64, 65, 128, 511, 512, 513, 1025])
+@pytest.mark.parametrize("act", ["float32", "float16", "bfloat16"])
+def test_row_counts_at_tile_edges(dev, cnt, act):
+    """One adapter with a number of rows on each side of the kernels' tiles and
+    ranges, beside others with one row and none."""
+    say(f"adapters with {cnt} rows of one adapter, {act}")
+    M, E = cnt + 5, 4
+    v = make(dev, M, 128, 256, 16, E, act, act, "none", seed=cnt)
+    import torch
+    ids = np.full(M, 2, np.int32)
+    ids[[0, M - 1]] = 0
+    ids[[1, 2, M // 2 + 1]] = -1
+    v["ids"] = ids
+    v["offsets"], v["order"], _ = blr.blr_route_sort(torch.from_numpy(ids).to(dev), E)
+    check_forward(v, act, acc=True)
+    check_backward(v, act, acc=False)
+
+
+@pytest.mark.gpu
 def test_plans_out_of_order_do_no_harm(dev):
     """Offsets that do not ascend or point outside, and rows outside [0, M):
     refused by nothing on the host, and the kernels' own limits keep every
