@@ -123,8 +123,12 @@ __device__ __forceinline__ int64_t row_of(const AdaptPlan &plan, int p) {
 }
 
 // Matrix instructions on 16-bit operands.
-__device__ __forceinline__ vf4 mfma8(vh8 a, vh8 b, vf4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
-__device__ __forceinline__ vf4 mfma8(vb8 a, vb8 b, vf4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ vf4 mfma8(vh8 a, vh8 b, vf4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ vf4 mfma8(vb8 a, vb8 b, vf4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
 
 // Walks a wave's n steps with two register sets (DEEP): the next step's loads
 // are in flight while one is used. The walk has no branch around a load (a
@@ -540,7 +544,8 @@ __device__ __forceinline__ float power_of(float top, bool itself) {
 // near one: each row enters divided by the power of two at its largest
 // element, and the result is multiplied back (both exact).
 template <typename T>
-__device__ __forceinline__ void two_terms(const float *s, float largest, typename Vec<T>::v &hi, typename Vec<T>::v &lo) {
+__device__ __forceinline__ void two_terms(const float *s, float largest, typename Vec<T>::v &hi,
+                                          typename Vec<T>::v &lo) {
     const float by = __is_same(T, _Float16) ? power_of(largest, false) : 1.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -841,7 +846,8 @@ __device__ void expand_tile_lds(const AdaptExpand &a, ExpandRows<TX, TW, RT, ACC
                 f *= back[i];
                 if (ACC) f += __builtin_convertvector(old[i], F);
             }
-            if (FULL || rows.in[i]) *reinterpret_cast<V *>(rows.row[i] + step * L::COLS) = __builtin_convertvector(f, V);
+            if (FULL || rows.in[i])
+                *reinterpret_cast<V *>(rows.row[i] + step * L::COLS) = __builtin_convertvector(f, V);
         }
         __builtin_amdgcn_sched_barrier(0);
         take((step + 1 - from) & 1);
@@ -1000,9 +1006,11 @@ struct GradStep16 {
             if constexpr (__is_same(T, __bf16)) {
                 vu4 pairs;  // element u of two rows each
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    pairs[j] = __builtin_amdgcn_perm(u < 2 ? x[2 * j + 1].x : x[2 * j + 1].y,
-                                                     u < 2 ? x[2 * j].x : x[2 * j].y, u & 1 ? 0x07060302u : 0x05040100u);
+                for (int j = 0; j < 4; ++j) {
+                    const uint2 even = x[2 * j], odd = x[2 * j + 1];
+                    pairs[j] = __builtin_amdgcn_perm(u < 2 ? odd.x : odd.y, u < 2 ? even.x : even.y,
+                                                     u & 1 ? 0x07060302u : 0x05040100u);
+                }
                 hi[u] = __builtin_bit_cast(vb8, pairs);
             } else {
 #pragma unroll

@@ -61,10 +61,16 @@ int64_t adapt_chunks(int64_t M, int64_t E, int64_t N) {
     return chunks > 8 ? chunks / 8 * 8 : chunks;  // a range of columns then stays on one XCD
 }
 
+// Enough ranges to fill the chip, but none so short that its partial (r floats
+// a column, written and read again) costs much beside its rows. 8192 rows of
+// rank 16 over 4096 + 4096 columns in eight adapters: both gradients' launches
+// and the reduction take 133 us with 256 rows a range, 140 with 512, 169 with
+// 1024. Up to 512 rows a second range never pays for the reduction's launch
+// (6 us of 36).
 int64_t adapt_range(int64_t M, int64_t d_in, int64_t d_out, int64_t r) {
     const int64_t cols = (d_in + 255) / 256 + (d_out + 255) / 256;
-    int64_t range = M * cols / (FILL / 2);
-    const int64_t least = 8 * r > 512 ? 8 * r : 512;  // a partial costs as much as 2 r rows
+    int64_t range = M * cols / FILL;
+    const int64_t least = M <= 512 ? M : 8 * r > 256 ? 8 * r : 256;
     range = range < least ? least : range;
     range = range < ADAPT_MAX_RANGE ? range : ADAPT_MAX_RANGE;
     range = range < M ? range : M;

@@ -240,7 +240,8 @@ __global__ __launch_bounds__(256) void route_combine_backward_kernel(RouteRows a
                     for (int o = 32; o > 0; o /= 2) dot[j] += __shfl_xor(dot[j], o);
                 if (W == 1) {
                     if (lane < 4 && j0 + lane < a.k)
-                        a.dw[t * a.k + j0 + lane] = lane == 0 ? dot[0] : lane == 1 ? dot[1] : lane == 2 ? dot[2] : dot[3];
+                        a.dw[t * a.k + j0 + lane] =
+                            lane == 0 ? dot[0] : lane == 1 ? dot[1] : lane == 2 ? dot[2] : dot[3];
                 } else {
                     __syncthreads();  // the last four's sums have been read
                     if (lane == 0) {

@@ -301,7 +301,7 @@ def test_long_ranges(dev):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("cnt", [1, 15, 16, 17, 63, 64, 65, 128, 511, 512, 513, 1025])
+@pytest.mark.parametrize("cnt", [1, 15, 16, 17, 63, 64, 65, 128, 507, 508, 512, 513, 769])
 @pytest.mark.parametrize("act", ["float32", "float16", "bfloat16"])
 def test_row_counts_at_tile_edges(dev, cnt, act):
     """One adapter with a number of rows on each side of the kernels' tiles and
