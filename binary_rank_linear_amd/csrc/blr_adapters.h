@@ -264,7 +264,10 @@ __device__ void shrink_tile(const AdaptShrink &a, const Tile &tile, int from, in
 // loads above. So eight lanes read 128 bytes of a row, and a wave turns its
 // step of X and of the weights round through 16-byte slots of its own (slot
 // h of row m stands at h ^ (m & 7), which spreads both sides over the banks);
-// no barrier, since no other wave reads them.
+// no barrier, since no other wave reads them. 28500 rows of 17408 bf16, rank
+// 64: 237 us (4.2 TB/s, what reads alone reach here) against 288 by the loads
+// above; 8192 of 4096 f32, rank 16: 41 against 44. Tiles of up to 16 rows keep
+// the loads above: their 64 would be mostly repeats.
 template <typename TX, typename TW, int RT>
 struct ShrinkLds {
     static constexpr int COLS = 128 / sizeof(TX);
@@ -656,7 +659,9 @@ __device__ void expand_tile(const AdaptExpand &a, const Tile &tile, int from, in
 // lane (q, c) ends with 16 consecutive bytes of each of rows 4 q .. 4 q + 3,
 // 256 bytes of a row in 16 lanes. The step's weights, which lie together, are
 // brought into operand order through LDS once for the four waves, in two
-// buffers, one barrier a step.
+// buffers, one barrier a step. 7400 rows of 12288 f32, rank 64, added to y: 198
+// us, of which the f32 matrix instructions are busy 83 and HBM 150; 295 by the
+// loads above.
 //
 // Operand slots of 16 bytes: [tile h][group of ranks][lane], the 16 lanes c of a
 // q at c ^ (4 q + v) with v counting the pieces of four slots in the order they
@@ -1054,7 +1059,10 @@ struct GradStep<__bf16, RT> : GradStep16<__bf16, RT> {};
 // rows x 256 columns, wave w 64 of them. A panel of 64 rows is up to three
 // times as many bytes as the 64 columns it meets, so the four waves share it
 // through LDS (in two buffers, one barrier a panel); the next panel and one
-// or three steps' rows are in flight while a step is multiplied.
+// or three steps' rows are in flight while a step is multiplied. Both gradients
+// of 28500 rows of 22528 columns in all, bf16, rank 64, took 360 us in a launch
+// of their own (3.6 TB/s), 520 with panels read by each wave for itself and 3800
+// on f32 instructions.
 template <typename TX, int RT>
 struct GradBlock {
     typedef GradStep<TX, RT> Step;

@@ -4,6 +4,9 @@
 //   dy   ds = c dy B and dB, which both read dy: their workgroups take the rows
 //        in the same order, so the second read finds dy in the last-level cache
 //   dx   dx = ds A, which writes, and dA, which reads x
+//
+// 8192 x 4096 -> 4096 f32, rank 16: 55 + 62 us; 30000 x 5120 -> 17408 bf16, rank
+// 64: 466 + 200 us. Reads bound the first: dy passes twice, at 4.3 TB/s.
 #include "blr_adapters.h"
 
 namespace blr {

@@ -10,7 +10,12 @@
 //            dw[t][j] = dy[t] . z[slot[t][j]] (zero if not placed)
 //
 // All three row kernels go token by token, so that x, y and dy cross HBM
-// once and only the experts' rows are addressed through slot.
+// once and only the experts' rows are addressed through slot. They are copies
+// with a little arithmetic, bound by HBM, where a 2 GiB device copy moves 4.9
+// TB/s: 8192 tokens to 8 of 128 experts, rows of 8 KB, take 118 us in the gather
+// (5.1 TB/s); 30000 back from 4 choices, rows of 10 KB, 302 us in the combine
+// (5.1 TB/s); 8192 with 8 choices, rows of 16 KB, 480 us in the backward (4.8
+// TB/s).
 #include "blr_internal.h"
 #include "blr_vec.h"
 
@@ -21,7 +26,8 @@ namespace {
 constexpr int SORT_WAVES = 16;
 constexpr int SORT_THREADS = 64 * SORT_WAVES;
 // Pairs that one workgroup places alone: a second workgroup needs the first's
-// counts, hence a launch before.
+// counts, hence a launch before. Both orders of size are bound by latency: one
+// launch of 64 pairs takes 4 us, two of 65536 over 128 experts 4 and 9 us.
 constexpr int64_t SORT_ONE = 8192;
 constexpr int64_t SORT_RANGE_MIN = 4096;
 constexpr int64_t SORT_RANGES_MAX = 256;
@@ -189,8 +195,8 @@ __global__ __launch_bounds__(256) void route_combine_kernel(RouteRows a, int64_t
     }
 }
 
-// W waves walk a token's row together (W = 1: four tokens a workgroup). Four
-// choices at a time: their rows are in flight together, and dy's row is read
+// W waves walk a token's row together (W = 1: four tokens a workgroup, for rows
+// of up to 4 KB). Four choices at a time: their rows are in flight together, and dy's row is read
 // once per four.
 template <typename T, int W>
 __global__ __launch_bounds__(256) void route_combine_backward_kernel(RouteRows a, int64_t nv) {

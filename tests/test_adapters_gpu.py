@@ -301,6 +301,25 @@ def test_long_ranges(dev):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act,wt", [("float32", "bfloat16"), ("bfloat16", "bfloat16")])
+def test_many_adapters_with_several_ranges(dev, act, wt):
+    """Adapters of several ranges on both sides of the 64th, in shuffled rows,
+    among many of a few rows or none."""
+    import torch
+    say(f"adapters: 200 of them, three with several ranges, {act}/{wt}")
+    M, E = 2500, 200
+    v = make(dev, M, 128, 256, 24, E, act, wt, "none")
+    rng = np.random.default_rng(3)
+    ids = rng.permutation(np.concatenate([np.full(900, 3), np.full(700, 70), np.full(600, 150),
+                                          rng.integers(-20, E, 300)]))
+    v["ids"] = np.where(ids < 0, -1, ids).astype(np.int32)
+    v["offsets"], v["order"], _ = blr.blr_route_sort(torch.from_numpy(v["ids"]).to(dev), E)
+    check_forward(v, act, acc=True)
+    check_backward(v, act, acc=True)
+    check_backward(v, act, acc=False)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("cnt", [1, 15, 16, 17, 63, 64, 65, 128, 507, 508, 512, 513, 769])
 @pytest.mark.parametrize("act", ["float32", "float16", "bfloat16"])
 def test_row_counts_at_tile_edges(dev, cnt, act):
