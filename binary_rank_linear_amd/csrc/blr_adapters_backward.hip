@@ -108,7 +108,7 @@ __global__ __launch_bounds__(256) void adapt_thin_kernel(AdaptThin a) {
     for (int i = threadIdx.x; i < TM * RT * 4; i += 256) {
         const int m = i / (RT * 4), k = i % (RT * 4) * 4;
         vf4 v = {0.f, 0.f, 0.f, 0.f};
-        if (m < tile.cnt && k < a.r) {  // r is a multiple of 8
+        if (m < tile.cnt && k < a.r && row_of(a.plan, tile.p0 + m) >= 0) {  // r is a multiple of 8
             const float *part = a.part + (int64_t)(tile.p0 + m) * a.r + k;
 #pragma unroll 8
             for (int sp = 0; sp < a.splits; ++sp) v += load4(part + sp * next);

@@ -371,6 +371,46 @@ def test_plans_out_of_order_do_no_harm(dev):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act", ["float32", "bfloat16"])
+def test_positions_without_a_row_add_nothing(dev, act):
+    """A plan's position whose row is outside [0, M) is left out of every
+    gradient, whatever the rows that the plan does name hold."""
+    import torch
+    say(f"adapters, positions without a row, {act}")
+    M, d_in, d_out, r, E = 150, 256, 128, 16, 3
+    v = make(dev, M, d_in, d_out, r, E, act, act, "tokens")
+    v["ids"][0] = 0  # row 0 is another adapter's than the positions that lose theirs
+    offsets, order, _ = blr.blr_route_sort(torch.from_numpy(v["ids"]).to(dev), E)
+    first, end = int(offsets[1]), int(offsets[3])
+    assert end - first > 4
+    lost = [first, first + 3, end - 1]
+    rows = order[lost].long()
+    order[lost] = torch.tensor([-1, M, 2 ** 31 - 1], dtype=torch.int32, device=dev)
+    tape = torch.randn((M, r), device=dev)
+
+    def run():
+        y, _ = blr.blr_adapters_forward(v["x"], v["down"], v["up"], offsets, order, v["scale"],
+                                        y=torch.full((M, d_out), 7.0, dtype=v["x"].dtype, device=dev))
+        return (y,) + blr.blr_adapters_backward(v["x"], v["dy"], v["down"], v["up"], offsets, order, v["scale"], tape,
+                                                dx=torch.full_like(v["x"], 7.0))
+
+    y, gd, gu, dx = run()
+    assert (y[rows] == 7).all() and (dx[rows] == 7).all()  # a row that no position names is not written
+    kept = v["ids"].copy()
+    kept[rows.cpu().numpy()] = -1
+    want, mag = ref.adapters_backward(num(v["x"]), num(v["dy"]), num(v["down"]), num(v["up"]), kept, num(v["scale"]),
+                                      num(tape))
+    ref.within(num(gd), want[0], mag[0], d_out + M + 4)
+    ref.within(num(gu), want[1], mag[1], M + 4)
+    v["x"][0] = float("nan")
+    v["dy"][0] = float("inf")
+    tape[0] = float("nan")
+    y2, gd2, gu2, dx2 = run()
+    assert torch.equal(gd2[1:], gd[1:]) and torch.equal(gu2[1:], gu[1:])
+    assert torch.equal(y2[1:], y[1:]) and torch.equal(dx2[1:], dx[1:])
+
+
+@pytest.mark.gpu
 def test_reruns_streams_and_graphs(dev):
     """The same bits on a rerun, on another stream, and from two captured
     graphs (each with a workspace of its own) replayed in turn on new inputs
