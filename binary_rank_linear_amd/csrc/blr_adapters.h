@@ -33,6 +33,7 @@ namespace blr {
 namespace {
 
 constexpr int TM = ADAPT_TM;
+typedef uint32_t vu2 __attribute__((ext_vector_type(2)));
 typedef uint32_t vu4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ vf4 mfma4(float a, float b, vf4 c) {
@@ -47,6 +48,13 @@ __device__ __forceinline__ int wave() { return __builtin_amdgcn_readfirstlane((i
 template <typename T>
 __device__ __forceinline__ const T *ahead(const T *base, unsigned bytes) {
     return reinterpret_cast<const T *>(reinterpret_cast<const char *>(base) + bytes);
+}
+
+// A vector V from p; ONCE: by a load that asks not to be kept in the caches.
+template <bool ONCE, typename V, typename T>
+__device__ __forceinline__ V fetch(const T *p) {
+    const V *v = reinterpret_cast<const V *>(p);
+    return ONCE ? __builtin_nontemporal_load(v) : *v;
 }
 
 // A tile of one group of the plan; group E is the rows without an adapter.
@@ -278,9 +286,10 @@ struct ShrinkLds {
     static constexpr int BYTES = X_BYTES + W_BYTES;
     vu4 x[8], w[W_LOADS];
 
+    template <bool ONCE>
     __device__ __forceinline__ void load(const TX *const *row, const TW *W, const unsigned *rank, int k0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const vu4 *>(row[i] + k0);
+        for (int i = 0; i < 8; ++i) x[i] = fetch<ONCE, vu4>(row[i] + k0);
 #pragma unroll
         for (int i = 0; i < W_LOADS; ++i) w[i] = *reinterpret_cast<const vu4 *>(ahead(W + k0, rank[i]));
     }
@@ -343,7 +352,7 @@ __device__ __forceinline__ void wave_lds_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-template <typename TX, typename TW, int RT>
+template <typename TX, typename TW, int RT, bool ONCE>
 __device__ void shrink_tile_lds(const AdaptShrink &a, const Tile &tile, int from, int to, char *lds,
                                 float (*red)[RT * 16 + 1]) {
     typedef ShrinkLds<TX, TW, RT> Step;
@@ -374,11 +383,12 @@ __device__ void shrink_tile_lds(const AdaptShrink &a, const Tile &tile, int from
     const int first = from + w, n = (to - first + 3) / 4;
     if (n > 0) {
         Step st;
-        st.load(x, W, rank, first * Step::COLS);
+        st.template load<ONCE>(x, W, rank, first * Step::COLS);
         for (int i = 0; i < n; ++i) {
             st.stage(mine, lane);
             wave_lds_fence();
-            st.load(x, W, rank, (first + 4 * (i + 1 < n ? i + 1 : i)) * Step::COLS);  // no branch: see walk
+            const int next = i + 1 < n ? i + 1 : i;  // no branch: see walk
+            st.template load<ONCE>(x, W, rank, (first + 4 * next) * Step::COLS);
             __builtin_amdgcn_sched_barrier(0);
             Step::multiply(mine, acc, q, c);
             wave_lds_fence();
@@ -409,6 +419,7 @@ struct ShrinkBlock {
     typedef ShrinkLds<TX, TW, RT> Lds;
     static constexpr int BYTES = 4 * Lds::BYTES;
 
+    template <bool ONCE>
     static __device__ void run(const AdaptShrink &a, int block, char *lds) {
         float(*red)[RT * 16 + 1] = reinterpret_cast<float(*)[RT * 16 + 1]>(lds);
         static_assert(sizeof(float) * TM * (RT * 16 + 1) <= BYTES, "the sums fit");
@@ -420,7 +431,7 @@ struct ShrinkBlock {
         if (tile.cnt <= 16)
             shrink_tile<TX, TW, RT>(a, tile, from, to, red);
         else
-            shrink_tile_lds<TX, TW, RT>(a, tile, from, to, lds, red);
+            shrink_tile_lds<TX, TW, RT, ONCE>(a, tile, from, to, lds, red);
         float *part = a.part + ((int64_t)split * a.plan.M + tile.p0) * a.r;
         const int per = a.r / 4;
         for (int i = threadIdx.x; i < tile.cnt * per; i += 256) {
@@ -960,12 +971,14 @@ struct GradStep {
     static constexpr int SLOTS = RT * 64;  // of a step's panel
     vf4 x[4];
 
+    template <bool ONCE>
     __device__ __forceinline__ void load(const TX *X, int N, const int *row, int q, int c) {
         const int4 at = *reinterpret_cast<const int4 *>(row + 4 * q);
         const int r[4] = {at.x, at.y, at.z, at.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            x[j] = load4((r[j] < 0 ? reinterpret_cast<const TX *>(zero_row) : X + (int64_t)r[j] * N) + 4 * c);
+            x[j] =
+                fetch<ONCE, vf4>((r[j] < 0 ? reinterpret_cast<const TX *>(zero_row) : X + (int64_t)r[j] * N) + 4 * c);
     }
     __device__ __forceinline__ void multiply(const vu4 *panel, vf4 (&acc)[4][RT], int lane) const {
         vf4 t[RT];
@@ -990,16 +1003,16 @@ template <typename T, int RT>
 struct GradStep16 {
     static constexpr int ROWS = 32;
     static constexpr int SLOTS = 3 * RT * 64;
-    uint2 x[8];  // four elements
+    vu2 x[8];  // four elements
 
+    template <bool ONCE>
     __device__ __forceinline__ void load(const T *X, int N, const int *row, int q, int c) {
         const int4 a = *reinterpret_cast<const int4 *>(row + 8 * q);
         const int4 b = *reinterpret_cast<const int4 *>(row + 8 * q + 4);
         const int r[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            x[j] = *reinterpret_cast<const uint2 *>(
-                (r[j] < 0 ? reinterpret_cast<const T *>(zero_row) : X + (int64_t)r[j] * N) + 4 * c);
+            x[j] = fetch<ONCE, vu2>((r[j] < 0 ? reinterpret_cast<const T *>(zero_row) : X + (int64_t)r[j] * N) + 4 * c);
     }
     __device__ __forceinline__ void multiply(const vu4 *panel, vf4 (&acc)[4][RT], int lane) const {
         vb8 hi[4], lo[4];
@@ -1012,7 +1025,7 @@ struct GradStep16 {
                 vu4 pairs;  // element u of two rows each
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint2 even = x[2 * j], odd = x[2 * j + 1];
+                    const vu2 even = x[2 * j], odd = x[2 * j + 1];
                     pairs[j] = __builtin_amdgcn_perm(u < 2 ? odd.x : odd.y, u < 2 ? even.x : even.y,
                                                      u & 1 ? 0x07060302u : 0x05040100u);
                 }
@@ -1071,6 +1084,7 @@ struct GradBlock {
     static_assert(4 % STEPS == 0 && 4 % SETS == 0, "the sets go round with the panels");
     static constexpr int BYTES = 4 * ADAPT_MAX_RANGE + 2 * 16 * SLOTS;
 
+    template <bool ONCE>
     static __device__ void run(const AdaptGrad &a, int which, int block, char *shared) {
         int *row = reinterpret_cast<int *>(shared);
         vu4(*lds)[SLOTS] = reinterpret_cast<vu4(*)[SLOTS]>(shared + 4 * ADAPT_MAX_RANGE);
@@ -1108,7 +1122,7 @@ struct GradBlock {
         const int steps = panels * STEPS;
         Step set[SETS];
         auto load_rows = [&](Step &st, int step) {
-            st.load(X, N, row + (step < steps ? step : steps - 1) * Step::ROWS, q, c);
+            st.template load<ONCE>(X, N, row + (step < steps ? step : steps - 1) * Step::ROWS, q, c);
         };
 #pragma unroll
         for (int i = 0; i < SETS - 1; ++i) load_rows(set[i], i);

@@ -12,7 +12,7 @@ constexpr int64_t FILL = 1024;
 template <typename TX, typename TW, int RT>
 __global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_shrink_kernel(AdaptShrink a) {
     __shared__ __align__(16) char lds[ShrinkBlock<TX, TW, RT>::BYTES];
-    ShrinkBlock<TX, TW, RT>::run(a, blockIdx.x, lds);
+    ShrinkBlock<TX, TW, RT>::template run<false>(a, blockIdx.x, lds);
 }
 
 template <typename TX, typename TW, int RT, bool ACC>

@@ -2,11 +2,13 @@
 // large launches pairs a contraction with the gradient beside it:
 //
 //   dy   ds = c dy B and dB, which both read dy: their workgroups take the rows
-//        in the same order, so the second read finds dy in the last-level cache
-//   dx   dx = ds A, which writes, and dA, which reads x
+//        in the same order, so that of a small dy the second read finds the
+//        last-level cache
+//   dx   dx = ds A, which writes, and dA, whose read of x is the last
 //
-// 8192 x 4096 -> 4096 f32, rank 16: 55 + 62 us; 30000 x 5120 -> 17408 bf16, rank
-// 64: 466 + 200 us. Reads bound the first: dy passes twice, at 4.3 TB/s.
+// 8192 x 4096 -> 4096 f32, rank 16: 58 + 64 us; 30000 x 5120 -> 17408 bf16, rank
+// 64: 425 + 196 us. Reads bound the first: dy passes twice, with the weights of
+// every tile of 64 rows 2.7 GB of reads, 2 GB of them dy.
 #include "blr_adapters.h"
 
 namespace blr {
@@ -120,24 +122,35 @@ __global__ __launch_bounds__(256) void adapt_thin_kernel(AdaptThin a) {
     write_panel<TX, RT>(a.panel, blockIdx.x, S);
 }
 
-// Which of two kinds of work workgroup b does, `one` workgroups of the first
-// kind spread evenly among `two` of the second, and its number in its kind.
-__device__ __forceinline__ bool is_first(int64_t b, int64_t one, int64_t two, int *number) {
-    const int64_t before = b * one / (one + two), upto = (b + 1) * one / (one + two);
-    *number = (int)(upto > before ? before : b - before);
+// The two kinds of work of a launch, `one` workgroups of the first kind spread
+// evenly among `two` of the second, eight of a kind at a time: one on each XCD
+// (single ones left an XCD more of one kind than of the other: 468 us of the
+// dy launch above, 451 in eights).
+struct Mix {
+    int one, two;
+};
+
+// Which kind workgroup b does, and its number in that kind; it does nothing
+// where that is past the kind's count.
+__device__ __forceinline__ bool is_first(const Mix &m, unsigned b, int *number) {
+    const int64_t one = (m.one + 7) / 8, two = (m.two + 7) / 8, g = b / 8;
+    const int64_t before = g * one / (one + two), upto = (g + 1) * one / (one + two);
+    *number = (int)((upto > before ? before : g - before) * 8 + b % 8);
     return upto > before;
 }
 
 template <typename TX, typename TW, int RT>
-__global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_dy_kernel(AdaptShrink sh, AdaptGrad gr, int shrinks,
-                                                                         int grads) {
+__global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_dy_kernel(AdaptShrink sh, AdaptGrad gr, Mix mix) {
     constexpr int A = ShrinkBlock<TX, TW, RT>::BYTES, B = GradBlock<TX, RT>::BYTES;
     __shared__ __align__(16) char lds[A > B ? A : B];
     int b;
-    if (is_first(blockIdx.x, shrinks, grads, &b))
-        ShrinkBlock<TX, TW, RT>::run(sh, b, lds);
+    const bool first = is_first(mix, blockIdx.x, &b);
+    if (b >= (first ? mix.one : mix.two)) return;
+    if (first)
+        sh.once ? ShrinkBlock<TX, TW, RT>::template run<true>(sh, b, lds)
+                : ShrinkBlock<TX, TW, RT>::template run<false>(sh, b, lds);
     else
-        GradBlock<TX, RT>::run(gr, 1, b, lds);
+        GradBlock<TX, RT>::template run<false>(gr, 1, b, lds);
 }
 
 // Two workgroups to a CU where that needs no spill.
@@ -146,14 +159,16 @@ constexpr int dx_per_cu = RT <= (__is_same(TX, _Float16) && ACC ? 2 : 4) ? 2 : 1
 
 template <typename TX, typename TW, int RT, bool ACC>
 __global__ __launch_bounds__(256, (dx_per_cu<TX, RT, ACC>)) void adapt_dx_kernel(AdaptExpand ex, AdaptGrad gr,
-                                                                                int chunks, int expands, int grads) {
+                                                                                int chunks, Mix mix) {
     constexpr int A = ExpandBlock<TX, TW, RT, ACC>::BYTES, B = GradBlock<TX, RT>::BYTES;
     __shared__ __align__(16) char lds[A > B ? A : B];
     int b;
-    if (is_first(blockIdx.x, expands, grads, &b))
+    const bool first = is_first(mix, blockIdx.x, &b);
+    if (b >= (first ? mix.one : mix.two)) return;
+    if (first)
         ExpandBlock<TX, TW, RT, ACC>::run(ex, chunks, b, lds);
     else
-        GradBlock<TX, RT>::run(gr, 0, b, lds);
+        GradBlock<TX, RT>::template run<true>(gr, 0, b, lds);
 }
 
 // The partials of an adapter of several ranges, added in range order.
@@ -217,25 +232,34 @@ int64_t grad_blocks(const AdaptGrad &a, int which) {
     return adapt_tiles(a.plan.M, a.plan.E, a.range) * ((a.job[which].N + 255) / 256);
 }
 
+unsigned mix_blocks(const Mix &m) { return (unsigned)(8 * ((m.one + 7) / 8 + (m.two + 7) / 8)); }
+
+// dy that the last-level cache (256 MB) cannot hold is read by ds with loads
+// that ask not to be kept, which leaves the caches to the weights and panels:
+// 30000 rows of 17408 bf16 (1 GB) 425 us, 451 with ordinary loads. Smaller dy is
+// still there when the gradient reads it: 8192 rows of 4096 f32 (134 MB) 58 us,
+// 66 if not kept.
+constexpr int64_t CACHE_BYTES = (int64_t)256 << 20;
+
 template <typename TX, typename TW, int RT>
-hipError_t dy_t(const AdaptShrink &sh, const AdaptGrad &gr, hipStream_t s) {
-    const int64_t shrinks = sh.splits * adapt_tiles(sh.plan.M, sh.plan.E, TM), grads = grad_blocks(gr, 1);
-    hipLaunchKernelGGL((adapt_dy_kernel<TX, TW, RT>), dim3((unsigned)(shrinks + grads)), dim3(256), 0, s, sh, gr,
-                       (int)shrinks, (int)grads);
+hipError_t dy_t(AdaptShrink sh, const AdaptGrad &gr, hipStream_t s) {
+    sh.once = (int64_t)sh.plan.M * sh.K * (int64_t)sizeof(TX) > CACHE_BYTES;
+    const Mix mix = {(int)(sh.splits * adapt_tiles(sh.plan.M, sh.plan.E, TM)), (int)grad_blocks(gr, 1)};
+    hipLaunchKernelGGL((adapt_dy_kernel<TX, TW, RT>), dim3(mix_blocks(mix)), dim3(256), 0, s, sh, gr, mix);
     return hipGetLastError();
 }
 
 template <typename TX, typename TW, int RT>
 hipError_t dx_t(const AdaptExpand &ex, const AdaptGrad &gr, hipStream_t s) {
-    const int64_t chunks = adapt_chunks(ex.plan.M, ex.plan.E, ex.N), grads = grad_blocks(gr, 0);
+    const int64_t chunks = adapt_chunks(ex.plan.M, ex.plan.E, ex.N);
     const int64_t expands = ex.out ? chunks * adapt_tiles(ex.plan.M, ex.plan.E, TM) : 0;
-    const dim3 grid((unsigned)(expands + grads));
+    const Mix mix = {(int)expands, (int)grad_blocks(gr, 0)};
     if (ex.acc)
-        hipLaunchKernelGGL((adapt_dx_kernel<TX, TW, RT, true>), grid, dim3(256), 0, s, ex, gr, (int)chunks,
-                           (int)expands, (int)grads);
+        hipLaunchKernelGGL((adapt_dx_kernel<TX, TW, RT, true>), dim3(mix_blocks(mix)), dim3(256), 0, s, ex, gr,
+                           (int)chunks, mix);
     else
-        hipLaunchKernelGGL((adapt_dx_kernel<TX, TW, RT, false>), grid, dim3(256), 0, s, ex, gr, (int)chunks,
-                           (int)expands, (int)grads);
+        hipLaunchKernelGGL((adapt_dx_kernel<TX, TW, RT, false>), dim3(mix_blocks(mix)), dim3(256), 0, s, ex, gr,
+                           (int)chunks, mix);
     return hipGetLastError();
 }
 

@@ -239,6 +239,7 @@ struct AdaptShrink {
     const void *X, *W;
     float *part;
     int K, r, splits, act, wt;
+    bool once;  // X is not worth keeping in the caches; set by the launcher of ds and grad_up
 };
 // out[row(p)][n] (+)= sum_k S[p][k] W_e[n][k], S[p] = scale_e sum over splits
 // of part[.][p]; W_e: [N][r]. S goes to s_row by row, unscaled (unless null).

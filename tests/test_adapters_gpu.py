@@ -270,6 +270,36 @@ def test_rows_past_32_bit_offsets(dev):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act,r", [("float32", 24), ("float16", 16), ("bfloat16", 72)])
+def test_gradients_of_a_dy_past_the_caches(dev, act, r):
+    """dy of over 256 MB, which ds reads without keeping it; 90 rows over two
+    adapters (a tile of 64 rows, and shorter ones) have one."""
+    import torch
+    say(f"adapters with 2100 rows of 131072, {act}, rank {r}")
+    M, d_in, d_out, E = 2100, 128, 131072, 2
+    t = getattr(torch, act)
+    torch.manual_seed(r)
+    ids = np.full(M, -1, np.int32)
+    at = np.sort(np.random.default_rng(r).choice(M, 90, replace=False))
+    ids[at] = np.arange(90) % 7 == 0
+    x = torch.randn((M, d_in), device=dev).to(t)
+    dy = torch.full((M, d_out), float("nan"), dtype=t, device=dev)
+    dy[at] = torch.randn((90, d_out), device=dev).to(t)
+    down = torch.randn((E, r, d_in), device=dev).to(t)
+    up = (torch.randn((E, d_out, r), device=dev) / 256).to(t)
+    scale = torch.tensor([0.5, -3.0], device=dev)
+    tape = torch.randn((M, r), device=dev)
+    offsets, order, _ = blr.blr_route_sort(torch.from_numpy(ids).to(dev), E)
+    gd, gu, dx = blr.blr_adapters_backward(x, dy, down, up, offsets, order, scale, tape)
+    want, mag = ref.adapters_backward(num(x[at]), num(dy[at]), num(down), num(up), ids[at], num(scale), num(tape[at]))
+    ref.within(num(gd), want[0], mag[0], d_out + 94)
+    ref.within(num(gu), want[1], mag[1], 94)
+    ref.within(num(dx[at]), want[2], mag[2], d_out + r + 4, act)
+    dx[at] = 0
+    assert not dx.any()
+
+
+@pytest.mark.gpu
 def test_long_ranges(dev):
     """Rows enough for several ranges of the greatest length (4096) in the
     gradients; their sums against 64 bits on the GPU, in runs of columns."""
