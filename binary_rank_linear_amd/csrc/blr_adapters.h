@@ -17,10 +17,9 @@
 // widened, which is exact. Rows of 16 bits run on the 16x16x32 instructions
 // (lane gives eight k: A[c][8 q + j], B[8 q + j][c]; D as above), whose
 // products are exact and whose sums are f32; s and ds, which are f32, enter
-// them as two or three 16-bit terms, so that their 16 or 24 leading bits take
-// part (see where they are made). Which column of a product a k index stands
-// for is free as long as A and B agree: the loads use that to read 16
-// consecutive bytes per lane.
+// them as three bf16 terms, so that all their 24 bits take part (see
+// take_term). Which column of a product a k index stands for is free as long as
+// A and B agree: the loads use that to read 16 consecutive bytes per lane.
 #pragma once
 
 #include <type_traits>
@@ -441,15 +440,46 @@ struct ShrinkBlock {
     }
 };
 
-// A term of s and what it leaves; nothing where s is not finite, so that an
-// infinity stays one.
-template <typename T>
-__device__ __forceinline__ T take_term(float &v) {
-    const T t = (T)v;
+// The bf16 nearest to v, and in v what it leaves; nothing where v is not
+// finite, so that an infinity stays one. Three such terms hold the 24 bits of
+// an f32 and two the 11 of an f16, whatever its size, since bf16 has f32's
+// exponents: no element loses bits to a larger neighbour. (Two f16 terms with
+// the row's largest element scaled near one lost every element 2^-25 below it;
+// two products instead of five, 8192 rows of 4096 -> 4096 added to y, the whole
+// call: 127 us against 147 at rank 128, 41 against 42 at rank 16. bf16 rows, two
+// terms against three: 39.4 us and 40.0 at rank 16, 116 and 117 of 4096 -> 12288
+// at rank 64.)
+__device__ __forceinline__ __bf16 take_term(float &v) {
+    const __bf16 t = (__bf16)v;
     const float left = v - (float)t;
     v = __builtin_isfinite(left) ? left : 0.f;
     return t;
 }
+
+// 16-bit weights as bf16 operands: bf16 as they are, f16 as the upper half of
+// the f32 of that value and what it leaves, both exact.
+template <typename T>
+constexpr int PARTS = __is_same(T, _Float16) ? 2 : 1;
+
+__device__ __forceinline__ void split(vb8 w, vb8 (&part)[1]) { part[0] = w; }
+__device__ __forceinline__ void split(vh8 w, vb8 (&part)[2]) {
+    vu4 hi, lo;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float a = (float)w[2 * j], b = (float)w[2 * j + 1];
+        const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+        const float la = a - __uint_as_float(ua & 0xffff0000u), lb = b - __uint_as_float(ub & 0xffff0000u);
+        hi[j] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
+        lo[j] = __builtin_amdgcn_perm(__float_as_uint(lb), __float_as_uint(la), 0x07060302u);
+    }
+    part[0] = __builtin_bit_cast(vb8, hi);
+    part[1] = __builtin_bit_cast(vb8, lo);
+}
+
+// Terms of s that part p of a weight meets: all three, but of the second part,
+// 2^-7 of the weight at most, only two (with the third, 2^-18 of s at most, it
+// would add 2^-25 of the whole product).
+__device__ constexpr int terms_for(int p) { return p == 0 ? 3 : 2; }
 
 // ------------------------------------------------------------------ thin --
 // A tile's ds or s, S[64][.] with zeros past the tile's end, as the gradients'
@@ -475,7 +505,7 @@ __device__ void write_panel(void *panels, int64_t tile, const float (*S)[STRIDE]
             for (int j = 0; j < 8; ++j) {
                 float v = S[t + j][k];
 #pragma unroll
-                for (int h = 0; h < 3; ++h) term[h][j] = take_term<__bf16>(v);
+                for (int h = 0; h < 3; ++h) term[h][j] = take_term(v);
             }
 #pragma unroll
             for (int h = 0; h < 3; ++h)
@@ -497,7 +527,7 @@ struct ExpandStep {
     static constexpr int COLS = 32;
     struct S {
         vf4 v[RT];
-        __device__ __forceinline__ void load(const float (*tile)[RT * 16 + 4], const float *, int q, int c) {
+        __device__ __forceinline__ void load(const float (*tile)[RT * 16 + 4], int q, int c) {
 #pragma unroll
             for (int n = 0; n < RT; ++n) v[n] = *reinterpret_cast<const vf4 *>(&tile[c][n * 16 + q * 4]);
         }
@@ -543,52 +573,32 @@ struct ExpandStep {
     }
 };
 
-// The power of two at the largest element of a row of s, or its inverse; 1
-// where that is zero or not finite.
-__device__ __forceinline__ float power_of(float top, bool itself) {
-    if (!(top > 0.f) || !__builtin_isfinite(top)) return 1.f;
-    int e = (int)((__float_as_uint(top) >> 23) & 255) - 127;  // subnormal: -127
-    e = e < -120 ? -120 : e > 120 ? 120 : e;
-    return __uint_as_float((unsigned)(127 + (itself ? e : -e)) << 23);
-}
-
-// Eight elements of a row of s (`largest`: of the row, for f16) in two terms
-// of 16 bits. out is rounded to 16 bits, so two terms (16 leading bits in
-// bf16, 22 in f16) leave an error far below that rounding. f16 terms need s
-// near one: each row enters divided by the power of two at its largest
-// element, and the result is multiplied back (both exact).
-template <typename T>
-__device__ __forceinline__ void two_terms(const float *s, float largest, typename Vec<T>::v &hi,
-                                          typename Vec<T>::v &lo) {
-    const float by = __is_same(T, _Float16) ? power_of(largest, false) : 1.f;
+// Elements k .. k + 7 of a row of s of RT * 16 elements, zero past its end, in
+// three terms.
+template <int RT>
+__device__ __forceinline__ void three_terms(const float *row, int k, vb8 (&term)[3]) {
+    const bool in = RT > 1 || k < RT * 16;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        float v = by * s[j];
-        hi[j] = take_term<T>(v);
-        lo[j] = take_term<T>(v);
+        const float at = row[(in ? k : 0) + j];
+        float v = in ? at : 0.f;
+#pragma unroll
+        for (int h = 0; h < 3; ++h) term[h][j] = take_term(v);
     }
 }
 
 // Rows of 16 bits: four tiles, 64 columns a step; column i of row 4 q' of tile
-// 2 g + h is 32 g + 8 q' + 4 h + i. Up to rank 16 both terms of s share one
-// instruction's 32 k.
+// 2 g + h is 32 g + 8 q' + 4 h + i.
 template <typename T, int RT>
 struct ExpandStep16 {
     static constexpr int COLS = 64;
-    static constexpr bool PACKED = RT == 1;
     static constexpr int KS = (RT + 1) / 2;  // steps of 32 ranks
     typedef typename Vec<T>::v V;
     struct S {
-        V hi[KS], lo[KS];
-        float back = 1.f;
-        __device__ __forceinline__ void load(const float (*tile)[RT * 16 + 4], const float *largest, int q, int c) {
-            const float top = __is_same(T, _Float16) ? largest[c] : 0.f;
-            if (__is_same(T, _Float16)) back = power_of(top, true);
+        vb8 t[KS][3];
+        __device__ __forceinline__ void load(const float (*tile)[RT * 16 + 4], int q, int c) {
 #pragma unroll
-            for (int kk = 0; kk < KS; ++kk) {
-                two_terms<T>(&tile[c][PACKED ? (q & 1) * 8 : kk * 32 + q * 8], top, hi[kk], lo[kk]);
-                if (PACKED && q >= 2) hi[kk] = lo[kk];
-            }
+            for (int kk = 0; kk < KS; ++kk) three_terms<RT>(tile[c], kk * 32 + q * 8, t[kk]);
         }
     };
     V w[4][KS], y[2];
@@ -603,7 +613,7 @@ struct ExpandStep16 {
         for (int h = 0; h < 4; ++h)
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
-                const int k = PACKED ? (q & 1) * 8 : kk * 32 + q * 8, kc = k < r ? k : 0;
+                const int k = kk * 32 + q * 8, kc = k < r ? k : 0;
                 w[h][kk] = *reinterpret_cast<const V *>(
                     ahead(W + (int64_t)(o0 + 32 * (h >> 1) + 4 * (h & 1)) * r,
                           (unsigned)((8 * (c >> 2) + (c & 3)) * r + kc) * (unsigned)sizeof(T)));
@@ -617,18 +627,21 @@ struct ExpandStep16 {
         for (int h = 0; h < 4; ++h) d[h] = vf4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
-            const bool past = (PACKED ? (q & 1) * 8 : kk * 32 + q * 8) >= r;  // s is zero there
+            const bool past = kk * 32 + q * 8 >= r;  // s is zero there
+            vb8 v[4][PARTS<T>];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const V v = past ? (V)(T)0 : w[h][kk];
-                d[h] = mfma8(v, s.hi[kk], d[h]);
-                if (!PACKED) d[h] = mfma8(v, s.lo[kk], d[h]);
-            }
+            for (int h = 0; h < 4; ++h) split(past ? (V)(T)0 : w[h][kk], v[h]);
+#pragma unroll
+            for (int p = 0; p < PARTS<T>; ++p)
+#pragma unroll
+                for (int i = 0; i < terms_for(p); ++i)
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) d[h] = mfma8(v[h][p], s.t[kk][i], d[h]);
         }
         if (out) {
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                const vf4 u = s.back * d[2 * g], v = s.back * d[2 * g + 1];
+                const vf4 u = d[2 * g], v = d[2 * g + 1];
                 F f = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
                 if (ACC) f += __builtin_convertvector(y[g], F);
                 *reinterpret_cast<V *>(out + o0 + 32 * g + 8 * q) = __builtin_convertvector(f, V);
@@ -643,15 +656,14 @@ struct ExpandStep<__bf16, __bf16, RT> : ExpandStep16<__bf16, RT> {};
 
 // A wave's steps (every fourth of [from, to)) over a tile of up to 16 rows.
 template <typename TX, typename TW, int RT, bool ACC>
-__device__ void expand_tile(const AdaptExpand &a, const Tile &tile, int from, int to, const float (*S)[RT * 16 + 4],
-                            const float *largest) {
+__device__ void expand_tile(const AdaptExpand &a, const Tile &tile, int from, int to, const float (*S)[RT * 16 + 4]) {
     typedef ExpandStep<TX, TW, RT> Step;
     const int lane = threadIdx.x & 63, w = wave();
     const int q = lane >> 4, c = lane & 15;
     const int64_t at = row_of(a.plan, tile.p0 + (c < tile.cnt ? c : tile.cnt - 1));
     TX *row = reinterpret_cast<TX *>(a.out) + (at < 0 ? 0 : at) * a.N, *out = c < tile.cnt && at >= 0 ? row : nullptr;
     typename Step::S s;
-    s.load(S, largest, q, c);
+    s.load(S, q, c);
     const TW *W = reinterpret_cast<const TW *>(a.W) + (int64_t)tile.e * a.r * a.N;
     const int first = from + w;
     walk<Step, RT <= 4>((to - first + 3) / 4,
@@ -683,10 +695,12 @@ struct ExpandLds {
     static constexpr bool WIDE = sizeof(TX) == 4;  // f32 rows: 4 ranks a slot, else 8
     static constexpr int H = 16 / sizeof(TX);      // tiles of a step, and elements of 16 bytes of a row
     static constexpr int COLS = 16 * H;
-    static constexpr bool PACKED = !WIDE && RT == 1;  // both terms of s in one instruction
     static constexpr int KS = WIDE ? RT : (RT + 1) / 2;
+    static constexpr int KS_RANKS = WIDE ? 16 : 32;  // of each of the KS
+    static constexpr int P = WIDE ? 1 : PARTS<TX>;   // of a weight
     static constexpr int SLOTS = H * KS * 64;
-    static constexpr int BUFFER = SLOTS + 64;  // and the spare ones
+    static constexpr int PART = SLOTS + 64;  // and the spare ones
+    static constexpr int BUFFER = P * PART;
     typedef typename Vec<TX>::v V;
     typedef typename std::conditional<WIDE, typename Vec<TW>::v4, vu4>::type Piece;  // a slot's ranks, as they lie
     static constexpr int RANKS = WIDE ? 4 : 8;
@@ -721,8 +735,10 @@ struct ExpandLds {
             if constexpr (WIDE)
                 *reinterpret_cast<vf4 *>(lds + at[j]) = __builtin_convertvector(w[j], vf4);
             else {
-                lds[at[j]] = w[j];
-                if (PACKED) lds[(at[j] + 32) ^ 8] = w[j];  // lanes q + 2: the second term's
+                vb8 part[P];
+                split(__builtin_bit_cast(V, w[j]), part);
+#pragma unroll
+                for (int p = 0; p < P; ++p) lds[p * PART + at[j]] = __builtin_bit_cast(vu4, part[p]);
             }
         }
     }
@@ -764,34 +780,26 @@ struct ExpandRows {
 // FULL: every row of the tile is written.
 template <typename TX, typename TW, int RT, bool ACC, bool FULL>
 __device__ void expand_tile_lds(const AdaptExpand &a, ExpandRows<TX, TW, RT, ACC> &rows, int from, int to,
-                                const float (*S)[RT * 16 + 4], const float *largest, vu4 *lds) {
+                                const float (*S)[RT * 16 + 4], vu4 *lds) {
     typedef ExpandLds<TX, TW, RT> L;
     typedef typename L::V V;
     typedef float F __attribute__((ext_vector_type(L::H)));
     const int lane = threadIdx.x & 63, w = wave();
     const int q = lane >> 4, c = lane & 15;
     const int spread = q * 16 + (c ^ (4 * q)), per4 = (a.r / L::RANKS + 3) / 4;  // the lane's slot: see ExpandLds
-    // s of row c as the A operand: f32, or two terms
+    // s of row c as the A operand: f32, or three terms
     const int m = 16 * w + c;
     vf4 s[RT];
-    V hi[L::KS], lo[L::KS];
-    float back[4] = {1.f, 1.f, 1.f, 1.f};
+    vb8 term[L::KS][3];
     if constexpr (L::WIDE) {
 #pragma unroll
         for (int n = 0; n < RT; ++n) s[n] = *reinterpret_cast<const vf4 *>(&S[m][n * 16 + q * 4]);
     } else {
-        if constexpr (__is_same(TX, _Float16)) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) back[i] = power_of(largest[16 * w + 4 * q + i], true);
-        }
-#pragma unroll
-        for (int kk = 0; kk < L::KS; ++kk) {
-            two_terms<TX>(&S[m][L::PACKED ? (q & 1) * 8 : kk * 32 + q * 8], largest[m], hi[kk], lo[kk]);
-            if (L::PACKED && q >= 2) hi[kk] = lo[kk];
-        }
+        for (int kk = 0; kk < L::KS; ++kk) three_terms<RT>(S[m], kk * 32 + q * 8, term[kk]);
     }
     __syncthreads();  // S lies in the same memory as the weights
-    if (a.r < RT * 16) {  // ranks past r stay zero
+    if (a.r < L::KS * L::KS_RANKS) {  // ranks past r stay zero
         for (int i = threadIdx.x; i < 2 * L::BUFFER; i += 256) lds[i] = vu4{0, 0, 0, 0};
         __syncthreads();
     }
@@ -826,30 +834,35 @@ __device__ void expand_tile_lds(const AdaptExpand &a, ExpandRows<TX, TW, RT, ACC
                 for (int i = 0; i < 4; ++i) d[h][i] = old[i][h];
             }
         }
-        vu4 slot[2][L::H];  // the next group's reads are in flight while one is multiplied
-        auto read = [&](int h, int kk) { return buf[(h * L::KS + kk) * 64 + (spread ^ ((h * per4 + kk) & 3))]; };
+        // groups of four tiles of one part; the next group's reads are in flight while one is multiplied
+        constexpr int SETS = L::H / 4, GROUPS = L::KS * L::P * SETS;
+        vu4 slot[2][4];
+        auto read = [&](int g, int t) {
+            const int kk = g / SETS / L::P, h = g % SETS * 4 + t;
+            return buf[g / SETS % L::P * L::PART + (h * L::KS + kk) * 64 + (spread ^ ((h * per4 + kk) & 3))];
+        };
 #pragma unroll
-        for (int h = 0; h < L::H; ++h) slot[0][h] = read(h, 0);
+        for (int t = 0; t < 4; ++t) slot[0][t] = read(0, t);
 #pragma unroll
-        for (int kk = 0; kk < L::KS; ++kk) {
-            if (kk + 1 < L::KS) {
+        for (int g = 0; g < GROUPS; ++g) {
+            const int kk = g / SETS / L::P, h = g % SETS * 4;
+            if (g + 1 < GROUPS) {
 #pragma unroll
-                for (int h = 0; h < L::H; ++h) slot[(kk + 1) & 1][h] = read(h, kk + 1);
+                for (int t = 0; t < 4; ++t) slot[(g + 1) & 1][t] = read(g + 1, t);
             }
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (L::WIDE) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int h = 0; h < L::H; ++h)
-                        d[h] = mfma4(s[kk][j], __builtin_bit_cast(vf4, slot[kk & 1][h])[j], d[h]);
+                    for (int t = 0; t < 4; ++t)
+                        d[h + t] = mfma4(s[kk][j], __builtin_bit_cast(vf4, slot[g & 1][t])[j], d[h + t]);
             } else {
 #pragma unroll
-                for (int h = 0; h < L::H; ++h) d[h] = mfma8(hi[kk], __builtin_bit_cast(V, slot[kk & 1][h]), d[h]);
-                if (!L::PACKED) {
+                for (int i = 0; i < terms_for(g / SETS % L::P); ++i)
 #pragma unroll
-                    for (int h = 0; h < L::H; ++h) d[h] = mfma8(lo[kk], __builtin_bit_cast(V, slot[kk & 1][h]), d[h]);
-                }
+                    for (int t = 0; t < 4; ++t)
+                        d[h + t] = mfma8(term[kk][i], __builtin_bit_cast(vb8, slot[g & 1][t]), d[h + t]);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -859,7 +872,6 @@ __device__ void expand_tile_lds(const AdaptExpand &a, ExpandRows<TX, TW, RT, ACC
 #pragma unroll
             for (int h = 0; h < L::H; ++h) f[h] = d[h][i];
             if constexpr (!L::WIDE) {
-                f *= back[i];
                 if (ACC) f += __builtin_convertvector(old[i], F);
             }
             if (FULL || rows.in[i])
@@ -889,12 +901,11 @@ struct ExpandBlock {
     typedef ExpandLds<TX, TW, RT> Lds;
     static constexpr int S_BYTES = sizeof(float) * TM * (RT * 16 + 4), W_BYTES = 2 * 16 * Lds::BUFFER;
     static constexpr int SHARED = S_BYTES > W_BYTES ? S_BYTES : W_BYTES;  // s, then the weights
-    static constexpr int BYTES = SHARED + TM * 4 + 16;
+    static constexpr int BYTES = SHARED + 16;
 
     static __device__ void run(const AdaptExpand &a, int chunks, int block, char *lds) {
         float(*S)[RT * 16 + 4] = reinterpret_cast<float(*)[RT * 16 + 4]>(lds);
-        float *largest = reinterpret_cast<float *>(lds + SHARED);
-        int &named = *reinterpret_cast<int *>(lds + SHARED + TM * 4);
+        int &named = *reinterpret_cast<int *>(lds + SHARED);
         const int chunk = block % chunks;
         const Tile tile = find_tile<false>(a.plan, a.plan.E + 1, TM, block / chunks);
         if (tile.e < 0) return;
@@ -933,22 +944,14 @@ struct ExpandBlock {
             zero_rows<TX>(a, tile, chunk, chunks, 256);
             return;
         }
-        if (__is_same(TX, _Float16)) {
-            if (threadIdx.x < rows) {
-                float top = 0.f;
-                for (int k = 0; k < RT * 16; ++k) top = fmaxf(top, fabsf(S[threadIdx.x][k]));
-                largest[threadIdx.x] = top;
-            }
-            __syncthreads();
-        }
         if (!large) {
             const int64_t steps = a.N / ExpandStep<TX, TW, RT>::COLS;
             const int from = (int)(steps * chunk / chunks), to = (int)(steps * (chunk + 1) / chunks);
-            expand_tile<TX, TW, RT, ACC>(a, tile, from, to, S, largest);
+            expand_tile<TX, TW, RT, ACC>(a, tile, from, to, S);
         } else if (named) {
-            expand_tile_lds<TX, TW, RT, ACC, true>(a, own, from, to, S, largest, reinterpret_cast<vu4 *>(lds));
+            expand_tile_lds<TX, TW, RT, ACC, true>(a, own, from, to, S, reinterpret_cast<vu4 *>(lds));
         } else {
-            expand_tile_lds<TX, TW, RT, ACC, false>(a, own, from, to, S, largest, reinterpret_cast<vu4 *>(lds));
+            expand_tile_lds<TX, TW, RT, ACC, false>(a, own, from, to, S, reinterpret_cast<vu4 *>(lds));
         }
     }
 };
@@ -998,7 +1001,7 @@ struct GradStep {
 // gradients are f32, so the thin operand takes part with 24 leading bits, in
 // three bf16 terms; an f16 element of X is exactly two (11 bits in 8 + 3), and
 // the product of its second with the third term, 2^-25 of the whole at most,
-// is left out. bf16 has f32's range, so no term needs a scale.
+// is left out.
 template <typename T, int RT>
 struct GradStep16 {
     static constexpr int ROWS = 32;
@@ -1034,8 +1037,8 @@ struct GradStep16 {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     float v = (float)__builtin_bit_cast(vh4, x[j])[u];
-                    hi[u][j] = take_term<__bf16>(v);
-                    lo[u][j] = take_term<__bf16>(v);
+                    hi[u][j] = take_term(v);
+                    lo[u][j] = take_term(v);
                 }
             }
         }

@@ -15,8 +15,16 @@ __global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_shrink_kernel(Adap
     ShrinkBlock<TX, TW, RT>::template run<false>(a, blockIdx.x, lds);
 }
 
+// Two workgroups to a CU. At ranks over 64 the adding form spills 100 bytes a
+// lane for it in bf16, and is the faster for it all the same (8192 rows of 4096 ->
+// 4096, rank 128, the whole call: 107 us against 130; f32, without a spill, 210
+// against 243). f16 weights of such ranks, in two parts and two buffers, take
+// 133 KB of LDS, which leaves room for one.
+template <typename TX, int RT>
+constexpr int expand_per_cu = __is_same(TX, _Float16) && RT > 4 ? 1 : 2;
+
 template <typename TX, typename TW, int RT, bool ACC>
-__global__ __launch_bounds__(256) void adapt_expand_kernel(AdaptExpand a, int chunks) {
+__global__ __launch_bounds__(256, (expand_per_cu<TX, RT>)) void adapt_expand_kernel(AdaptExpand a, int chunks) {
     __shared__ __align__(16) char lds[ExpandBlock<TX, TW, RT, ACC>::BYTES];
     ExpandBlock<TX, TW, RT, ACC>::run(a, chunks, blockIdx.x, lds);
 }

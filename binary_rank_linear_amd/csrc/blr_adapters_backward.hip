@@ -153,13 +153,9 @@ __global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_dy_kernel(AdaptShr
         GradBlock<TX, RT>::template run<false>(gr, 1, b, lds);
 }
 
-// Two workgroups to a CU where that needs no spill.
-template <typename TX, int RT, bool ACC>
-constexpr int dx_per_cu = RT <= (__is_same(TX, _Float16) && ACC ? 2 : 4) ? 2 : 1;
-
 template <typename TX, typename TW, int RT, bool ACC>
-__global__ __launch_bounds__(256, (dx_per_cu<TX, RT, ACC>)) void adapt_dx_kernel(AdaptExpand ex, AdaptGrad gr,
-                                                                                int chunks, Mix mix) {
+__global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_dx_kernel(AdaptExpand ex, AdaptGrad gr, int chunks,
+                                                                       Mix mix) {
     constexpr int A = ExpandBlock<TX, TW, RT, ACC>::BYTES, B = GradBlock<TX, RT>::BYTES;
     __shared__ __align__(16) char lds[A > B ? A : B];
     int b;

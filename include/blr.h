@@ -293,8 +293,7 @@ int blr_route_combine_backward(int64_t T, int64_t k, int64_t experts, int64_t d,
  * shorter adapters with zero rank rows and columns), 1 <= M < 2^31 - 65536,
  * 1 <= E <= 1024. Sums are f32. Products of f32 rows are f32 (16-bit adapters
  * are exact in it), those of 16-bit rows exact, with s and ds (f32) taking part
- * in 16 or more leading bits where the output has 16 bits and in 24 where it is
- * f32; outputs of 16 bits are rounded once. Where a factor is infinite the
+ * with all their 24 bits; outputs of 16 bits are rounded once. Where a factor is infinite the
  * result is not finite, but may be NaN in place of an infinity. Rows, adapters
  * and gradients that do not meet do not touch each other, whatever they hold.
  * Results are the same on every run.

@@ -1,0 +1,87 @@
+"""GPU tests of the low-rank adapters on rows of 16 bits whose s or ds spans many
+binades, or cancels: every rank takes part with all its bits."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import _operators_ref as ref
+import binary_rank_linear_amd as blr
+from _gpu_util import host, say
+
+
+def num(t):
+    return host(t.double())
+
+
+def wide_case(dev, M, d_in, d_out, r, act, kind, seed):
+    """(x, down, up, ids, s): s of 24 bits each, exact in f32, over 30 binades.
+
+    s_j = n 2^(k - 23) with 2^23 <= n < 2^24 comes from three elements of x, of
+    8 bits each, so that the sum x down^T is exact in any order. "zeros": of a
+    column's ranks only the smaller ones have weights, of 2^-k, so that the
+    sum is near one beside ranks up to 2^30 times as large. "cancel": ranks in
+    pairs whose s differ by less than 2^-16, with weights of opposite sign."""
+    import torch
+    rng = np.random.default_rng(seed)
+    x, down, up = np.zeros((M, d_in)), np.zeros((2, r, d_in)), np.zeros((2, d_out, r))
+    assert d_in >= 3 * r
+    k = rng.integers(-5, 25, r)  # of rank j, shared with its partner
+    k[1::2] = k[::2]
+    n = rng.integers(1 << 23, 1 << 24, (M, r))
+    n[:, 1::2] = n[:, ::2] ^ rng.integers(1, 128, (M, r // 2))
+    kx = np.clip(k, -14, 8)  # what x holds of the scale; the rest is down's
+    for i, shift in enumerate((16, 8, 0)):
+        x[:, i:3 * r:3] = (n >> shift & 255) * 2.0 ** kx
+        down[:, np.arange(r), 3 * np.arange(r) + i] = 2.0 ** (shift - 23 + k - kx)
+    for o in range(d_out):
+        w = rng.integers(1, 256, (2, r)) * 2.0 ** (3 - k)
+        if kind == "zeros":
+            up[:, o] = np.where(k <= rng.integers(-5, 25), w * 2.0 ** -10, 0.0)
+        else:
+            up[:, o] = np.repeat(w[:, ::2], 2, axis=1) * np.tile([1.0, -1.0], r // 2)
+    ids = np.zeros(M, np.int32)
+    ids[M // 2] = 1
+    put = lambda a: torch.from_numpy(a).to(dev).to(getattr(torch, act))  # noqa: E731
+    x, down, up = put(x), put(down), put(up)
+    s = np.stack([num(x)[t] @ num(down)[e].T for t, e in enumerate(ids)])
+    assert np.array_equal(s, n * 2.0 ** (k - 23.0))  # nothing was lost to the types
+    return x, down, up, ids, s
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["zeros", "cancel"])
+@pytest.mark.parametrize("r", [8, 16, 24, 64, 104, 128])
+@pytest.mark.parametrize("M", [5, 17, 70])
+@pytest.mark.parametrize("act", ["float16", "bfloat16"])
+def test_small_ranks_beside_large_ones(dev, act, M, r, kind):
+    """Forward, and dx by the same numbers (dy as x, up as down^T, down as
+    up^T). s is exact, so what is left is the second sum: an element of s
+    meets a weight in at most five products, of parts whose absolute values
+    add up to at most (1 + 2^-6) of the whole, and what is left out is 2^-25 of
+    it: 5 r + 1 roundings, with 2 r for the parts' 2^-6, and the addition to y."""
+    import torch
+    say(f"adapters, s over 30 binades, M={M} r={r} {act} {kind}")
+    d_in, d_out = 384, 256
+    x, down, up, ids, s = wide_case(dev, M, d_in, d_out, r, act, kind, seed=M + r)
+    W = num(up)
+    want = np.stack([W[e] @ s[t] for t, e in enumerate(ids)])
+    mag = np.stack([np.abs(W[e]) @ np.abs(s[t]) for t, e in enumerate(ids)])
+    offsets, order, _ = blr.blr_route_sort(torch.from_numpy(ids).to(dev), 2)
+    y0 = torch.randn((M, d_out), device=dev).to(x.dtype)
+    terms = 7 * r + 2
+
+    y, tape = blr.blr_adapters_forward(x, down, up, offsets, order, keep_tape=True)
+    assert np.array_equal(num(tape), s)
+    ref.within(num(y), want, mag, terms, act)
+    y, _ = blr.blr_adapters_forward(x, down, up, offsets, order, y=y0.clone(), accumulate_y=True)
+    ref.within(num(y), num(y0) + want, mag + np.abs(num(y0)), terms, act)
+
+    up_t, down_t = down.transpose(1, 2).contiguous(), up.transpose(1, 2).contiguous()
+    _, _, dx = blr.blr_adapters_backward(None, x, down_t, up_t, offsets, order, grads=False)
+    ref.within(num(dx), want, mag, terms, act)
+    gd, gu, dx2 = blr.blr_adapters_backward(y0, x, down_t, up_t, offsets, order, None, tape)
+    assert torch.equal(dx2, dx)
+    _, _, dx = blr.blr_adapters_backward(None, x, down_t, up_t, offsets, order, grads=False, dx=y0.clone(),
+                                         accumulate_dx=True)
+    ref.within(num(dx), num(y0) + want, mag + np.abs(num(y0)), terms, act)
