@@ -25,6 +25,7 @@
 #include <type_traits>
 
 #include "blr_internal.h"
+#include "blr_plan.h"
 #include "blr_vec.h"
 
 namespace blr {
@@ -86,11 +87,9 @@ __device__ Tile find_tile(const AdaptPlan &plan, int groups, int tm, int b) {
         const int e = base + lane;
         int lo = 0, cnt = 0;
         if (e < groups) {
-            lo = plan.offsets[e];
-            const int hi = e < plan.E ? plan.offsets[e + 1] : plan.M;
-            lo = lo < 0 ? 0 : lo > plan.M ? plan.M : lo;
-            cnt = (hi > plan.M ? plan.M : hi) - lo;
-            cnt = cnt < 0 ? 0 : cnt;
+            const int offset = plan.offsets[e];
+            lo = plan_at(offset, plan.M);
+            cnt = plan_rows(offset, e < plan.E ? plan.offsets[e + 1] : plan.M, plan.M);
         }
         const int nt = cnt / tm + (cnt % tm ? 1 : 0);
         const int incl = scan(nt, groups - base, lane);

@@ -80,7 +80,7 @@ __global__ __launch_bounds__(256) void adapt_prepare_kernel(AdaptPrepare a) {
             continue;
         }
         const int e = (int)((b - a.panels) / per), t = (int)((b - a.panels) % per);
-        const bool empty = a.plan.offsets[e + 1] <= a.plan.offsets[e];
+        const bool empty = plan_rows(a.plan.offsets[e], a.plan.offsets[e + 1], a.plan.M) == 0;
         if (t < transposes) {
             const int job = t >= a.tiles[0];
             if (!empty)
@@ -175,12 +175,7 @@ __global__ __launch_bounds__(256) void adapt_reduce_kernel(AdaptGrad a) {
     const int64_t size = (int64_t)a.r * job.N;
     const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if ((int64_t)blockIdx.x * 1024 >= size) return;
-    auto rows = [&](int f) {
-        int lo = a.plan.offsets[f], hi = a.plan.offsets[f + 1];
-        lo = lo < 0 ? 0 : lo > a.plan.M ? a.plan.M : lo;
-        hi = hi > a.plan.M ? a.plan.M : hi;
-        return hi > lo ? hi - lo : 0;
-    };
+    auto rows = [&](int f) { return plan_rows(a.plan.offsets[f], a.plan.offsets[f + 1], a.plan.M); };
     const int cnt = rows(e);
     if (cnt <= a.range) return;
     // partials of the adapters before: every wave sums for itself

@@ -278,10 +278,10 @@ int blr_route_combine_backward(int64_t T, int64_t k, int64_t experts, int64_t d,
  *     act = BLR_F32 with any wt, or wt = act. scale f32 [E] or NULL (all 1).
  *   offsets [E + 1], order [M]: the plan that blr_route_sort makes of the
  *     rows' adapter ids; order NULL: the rows lie by adapter already (those of
- *     blr_route_gather). One plan serves every layer of a model. Offsets that
- *     do not ascend cannot lead outside the arrays; a position whose row is
- *     outside [0, M) is left out; a row at two positions leaves that row of y
- *     and dx undefined.
+ *     blr_route_gather). One plan serves every layer of a model. An offset
+ *     outside [0, M] counts as its nearer end, and an adapter whose end comes
+ *     before its start has no rows; a position whose row is outside [0, M) is
+ *     left out; a row at two positions leaves that row of y and dx undefined.
  *   Rows without an adapter: y and dx are zero, or unchanged when adding.
  *     Adapters without rows: their gradients are zero, or unchanged.
  *   tape_s f32 [M][r]: s by row (zero without an adapter), which the backward
