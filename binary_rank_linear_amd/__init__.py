@@ -78,6 +78,8 @@ def load():
     lib.blr_route_combine_backward.restype = i32
     lib.blr_adapters_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
     lib.blr_adapters_workspace_bytes.restype = sz
+    lib.blr_adapters_forward_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+    lib.blr_adapters_forward_workspace_bytes.restype = sz
     lib.blr_adapters_forward.argtypes = [i64, i64, i64, i64, i64, i32, i32, p, p, p, p, p, p, p, i32, p, p, sz, p]
     lib.blr_adapters_forward.restype = i32
     lib.blr_adapters_backward.argtypes = [i64, i64, i64, i64, i64, i32, i32, p, p, p, p, p, p, p, p, p, p, i32, p, i32,
@@ -594,18 +596,20 @@ def blr_route_combine_backward(dy, z, offsets, slot, weights=None, *, dz=None, d
     return dz, dw
 
 
-def workspace_adapters(M: int, d_in: int, d_out: int, r: int, adapters: int, device=None):
+def workspace_adapters(M: int, d_in: int, d_out: int, r: int, adapters: int, device=None, forward: bool = False):
+    """A workspace of both adapter calls; with `forward`, of the forward alone."""
     import torch
-    n = int(load().blr_adapters_workspace_bytes(M, d_in, d_out, r, adapters))
+    name = "blr_adapters_forward_workspace_bytes" if forward else "blr_adapters_workspace_bytes"
+    n = int(getattr(load(), name)(M, d_in, d_out, r, adapters))
     if n == 0:
-        raise BlrError(-2, "blr_adapters_workspace_bytes")
+        raise BlrError(-2, name)
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
-def _adapters(rows, name, down, up, offsets, order, scale, ws, stream):
-    """Checks that both adapter calls share; `rows` is x or dy. Returns
-    (sizes and types, addresses of down .. scale, ws, its (address, bytes),
-    GPU)."""
+def _adapters(rows, name, down, up, offsets, order, scale, ws, query, stream):
+    """Checks that both adapter calls share; `rows` is x or dy, `query` tells
+    the size of a workspace. Returns (sizes and types, addresses of down ..
+    scale, ws, its (address, bytes), GPU)."""
     f32, i32, wide, _, codes = _types()
     act, M, _, dev = _rows(rows, name, stream)
     E, r, d_in = _shape(down, "down", 3)
@@ -613,8 +617,8 @@ def _adapters(rows, name, down, up, offsets, order, scale, ws, stream):
     at = (_at(down, "down", wide, (E, r, d_in), dev), _at(up, "up", (down.dtype,), (E, d_out, r), dev),
           _at(offsets, "offsets", i32, (E + 1,), dev), None if order is None else _at(order, "order", i32, (M,), dev),
           None if scale is None else _at(scale, "scale", f32, (E,), dev))
-    need = load().blr_adapters_workspace_bytes(M, d_in, d_out, r, E) if ws is None else 0
-    ws, work = _ws(ws, need, "blr_adapters_workspace_bytes", dev, stream)
+    need = getattr(load(), query)(M, d_in, d_out, r, E) if ws is None else 0
+    ws, work = _ws(ws, need, query, dev, stream)
     return (M, d_in, d_out, r, E, act, codes[down.dtype]), at, ws, work, dev
 
 
@@ -629,7 +633,8 @@ def blr_adapters_forward(x, down, up, offsets, order=None, scale=None, *, y=None
     kept when tape_s is given or keep_tape is set. Returns (y, tape_s)."""
     if y is None and accumulate_y:
         raise ValueError("accumulate_y needs y")
-    sizes, at, ws, work, dev = _adapters(x, "x", down, up, offsets, order, scale, ws, stream)
+    sizes, at, ws, work, dev = _adapters(x, "x", down, up, offsets, order, scale, ws,
+                                         "blr_adapters_forward_workspace_bytes", stream)
     M, d_in, d_out, r = sizes[:4]
     at_x = _at(x, "x", (x.dtype,), (M, d_in), dev)
     y, at_y = _out(y, "y", x.dtype, (M, d_out), dev, stream)
@@ -655,7 +660,8 @@ def blr_adapters_backward(x, dy, down, up, offsets, order=None, scale=None, tape
         raise ValueError("grad_down and grad_up are given, but grads is False")
     if not need_dx and dx is not None:
         raise ValueError("dx is given, but need_dx is False")
-    sizes, at, ws, work, dev = _adapters(dy, "dy", down, up, offsets, order, scale, ws, stream)
+    sizes, at, ws, work, dev = _adapters(dy, "dy", down, up, offsets, order, scale, ws,
+                                         "blr_adapters_workspace_bytes", stream)
     M, d_in, d_out, r, E = sizes[:5]
     f32 = _types()[0]
     at_dy = _at(dy, "dy", (dy.dtype,), (M, d_out), dev)

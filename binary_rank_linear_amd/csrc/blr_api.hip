@@ -763,14 +763,23 @@ AdaptLayout adapt_layout(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int6
     return L;
 }
 
+// What the forward needs: the splits' partials of s. Up to a megabyte a buffer
+// for both calls costs nobody anything, so below that the two sizes are one.
+size_t adapt_forward_bytes(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t E) {
+    const size_t own = up((size_t)adapt_splits(M, E, d_in) * M * r * 4), least = (size_t)1 << 20;
+    const size_t both = adapt_layout(M, d_in, d_out, r, E).total;
+    return own > least ? own : both < least ? both : least;
+}
+
 // Checks that both calls share.
 int adapt_check(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t E, int act, int wt, const void *down,
                 const void *up_, const int32_t *offsets, const int32_t *order, const float *scale,
-                const void *workspace, size_t workspace_bytes, size_t *need) {
+                const void *workspace, size_t workspace_bytes, bool forward, size_t *need) {
     if (!down || !up_ || !offsets) return BLR_ERR_NULL;
     if (!dtype_ok(act) || !dtype_ok(wt) || (act != BLR_F32 && wt != act)) return BLR_ERR_DTYPE;
     if (!adapt_shape_ok(M, d_in, d_out, r, E)) return BLR_ERR_SHAPE;
-    *need = adapt_layout(M, d_in, d_out, r, E).total;  // whatever wt is
+    // whatever wt is
+    *need = forward ? adapt_forward_bytes(M, d_in, d_out, r, E) : adapt_layout(M, d_in, d_out, r, E).total;
     if (workspace == nullptr || workspace_bytes < *need) return BLR_ERR_WORKSPACE;
     if (!aligned16(down) || !aligned16(up_) || !aligned4(offsets) || !aligned4(order) || !aligned4(scale) ||
         !aligned16(workspace))
@@ -784,6 +793,11 @@ size_t blr_adapters_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out, int6
     return adapt_layout(M, d_in, d_out, r, adapters).total;
 }
 
+size_t blr_adapters_forward_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t adapters) {
+    if (!adapt_shape_ok(M, d_in, d_out, r, adapters)) return 0;
+    return adapt_forward_bytes(M, d_in, d_out, r, adapters);
+}
+
 int blr_adapters_forward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t adapters, int act, int wt,
                          const void *x, const void *down, const void *up, const int32_t *offsets,
                          const int32_t *order, const float *scale, void *y, int accumulate_y, float *tape_s,
@@ -791,7 +805,7 @@ int blr_adapters_forward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int6
     if (!x || !y) return BLR_ERR_NULL;
     size_t need = 0;
     int st = adapt_check(M, d_in, d_out, r, adapters, act, wt, down, up, offsets, order, scale, workspace,
-                         workspace_bytes, &need);
+                         workspace_bytes, true, &need);
     if (st != BLR_OK) return st;
     if (!aligned16(x) || !aligned16(y) || !aligned16(tape_s)) return BLR_ERR_ALIGN;
     const size_t a = size_of(act), w = (size_t)adapters * r * size_of(wt);
@@ -840,7 +854,7 @@ int blr_adapters_backward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int
     if (grad_down && (!x || !tape_s)) return BLR_ERR_NULL;
     size_t need = 0;
     int st = adapt_check(M, d_in, d_out, r, adapters, act, wt, down, up, offsets, order, scale, workspace,
-                         workspace_bytes, &need);
+                         workspace_bytes, false, &need);
     if (st != BLR_OK) return st;
     const void *arrays[] = {x, dy, tape_s, grad_down, grad_up, dx};
     for (const void *p : arrays)

@@ -298,9 +298,12 @@ int blr_route_combine_backward(int64_t T, int64_t k, int64_t experts, int64_t d,
  * and gradients that do not meet do not touch each other, whatever they hold.
  * Results are the same on every run.
  * Arrays 16-byte aligned, offsets and order 4-byte. Workspace:
- * blr_adapters_workspace_bytes, for both calls; 0 for invalid sizes.
+ * blr_adapters_workspace_bytes serves both calls, a forward by itself needs
+ * blr_adapters_forward_workspace_bytes, which does not grow with the adapters:
+ * at most 128 M r bytes, or 1 MiB where that is less. 0 for invalid sizes.
  */
 size_t blr_adapters_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t adapters);
+size_t blr_adapters_forward_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t adapters);
 int blr_adapters_forward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t adapters, int act, int wt,
                          const void *x, const void *down, const void *up, const int32_t *offsets,
                          const int32_t *order, const float *scale, void *y, int accumulate_y, float *tape_s,
