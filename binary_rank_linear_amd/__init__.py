@@ -36,6 +36,9 @@ def load():
         return _lib
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m binary_rank_linear_amd.build`")
+    # torch brings a HIP runtime of its own. The library has to find that one in the process: loaded first it would
+    # bring the system's, and torch's streams and memory mean nothing to another runtime.
+    import torch  # noqa: F401
     lib = ctypes.CDLL(LIB_PATH)
     i64, p, i32, f32, sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
     lib.blr_status_string.argtypes = [i32]
