@@ -455,6 +455,19 @@ __device__ __forceinline__ __bf16 take_term(float &v) {
     return t;
 }
 
+// Element j of the three terms of an f32. A finite v past bf16's largest value,
+// the last 2^-9 of f32's range, would round to an infinite first term; that
+// term is the largest value then.
+__device__ __forceinline__ void put_terms(float v, int j, vb8 (&term)[3]) {
+    constexpr float largest = 0x1.fep127f;
+    float first = __builtin_isfinite(v) ? fminf(fmaxf(v, -largest), largest) : v;
+    term[0][j] = take_term(first);
+    v -= (float)term[0][j];
+    v = __builtin_isfinite(v) ? v : 0.f;
+    term[1][j] = take_term(v);
+    term[2][j] = take_term(v);
+}
+
 // 16-bit weights as bf16 operands: bf16 as they are, f16 as the upper half of
 // the f32 of that value and what it leaves, both exact.
 template <typename T>
@@ -501,11 +514,7 @@ __device__ void write_panel(void *panels, int64_t tile, const float (*S)[STRIDE]
             const int k = n * 16 + (lane & 15), t = step * 32 + (lane >> 4) * 8;
             vb8 term[3];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float v = S[t + j][k];
-#pragma unroll
-                for (int h = 0; h < 3; ++h) term[h][j] = take_term(v);
-            }
+            for (int j = 0; j < 8; ++j) put_terms(S[t + j][k], j, term);
 #pragma unroll
             for (int h = 0; h < 3; ++h)
                 *reinterpret_cast<vb8 *>(to + (((step * 3 + h) * RT + n) * 64 + lane) * 8) = term[h];
@@ -580,9 +589,7 @@ __device__ __forceinline__ void three_terms(const float *row, int k, vb8 (&term)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const float at = row[(in ? k : 0) + j];
-        float v = in ? at : 0.f;
-#pragma unroll
-        for (int h = 0; h < 3; ++h) term[h][j] = take_term(v);
+        put_terms(in ? at : 0.f, j, term);
     }
 }
 

@@ -85,3 +85,40 @@ def test_small_ranks_beside_large_ones(dev, act, M, r, kind):
     _, _, dx = blr.blr_adapters_backward(None, x, down_t, up_t, offsets, order, grads=False, dx=y0.clone(),
                                          accumulate_dx=True)
     ref.within(num(dx), num(y0) + want, mag + np.abs(num(y0)), terms, act)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [3, 40])
+@pytest.mark.parametrize("act", ["float16", "bfloat16"])
+def test_the_largest_values_stay_finite(dev, act, M):
+    """s, ds and the tape at 2^128 - 2^118, past the largest bf16, with other
+    factors of 2^-20: results of 2^108 - 2^98, one product each, so exact but
+    for the rounding to the output's type."""
+    import torch
+    say(f"adapters with s past the largest bf16, M={M} {act}")
+    t = getattr(torch, act)
+    top = 2.0 ** 128 - 2.0 ** 118
+    z = lambda *s: torch.zeros(s, dtype=t, device=dev)  # noqa: E731
+    # the sum of two products, exact in f32; f16 reaches it by way of the scale
+    big = (2.0 ** 127, 2.0 ** 119) if act == "bfloat16" else (2.0 ** 15, 2.0 ** 7)
+    scale = torch.tensor([1.0 if act == "bfloat16" else 2.0 ** 112], device=dev)
+    a, ends = z(M, 256), z(1, 8, 256)
+    a[:, 5], a[:, 9] = big
+    ends[0, 2, 5], ends[0, 2, 9] = 255 / 128, 1.5  # 255 2^120 + 1.5 2^119
+    other = z(1, 128, 8)
+    other[0, :, 2] = 2.0 ** -20
+    offsets = torch.tensor([0, M], dtype=torch.int32, device=dev)
+    # the gradients take one row (the others' are zero), of x or dy 2^-20
+    small = z(M, 128)
+    small[M - 1] = 2.0 ** -20
+    tape = torch.zeros((M, 8), device=dev)
+    tape[M - 1, 2] = top
+    down, up = other.transpose(1, 2).contiguous(), ends.transpose(1, 2).contiguous()
+    gd, _, dx = blr.blr_adapters_backward(small, a, down, up, offsets, None, scale, tape)
+    _, gu, _ = blr.blr_adapters_backward(a, small, ends, other, offsets, None, None, tape)
+    assert (num(gd)[0, 2] == top * 2.0 ** -20).all() and not num(gd)[0, 3].any()
+    assert (num(gu)[0, :, 2] == top * 2.0 ** -20).all() and not num(gu)[0, :, 3].any()
+    if act == "bfloat16":
+        y, s = blr.blr_adapters_forward(a, ends, other, offsets, keep_tape=True)
+        assert (num(s)[:, 2] == top).all()
+        assert (num(y) == 2.0 ** 108).all() and (num(dx) == 2.0 ** 108).all()
