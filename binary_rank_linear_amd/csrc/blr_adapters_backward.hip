@@ -4,7 +4,7 @@
 //   dy   ds = c dy B and dB, which both read dy: their workgroups take the rows
 //        in the same order, so that of a small dy the second read finds the
 //        last-level cache
-//   dx   dx = ds A, which writes, and dA, whose read of x is the last
+//   dx   dx = ds A, which writes, and dA, whose read of x is the only one
 //
 // 8192 x 4096 -> 4096 f32, rank 16: 58 + 64 us; 30000 x 5120 -> 17408 bf16, rank
 // 64: 425 + 196 us. Reads bound the first: dy passes twice, with the weights of
@@ -164,7 +164,8 @@ __global__ __launch_bounds__(256, RT <= 4 ? 2 : 1) void adapt_dx_kernel(AdaptExp
     if (first)
         ExpandBlock<TX, TW, RT, ACC>::run(ex, chunks, b, lds);
     else
-        GradBlock<TX, RT>::template run<true>(gr, 0, b, lds);
+        gr.once ? GradBlock<TX, RT>::template run<true>(gr, 0, b, lds)
+                : GradBlock<TX, RT>::template run<false>(gr, 0, b, lds);
 }
 
 // The partials of an adapter of several ranges, added in range order.
@@ -225,23 +226,34 @@ int64_t grad_blocks(const AdaptGrad &a, int which) {
 
 unsigned mix_blocks(const Mix &m) { return (unsigned)(8 * ((m.one + 7) / 8 + (m.two + 7) / 8)); }
 
-// dy that the last-level cache (256 MB) cannot hold is read by ds with loads
-// that ask not to be kept, which leaves the caches to the weights and panels:
-// 30000 rows of 17408 bf16 (1 GB) 425 us, 451 with ordinary loads. Smaller dy is
-// still there when the gradient reads it: 8192 rows of 4096 f32 (134 MB) 58 us,
-// 66 if not kept.
+// Rows that the last-level cache (256 MB) cannot hold are read with loads that
+// ask not to be kept where nothing reads them again while they could be there.
+// dy by ds, which leaves the caches to the weights and panels: 30000 rows of
+// 17408 bf16 (1 GB) 425 us, 451 with ordinary loads; smaller dy is still there
+// when the gradient reads it: 8192 rows of 4096 f32 (134 MB) 58 us, 66 if not
+// kept. x by its gradient, the call's only read of it, if over a quarter of the
+// cache, which it shares with dy, dx and the next call's: 16384 rows of 4096 f32
+// (268 MB), rank 16, 238 us a call, 242 with ordinary loads; 8192 rows 134 and 133,
+// with a layer's backward on the same x 290 and 295; 4096 rows (67 MB) 84 and
+// 79, with the layer 183 and 179.
 constexpr int64_t CACHE_BYTES = (int64_t)256 << 20;
+
+template <typename TX>
+int64_t row_bytes(int64_t rows, int64_t columns) {
+    return rows * columns * (int64_t)sizeof(TX);
+}
 
 template <typename TX, typename TW, int RT>
 hipError_t dy_t(AdaptShrink sh, const AdaptGrad &gr, hipStream_t s) {
-    sh.once = (int64_t)sh.plan.M * sh.K * (int64_t)sizeof(TX) > CACHE_BYTES;
+    sh.once = row_bytes<TX>(sh.plan.M, sh.K) > CACHE_BYTES;
     const Mix mix = {(int)(sh.splits * adapt_tiles(sh.plan.M, sh.plan.E, TM)), (int)grad_blocks(gr, 1)};
     hipLaunchKernelGGL((adapt_dy_kernel<TX, TW, RT>), dim3(mix_blocks(mix)), dim3(256), 0, s, sh, gr, mix);
     return hipGetLastError();
 }
 
 template <typename TX, typename TW, int RT>
-hipError_t dx_t(const AdaptExpand &ex, const AdaptGrad &gr, hipStream_t s) {
+hipError_t dx_t(const AdaptExpand &ex, AdaptGrad gr, hipStream_t s) {
+    gr.once = row_bytes<TX>(gr.plan.M, gr.job[0].N) > CACHE_BYTES / 4;
     const int64_t chunks = adapt_chunks(ex.plan.M, ex.plan.E, ex.N);
     const int64_t expands = ex.out ? chunks * adapt_tiles(ex.plan.M, ex.plan.E, TM) : 0;
     const Mix mix = {(int)expands, (int)grad_blocks(gr, 0)};

@@ -296,6 +296,7 @@ struct AdaptGrad {
     int r, act, acc, range;
     int64_t panels;  // that exist
     int64_t slots;   // partials that each `part` has room for
+    bool once;       // job 0's X is not worth keeping in the caches; set by its launcher
 };
 hipError_t launch_adapt_prepare(const AdaptPrepare &a, hipStream_t s);
 // id: the kernel kind that the launch is timed as.

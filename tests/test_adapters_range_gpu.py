@@ -122,3 +122,27 @@ def test_the_largest_values_stay_finite(dev, act, M):
         y, s = blr.blr_adapters_forward(a, ends, other, offsets, keep_tape=True)
         assert (num(s)[:, 2] == top).all()
         assert (num(y) == 2.0 ** 108).all() and (num(dx) == 2.0 ** 108).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act,d_in,r", [("float32", 65536, 24), ("float16", 131072, 8), ("bfloat16", 131072, 72)])
+def test_gradients_of_an_x_past_the_caches(dev, act, d_in, r):
+    """x of over 64 MB, which its gradient reads without keeping it, against the
+    formula in 64 bits: 3 products a row and a term for the roundings of ds."""
+    import torch
+    say(f"adapters, 300 rows of {d_in}, {act}, rank {r}")
+    M, d_out, E = 300, 128, 3
+    t = getattr(torch, act)
+    torch.manual_seed(r)
+    ids = torch.randint(-1, E, (M,), device=dev).int()
+    x, dy = torch.randn((M, d_in), device=dev).to(t), torch.randn((M, d_out), device=dev).to(t)
+    down, up = torch.randn((E, r, d_in), device=dev).to(t), torch.randn((E, d_out, r), device=dev).to(t)
+    tape = torch.randn((M, r), device=dev)
+    offsets, order, _ = blr.blr_route_sort(ids, E)
+    gd, _, none = blr.blr_adapters_backward(x, dy, down, up, offsets, order, None, tape, need_dx=False)
+    assert none is None
+    for e in range(E):
+        at = torch.nonzero(ids == e).flatten()
+        dys, xs, B = dy[at].double(), x[at].double(), up[e].double()
+        want, mag = (dys @ B).T @ xs, (dys.abs() @ B.abs()).T @ xs.abs()
+        ref.within(num(gd[e]), host(want), host(mag), 3 * len(at) + d_out + 4)
