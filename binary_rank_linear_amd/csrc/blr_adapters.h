@@ -9,8 +9,13 @@
 //
 // Rows are taken by the plan of the sort (blr_route.hip): a workgroup has a
 // tile of rows of one adapter, found from offsets by every wave for itself.
-// The rank is small, so every contraction is bound by its rows' bytes; the
-// kernels read them from memory straight into matrix operands, once.
+// The rank is small, so a contraction of 16-bit rows is bound by the rows' bytes.
+// So is one of f32 rows up to rank 32; 2 r flop for the 4 bytes of an element,
+// at the 153.6 TFLOP/s and 4.92 TB/s of large products and copies, meet at rank
+// 62, and ranks of 33 to 64 count as 64 here, larger ones as 128: there the
+// matrix instructions bound all of them but the forward's expand, which reads
+// y and writes it. A contraction takes its rows from memory once; ds and the
+// gradient of B each read dy.
 //
 // Rows of f32 run on v_mfma_f32_16x16x4_f32 (D += A B: lane l = 16 q + c gives
 // A[c][q] and B[q][c], and holds D[4 q + i][c], i < 4), with 16-bit adapters
@@ -692,10 +697,10 @@ __device__ void expand_tile(const AdaptExpand &a, const Tile &tile, int from, in
 // us, of which the f32 matrix instructions are busy 83 and HBM 150; 295 by the
 // loads above.
 //
-// Operand slots of 16 bytes: [tile h][group of ranks][lane], the 16 lanes c of a
-// q at c ^ (4 q + v) with v counting the pieces of four slots in the order they
-// lie in memory: then both the writes (along the ranks) and the reads (along
-// the lanes) spread over the banks.
+// Operand slots of 16 bytes: [part of an f16 weight][tile h][group of
+// ranks][lane], the 16 lanes c of a q at c ^ (4 q + v) with v counting the
+// pieces of four slots in the order they lie in memory: then both the writes
+// (along the ranks) and the reads (along the lanes) spread over the banks.
 template <typename TX, typename TW, int RT>
 struct ExpandLds {
     static constexpr bool WIDE = sizeof(TX) == 4;  // f32 rows: 4 ranks a slot, else 8

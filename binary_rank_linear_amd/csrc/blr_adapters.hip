@@ -73,8 +73,10 @@ int64_t adapt_chunks(int64_t M, int64_t E, int64_t N) {
 // a column, written and read again) costs much beside its rows. 8192 rows of
 // rank 16 over 4096 + 4096 columns in eight adapters: both gradients' launches
 // and the reduction take 133 us with 256 rows a range, 140 with 512, 169 with
-// 1024. Up to 512 rows a second range never pays for the reduction's launch
-// (6 us of 36).
+// 1024. Up to 512 rows there is one range: a second did not pay for the
+// reduction's launch in the one case measured, 300 f16 rows of rank 24 (6 us of
+// 36). Neither limit was measured for f32 at ranks over 32, where a range's
+// products take longest and a narrow layer leaves few workgroups.
 int64_t adapt_range(int64_t M, int64_t d_in, int64_t d_out, int64_t r) {
     const int64_t cols = (d_in + 255) / 256 + (d_out + 255) / 256;
     int64_t range = M * cols / FILL;
