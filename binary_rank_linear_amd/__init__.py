@@ -15,6 +15,7 @@ of the finite check and the power-of-two loss scale.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -38,7 +39,8 @@ def load():
         raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m binary_rank_linear_amd.build`")
     # torch brings a HIP runtime of its own. The library has to find that one in the process: loaded first it would
     # bring the system's, and torch's streams and memory mean nothing to another runtime.
-    import torch  # noqa: F401
+    with contextlib.suppress(ImportError):  # without torch there is one runtime, and the calls on sizes still work
+        import torch  # noqa: F401
     lib = ctypes.CDLL(LIB_PATH)
     i64, p, i32, f32, sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
     lib.blr_status_string.argtypes = [i32]

@@ -16,3 +16,11 @@ def test_one_runtime(first, second):
     r = subprocess.run([sys.executable, "-c", f"{first}\n{second}\n{LOOK}"], cwd=ROOT, capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and r.stdout.split() == ["1"], r.stdout + r.stderr
+
+
+def test_sizes_without_torch():
+    """A machine without torch can still ask for sizes and status texts."""
+    code = "import sys; sys.modules['torch'] = None\nimport binary_rank_linear_amd as b\n" \
+           "assert b.blr_workspace_bytes(64, 256, 256, 128) > 0 and b.status_string(-2)"
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
