@@ -9,7 +9,9 @@ gfx950, the calls raise.
 The functions carry the C names: `blr_expand_signs`, `blr_forward`,
 `blr_forward_noalloc`, `blr_backward`, `blr_backward_signs`, `blr_plane_linear`, `blr_sumsq`, `blr_workspace_bytes`,
 the token routing (`blr_route_sort`, `blr_route_gather`, `blr_route_combine`, `blr_route_combine_backward`) and the
-low-rank adapters beside a layer (`blr_adapters_forward`, `blr_adapters_backward`), plus the profiling calls;
+low-rank adapters beside a layer (`blr_adapters_forward`, `blr_adapters_backward`), the norms around a block
+(`blr_norm_forward`, `blr_norm_backward`) and rows kept in 8 bits (`blr_checkpoint_save`, `blr_checkpoint_load`), plus
+the profiling calls;
 `all_finite` and `next_gscale` are the host side
 of the finite check and the power-of-two loss scale.
 """
@@ -90,6 +92,18 @@ def load():
     lib.blr_adapters_backward.argtypes = [i64, i64, i64, i64, i64, i32, i32, p, p, p, p, p, p, p, p, p, p, i32, p, i32,
                                           p, sz, p]
     lib.blr_adapters_backward.restype = i32
+    lib.blr_checkpoint_save.argtypes = [i64, i64, i32, p, p, p, p]
+    lib.blr_checkpoint_save.restype = i32
+    lib.blr_checkpoint_load.argtypes = [i64, i64, i32, p, p, p, p]
+    lib.blr_checkpoint_load.restype = i32
+    lib.blr_norm_forward.argtypes = [i64, i64, i32, i32, i32, p, p, i32, p, p, i32, i64, f32, f32, p, f32, p, p, p, p, p,
+                                     p]
+    lib.blr_norm_forward.restype = i32
+    lib.blr_norm_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.blr_norm_workspace_bytes.restype = sz
+    lib.blr_norm_backward.argtypes = [i64, i64, i32, i32, i32, p, p, p, p, p, i32, p, p, p, i32, p, p, i32, i64, f32,
+                                      f32, p, p, p, p, p, p, p, i32, p, sz, p]
+    lib.blr_norm_backward.restype = i32
     lib.blr_profile_enable.argtypes = [i32]
     lib.blr_profile_enable.restype = i32
     lib.blr_profile_read.argtypes = [ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(i64),
@@ -681,6 +695,190 @@ def blr_adapters_backward(x, dy, down, up, offsets, order=None, scale=None, tape
     _launch("blr_adapters_backward", dev, stream, *sizes, at_x, at_dy, *at, at_tape, at_down, at_up,
             1 if accumulate_grads else 0, at_dx, 1 if accumulate_dx else 0, *work)
     return grad_down, grad_up, dx
+
+
+def _kept(t, name, shape, dev):
+    """Addresses of a checkpoint (q, b) of rows of this shape."""
+    import torch
+    try:
+        q, b = t
+    except (TypeError, ValueError):
+        raise TypeError(f"{name} must be a tensor of rows or a checkpoint (q, b)") from None
+    return (_at(q, f"{name} (q)", (torch.int8,), shape, dev),
+            _at(b, f"{name} (b)", (torch.uint8,), (*shape[:-1], shape[-1] // 32), dev))
+
+
+def _new_kept(kept, shape, dev, stream):
+    """(kept, its addresses), the pair allocated when it is True."""
+    import torch
+    if kept is True:
+        kept = (_new(shape, torch.int8, dev, stream), _new((*shape[:-1], shape[-1] // 32), torch.uint8, dev, stream))
+    return tuple(kept), _kept(kept, "kept", shape, dev)
+
+
+def blr_checkpoint_save(x, *, kept=True, stream=None):
+    """Rows x [M][d] in 8 bits: q [M][d] (int8) and b [M][d / 32] (uint8), each
+    32 values sharing the step 2^(b - 133). Returns (q, b), the given pair when
+    `kept` is one."""
+    code, M, d, dev = _rows(x, "x", stream)
+    if d % 32:
+        raise BlrError(-2, "blr_checkpoint_save")
+    at_x = _at(x, "x", (x.dtype,), (M, d), dev)
+    kept, at = _new_kept(kept, (M, d), dev, stream)
+    _launch("blr_checkpoint_save", dev, stream, M, d, code, at_x, *at)
+    return kept
+
+
+def blr_checkpoint_load(q, b, dtype, *, x=None, stream=None):
+    """The rows that a checkpoint stands for, in `dtype`. Returns x [M][d]."""
+    import torch
+    codes = _types()[4]
+    dev = _device(q, "q", (torch.int8,), stream)
+    M, d = _shape(q, "q", 2)
+    at = _kept((q, b), "kept", (M, d), dev)
+    if dtype not in codes:
+        raise TypeError(f"dtype is {dtype}, expected one of {_types()[2]}")
+    x, at_x = _out(x, "x", dtype, (M, d), dev, stream)
+    _launch("blr_checkpoint_load", dev, stream, M, d, codes[dtype], *at, at_x)
+    return x
+
+
+# how a gate opens
+GATE_LINEAR, GATE_SIGMOID, GATE_SILU = 0, 1, 2
+
+
+def workspace_norm(M: int, d: int, span: int = 1, device=None):
+    import torch
+    n = int(load().blr_norm_workspace_bytes(M, d, span))
+    if n == 0:
+        raise BlrError(-2, "blr_norm_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _norm_columns(d, w, w_after, gate, gate_rows, ft, dev):
+    """Addresses of w, w_after and the gate [gate_rows][d]."""
+    f32 = _types()[0]
+    return (None if w is None else _at(w, "w", f32, (d,), dev),
+            None if w_after is None else _at(w_after, "w_after", f32, (d,), dev),
+            None if gate is None else _at(gate, "gate", (ft,), (gate_rows, d), dev))
+
+
+def blr_norm_forward(x, f=None, w=None, *, norm_f=False, w_after=None, gate=None, gate_kind=GATE_LINEAR, span=1,
+                     skip=1.0, scale=1.0, eps=1e-6, n_dtype=None, need_n=True, out=None, n=None, stats=None,
+                     need_stats=True, keep=False, kept=None, stream=None):
+    """The residual stream after a block and the next block's normed rows:
+    out = skip x + scale phi(gate) v, v = f w_after (normed first with norm_f),
+    n = out rstd w. Without f, n is x normed and out is None. gate
+    [ceil(M / span)][d] in f's type: a row for every `span` rows. n has n_dtype
+    (x's type when not given). stats [2][M] is what the backward reads. With
+    `keep` (or a pair `kept` to write to) the checkpoint of out, or of x without
+    f, is formed too. Returns (out, n, stats, kept), None for what was not
+    formed."""
+    code, M, d, dev = _rows(x, "x", stream)
+    f32, _, wide, _, codes = _types()
+    at_x = _at(x, "x", (x.dtype,), (M, d), dev)
+    at_f = at_out = at_n = at_stats = None
+    ft = n_dtype if f is None else getattr(f, "dtype", None)
+    n_dtype = n_dtype or x.dtype
+    ft = ft or x.dtype
+    if f is not None:
+        at_f = _at(f, "f", wide, (M, d), dev)
+    elif out is not None or gate is not None or w_after is not None or norm_f:
+        raise ValueError("out, gate, w_after and norm_f need f")
+    if span < 1:
+        raise BlrError(-2, "blr_norm_forward")
+    if n_dtype not in codes:
+        raise TypeError(f"n_dtype is {n_dtype}, expected one of {wide}")
+    at_w, at_after, at_gate = _norm_columns(d, w, w_after, gate, -(-M // span), ft, dev)
+    if f is not None:
+        out, at_out = _out(out, "out", x.dtype, (M, d), dev, stream)
+    if need_n or n is not None:
+        n, at_n = _out(n, "n", n_dtype, (M, d), dev, stream)
+    if need_stats or stats is not None:
+        stats, at_stats = _out(stats, "stats", f32[0], (2, M), dev, stream)
+    at_kept = (None, None)
+    if keep or kept is not None:
+        if d % 32:
+            raise BlrError(-2, "blr_norm_forward")
+        kept, at_kept = _new_kept(True if kept is None else kept, (M, d), dev, stream)
+    _launch("blr_norm_forward", dev, stream, M, d, code, codes[ft], codes[n_dtype], at_x, at_f, 1 if norm_f else 0,
+            at_after, at_gate, gate_kind, span, skip, scale, at_w, eps, at_out, at_n, at_stats, *at_kept)
+    return out, n, stats, kept
+
+
+def blr_norm_backward(dn, dout, out, f=None, w=None, stats=None, *, has_f=None, f_dtype=None, x_dtype=None,
+                      norm_f=False, w_after=None, gate=None, gate_kind=GATE_LINEAR, span=1, skip=1.0, scale=1.0,
+                      dx=None, need_dx=True, df=None, need_df=True, dgate=None, dw=None, dw_after=None, grads=True,
+                      accumulate_grads=False, ws=None, stream=None):
+    """Gradients of blr_norm_forward, dn and dout those of n and of out (None: a
+    zero, for one of them). out and f are rows or checkpoints (q, b); the types
+    that neither they nor dout tell are x_dtype and f_dtype. f None: the forward
+    had none (has_f=True: it had, but its values do not take part). With `grads`
+    the gradients of w, w_after and gate are formed where these are given and
+    take part; overwritten unless accumulate_grads (dgate of span 1 always is).
+    Returns (dx, df, dgate, dw, dw_after), None for what was not formed."""
+    f32, _, wide, _, codes = _types()
+    rows, name = (dout, "dout") if dn is None else (dn, "dn")
+    code, M, d, dev = _rows(rows, name, stream)
+    has_f = f is not None if has_f is None else has_f
+    if not has_f and (f is not None or gate is not None or w_after is not None or norm_f):
+        raise ValueError("f, gate, w_after and norm_f need has_f")
+    if not grads and (dgate is not None or dw is not None or dw_after is not None):
+        raise ValueError("gradients are given, but grads is False")
+    if (dx is not None and not need_dx) or (df is not None and not (need_df and has_f)):
+        raise ValueError("dx or df is given, but not to be formed")
+    if (dw is not None and (w is None or dn is None)) or (dw_after is not None and w_after is None) or \
+            (dgate is not None and gate is None):
+        raise ValueError("dw needs w and dn, dw_after w_after, and dgate gate")
+    if span < 1:
+        raise BlrError(-2, "blr_norm_backward")
+    nt = rows.dtype if dn is not None else None
+    xt = dout.dtype if dout is not None else getattr(out, "dtype", None) or x_dtype
+    ft = getattr(f, "dtype", None) or f_dtype or (xt if not has_f else None)
+    if xt not in codes or ft not in codes:
+        raise TypeError(f"the type of the stream is {xt}, that of f {ft}: give x_dtype and f_dtype, of {wide}")
+    if xt != wide[0]:
+        nt = nt or xt
+    else:
+        nt = nt or wide[0]
+    shape = (M, d)
+
+    def given(t, name, dtype):
+        if t is None:
+            return None, (None, None)
+        if hasattr(t, "dtype"):
+            return _at(t, name, (dtype,), shape, dev), (None, None)
+        return None, _kept(t, name, shape, dev)
+
+    at_dn = None if dn is None else _at(dn, "dn", (nt,), shape, dev)
+    at_dout = None if dout is None else _at(dout, "dout", (xt,), shape, dev)
+    at_o, at_okept = given(out, "out", xt)
+    at_f, at_fkept = given(f, "f", ft)
+    gate_rows = -(-M // span)
+    at_w, at_after, at_gate = _norm_columns(d, w, w_after, gate, gate_rows, ft, dev)
+    at_stats = None if stats is None else _at(stats, "stats", f32, (2, M), dev)
+    form = dict(dgate=grads and gate is not None, dw=grads and w is not None and dn is not None,
+                dw_after=grads and w_after is not None)
+    if accumulate_grads and ((form["dw"] and dw is None) or (form["dw_after"] and dw_after is None) or
+                             (form["dgate"] and span > 1 and dgate is None)):
+        raise ValueError("what is accumulated into has to be given")
+    at_dx = at_df = at_dgate = at_dw = at_dafter = None
+    need = load().blr_norm_workspace_bytes(M, d, span) if ws is None else 0
+    ws, work = _ws(ws, need, "blr_norm_workspace_bytes", dev, stream)
+    if need_dx:
+        dx, at_dx = _out(dx, "dx", xt, shape, dev, stream)
+    if need_df and has_f:
+        df, at_df = _out(df, "df", ft, shape, dev, stream)
+    if form["dgate"]:
+        dgate, at_dgate = _out(dgate, "dgate", ft if span == 1 else f32[0], (gate_rows, d), dev, stream)
+    if form["dw"]:
+        dw, at_dw = _out(dw, "dw", f32[0], (d,), dev, stream)
+    if form["dw_after"]:
+        dw_after, at_dafter = _out(dw_after, "dw_after", f32[0], (d,), dev, stream)
+    _launch("blr_norm_backward", dev, stream, M, d, codes[xt], codes[ft], codes[nt], at_dn, at_dout, at_o, *at_okept,
+            1 if has_f else 0, at_f, *at_fkept, 1 if norm_f else 0, at_after, at_gate, gate_kind, span, skip, scale,
+            at_w, at_stats, at_dx, at_df, at_dgate, at_dw, at_dafter, 1 if accumulate_grads else 0, *work)
+    return dx, df, dgate, dw, dw_after
 
 
 def blr_sumsq(a, nparts: int = 64, stream=None) -> float:

@@ -936,6 +936,199 @@ int blr_adapters_backward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int
     return BLR_OK;
 }
 
+// ---------------------------------------------------- norms, checkpoints --
+namespace {
+constexpr int64_t MAX_WIDTH = (int64_t)1 << 20;
+
+bool rows_ok(int64_t M) { return M >= 1 && M < MAX_POSITIONS; }
+
+int checkpoint(int64_t M, int64_t d, int dtype, const void *x, const int8_t *q, const uint8_t *b, bool save,
+               void *stream) {
+    if (!x || !q || !b) return BLR_ERR_NULL;
+    if (!dtype_ok(dtype)) return BLR_ERR_DTYPE;
+    if (!rows_ok(M) || d < 32 || d % 32 || d > MAX_WIDTH) return BLR_ERR_SHAPE;
+    if (!aligned16(x) || !aligned16(q)) return BLR_ERR_ALIGN;
+    const size_t n = (size_t)(M * d);
+    const Span spans[] = {{x, n * size_of(dtype), !save}, {q, n, save}, {b, n / 32, save}};
+    if (!apart(spans, 3)) return BLR_ERR_OVERLAP;
+    const int st = current_device_ok();
+    if (st != BLR_OK) return st;
+    const Checkpoint a = {const_cast<void *>(x), const_cast<int8_t *>(q), const_cast<uint8_t *>(b), (int64_t)n, dtype};
+    BLR_TRY(launch_checkpoint(a, save, (hipStream_t)stream));
+    return BLR_OK;
+}
+
+bool norm_shape_ok(int64_t M, int64_t d, int64_t span) {
+    return rows_ok(M) && d >= 8 && d % 8 == 0 && d <= NORM_MAX_D && span >= 1;
+}
+
+bool norm_types_ok(int xt, int ft, int nt) {
+    return dtype_ok(xt) && dtype_ok(ft) && dtype_ok(nt) && (xt == BLR_F32 || (ft == xt && nt == xt));
+}
+
+// Sums of ranges: of dw, of dw_after, and two gates' parts where rows share gates.
+struct NormLayout {
+    size_t part_a, part_z, total;
+    int64_t per, ranges;
+};
+NormLayout norm_layout(int64_t M, int64_t d, int64_t span) {
+    NormLayout L;
+    L.ranges = norm_ranges(M, d, &L.per);
+    const size_t one = up((size_t)(L.ranges * d) * 4);
+    L.part_a = one;
+    L.part_z = 2 * one;
+    L.total = (span > 1 ? 4 : 2) * one;
+    return L;
+}
+
+// `a` all aligned to 16 bytes, and every output apart from the rest and from `more`.
+int arrays_ok(const Span *a, int n, const Span *more, int extra) {
+    Span spans[24];
+    for (int i = 0; i < n; ++i) {
+        if (!aligned16(a[i].p)) return BLR_ERR_ALIGN;
+        spans[i] = a[i];
+    }
+    for (int i = 0; i < extra; ++i) spans[n + i] = more[i];
+    return apart(spans, n + extra) ? BLR_OK : BLR_ERR_OVERLAP;
+}
+}  // namespace
+
+int blr_checkpoint_save(int64_t M, int64_t d, int dtype, const void *x, int8_t *q, uint8_t *b, void *stream) {
+    return checkpoint(M, d, dtype, x, q, b, true, stream);
+}
+
+int blr_checkpoint_load(int64_t M, int64_t d, int dtype, const int8_t *q, const uint8_t *b, void *x, void *stream) {
+    return checkpoint(M, d, dtype, x, q, b, false, stream);
+}
+
+int blr_norm_forward(int64_t M, int64_t d, int xt, int ft, int nt, const void *x, const void *f, int norm_f,
+                     const float *w_after, const void *gate, int gate_kind, int64_t span, float skip, float scale,
+                     const float *w, float eps, void *out, void *n, float *stats, int8_t *q, uint8_t *b,
+                     void *stream) {
+    if (!x || (f == nullptr) != (out == nullptr) || (q == nullptr) != (b == nullptr)) return BLR_ERR_NULL;
+    if (!f && !n && !stats && !q) return BLR_ERR_NULL;
+    if (!norm_types_ok(xt, ft, nt) || gate_kind < BLR_GATE_LINEAR || gate_kind > BLR_GATE_SILU) return BLR_ERR_DTYPE;
+    if (!norm_shape_ok(M, d, span) || (q && d % 32)) return BLR_ERR_SHAPE;
+    if (!aligned4(stats)) return BLR_ERR_ALIGN;
+    if (!f) w_after = nullptr, gate = nullptr, norm_f = 0;
+    if (span > M) span = M;
+    const size_t rows = (size_t)(M * d), col = (size_t)d * 4;
+    const Span arrays[] = {{x, rows * size_of(xt), false}, {f, rows * size_of(ft), false},
+                            {gate, (size_t)(ceil_div(M, span) * d) * size_of(ft), false}, {w_after, col, false},
+                            {w, col, false}, {out, rows * size_of(xt), true}, {n, rows * size_of(nt), true},
+                            {q, rows, true}};
+    const Span more[] = {{stats, (size_t)M * 8, true}, {b, rows / 32, true}};
+    int st = arrays_ok(arrays, 8, more, 2);
+    if (st != BLR_OK) return st;
+    st = current_device_ok();
+    if (st != BLR_OK) return st;
+    NormForward a = {};
+    a.x = x;
+    a.f = f;
+    a.gate = gate;
+    a.w_after = w_after;
+    a.w = w;
+    a.out = out;
+    a.n = n;
+    a.stats = stats;
+    a.q = q;
+    a.b = b;
+    a.M = M;
+    a.d = d;
+    a.span = (uint32_t)span;
+    a.xt = xt;
+    a.ft = ft;
+    a.nt = nt;
+    a.gate_kind = gate_kind;
+    a.norm_f = norm_f ? 1 : 0;
+    a.skip = skip;
+    a.scale = scale;
+    a.eps = eps;
+    BLR_TRY(launch_norm_forward(a, (hipStream_t)stream));
+    return BLR_OK;
+}
+
+size_t blr_norm_workspace_bytes(int64_t M, int64_t d, int64_t span) {
+    return norm_shape_ok(M, d, span) ? norm_layout(M, d, span).total : 0;
+}
+
+int blr_norm_backward(int64_t M, int64_t d, int xt, int ft, int nt, const void *dn, const void *dout, const void *out,
+                      const int8_t *out_q, const uint8_t *out_b, int has_f, const void *f, const int8_t *f_q,
+                      const uint8_t *f_b, int norm_f, const float *w_after, const void *gate, int gate_kind,
+                      int64_t span, float skip, float scale, const float *w, const float *stats, void *dx, void *df,
+                      void *dgate, float *dw, float *dw_after, int accumulate_grads, void *workspace,
+                      size_t workspace_bytes, void *stream) {
+    if (!has_f) {
+        // f's arguments mean nothing, and none of its gradients can be asked for
+        if (df || dgate || dw_after) return BLR_ERR_NULL;
+        f = f_q = nullptr, f_b = nullptr, norm_f = 0, w_after = nullptr, gate = nullptr, skip = 1.0f;
+    }
+    if ((out_q == nullptr) != (out_b == nullptr) || (f_q == nullptr) != (f_b == nullptr)) return BLR_ERR_NULL;
+    if ((out && out_q) || (f && f_q)) return BLR_ERR_NULL;  // one form or the other
+    if ((!dn && !dout) || (dn && !out && !out_q) || (dw && !dn) || (dgate && !gate)) return BLR_ERR_NULL;
+    const bool need_f = has_f && (norm_f || dw_after || dgate);
+    if (need_f && !f && !f_q) return BLR_ERR_NULL;
+    if ((dn || norm_f) && !stats) return BLR_ERR_NULL;
+    if (!dx && !df && !dgate && !dw && !dw_after) return BLR_ERR_NULL;
+    if (!norm_types_ok(xt, ft, nt) || gate_kind < BLR_GATE_LINEAR || gate_kind > BLR_GATE_SILU) return BLR_ERR_DTYPE;
+    if (!norm_shape_ok(M, d, span) || ((out_q || f_q) && d % 32)) return BLR_ERR_SHAPE;
+    const NormLayout L = norm_layout(M, d, span);
+    if (workspace == nullptr || workspace_bytes < L.total) return BLR_ERR_WORKSPACE;
+    if (!aligned4(stats)) return BLR_ERR_ALIGN;
+    const bool summed = span > 1;
+    if (span > M) span = M;
+    const size_t rows = (size_t)(M * d), col = (size_t)d * 4, x_size = rows * size_of(xt), f_size = rows * size_of(ft);
+    const size_t gates = (size_t)(ceil_div(M, span) * d);
+    const Span arrays[] = {{dn, rows * size_of(nt), false}, {dout, x_size, false}, {out, x_size, false},
+                            {out_q, rows, false}, {f, f_size, false}, {f_q, rows, false},
+                            {gate, gates * size_of(ft), false}, {w_after, col, false}, {w, col, false},
+                            {dx, x_size, true}, {df, f_size, true}, {dgate, gates * (summed ? 4 : size_of(ft)), true},
+                            {dw, col, true}, {dw_after, col, true}, {workspace, L.total, true}};
+    const Span more[] = {{stats, (size_t)M * 8, false}, {out_b, rows / 32, false}, {f_b, rows / 32, false}};
+    int st = arrays_ok(arrays, 15, more, 3);
+    if (st != BLR_OK) return st;
+    st = current_device_ok();
+    if (st != BLR_OK) return st;
+    NormBackward a = {};
+    a.dn = dn;
+    a.dout = dout;
+    a.out = dn ? out : nullptr;
+    a.out_q = out_q;
+    a.out_b = out_b;
+    a.f = f;
+    a.f_q = f_q;
+    a.f_b = f_b;
+    a.gate = gate;
+    a.w = w;
+    a.w_after = w_after;
+    a.stats = stats;
+    a.dx = dx;
+    a.df = df;
+    a.dgate = dgate;
+    a.dw = dw;
+    a.dw_after = dw_after;
+    a.part_w = (float *)workspace;
+    a.part_a = (float *)((char *)workspace + L.part_a);
+    a.part_z = (float *)((char *)workspace + L.part_z);
+    a.M = M;
+    a.d = d;
+    a.per = L.per;
+    a.ranges = L.ranges;
+    a.span = (uint32_t)span;
+    a.xt = xt;
+    a.ft = ft;
+    a.nt = nt;
+    a.gate_kind = gate_kind;
+    a.norm_f = norm_f ? 1 : 0;
+    a.acc = accumulate_grads ? 1 : 0;
+    a.need_f = need_f;
+    a.summed = summed;
+    a.skip = skip;
+    a.scale = has_f ? scale : 0.0f;
+    BLR_TRY(launch_norm_backward(a, (hipStream_t)stream));
+    return BLR_OK;
+}
+
 int blr_profile_enable(int max_launches) {
     std::lock_guard<std::mutex> lk(g_prof_mu);
     prof_release();

@@ -48,6 +48,11 @@ enum KernelId {
     K_ADAPT_THIN,   // adapters: ds as the gradient's operand
     K_ADAPT_DX_GRAD, // adapters: dx, and the gradient of A
     K_ADAPT_REDUCE, // adapters: the ranges' partials summed in order
+    K_NORM,         // norms: the stream after a block, the next block's rows
+    K_NORM_BWD,     // norms: gradients of rows, partials of the weights'
+    K_NORM_FINISH,  // norms: the ranges' partials summed in order
+    K_CHECKPOINT_SAVE, // rows to 8 bits
+    K_CHECKPOINT_LOAD, // and back
     K_COUNT
 };
 const char *kernel_name(int id);
@@ -314,6 +319,52 @@ int adapt_splits(int64_t M, int64_t E, int64_t K);
 int64_t adapt_range(int64_t M, int64_t d_in, int64_t d_out, int64_t r);
 // Partials of ranges that a gradient over M rows can leave.
 int64_t adapt_range_slots(int64_t M, int64_t E, int64_t range);
+
+// ------------------------------------------------- norms and checkpoints --
+// Widest row of the norms: 16 waves of 16 columns a thread.
+constexpr int64_t NORM_MAX_D = 16384;
+// Arrays as in include/blr.h; null where the call has none.
+struct NormForward {
+    const void *x, *f, *gate;
+    const float *w_after, *w;
+    void *out, *n;
+    float *stats;  // [2][M]
+    int8_t *q;     // checkpoint of out (of x without f)
+    uint8_t *b;
+    int64_t M, d;
+    uint32_t span;  // rows of a gate, at most M
+    int xt, ft, nt, gate_kind, norm_f;
+    float skip, scale, eps;
+};
+struct NormBackward {
+    const void *dn, *dout, *out, *f, *gate;
+    const int8_t *out_q, *f_q;  // instead of out, f
+    const uint8_t *out_b, *f_b;
+    const float *w, *w_after, *stats;
+    void *dx, *df, *dgate;
+    float *dw, *dw_after;
+    // sums of ranges: [ranges][d] each, and [ranges][2][d] of the gates that a
+    // range has only a part of
+    float *part_w, *part_a, *part_z;
+    int64_t M, d, per, ranges;
+    uint32_t span;
+    int xt, ft, nt, gate_kind, norm_f, acc;
+    bool need_f;  // f's values take part
+    bool summed;  // dgate is f32, a sum over the rows of each gate (also where that is one row)
+    float skip, scale;
+};
+hipError_t launch_norm_forward(const NormForward &a, hipStream_t s);
+hipError_t launch_norm_backward(const NormBackward &a, hipStream_t s);
+// Ranges of rows of the backward, and the rows of one.
+int64_t norm_ranges(int64_t M, int64_t d, int64_t *per);
+struct Checkpoint {
+    void *x;  // read by save, written by load
+    int8_t *q;
+    uint8_t *b;
+    int64_t n;  // values, a multiple of 32
+    int dtype;
+};
+hipError_t launch_checkpoint(const Checkpoint &a, bool save, hipStream_t s);
 
 // Profiling hooks around each launch (no-ops unless enabled).
 void prof_begin(int id, hipStream_t s);

@@ -2112,6 +2112,11 @@ const char *kernel_name(int id) {
         case K_ADAPT_DY: return "adapters_ds_grad_up";
         case K_ADAPT_DX_GRAD: return "adapters_dx_grad_down";
         case K_ADAPT_REDUCE: return "adapters_grad_reduce";
+        case K_NORM: return "norm";
+        case K_NORM_BWD: return "norm_backward";
+        case K_NORM_FINISH: return "norm_finish";
+        case K_CHECKPOINT_SAVE: return "checkpoint_save";
+        case K_CHECKPOINT_LOAD: return "checkpoint_load";
     }
     return "?";
 }

@@ -1,0 +1,508 @@
+// Norms before and after a block for gfx950, and rows kept in 8 bits.
+//
+//   forward   v = (norm_f ? f rstd_f : f) w_after   out = skip x + scale phi(z) v   n = out rstd w
+//             (without f: out is x), rstd = 1 / sqrt(mean(row^2) + eps)
+//   backward  dO = dout + J(w dn; out, rstd)        dx = skip dO
+//             p = scale phi(z) dO                   df = norm_f ? J(w_after p; f, rstd_f) : w_after p
+//             dw = sum dn out rstd                  dw_after = sum p (norm_f ? f rstd_f : f)
+//             dz = scale phi'(z) v dO, summed over the rows that share z
+//             with J(v; x, r) = r (v - x^ mean(v x^)), x^ = x r
+//
+// Both are passes over rows, bound by HBM. A workgroup takes a row whole, each
+// thread 8 C of its columns, in registers from the load to the last store, so
+// that every array crosses memory once. Sums over a row are f32: along a wave
+// by lane moves, over the row's waves through LDS, in a fixed order.
+#include "blr_internal.h"
+#include "blr_keep8.h"
+
+namespace blr {
+
+namespace {
+
+constexpr int MAX_WAVES = 16;
+
+// lane's value plus the one that a lane move of the row of 16 brings
+template <int CTRL>
+__device__ __forceinline__ float plus_dpp(float v) {
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+// The sum over a wave, in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+    v = plus_dpp<0xB1>(v);   // lane ^ 1
+    v = plus_dpp<0x4E>(v);   // lane ^ 2
+    v = plus_dpp<0x141>(v);  // mirrored within 8
+    v = plus_dpp<0x140>(v);  // mirrored within 16
+    const int i = __builtin_bit_cast(int, v);
+    auto lane = [i](int l) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(i, l)); };
+    return (lane(0) + lane(16)) + (lane(32) + lane(48));
+}
+
+// phi(z) and its slope. With e = exp(-|z|), 1 / (1 + e) and e / (1 + e) are
+// sigmoid(|z|) and sigmoid(-|z|), so that s (1 - s) loses nothing at the far
+// ends, and nothing overflows.
+__device__ __forceinline__ float phi(int kind, float z, float *slope) {
+    if (kind == 0) {
+        *slope = 1.0f;
+        return z;
+    }
+    const float e = expf(-fabsf(z)), big = 1.0f / (1.0f + e), small = e * big;
+    const float s = z >= 0.0f ? big : small, r = big * small;
+    *slope = kind == 1 ? r : s + z * r;
+    return kind == 1 ? s : z * s;
+}
+
+struct Team {
+    int tid, waves, team;
+    __device__ Team() : tid(threadIdx.x), waves(blockDim.x >> 6), team(__builtin_amdgcn_readfirstlane(threadIdx.y)) {}
+    // Sums of N values over the threads of a row; `slot` alternates between
+    // calls, so that one barrier a call is enough.
+    template <int N>
+    __device__ void sum(float *v, float *lds, int slot) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+        if (waves == 1) return;
+        float *at = lds + slot * N * MAX_WAVES;
+        if ((tid & 63) == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) at[i * MAX_WAVES + (tid >> 6)] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v[i] = 0.0f;
+            for (int w = 0; w < waves; ++w) v[i] += at[i * MAX_WAVES + w];
+        }
+    }
+};
+
+template <typename XT, typename FT, typename NT, int C>
+__global__ __launch_bounds__(64 * MAX_WAVES) void norm_forward_kernel(NormForward a) {
+    __shared__ float red[2 * MAX_WAVES];
+    const Team t;
+    const int64_t row = (int64_t)blockIdx.x * blockDim.y + t.team;
+    if (row >= a.M) return;  // whole waves: a workgroup of several rows has one wave for each
+    const int d = (int)a.d, chunks = d / 8, step = 64 * t.waves;
+    const float inv_d = 1.0f / (float)d;
+    const XT *x = (const XT *)a.x + row * d;
+    float v[C][8];
+    if (a.f) {
+        const FT *f = (const FT *)a.f + row * d;
+        const FT *z = (const FT *)a.gate + (a.gate ? (int64_t)((uint32_t)row / a.span) * d : 0);
+        Raw8<XT> xr[C];
+        Raw8<FT> fr[C], zr[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = t.tid + c * step;
+            if (k < chunks) {
+                fr[c] = raw8(f + 8 * k);
+                xr[c] = raw8(x + 8 * k);
+                if (a.gate) zr[c] = raw8(z + 8 * k);
+            }
+        }
+        float rf = 1.0f;
+        if (a.norm_f) {
+            float s = 0.0f;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (t.tid + c * step < chunks) {
+                    float e[8];
+                    widen8(fr[c], e);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s += e[i] * e[i];
+                }
+            t.sum<1>(&s, red, 0);
+            rf = 1.0f / sqrtf(s * inv_d + a.eps);
+        }
+        if (t.tid == 0 && a.stats) a.stats[a.M + row] = a.norm_f ? rf : 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = t.tid + c * step;
+            if (k >= chunks) continue;
+            float e[8], w[8], g[8];
+            widen8(fr[c], e);
+            if (a.w_after) {
+                widen8(raw8(a.w_after + 8 * k), w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e[i] = e[i] * rf * w[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e[i] = e[i] * rf;
+            }
+            if (a.gate) {
+                widen8(zr[c], g);
+                float unused;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e[i] *= phi(a.gate_kind, g[i], &unused);
+            }
+            widen8(xr[c], v[c]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[c][i] = a.skip * v[c][i] + a.scale * e[i];
+            const Raw8<XT> o = narrow8<XT>(v[c]);
+            put8((XT *)a.out + row * d + 8 * k, o);
+            widen8(o, v[c]);  // the norm, like the checkpoint, is of the rows as they are stored
+        }
+    } else {
+        if (t.tid == 0 && a.stats) a.stats[a.M + row] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            if (t.tid + c * step < chunks) widen8(raw8(x + 8 * (t.tid + c * step)), v[c]);
+    }
+    if (a.q)
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = t.tid + c * step;
+            if (k >= chunks) continue;  // four lanes together: d is a multiple of 32 here
+            const int b = keep_exponent(top_of_quad(top8(v[c])), KEEP_MAX<XT>);
+            *reinterpret_cast<uint2 *>(a.q + row * d + 8 * k) = keep8(v[c], b);
+            if ((t.tid & 3) == 0) a.b[row * (d / 32) + k / 4] = (uint8_t)b;
+        }
+    if (!a.n && !a.stats) return;
+    float s = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        if (t.tid + c * step < chunks)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += v[c][i] * v[c][i];
+    t.sum<1>(&s, red, 1);
+    const float r = 1.0f / sqrtf(s * inv_d + a.eps);
+    if (t.tid == 0 && a.stats) a.stats[row] = r;
+    if (!a.n) return;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int k = t.tid + c * step;
+        if (k >= chunks) continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c][i] *= r;
+        if (a.w) {
+            float w[8];
+            widen8(raw8(a.w + 8 * k), w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[c][i] *= w[i];
+        }
+        put8((NT *)a.n + row * d + 8 * k, narrow8<NT>(v[c]));
+    }
+}
+
+// What a row of the backward reads, in one chunk of 8 columns.
+template <typename XT, typename FT, typename NT>
+struct NormRow {
+    Raw8<XT> dout, out;
+    Raw8<FT> f, z;
+    Raw8<NT> dn;
+    int out_b, f_b;
+
+    __device__ __forceinline__ void load(const NormBackward &a, int64_t row, int k) {
+        const int64_t at = row * a.d + 8 * k;
+        if (a.dout) dout = raw8((const XT *)a.dout + at);
+        if (a.dn) {
+            dn = raw8((const NT *)a.dn + at);
+            if (a.out_q) {
+                const uint2 q = *reinterpret_cast<const uint2 *>(a.out_q + at);
+                __builtin_memcpy(&out, &q, 8);
+                out_b = a.out_b[row * (a.d / 32) + k / 4];
+            } else {
+                out = raw8((const XT *)a.out + at);
+            }
+        }
+        if (a.need_f) {
+            if (a.f_q) {
+                const uint2 q = *reinterpret_cast<const uint2 *>(a.f_q + at);
+                __builtin_memcpy(&f, &q, 8);
+                f_b = a.f_b[row * (a.d / 32) + k / 4];
+            } else {
+                f = raw8((const FT *)a.f + at);
+            }
+        }
+        if (a.gate) z = raw8((const FT *)a.gate + (int64_t)((uint32_t)row / a.span) * a.d + 8 * k);
+    }
+    template <typename T>
+    __device__ __forceinline__ static void rows(const Raw8<T> &r, bool kept, int b, float *o) {
+        if (kept) {
+            uint2 q;
+            __builtin_memcpy(&q, &r, 8);
+            kept8(q, b, o);
+        } else {
+            widen8(r, o);
+        }
+    }
+};
+
+__device__ __forceinline__ void put_sums(float *p, const float *v, bool add) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        vf4 *at = reinterpret_cast<vf4 *>(p) + h;
+        vf4 s = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+        if (add) s += *at;
+        *at = s;
+    }
+}
+
+// A team (a workgroup, or one of its waves for short rows) takes a range of
+// consecutive rows and keeps the sums over them in registers; they go to the
+// workspace, a row for each range, and the next launch adds those in order.
+// The row after the present one is loaded before the present one's sums.
+// m1 = mean(w dn x^) and the mean that df needs come out of one exchange:
+// with k = scale w_after phi f^, sum(k dO) = sum(k (dout + r w dn)) - r m1 sum(k x^).
+template <typename XT, typename FT, typename NT, int C, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void norm_backward_kernel(NormBackward a) {
+    __shared__ float red[2 * 3 * MAX_WAVES];
+    const Team t;
+    const int64_t range = (int64_t)blockIdx.x * blockDim.y + t.team;
+    if (range >= a.ranges) return;  // whole waves, as in the forward
+    const int64_t lo = range * a.per, hi = lo + a.per < a.M ? lo + a.per : a.M;
+    const int d = (int)a.d, chunks = d / 8, step = 64 * t.waves;
+    const float inv_d = 1.0f / (float)d;
+    float w[C][8], wa[C][8], sw[C][8], sa[C][8], sz[C][8];
+    NormRow<XT, FT, NT> in[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int k = t.tid + c * step;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            w[c][i] = wa[c][i] = 1.0f;
+            sw[c][i] = sa[c][i] = sz[c][i] = 0.0f;
+        }
+        if (k >= chunks) continue;
+        if (a.w) widen8(raw8(a.w + 8 * k), w[c]);
+        if (a.w_after) widen8(raw8(a.w_after + 8 * k), wa[c]);
+        in[c].load(a, lo, k);
+    }
+    const bool shared = a.dgate && a.summed;
+    for (int64_t row = lo; row < hi; ++row) {
+        const float r = a.dn ? a.stats[row] : 0.0f, rf = a.norm_f ? a.stats[a.M + row] : 1.0f;
+        float xh[C][8], fh[C][8], g[C][8], o[C][8], ph[C][8], sl[C][8];
+        float s[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = t.tid + c * step;
+            if (k >= chunks) continue;
+            if (a.dn) {
+                NormRow<XT, FT, NT>::rows(in[c].out, a.out_q != nullptr, in[c].out_b, xh[c]);
+                widen8(in[c].dn, g[c]);
+            }
+            if (a.dout) widen8(in[c].dout, o[c]);
+            if (a.need_f) NormRow<XT, FT, NT>::rows(in[c].f, a.f_q != nullptr, in[c].f_b, fh[c]);
+            if (a.gate) {
+                float z[8];
+                widen8(in[c].z, z);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ph[c][i] = phi(a.gate_kind, z[i], &sl[c][i]);
+            }
+            if (row + 1 < hi) in[c].load(a, row + 1, k);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (!a.dn) xh[c][i] = g[c][i] = 0.0f;
+                if (!a.dout) o[c][i] = 0.0f;
+                if (!a.need_f) fh[c][i] = 0.0f;
+                if (!a.gate) ph[c][i] = 1.0f, sl[c][i] = 0.0f;
+                xh[c][i] *= r;
+                fh[c][i] *= rf;
+                sw[c][i] += g[c][i] * xh[c][i];
+                g[c][i] *= w[c][i];
+                s[0] += g[c][i] * xh[c][i];
+                o[c][i] += r * g[c][i];
+                const float q = a.scale * wa[c][i] * ph[c][i] * fh[c][i];
+                s[1] += q * o[c][i];
+                s[2] += q * xh[c][i];
+            }
+        }
+        t.sum<3>(s, red, (int)(row & 1));
+        const float m1 = r * s[0] * inv_d;
+        const float m2 = (s[1] - m1 * s[2]) * inv_d;
+        const bool last = shared && ((uint32_t)(row + 1) % a.span == 0 || row + 1 == hi);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = t.tid + c * step;
+            if (k >= chunks) continue;
+            const int64_t at = row * d + 8 * k;
+            float dx[8], df[8], dz[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float dO = o[c][i] - m1 * xh[c][i];
+                const float p = a.scale * ph[c][i] * dO;
+                dx[i] = a.skip * dO;
+                df[i] = wa[c][i] * p;
+                if (a.norm_f) df[i] = rf * (df[i] - fh[c][i] * m2);
+                sa[c][i] += p * fh[c][i];
+                dz[i] = a.scale * sl[c][i] * wa[c][i] * fh[c][i] * dO;
+                sz[c][i] += dz[i];
+            }
+            if (a.dx) put8((XT *)a.dx + at, narrow8<XT>(dx));
+            if (a.df) put8((FT *)a.df + at, narrow8<FT>(df));
+            if (a.dgate && !shared) put8((FT *)a.dgate + at, narrow8<FT>(dz));
+            if (last) {
+                // the rows of this gate end here, or the range does: whole
+                // gates go to their place, parts of one to the workspace,
+                // slot 0 where it began before the range, 1 where it goes on
+                const int64_t group = (uint32_t)row / a.span, first = group * a.span, end = first + a.span < a.M ? first + a.span : a.M;
+                if (first >= lo && end <= hi)
+                    put_sums((float *)a.dgate + group * d + 8 * k, sz[c], a.acc);
+                else
+                    put_sums(a.part_z + (2 * range + (first >= lo ? 1 : 0)) * d + 8 * k, sz[c], false);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sz[c][i] = 0.0f;
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int k = t.tid + c * step;
+        if (k >= chunks) continue;
+        const bool one = a.ranges == 1;
+        if (a.dw) put_sums((one ? a.dw : a.part_w + range * d) + 8 * k, sw[c], one && a.acc);
+        if (a.dw_after) put_sums((one ? a.dw_after : a.part_a + range * d) + 8 * k, sa[c], one && a.acc);
+    }
+}
+
+// The ranges' sums in order: 32 columns to a workgroup, 32 lines of its
+// threads down the ranges, then the lines. blockIdx.y: dw, dw_after, and from
+// 2 on the gate whose rows begin in that range and go on past it.
+__global__ __launch_bounds__(256) void norm_finish_kernel(NormBackward a) {
+    __shared__ vf4 line[32][8];
+    const int d = (int)a.d, col = blockIdx.x * 32 + 4 * (threadIdx.x & 7), l = threadIdx.x >> 3;
+    const bool in = col < d;
+    const float *part;
+    float *out;
+    int64_t first, count, stride = d;
+    if (blockIdx.y < 2) {
+        part = blockIdx.y == 0 ? a.part_w : a.part_a;
+        out = blockIdx.y == 0 ? a.dw : a.dw_after;
+        if (!out) return;
+        first = 0;
+        count = a.ranges;
+    } else {
+        const int64_t range = blockIdx.y - 2, lo = range * a.per;
+        const int64_t hi = lo + a.per < a.M ? lo + a.per : a.M;
+        const int64_t group = (hi - 1) / a.span, begin = group * a.span;
+        const int64_t end = begin + a.span < a.M ? begin + a.span : a.M;
+        if (begin < lo || end <= hi) return;
+        part = a.part_z;
+        out = (float *)a.dgate + group * d;
+        stride = 2 * d;
+        first = range;
+        count = (end + a.per - 1) / a.per - range;
+    }
+    vf4 s = {};
+    if (in)
+        for (int64_t i = l; i < count; i += 32) {
+            const float *p = part + (first + i) * stride + col;
+            if (stride != d && i == 0) p += d;  // where the gate begins its sum lies in slot 1
+            s += *reinterpret_cast<const vf4 *>(p);
+        }
+    line[l][threadIdx.x & 7] = s;
+    __syncthreads();
+    if (l || !in) return;
+    s = a.acc ? *reinterpret_cast<vf4 *>(out + col) : vf4{};
+    vf4 sum = {};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sum += line[i][threadIdx.x & 7];
+    *reinterpret_cast<vf4 *>(out + col) = s + sum;
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void checkpoint_save_kernel(Checkpoint a) {
+    const int64_t n = a.n / 8, grid = (int64_t)gridDim.x * 256;
+    for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < n; k += grid) {  // n is a multiple of 4
+        float v[8];
+        widen8(raw8((const T *)a.x + 8 * k), v);
+        const int b = keep_exponent(top_of_quad(top8(v)), KEEP_MAX<T>);
+        *reinterpret_cast<uint2 *>(a.q + 8 * k) = keep8(v, b);
+        if ((threadIdx.x & 3) == 0) a.b[k / 4] = (uint8_t)b;
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void checkpoint_load_kernel(Checkpoint a) {
+    const int64_t n = a.n / 8, grid = (int64_t)gridDim.x * 256;
+    for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < n; k += grid) {
+        float v[8];
+        kept8(*reinterpret_cast<const uint2 *>(a.q + 8 * k), a.b[k / 4], v);
+        put8((T *)a.x + 8 * k, narrow8<T>(v));
+    }
+}
+
+struct Shape {
+    int c, waves, teams;
+};
+// Rows up to 512 C columns are one wave's, four rows to a workgroup; longer
+// ones a workgroup's, with as few waves as hold them.
+Shape shape_of(int64_t d, int c) {
+    const int waves = (int)((d + 512 * c - 1) / (512 * c));
+    return {c, waves, waves == 1 ? 4 : 1};
+}
+// Chunks of 8 columns per thread. Forward: one while 16 waves hold the row.
+int forward_chunks(int64_t d) { return d <= 512 * MAX_WAVES ? 1 : 2; }
+// Backward: one while 8 waves do, for with more a thread has 128 registers and
+// not the 256 that its sums and two rows want.
+int backward_chunks(int64_t d) { return d <= 512 * 8 ? 1 : 2; }
+
+template <typename F>
+hipError_t with_types(int xt, int ft, int nt, F f) {
+    if (xt == 1) return f(_Float16(), _Float16(), _Float16());
+    if (xt == 2) return f(__bf16(), __bf16(), __bf16());
+    auto third = [&](auto ftag) {
+        return nt == 0 ? f(float(), ftag, float()) : nt == 1 ? f(float(), ftag, _Float16()) : f(float(), ftag, __bf16());
+    };
+    return ft == 0 ? third(float()) : ft == 1 ? third(_Float16()) : third(__bf16());
+}
+
+template <typename K, typename A>
+hipError_t launch(int id, K kernel, dim3 grid, dim3 block, const A &a, hipStream_t s) {
+    prof_begin(id, s);
+    kernel<<<grid, block, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    prof_end(s);
+    return e;
+}
+
+}  // namespace
+
+hipError_t launch_norm_forward(const NormForward &a, hipStream_t s) {
+    const Shape sh = shape_of(a.d, forward_chunks(a.d));
+    const dim3 block(64 * sh.waves, sh.teams), grid((unsigned)((a.M + sh.teams - 1) / sh.teams));
+    return with_types(a.xt, a.ft, a.nt, [&](auto x, auto f, auto n) {
+        using X = decltype(x);
+        using F = decltype(f);
+        using N = decltype(n);
+        return launch(K_NORM, sh.c == 1 ? norm_forward_kernel<X, F, N, 1> : norm_forward_kernel<X, F, N, 2>, grid, block,
+                      a, s);
+    });
+}
+
+int64_t norm_ranges(int64_t M, int64_t d, int64_t *per) {
+    // two workgroups a CU: with more the partial sums cost more than the
+    // occupancy brings
+    const int64_t most = 512 * shape_of(d, backward_chunks(d)).teams;
+    *per = (M + most - 1) / most;
+    return (M + *per - 1) / *per;
+}
+
+hipError_t launch_norm_backward(const NormBackward &a, hipStream_t s) {
+    const Shape sh = shape_of(a.d, backward_chunks(a.d));
+    const dim3 block(64 * sh.waves, sh.teams), grid((unsigned)((a.ranges + sh.teams - 1) / sh.teams));
+    const hipError_t e = with_types(a.xt, a.ft, a.nt, [&](auto x, auto f, auto n) {
+        using X = decltype(x);
+        using F = decltype(f);
+        using N = decltype(n);
+        return launch(K_NORM_BWD, sh.c == 1      ? norm_backward_kernel<X, F, N, 1, 8>
+                                  : sh.waves <= 8 ? norm_backward_kernel<X, F, N, 2, 8>
+                                                  : norm_backward_kernel<X, F, N, 2, 16>,
+                      grid, block, a, s);
+    });
+    const bool gates = a.dgate && a.summed;
+    if (e != hipSuccess || a.ranges == 1 || !(a.dw || a.dw_after || gates)) return e;
+    return launch(K_NORM_FINISH, norm_finish_kernel,
+                  dim3((unsigned)((a.d + 31) / 32), gates ? 2 + (unsigned)a.ranges : 2), dim3(256), a, s);
+}
+
+hipError_t launch_checkpoint(const Checkpoint &a, bool save, hipStream_t s) {
+    const int64_t n = (a.n / 8 + 255) / 256, most = 256 * 32;
+    const dim3 grid((unsigned)(n < most ? n : most)), block(256);
+    auto run = [&](auto t) {
+        using T = decltype(t);
+        return save ? launch(K_CHECKPOINT_SAVE, checkpoint_save_kernel<T>, grid, block, a, s)
+                    : launch(K_CHECKPOINT_LOAD, checkpoint_load_kernel<T>, grid, block, a, s);
+    };
+    return a.dtype == 0 ? run(float()) : a.dtype == 1 ? run(_Float16()) : run(__bf16());
+}
+
+}  // namespace blr

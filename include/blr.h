@@ -61,7 +61,7 @@ typedef enum {
     BLR_ERR_ALIGN = -7,     /* a pointer is not 16-byte aligned */
     BLR_ERR_SCRATCH = -8,   /* sizes exceed the allocation-free forward's scratch */
     BLR_ERR_DTYPE = -9,     /* an element type, or a pair of them, that the call does not take */
-    BLR_ERR_OVERLAP = -10   /* an output shares memory with another argument (routing and adapter calls) */
+    BLR_ERR_OVERLAP = -10   /* an output shares memory with another argument (calls with element types, and the sort) */
 } blr_status;
 
 /* Human-readable text of a status code (static storage). */
@@ -220,7 +220,7 @@ int blr_plane_linear(int64_t M, int64_t n, int64_t k, const float *x, const uint
  */
 int blr_sumsq(const float *a, int64_t n, float *partials, int nparts, void *stream);
 
-/* Element types of the routing and adapter calls below. */
+/* Element types of the calls below. */
 typedef enum { BLR_F32 = 0, BLR_F16 = 1, BLR_BF16 = 2 } blr_dtype;
 
 /*
@@ -313,6 +313,80 @@ int blr_adapters_backward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int
                           const int32_t *order, const float *scale, const float *tape_s, float *grad_down,
                           float *grad_up, int accumulate_grads, void *dx, int accumulate_dx, void *workspace,
                           size_t workspace_bytes, void *stream);
+
+/*
+ * Activation checkpoints in 8 bits: rows [M][d] (of dtype) held as q [M][d]
+ * int8 and b [M][d / 32], a byte for each 32 consecutive values of a row.
+ * Value i of a block stands for q_i 2^(b - 133). save takes the least b for
+ * which the block's largest value rounds to at most 127 of those steps, and
+ * q_i = x_i 2^(133 - b) rounded to the nearest whole number, ties to even: no
+ * value is off by more than half a step, a 127th of the block's largest or
+ * less. Two cases stand apart. Types end: past 127 steps of their widest step
+ * (b = 142 for f16, 254 for f32 and bf16) values are cut off at 127 steps. And
+ * where a value is not finite, b is 255 and the whole block stands for NaN.
+ * load gives the values, rounded once where the type needs it; from a save of
+ * the same type they are exact. d a multiple of 32 up to 2^20, 1 <= M < 2^31 -
+ * 65536. Rows and q 16-byte aligned.
+ */
+int blr_checkpoint_save(int64_t M, int64_t d, int dtype, const void *x, int8_t *q, uint8_t *b, void *stream);
+int blr_checkpoint_load(int64_t M, int64_t d, int dtype, const int8_t *q, const uint8_t *b, void *x, void *stream);
+
+/* How a gate opens: phi(z) = z, 1 / (1 + exp(-z)), z / (1 + exp(-z)). */
+typedef enum { BLR_GATE_LINEAR = 0, BLR_GATE_SIGMOID = 1, BLR_GATE_SILU = 2 } blr_gate;
+
+/*
+ * Norms before and after a block, with its gate and residual scale, in one
+ * pass: the residual stream x [M][d] takes the block's result f [M][d], and
+ * the rows n that the next block reads are normed (root mean square):
+ *   v = f rstd_f w_after (norm_f = 1) or f w_after (norm_f = 0)
+ *   out = skip x + scale phi(z) v          n = out rstd w
+ *   rstd = 1 / sqrt(mean(out^2) + eps), rstd_f of f likewise
+ * x, out have type xt, f and the gate z type ft, n type nt: xt = BLR_F32 with
+ * any ft and nt, or all three the same 16-bit type. Weights are f32 [d], NULL
+ * for ones.
+ *   f NULL: the block's first norm; out is x (pass NULL), and norm_f, w_after,
+ *     gate, skip and scale are not read.
+ *   gate z [ceil(M / span)][d]: row t has z[t / span]; span = 1 is a gate for
+ *     each row, the rows of a sequence one for each sequence, span >= M one
+ *     for all. NULL: phi = 1. 1 <= span.
+ *   n NULL: not formed. stats f32 [2][M] (rstd, then rstd_f; zero where f is
+ *     not normed), which the backward reads; NULL: not kept (n NULL too: out
+ *     alone).
+ *   q, b: the checkpoint of out (of x when f is NULL), both or neither; then d
+ *     is a multiple of 32.
+ * n and the checkpoint are of out as it is stored, in its type.
+ *
+ * Backward, dn and dout the gradients that reach n and out (either may be
+ * NULL, a zero):
+ *   dO = dout + J(w dn; out, rstd)     dx = skip dO
+ *   p = scale phi(z) dO                df = J(w_after p; f, rstd_f) or w_after p
+ *   dw = sum dn out rstd               dw_after = sum p f rstd_f (or sum p f)
+ *   dgate = scale phi'(z) v dO, for span > 1 summed over the gate's rows
+ *   J(u; y, r) = r (u - y r mean(u y r))
+ * with out and f as rows or as checkpoints (out_q, out_b; f_q, f_b, and the
+ * rows NULL). f has to be given in one form or the other unless the forward
+ * had none, which has_f says; out may be left out with dn NULL, and f's values
+ * where norm_f = 0 and neither dw_after nor dgate is formed. Gradients not
+ * wanted are NULL. Without f dx = dO. dx has type xt, df ft; dgate ft with
+ * span = 1, f32 otherwise; dw, dw_after f32 [d]. accumulate_grads = 0
+ * overwrites dw, dw_after and the dgate of a span over 1, 1 adds to them.
+ *
+ * d a multiple of 8 up to 16384, 1 <= M < 2^31 - 65536; row arrays, q and
+ * weights 16-byte aligned, stats 4-byte. All arithmetic is f32, outputs of 16
+ * bits are rounded once. Results are the same on every run. Workspace of the
+ * backward: blr_norm_workspace_bytes, 0 for invalid sizes.
+ */
+int blr_norm_forward(int64_t M, int64_t d, int xt, int ft, int nt, const void *x, const void *f, int norm_f,
+                     const float *w_after, const void *gate, int gate_kind, int64_t span, float skip, float scale,
+                     const float *w, float eps, void *out, void *n, float *stats, int8_t *q, uint8_t *b,
+                     void *stream);
+size_t blr_norm_workspace_bytes(int64_t M, int64_t d, int64_t span);
+int blr_norm_backward(int64_t M, int64_t d, int xt, int ft, int nt, const void *dn, const void *dout, const void *out,
+                      const int8_t *out_q, const uint8_t *out_b, int has_f, const void *f, const int8_t *f_q,
+                      const uint8_t *f_b, int norm_f, const float *w_after, const void *gate, int gate_kind,
+                      int64_t span, float skip, float scale, const float *w, const float *stats, void *dx, void *df,
+                      void *dgate, float *dw, float *dw_after, int accumulate_grads, void *workspace,
+                      size_t workspace_bytes, void *stream);
 
 /*
  * Per-kernel timing with HIP events (the role of the page's trainer
