@@ -10,8 +10,8 @@ The functions carry the C names: `blr_expand_signs`, `blr_forward`,
 `blr_forward_noalloc`, `blr_backward`, `blr_backward_signs`, `blr_plane_linear`, `blr_sumsq`, `blr_workspace_bytes`,
 the token routing (`blr_route_sort`, `blr_route_gather`, `blr_route_combine`, `blr_route_combine_backward`) and the
 low-rank adapters beside a layer (`blr_adapters_forward`, `blr_adapters_backward`), the norms around a block
-(`blr_norm_forward`, `blr_norm_backward`) and rows kept in 8 bits (`blr_checkpoint_save`, `blr_checkpoint_load`), plus
-the profiling calls;
+(`blr_norm_forward`, `blr_norm_backward`), the gated feed-forward (`blr_gated_forward`, `blr_gated_backward`) and rows
+kept in 8 bits (`blr_checkpoint_save`, `blr_checkpoint_load`), plus the profiling calls;
 `all_finite` and `next_gscale` are the host side
 of the finite check and the power-of-two loss scale.
 """
@@ -104,6 +104,13 @@ def load():
     lib.blr_norm_backward.argtypes = [i64, i64, i32, i32, i32, p, p, p, p, p, i32, p, p, p, i32, p, p, i32, i64, f32,
                                       f32, p, p, p, p, p, p, p, i32, p, sz, p]
     lib.blr_norm_backward.restype = i32
+    lib.blr_gated_forward.argtypes = [i64, i64, i64, i32, i32, p, p, p, i32, p, p, p, p]
+    lib.blr_gated_forward.restype = i32
+    lib.blr_gated_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.blr_gated_workspace_bytes.restype = sz
+    lib.blr_gated_backward.argtypes = [i64, i64, i64, i32, i32, i32, p, p, p, p, p, p, i32, p, p, f32, p, i32, p, p, i32,
+                                       p, sz, p]
+    lib.blr_gated_backward.restype = i32
     lib.blr_profile_enable.argtypes = [i32]
     lib.blr_profile_enable.restype = i32
     lib.blr_profile_read.argtypes = [ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(i64),
@@ -879,6 +886,100 @@ def blr_norm_backward(dn, dout, out, f=None, w=None, stats=None, *, has_f=None, 
             1 if has_f else 0, at_f, *at_fkept, 1 if norm_f else 0, at_after, at_gate, gate_kind, span, skip, scale,
             at_w, at_stats, at_dx, at_df, at_dgate, at_dw, at_dafter, 1 if accumulate_grads else 0, *work)
     return dx, df, dgate, dw, dw_after
+
+
+# the gated feed-forward's activation
+ACT_SILU, ACT_GELU = 0, 1
+
+
+def workspace_gated(M: int, d: int, ff: int, device=None):
+    import torch
+    n = int(load().blr_gated_workspace_bytes(M, d, ff))
+    if n == 0:
+        raise BlrError(-2, "blr_gated_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _gated_weights(w_gate, w_up, stream):
+    """(ff, d, type, its number, GPU, the two addresses)."""
+    code, ff, d, dev = _rows(w_gate, "w_gate", stream)
+    t = w_gate.dtype
+    if code == 0:
+        raise BlrError(-9, "w_gate")
+    return ff, d, t, code, dev, (_at(w_gate, "w_gate", (t,), (ff, d), dev), _at(w_up, "w_up", (t,), (ff, d), dev))
+
+
+def _tape(tape, M, ff, dev):
+    """Addresses of g and u kept in 8 bits: q [2][M][ff], b [2][M][ff / 32]."""
+    return _kept(tape, "tape", (2, M, ff), dev)
+
+
+def blr_gated_forward(x, w_gate, w_up, *, kind=ACT_SILU, h_dtype=None, h=None, keep=False, tape=None, stream=None):
+    """h = act(x w_gate^T) * (x w_up^T) in one kernel: x [M][d], w_gate and w_up
+    [ff][d], all f16 or all bf16; h [M][ff] of h_dtype, theirs or f32. With `keep`
+    (or a pair `tape` to write to) the two projections are kept in 8 bits for
+    the backward: tape = (q [2][M][ff], b [2][M][ff / 32]). Returns (h, tape),
+    tape None when not kept."""
+    ff, d, t, code, dev, at_w = _gated_weights(w_gate, w_up, stream)
+    codes = _types()[4]
+    M = _shape(x, "x", 2)[0]
+    at_x = _at(x, "x", (t,), (M, d), dev)
+    h_dtype = h.dtype if h_dtype is None and h is not None else h_dtype or t
+    if h_dtype not in codes:
+        raise TypeError(f"h_dtype is {h_dtype}, expected one of {_types()[2]}")
+    h, at_h = _out(h, "h", h_dtype, (M, ff), dev, stream)
+    at_tape = (None, None)
+    if keep or tape is not None:
+        if ff % 32:
+            raise BlrError(-2, "blr_gated_forward")
+        tape, at_tape = _new_kept(True if tape is None else tape, (2, M, ff), dev, stream)
+    _launch("blr_gated_forward", dev, stream, M, d, ff, code, codes[h_dtype], at_x, *at_w, kind, at_h, *at_tape)
+    return h, tape
+
+
+def blr_gated_backward(x, dh, w_gate, w_up, tape=None, *, kind=ACT_SILU, gscale=1.0, dx=None, need_dx=True,
+                       accumulate_dx=False, dw_gate=None, dw_up=None, grads=True, grad_dtype=None,
+                       accumulate_grads=False, ws=None, stream=None):
+    """Gradients of blr_gated_forward from dh [M][ff] (of the weights' type, or
+    f32). x is rows or a checkpoint (q, b); the two projections come from the
+    tape, or are formed again without one. gscale: the power of two under which
+    dg and du are rounded to the weights' type. dw_gate and dw_up have
+    grad_dtype, the weights' type or f32. grads=False forms dx alone (x may then
+    be None with a tape), need_dx=False the weights' gradients alone. Outputs
+    not given are allocated; overwritten unless accumulate_dx /
+    accumulate_grads. Returns (dx, dw_gate, dw_up), None for what was not
+    formed."""
+    if (accumulate_grads and (dw_gate is None or dw_up is None)) or (accumulate_dx and dx is None):
+        raise ValueError("what is accumulated into has to be given")
+    if not grads and (dw_gate is not None or dw_up is not None):
+        raise ValueError("dw_gate and dw_up are given, but grads is False")
+    if not need_dx and dx is not None:
+        raise ValueError("dx is given, but need_dx is False")
+    ff, d, t, code, dev, at_w = _gated_weights(w_gate, w_up, stream)
+    f32, _, wide, _, codes = _types()
+    M = _shape(dh, "dh", 2)[0]
+    at_dh = _at(dh, "dh", (t, *f32), (M, ff), dev)
+    at_x, at_xkept = None, (None, None)
+    if x is not None and hasattr(x, "dtype"):
+        at_x = _at(x, "x", (t,), (M, d), dev)
+    elif x is not None:
+        at_xkept = _kept(x, "x", (M, d), dev)
+    at_tape = (None, None) if tape is None else _tape(tape, M, ff, dev)
+    grad_dtype = dw_gate.dtype if grad_dtype is None and dw_gate is not None else grad_dtype or t
+    if grad_dtype not in codes:
+        raise TypeError(f"grad_dtype is {grad_dtype}, expected one of {wide}")
+    need = load().blr_gated_workspace_bytes(M, d, ff) if ws is None else 0
+    ws, work = _ws(ws, need, "blr_gated_workspace_bytes", dev, stream)
+    at_dx = at_gate = at_up = None
+    if need_dx:
+        dx, at_dx = _out(dx, "dx", t, (M, d), dev, stream)
+    if grads:
+        dw_gate, at_gate = _out(dw_gate, "dw_gate", grad_dtype, (ff, d), dev, stream)
+        dw_up, at_up = _out(dw_up, "dw_up", grad_dtype, (ff, d), dev, stream)
+    _launch("blr_gated_backward", dev, stream, M, d, ff, code, codes[dh.dtype], codes[grad_dtype], at_x, *at_xkept, at_dh,
+            *at_w, kind, *at_tape, gscale, at_dx, 1 if accumulate_dx else 0, at_gate, at_up,
+            1 if accumulate_grads else 0, *work)
+    return dx, dw_gate, dw_up
 
 
 def blr_sumsq(a, nparts: int = 64, stream=None) -> float:

@@ -12,7 +12,8 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("blr_kernels.hip", "blr_route.hip", "blr_adapters.hip",
-                                                     "blr_adapters_backward.hip", "blr_norm.hip", "blr_api.hip")]
+                                                     "blr_adapters_backward.hip", "blr_norm.hip", "blr_gated.hip",
+                                                     "blr_api.hip")]
 HEADERS = [os.path.join(HERE, "csrc", f) for f in ("blr_internal.h", "blr_plan.h", "blr_vec.h", "blr_adapters.h",
                                                      "blr_keep8.h")] + \
     [os.path.join(ROOT, "include", "blr.h")]

@@ -1129,6 +1129,134 @@ int blr_norm_backward(int64_t M, int64_t d, int xt, int ft, int nt, const void *
     return BLR_OK;
 }
 
+// ---------------------------------------------------- gated feed-forward --
+namespace {
+bool gated_shape_ok(int64_t M, int64_t d, int64_t ff) {
+    return rows_ok(M) && d >= 128 && d % 128 == 0 && d <= MAX_WIDTH && ff >= 128 && ff % 128 == 0 && ff <= MAX_WIDTH &&
+           ceil_div(M, 128) * (ff / 64) < ((int64_t)1 << 31);
+}
+// dg and du side by side, then x out of its checkpoint.
+size_t gated_rows_at(int64_t M, int64_t ff) { return up((size_t)(M * ff) * 4); }
+bool half_type(int t) { return t == BLR_F16 || t == BLR_BF16; }
+}  // namespace
+
+int blr_gated_forward(int64_t M, int64_t d, int64_t ff, int dtype, int ht, const void *x, const void *w_gate,
+                      const void *w_up, int act, void *h, int8_t *tape_q, uint8_t *tape_b, void *stream) {
+    if (!x || !w_gate || !w_up || !h || (tape_q == nullptr) != (tape_b == nullptr)) return BLR_ERR_NULL;
+    if (!half_type(dtype) || (ht != dtype && ht != BLR_F32) || act < BLR_ACT_SILU || act > BLR_ACT_GELU)
+        return BLR_ERR_DTYPE;
+    if (!gated_shape_ok(M, d, ff)) return BLR_ERR_SHAPE;
+    const size_t w = (size_t)(ff * d) * 2, mid = (size_t)(M * ff);
+    const Span arrays[] = {{x, (size_t)(M * d) * 2, false}, {w_gate, w, false}, {w_up, w, false},
+                           {h, mid * size_of(ht), true}, {tape_q, 2 * mid, true}};
+    const Span more[] = {{tape_b, mid / 16, true}};
+    int st = arrays_ok(arrays, 5, more, 1);
+    if (st != BLR_OK) return st;
+    st = current_device_ok();
+    if (st != BLR_OK) return st;
+    GatedGemm a = {};
+    a.A = x;
+    a.B = w_gate;
+    a.B2 = w_up;
+    a.out = h;
+    a.tape_q = tape_q;
+    a.tape_b = tape_b;
+    a.M = M;
+    a.K = d;
+    a.lda = d;
+    a.ldb = d;
+    a.ff = ff;
+    a.dtype = dtype;
+    a.kind = act;
+    a.out_f32 = ht == BLR_F32;
+    BLR_TRY(launch_gated_forward(a, (hipStream_t)stream));
+    return BLR_OK;
+}
+
+size_t blr_gated_workspace_bytes(int64_t M, int64_t d, int64_t ff) {
+    return gated_shape_ok(M, d, ff) ? gated_rows_at(M, ff) + up((size_t)(M * d) * 2) : 0;
+}
+
+int blr_gated_backward(int64_t M, int64_t d, int64_t ff, int dtype, int ht, int gt, const void *x, const int8_t *x_q,
+                       const uint8_t *x_b, const void *dh, const void *w_gate, const void *w_up, int act,
+                       const int8_t *tape_q, const uint8_t *tape_b, float gscale, void *dx, int accumulate_dx,
+                       void *dw_gate, void *dw_up, int accumulate_grads, void *workspace, size_t workspace_bytes,
+                       void *stream) {
+    if (!dh || !w_gate || !w_up || (tape_q == nullptr) != (tape_b == nullptr) || (x_q == nullptr) != (x_b == nullptr) ||
+        (x && x_q) || (dw_gate == nullptr) != (dw_up == nullptr) || (!dx && !dw_gate))
+        return BLR_ERR_NULL;
+    if ((dw_gate || !tape_q) && !x && !x_q) return BLR_ERR_NULL;
+    if (!half_type(dtype) || (ht != dtype && ht != BLR_F32) || (gt != dtype && gt != BLR_F32) || act < BLR_ACT_SILU ||
+        act > BLR_ACT_GELU)
+        return BLR_ERR_DTYPE;
+    if (!gated_shape_ok(M, d, ff)) return BLR_ERR_SHAPE;
+    if (!pow2_scale_ok(gscale)) return BLR_ERR_SCALE;
+    const size_t need = blr_gated_workspace_bytes(M, d, ff);
+    if (workspace == nullptr || workspace_bytes < need) return BLR_ERR_WORKSPACE;
+    const size_t n = (size_t)(ff * d), mid = (size_t)(M * ff), rows = (size_t)(M * d);
+    const Span arrays[] = {{x, rows * 2, false}, {x_q, rows, false}, {dh, mid * size_of(ht), false},
+                           {w_gate, n * 2, false}, {w_up, n * 2, false}, {tape_q, 2 * mid, false}, {dx, rows * 2, true},
+                           {dw_gate, n * size_of(gt), true}, {dw_up, n * size_of(gt), true}, {workspace, need, true}};
+    const Span more[] = {{x_b, rows / 32, false}, {tape_b, mid / 16, false}};
+    int st = arrays_ok(arrays, 10, more, 2);
+    if (st != BLR_OK) return st;
+    st = current_device_ok();
+    if (st != BLR_OK) return st;
+    hipStream_t s = (hipStream_t)stream;
+    if (x_q && (dw_gate || !tape_q)) {
+        void *rows_x = (char *)workspace + gated_rows_at(M, ff);
+        const Checkpoint c = {rows_x, const_cast<int8_t *>(x_q), const_cast<uint8_t *>(x_b), M * d, dtype};
+        BLR_TRY(launch_checkpoint(c, false, s));
+        x = rows_x;
+    }
+    GatedGemm a = {};
+    a.dtype = dtype;
+    a.kind = act;
+    a.ff = ff;
+    // dg and du times gscale
+    GatedGemm g = a;
+    g.A = x;
+    g.B = w_gate;
+    g.B2 = w_up;
+    g.dh = dh;
+    g.out = workspace;
+    g.tape_q = const_cast<int8_t *>(tape_q);
+    g.tape_b = const_cast<uint8_t *>(tape_b);
+    g.M = M;
+    g.K = d;
+    g.lda = d;
+    g.ldb = d;
+    g.out_f32 = ht == BLR_F32;
+    g.scale = gscale;
+    BLR_TRY(tape_q ? launch_gated_gradients(g, s) : launch_gated_again(g, s));
+    a.scale = 1.0f / gscale;
+    a.N = (int)d;
+    a.A = workspace;
+    a.lda = 2 * ff;
+    a.ldb = d;
+    if (dx) {
+        GatedGemm v = a;
+        v.B = w_gate;
+        v.B2 = w_up;
+        v.out = dx;
+        v.M = M;
+        v.K = 2 * ff;
+        v.acc = accumulate_dx ? 1 : 0;
+        BLR_TRY(launch_gated_dx(v, s));
+    }
+    if (dw_gate) {
+        a.B = a.B2 = x;
+        a.out = dw_gate;
+        a.out2 = dw_up;
+        a.M = 2 * ff;
+        a.K = M;
+        a.out_f32 = gt == BLR_F32;
+        a.acc = accumulate_grads ? 1 : 0;
+        BLR_TRY(launch_gated_dw(a, s));
+    }
+    return BLR_OK;
+}
+
 int blr_profile_enable(int max_launches) {
     std::lock_guard<std::mutex> lk(g_prof_mu);
     prof_release();

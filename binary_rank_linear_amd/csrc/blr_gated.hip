@@ -1,0 +1,444 @@
+// The gated feed-forward for gfx950: h = act(g) * u, g = x Wg^T, u = x Wu^T,
+// and its backward, with dense f16 or bf16 rows and weights.
+//
+//   forward   one contraction over d for both projections; h in its epilogue
+//   backward  dg = dh u act'(g), du = dh act(g), side by side as D [M][2 ff]
+//             (from the projections kept in 8 bits, or by the forward's
+//             contraction again); then dx = D [Wg; Wu] and [dWg; dWu] = D^T x
+//
+// Products of 16-bit values are exact in the matrix instructions' f32 sums. D
+// is rounded to the rows' type once (times gscale, as f16 needs it for small
+// gradients): the products after it are of 16 bits, and its rounding is of
+// the size of the results' own.
+//
+// All three contractions are one kernel over tiles in LDS, bound by the matrix
+// units. An operand lies in memory with the contracted index innermost (x and
+// the weights of the forward, D of dx) or outermost (the weights of dx, both
+// operands of the weights' gradients). Either is copied to LDS as it lies,
+// 16 bytes a lane, without passing through registers; the first kind is read
+// back 8 contracted values to a lane, the second through the LDS's transposing
+// reads. Lanes copy their 16 bytes from a place XORed with the row, so that
+// neither read meets the same bank twice.
+#include "blr_internal.h"
+#include "blr_keep8.h"
+
+namespace blr {
+
+namespace {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+#define LDS_PTR(T) __attribute__((address_space(3))) T *
+
+__device__ __forceinline__ vf4 mma(s16x8 a, s16x8 b, vf4 c, _Float16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(vh8, a), __builtin_bit_cast(vh8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ vf4 mma(s16x8 a, s16x8 b, vf4 c, __bf16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(vb8, a), __builtin_bit_cast(vb8, b), c, 0, 0, 0);
+}
+
+// exp(v) to about 1e-7: the product with log2(e) is kept to twice its length,
+// whose tail enters as 1 + tail ln 2.
+__device__ __forceinline__ float exp_of(float v) {
+    const float L = 1.44269504088896340736f;
+    const float t = v * L, tail = fmaf(v, L, -t) + v * 1.92596299112661746887e-8f;
+    const float e = __builtin_amdgcn_exp2f(t);
+    return fmaf(e, tail * 0.69314718055994530942f, e);
+}
+// 1 / v, v >= 1, with one Newton step.
+__device__ __forceinline__ float inverse(float v) {
+    const float r = __builtin_amdgcn_rcpf(v);
+    return fmaf(fmaf(-v, r, 1.0f), r, r);
+}
+// act(g) and its slope. gelu is the form with tanh: 0.5 g (1 + tanh y) is
+// g sigmoid(2 y), y = sqrt(2 / pi) (g + 0.044715 g^3). Both ends stay finite:
+// the exponential is of -|.|.
+__device__ __forceinline__ float act(int kind, float g, float *slope) {
+    float y = g, dy = 1.0f;
+    if (kind) {
+        const float a = 1.59576912160573071176f, b = 0.044715f;  // 2 sqrt(2 / pi)
+        const float gg = g * g;
+        y = a * g * fmaf(b, gg, 1.0f);
+        dy = a * fmaf(3.0f * b, gg, 1.0f);
+    }
+    // past 200 the exponential is zero; y itself may be infinite. A NaN stays one.
+    if (fabsf(y) > 200.0f) y = copysignf(200.0f, y);
+    const float e = exp_of(-fabsf(y)), big = inverse(1.0f + e), small = e * big;
+    const float s = y >= 0.0f ? big : small;
+    // far out the slope's second term is zero, whatever y has grown to
+    const float r = big * small;
+    *slope = r == 0.0f ? s : fmaf(g * dy, r, s);
+    return g * s;
+}
+
+// ------------------------------------------------------------ contraction --
+// out[m][n] = sum_k A(m, k) B(n, k), tiles of BM x BN by 2 x BN / 64 waves, each
+// BM / 2 rows by 64 columns, in steps of 64 over k. The matrix instruction's
+// rows are n and its columns m, so that a lane holds neighbouring n of one m.
+constexpr int BK = 64;
+
+// n of row p (0 .. 15) of instruction tile j (0 .. 3) in a wave's 64 columns:
+// a lane has rows 4 (lane / 16) + 0 .. 3 of each tile, which makes 16
+// neighbouring columns; gated, 8 neighbouring columns of the gate (j = 0, 1)
+// and the same 8 of up (j = 2, 3).
+__device__ __forceinline__ int col_of(bool gated, int j, int p) {
+    return gated ? (p >> 2) * 8 + (j & 1) * 4 + (p & 3) : (p >> 2) * 16 + j * 4 + (p & 3);
+}
+
+__device__ __forceinline__ i32x4 resource(const void *p, uint32_t bytes) {
+    const uint64_t a = (uint64_t)p;
+    i32x4 r = {__builtin_amdgcn_readfirstlane((int)(uint32_t)a), __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)),
+               __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+    return r;
+}
+// 16 bytes a lane from rsrc + voff to LDS at lds + 16 lane; zeros from past the
+// resource's end. It is complete after a wait for vmcnt.
+#pragma clang diagnostic ignored "-Winline-asm"  // m0 is always the compiler's; it is named below all the same
+__device__ __forceinline__ void copy_to_lds(i32x4 rsrc, int voff, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(rsrc)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void wait_all() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void barrier() {
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+enum Role { FORWARD, AGAIN, DX, DW };
+
+// XOR of a 16-byte place in an LDS row of the second kind, by its contracted
+// index: rows of the matrix instruction's columns (m) take 32 bytes of each of
+// 8 LDS rows at once, those of its rows (n) 8 bytes of 4 places in each.
+__device__ __forceinline__ int twist_m(int k) { return ((k & 3) | ((k >> 1) & 4)) << 1; }
+__device__ __forceinline__ int twist_n(int k) { return (k & 1) | (k & 8); }
+
+template <typename T, Role R, int BM, int BN>
+struct Tile {
+    static constexpr bool gated = R == FORWARD || R == AGAIN;
+    static constexpr bool a_inner = R != DW, b_inner = gated;  // contracted index innermost
+    static constexpr int WN = BN / 64, WAVES = 2 * WN, MT = BM / 32;
+    static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, STAGE = A_BYTES + B_BYTES;
+    static constexpr int COPIES = 4;  // of either operand, by each wave
+    static_assert(A_BYTES == COPIES * WAVES * 1024 && B_BYTES == COPIES * WAVES * 1024, "copies fill the tiles");
+};
+
+template <typename T, Role R, int BM, int BN>
+__global__ __launch_bounds__(128 * (BN / 64)) void gated_kernel(GatedGemm a) {
+    using G = Tile<T, R, BM, BN>;
+    __shared__ __attribute__((aligned(1024))) char smem[2 * G::STAGE];
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS_PTR(char))smem;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wn = w % G::WN, wm = w / G::WN, p = lane & 15, g4 = lane >> 4;
+
+    // tiles of one XCD lie together, a group of rows' tiles beside each column's
+    int64_t tile = blockIdx.x;
+    {
+        const int64_t total = gridDim.x, per = total / 8, rest = total % 8, x = tile % 8;
+        tile = x * per + (x < rest ? x : rest) + tile / 8;
+    }
+    const int64_t group = tile / (a.group * a.tiles_n), in_group = tile % (a.group * a.tiles_n);
+    const int64_t first = group * a.group, rows = a.tiles_m - first < a.group ? a.tiles_m - first : a.group;
+    const int64_t m0 = (first + in_group % rows) * BM;
+    const int n0 = (int)(in_group / rows) * (G::gated ? BN / 2 : BN);
+
+    // what each lane copies: byte offsets from the tile's corner
+    int off_a[G::COPIES], off_b[G::COPIES];
+#pragma unroll
+    for (int i = 0; i < G::COPIES; ++i) {
+        const int c = w * G::COPIES + i;  // 1 KB of the tile
+        if constexpr (G::a_inner) {
+            const int row = c * 8 + (lane >> 3), at = (lane & 7) ^ (row & 7);
+            const int64_t left = a.M - 1 - m0;
+            const int64_t r = row < left ? row : left;  // rows past the last one are that one
+            off_a[i] = (int)(r * a.lda * 2 + at * 16);
+        } else {
+            constexpr int PLACES = BM / 8;
+            const int k = (c * 64 + lane) / PLACES, at = ((c * 64 + lane) % PLACES) ^ twist_m(k);
+            off_a[i] = (int)(k * a.lda * 2 + at * 16);
+            if (m0 + at * 8 >= a.M) off_a[i] = 0x7fffffff;  // past every resource's end: zeros
+        }
+        if constexpr (G::b_inner) {
+            const int row = c * 8 + (lane >> 3), at = (lane & 7) ^ (row & 7);
+            const int n = (row >> 6) * 32 + col_of(true, (row >> 4) & 3, row & 15);
+            off_b[i] = (int)((int64_t)n * a.ldb * 2 + at * 16);
+        } else {
+            constexpr int PLACES = BN / 8;
+            const int k = (c * 64 + lane) / PLACES, at = ((c * 64 + lane) % PLACES) ^ twist_n(k);
+            off_b[i] = (int)(k * a.ldb * 2 + at * 16);
+            if (n0 + at * 8 >= a.N) off_b[i] = 0x7fffffff;
+        }
+    }
+    const char *pa = (const char *)a.A + (G::a_inner ? m0 * a.lda * 2 : m0 * 2);
+    // forward: of the LDS rows that a wave copies all are of the gate or all of up
+    const char *pb = (const char *)(G::b_inner && (w & 1) ? a.B2 : a.B) + (G::b_inner ? (int64_t)n0 * a.ldb * 2 : (int64_t)n0 * 2);
+    const int64_t hop = (const char *)a.B2 - (const char *)a.B;
+
+    auto stage = [&](int64_t k0, int buf) {
+        const uint32_t at = lds0 + buf * G::STAGE + w * G::COPIES * 1024;
+        const int64_t left = a.K - k0 < BK ? a.K - k0 : BK;
+        i32x4 ra = G::a_inner ? resource(pa + k0 * 2, 0x7ffffffe)
+                                    : resource(pa + k0 * a.lda * 2, (uint32_t)((left * a.lda - m0) * 2));
+        const char *b = pb;
+        i32x4 rb;
+        if constexpr (G::b_inner) {
+            rb = resource(b + k0 * 2, 0x7ffffffe);
+        } else {
+            // dx: the contraction runs through Wg, then Wu
+            int64_t kb = k0;
+            if (R == DX && k0 >= a.K / 2) b += hop, kb -= a.K / 2;
+            rb = resource(b + kb * a.ldb * 2, (uint32_t)((left * a.ldb - n0) * 2));
+        }
+        // a vector instruction may have written them last, and the copies, which
+        // the compiler does not see as loads, need five cycles' distance from it
+        asm volatile("s_nop 4" : "+s"(ra), "+s"(rb));
+#pragma unroll
+        for (int i = 0; i < G::COPIES; ++i) copy_to_lds(ra, off_a[i], at + i * 1024);
+#pragma unroll
+        for (int i = 0; i < G::COPIES; ++i) copy_to_lds(rb, off_b[i], at + G::A_BYTES + i * 1024);
+    };
+
+    // an operand's 16 x 32 piece: lane = row (p), 8 contracted values (8 g4 on)
+    auto frag_a = [&](const char *s, int i, int kk) -> s16x8 {
+        if constexpr (G::a_inner) {
+            const int row = wm * (BM / 2) + i * 16 + p, at = (kk * 4 + g4) ^ (p & 7);
+            return *(const s16x8 *)(s + row * (BK * 2) + at * 16);
+        } else {
+            s16x8 v;
+            const int r = p >> 2, c = p & 3;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = kk * 32 + g4 * 8 + h * 4 + r;
+                const int at = ((wm * (BM / 2) + i * 16) / 8 + (c >> 1)) ^ twist_m(g4 * 8 + r);
+                const s16x4 q = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (LDS_PTR(s16x4))(s + k * (BM * 2) + at * 16 + (c & 1) * 8));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[4 * h + e] = q[e];
+            }
+            return v;
+        }
+    };
+    auto frag_b = [&](const char *s, int j, int kk) -> s16x8 {
+        if constexpr (G::b_inner) {
+            const int row = wn * 64 + j * 16 + p, at = (kk * 4 + g4) ^ (p & 7);
+            return *(const s16x8 *)(s + row * (BK * 2) + at * 16);
+        } else {
+            s16x8 v;
+            const int r = p >> 2, c = p & 3;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = kk * 32 + g4 * 8 + h * 4 + r;
+                const int at = (wn * 8 + c * 2 + (j >> 1)) ^ twist_n(g4 * 8 + r);
+                const s16x4 q = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (LDS_PTR(s16x4))(s + k * (BN * 2) + at * 16 + (j & 1) * 8));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[4 * h + e] = q[e];
+            }
+            return v;
+        }
+    };
+
+    vf4 acc[G::MT][4];
+#pragma unroll
+    for (int i = 0; i < G::MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = vf4{};
+
+    const int64_t steps = (a.K + BK - 1) / BK;
+    s16x8 xa[G::MT], xb[4], ya[G::MT], yb[4];
+    auto read = [&](s16x8 *fa, s16x8 *fb, int buf, int kk) {
+        const char *s = smem + buf * G::STAGE;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) fb[j] = frag_b(s + G::A_BYTES, j, kk);
+#pragma unroll
+        for (int i = 0; i < G::MT; ++i) fa[i] = frag_a(s, i, kk);
+    };
+    auto multiply = [&](const s16x8 *fa, const s16x8 *fb) {
+#pragma unroll
+        for (int i = 0; i < G::MT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = mma(fb[j], fa[i], acc[i][j], T());
+    };
+
+    // A step's second half is read while the first multiplies, the next step's
+    // first half while the second does; between them one barrier, at which the
+    // step's buffer is free and the next one's copies have arrived. Its own
+    // copies then have a whole step to arrive in.
+    stage(0, 0);
+    wait_all();
+    barrier();
+    if (steps > 1) stage(BK, 1);
+    read(xa, xb, 0, 0);
+    for (int64_t t = 0; t < steps; ++t) {
+        const int buf = (int)(t & 1);
+        read(ya, yb, buf, 1);
+        multiply(xa, xb);
+        wait_all();
+        barrier();
+        if (t + 2 < steps) stage((t + 2) * BK, buf);
+        if (t + 1 < steps) read(xa, xb, buf ^ 1, 0);
+        multiply(ya, yb);
+    }
+
+    // lane: row m, columns from n on
+#pragma unroll
+    for (int i = 0; i < G::MT; ++i) {
+        const int64_t m = m0 + wm * (BM / 2) + i * 16 + p;
+        if (m >= a.M) continue;  // whole quads of lanes with the same p
+        if constexpr (G::gated) {
+            const int n = n0 + wn * 32 + g4 * 8;
+            float gate[8], up[8], o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                gate[e] = acc[i][e >> 2][e & 3];
+                up[e] = acc[i][2 + (e >> 2)][e & 3];
+            }
+            const int64_t at = m * a.ff + n;
+            if constexpr (R == FORWARD) {
+                float unused;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = act(a.kind, gate[e], &unused) * up[e];
+                if (a.out_f32)
+                    put8((float *)a.out + at, narrow8<float>(o));
+                else
+                    put8((T *)a.out + at, narrow8<T>(o));
+                if (a.tape_q) {
+                    // the 32 columns of a block are those of the four lanes with this row
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float *v = h ? up : gate;
+                        uint32_t top = top8(v);
+                        top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+                        top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+                        const int b = keep_exponent(top, KEEP_MAX<float>);
+                        *(uint2 *)(a.tape_q + h * a.M * a.ff + at) = keep8(v, b);
+                        if (g4 == 0) a.tape_b[(h * a.M * a.ff + at) / 32] = (uint8_t)b;
+                    }
+                }
+            } else {
+                float dh[8], q[8];
+                if (a.out_f32)
+                    widen8(raw8((const float *)a.dh + at), dh);
+                else
+                    widen8(raw8((const T *)a.dh + at), dh);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float slope;
+                    const float v = dh[e] * a.scale;
+                    q[e] = v * act(a.kind, gate[e], &slope);
+                    o[e] = v * up[e] * slope;
+                }
+                T *d = (T *)a.out + m * 2 * a.ff + n;
+                put8(d, narrow8<T>(o));
+                put8(d + a.ff, narrow8<T>(q));
+            }
+        } else {
+            const int n = n0 + wn * 64 + g4 * 16;
+            if (n >= a.N) continue;  // N is a multiple of 16
+            char *out = (char *)a.out;
+            int64_t row = m;
+            if (R == DW && m >= a.M / 2) {
+                out = (char *)a.out2;
+                row -= a.M / 2;
+            }
+            const int64_t at = row * a.N + n;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float v[8], o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = acc[i][2 * h + (e >> 2)][e & 3] * a.scale;
+                if (a.out_f32) {
+                    float *q = (float *)out + at + 8 * h;
+                    if (a.acc) {
+                        widen8(raw8(q), o);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] += o[e];
+                    }
+                    put8(q, narrow8<float>(v));
+                } else {
+                    T *q = (T *)out + at + 8 * h;
+                    if (a.acc) {
+                        widen8(raw8(q), o);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] += o[e];
+                    }
+                    put8(q, narrow8<T>(v));
+                }
+            }
+        }
+    }
+}
+
+// D from the projections kept in 8 bits: rows down the grid's y, 8 columns a
+// thread along x.
+template <typename T>
+__global__ __launch_bounds__(256) void gated_gradients_kernel(GatedGemm a) {
+    const int64_t n = 8 * ((int64_t)blockIdx.x * blockDim.x + threadIdx.x), ups = a.M * a.ff;
+    if (n >= a.ff) return;
+    for (int64_t row = blockIdx.y; row < a.M; row += gridDim.y) {
+        const int64_t at = row * a.ff + n;
+        float gate[8], up[8], dh[8], o[8], q[8];
+        if (a.out_f32)
+            widen8(raw8((const float *)a.dh + at), dh);
+        else
+            widen8(raw8((const T *)a.dh + at), dh);
+        kept8(*(const uint2 *)(a.tape_q + at), a.tape_b[at / 32], gate);
+        kept8(*(const uint2 *)(a.tape_q + ups + at), a.tape_b[(ups + at) / 32], up);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float slope;
+            const float v = dh[e] * a.scale;
+            q[e] = v * act(a.kind, gate[e], &slope);
+            o[e] = v * up[e] * slope;
+        }
+        T *d = (T *)a.out + row * 2 * a.ff + n;
+        put8(d, narrow8<T>(o));
+        put8(d + a.ff, narrow8<T>(q));
+    }
+}
+
+constexpr int64_t GROUP = 8;
+
+template <typename T, Role R, int B>
+hipError_t contract(int id, GatedGemm a, hipStream_t s) {
+    a.tiles_m = (a.M + B - 1) / B;
+    const int64_t cols = Tile<T, R, B, B>::gated ? B / 2 : B, N = Tile<T, R, B, B>::gated ? a.ff : a.N;
+    a.tiles_n = (N + cols - 1) / cols;
+    a.group = a.tiles_m < GROUP ? a.tiles_m : GROUP;
+    prof_begin(id, s);
+    gated_kernel<T, R, B, B><<<dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(128 * (B / 64)), 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    prof_end(s);
+    return e;
+}
+
+template <Role R>
+hipError_t contract(int id, const GatedGemm &a, hipStream_t s) {
+    const bool gated = R == FORWARD || R == AGAIN;
+    const int64_t tiles = ((a.M + 255) / 256) * (((gated ? 2 * a.ff : a.N) + 255) / 256);
+    if (tiles >= 256)
+        return a.dtype == 1 ? contract<_Float16, R, 256>(id, a, s) : contract<__bf16, R, 256>(id, a, s);
+    return a.dtype == 1 ? contract<_Float16, R, 128>(id, a, s) : contract<__bf16, R, 128>(id, a, s);
+}
+
+}  // namespace
+
+hipError_t launch_gated_forward(const GatedGemm &a, hipStream_t s) { return contract<FORWARD>(K_GATED, a, s); }
+hipError_t launch_gated_again(const GatedGemm &a, hipStream_t s) { return contract<AGAIN>(K_GATED_AGAIN, a, s); }
+hipError_t launch_gated_dx(const GatedGemm &a, hipStream_t s) { return contract<DX>(K_GATED_DX, a, s); }
+hipError_t launch_gated_dw(const GatedGemm &a, hipStream_t s) { return contract<DW>(K_GATED_DW, a, s); }
+
+hipError_t launch_gated_gradients(const GatedGemm &a, hipStream_t s) {
+    const int64_t lanes = a.ff / 8, threads = lanes < 256 ? (lanes + 63) / 64 * 64 : 256;
+    const dim3 grid((unsigned)((lanes + threads - 1) / threads), (unsigned)(a.M < 16384 ? a.M : 16384)), block((unsigned)threads);
+    prof_begin(K_GATED_GRADIENTS, s);
+    if (a.dtype == 1)
+        gated_gradients_kernel<_Float16><<<grid, block, 0, s>>>(a);
+    else
+        gated_gradients_kernel<__bf16><<<grid, block, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    prof_end(s);
+    return e;
+}
+
+}  // namespace blr

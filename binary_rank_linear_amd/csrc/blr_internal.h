@@ -53,6 +53,11 @@ enum KernelId {
     K_NORM_FINISH,  // norms: the ranges' partials summed in order
     K_CHECKPOINT_SAVE, // rows to 8 bits
     K_CHECKPOINT_LOAD, // and back
+    K_GATED,        // gated feed-forward: both projections, act(g) u
+    K_GATED_AGAIN,  // both projections again, dg and du
+    K_GATED_GRADIENTS, // dg and du from the projections in 8 bits
+    K_GATED_DX,     // dx = dg Wg + du Wu
+    K_GATED_DW,     // dWg, dWu = dg^T x, du^T x
     K_COUNT
 };
 const char *kernel_name(int id);
@@ -365,6 +370,32 @@ struct Checkpoint {
     int dtype;
 };
 hipError_t launch_checkpoint(const Checkpoint &a, bool save, hipStream_t s);
+
+// ------------------------------------------------------ gated feed-forward --
+// One contraction out[m][n] = sum_k A(m, k) B(n, k) of 16-bit operands:
+//   forward, again  A = x [M][K], B = w_gate, B2 = w_up [ff][K]
+//   dx              A = D [M][K = 2 ff], B, B2 = w_gate, w_up [ff][N = d]
+//   dw              A = D [K tokens][M = 2 ff], B = x [K][N = d], out and out2
+//                   the upper and the lower half of the rows
+struct GatedGemm {
+    const void *A, *B, *B2;
+    const void *dh;  // again, gradients: [M][ff]
+    void *out, *out2;
+    int8_t *tape_q;  // [2][M][ff]: forward writes, gradients reads; null: none
+    uint8_t *tape_b;
+    int64_t M, K, lda, ldb;
+    int64_t tiles_m, tiles_n, group;  // filled by the launcher
+    int64_t ff;
+    int N, dtype, kind;
+    int out_f32;  // out (again, gradients: dh) is f32, not dtype
+    int acc;      // dx, dw: added to what out holds
+    float scale;  // of the product (again, gradients: of dh)
+};
+hipError_t launch_gated_forward(const GatedGemm &a, hipStream_t s);
+hipError_t launch_gated_again(const GatedGemm &a, hipStream_t s);
+hipError_t launch_gated_gradients(const GatedGemm &a, hipStream_t s);
+hipError_t launch_gated_dx(const GatedGemm &a, hipStream_t s);
+hipError_t launch_gated_dw(const GatedGemm &a, hipStream_t s);
 
 // Profiling hooks around each launch (no-ops unless enabled).
 void prof_begin(int id, hipStream_t s);

@@ -45,9 +45,9 @@ __device__ __forceinline__ void put8(T *p, const Raw8<T> &r) {
 // to 65536, which f16 does not hold, and f32's have no wider one. The values
 // above 127 steps are cut off there.
 template <typename T>
-constexpr int KEEP_MAX = 254;
+inline constexpr int KEEP_MAX = 254;
 template <>
-constexpr int KEEP_MAX<_Float16> = 142;
+inline constexpr int KEEP_MAX<_Float16> = 142;
 
 // Largest |v| as bits (so that a NaN is the largest of all) of the 8 values.
 __device__ __forceinline__ uint32_t top8(const float *v) {

@@ -2117,6 +2117,11 @@ const char *kernel_name(int id) {
         case K_NORM_FINISH: return "norm_finish";
         case K_CHECKPOINT_SAVE: return "checkpoint_save";
         case K_CHECKPOINT_LOAD: return "checkpoint_load";
+        case K_GATED: return "gated";
+        case K_GATED_AGAIN: return "gated_again";
+        case K_GATED_GRADIENTS: return "gated_gradients";
+        case K_GATED_DX: return "gated_dx";
+        case K_GATED_DW: return "gated_dw";
     }
     return "?";
 }

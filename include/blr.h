@@ -388,6 +388,48 @@ int blr_norm_backward(int64_t M, int64_t d, int xt, int ft, int nt, const void *
                       void *dgate, float *dw, float *dw_after, int accumulate_grads, void *workspace,
                       size_t workspace_bytes, void *stream);
 
+/* The gated feed-forward's activation: g / (1 + exp(-g)), or 0.5 g (1 +
+ * tanh(sqrt(2 / pi) (g + 0.044715 g^3))). */
+typedef enum { BLR_ACT_SILU = 0, BLR_ACT_GELU = 1 } blr_act;
+
+/*
+ * The gated feed-forward, both projections, activation and product in one
+ * kernel, with dense 16-bit rows and weights (a projection of blr_forward or
+ * blr_plane_linear brings h, f32 where they read it, back to d):
+ *   forward   g = x w_gate^T, u = x w_up^T       h = act(g) u
+ *   backward  dg = dh u act'(g), du = dh act(g)
+ *             dx (+)= dg w_gate + du w_up
+ *             dw_gate (+)= dg^T x    dw_up (+)= du^T x
+ *   x, dx [M][d], w_gate, w_up [ff][d] of dtype BLR_F16 or BLR_BF16; h, dh
+ *     [M][ff] of type ht, dw_gate, dw_up [ff][d] of type gt: dtype or BLR_F32.
+ *   tape_q [2][M][ff], tape_b [2][M][ff / 32]: g and u (f32) as checkpoints in
+ *     8 bits. The forward writes them, the backward takes g and u from them;
+ *     NULL (both): not kept, and formed again from x in the backward.
+ *   The backward's x as rows, or as a checkpoint (x_q, x_b, with x NULL), whose
+ *     values it takes in dtype; none where g and u come from the tape and no
+ *     weights' gradients are formed.
+ *   gscale, a positive finite power of two: dg and du are rounded to dtype
+ *     times gscale, and the products after them are divided by it, as in
+ *     blr_backward. In f16 it keeps small gradients out of the subnormals; in
+ *     bf16 1 does.
+ *   dx or the pair dw_gate, dw_up may be NULL (not formed). accumulate_dx and
+ *     accumulate_grads = 0 overwrite, 1 adds (in f32, then rounds).
+ * d, ff multiples of 128 up to 2^20, 1 <= M < 2^31 - 65536, with M / 128 ff / 64
+ * below 2^31. Products are exact and sums f32; h and the gradients are rounded
+ * once, and between the backward's contractions dg and du are of dtype. Rows do
+ * not touch each other in h and dx, whatever they hold. Results are the same
+ * on every run. Arrays 16-byte aligned (tape_b and x_b any). The backward's
+ * workspace: blr_gated_workspace_bytes, 0 for invalid sizes.
+ */
+int blr_gated_forward(int64_t M, int64_t d, int64_t ff, int dtype, int ht, const void *x, const void *w_gate,
+                      const void *w_up, int act, void *h, int8_t *tape_q, uint8_t *tape_b, void *stream);
+size_t blr_gated_workspace_bytes(int64_t M, int64_t d, int64_t ff);
+int blr_gated_backward(int64_t M, int64_t d, int64_t ff, int dtype, int ht, int gt, const void *x, const int8_t *x_q,
+                       const uint8_t *x_b, const void *dh, const void *w_gate, const void *w_up, int act,
+                       const int8_t *tape_q, const uint8_t *tape_b, float gscale, void *dx, int accumulate_dx,
+                       void *dw_gate, void *dw_up, int accumulate_grads, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
 /*
  * Per-kernel timing with HIP events (the role of the page's trainer
  * profiling marks). blr_profile_enable(n) creates a pool of event pairs for

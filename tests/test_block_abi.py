@@ -1,4 +1,4 @@
-"""Refusals of the norms' and checkpoints' calls (no GPU: every call fails its
+"""Refusals of the norms', checkpoints' and gated feed-forward's calls (no GPU: every call fails its
 checks before any device work, so its pointers are never followed)."""
 import ctypes
 
@@ -139,11 +139,75 @@ def test_norm_backward_refuses():
                     assert backward(**{**form, o: at(0), other: at(0)}) == E_OVERLAP, (o, other)
 
 
+GFWD = ("x", "w_gate", "w_up", "h", "tape_q", "tape_b")
+GBWD = ("x", "x_q", "x_b", "dh", "w_gate", "w_up", "tape_q", "tape_b", "dx", "dw_gate", "dw_up", "ws")
+
+
+def gated(M=4, d=128, ff=256, dtype=BF16, ht=BF16, kind=0, **kw):
+    return call("blr_gated_forward", (M, d, ff, dtype, ht, "x", "w_gate", "w_up", kind, "h", "tape_q", "tape_b"), GFWD, kw)
+
+
+def gated_backward(M=4, d=128, ff=256, dtype=BF16, ht=BF16, gt=BF16, kind=0, gscale=1.0, ws_bytes=BIG, **kw):
+    kw = {"x_q": None, "x_b": None, **kw}
+    return call("blr_gated_backward",
+                (M, d, ff, dtype, ht, gt, "x", "x_q", "x_b", "dh", "w_gate", "w_up", kind, "tape_q", "tape_b",
+                 f32(gscale), "dx", 0, "dw_gate", "dw_up", 0, "ws", ws_bytes), GBWD, kw)
+
+
+@pytest.mark.parametrize("caller", [gated, gated_backward])
+def test_gated_refuses(caller):
+    assert caller() in NO_GPU and caller(tape_q=None, tape_b=None) in NO_GPU
+    assert caller(dtype=F16, ht=F32, **({"gt": F16} if caller is gated_backward else {})) in NO_GPU
+    for kw in (dict(dtype=F32), dict(dtype=F32, ht=F32), dict(ht=F16), dict(dtype=3), dict(ht=-1), dict(kind=2),
+               dict(kind=-1)):
+        assert caller(**kw) == E_DTYPE, kw
+    for M, d, ff in [(0, 128, 128), ((1 << 31) - 65536, 128, 128), (4, 64, 128), (4, 192, 128), (4, 128, 0),
+                     (4, 128, 160), (4, (1 << 20) + 128, 128), (4, 128, (1 << 20) + 128), (1 << 30, 128, 1 << 20)]:
+        assert caller(M, d, ff) == E_SHAPE, (M, d, ff)
+        assert blr.load().blr_gated_workspace_bytes(M, d, ff) == 0
+    for k in ("w_gate", "w_up", "tape_q", "tape_b"):
+        assert caller(**{k: None}) == E_NULL, k
+    for k in ("x", "w_gate", "w_up", "tape_q"):
+        assert caller(**{k: 8}) == E_ALIGN, k
+    outs = ("h", "tape_q", "tape_b") if caller is gated else ("dx", "dw_gate", "dw_up", "ws")
+    there = GFWD if caller is gated else [k for k in GBWD if k not in ("x_q", "x_b")]
+    for o in outs:
+        for other in there:
+            if o != other:
+                assert caller(**{o: at(0), other: at(0)}) == E_OVERLAP, (o, other)
+
+
+def test_gated_forward_refuses():
+    for k in ("x", "h"):
+        assert gated(**{k: None}) == E_NULL, k
+    assert gated(h=8) == E_ALIGN
+
+
+def test_gated_backward_refuses():
+    for gt in (F16, 3):
+        assert gated_backward(gt=gt) == E_DTYPE
+    for g in (0.0, -1.0, 3.0, float("inf"), float("nan")):
+        assert gated_backward(gscale=g) == -3, g
+    for kw in (dict(dh=None), dict(x=None), dict(dw_up=None), dict(dx=None, dw_gate=None, dw_up=None),
+               dict(x_q=0, x_b=0), dict(x=None, x_q=0), dict(x=None, dw_gate=None, dw_up=None, tape_q=None, tape_b=None)):
+        assert gated_backward(**kw) == E_NULL, kw
+    for kw in (dict(x=None, x_q=0, x_b=0), dict(x=None, dw_gate=None, dw_up=None), dict(dx=None)):
+        assert gated_backward(**kw) in NO_GPU, kw
+    for k in ("dh", "dx", "dw_gate", "dw_up", "ws"):
+        assert gated_backward(**{k: 8}) == E_ALIGN, k
+    need = blr.load().blr_gated_workspace_bytes(1000, 128, 256)
+    assert need > 0 and gated_backward(1000, ws_bytes=need - 1) == E_WS and gated_backward(ws=None) == E_WS
+    assert gated_backward(1000, ws_bytes=need) in NO_GPU
+    for k in ("x_q", "x_b"):
+        assert gated_backward(**{**dict(x=None, x_q=0, x_b=0), k: at(0), "dx": at(0)}) == E_OVERLAP, k
+
+
 def test_binding_refuses():
     """The binding names what is wrong before it asks the library."""
     import torch
     x = torch.zeros((4, 64))
     for f in (lambda: blr.blr_norm_forward(x), lambda: blr.blr_checkpoint_save(x),
-              lambda: blr.blr_norm_backward(x, x, x), lambda: blr.blr_checkpoint_load(x, x, torch.float32)):
+              lambda: blr.blr_norm_backward(x, x, x), lambda: blr.blr_gated_forward(x, x, x),
+              lambda: blr.blr_gated_backward(x, x, x, x), lambda: blr.blr_checkpoint_load(x, x, torch.float32)):
         with pytest.raises((TypeError, ValueError)):
             f()
