@@ -1135,8 +1135,19 @@ bool gated_shape_ok(int64_t M, int64_t d, int64_t ff) {
     return rows_ok(M) && d >= 128 && d % 128 == 0 && d <= MAX_WIDTH && ff >= 128 && ff % 128 == 0 && ff <= MAX_WIDTH &&
            ceil_div(M, 128) * (ff / 64) < ((int64_t)1 << 31);
 }
-// dg and du side by side, then x out of its checkpoint.
-size_t gated_rows_at(int64_t M, int64_t ff) { return up((size_t)(M * ff) * 4); }
+// dg and du side by side, x out of its checkpoint, the sums of dx's splits.
+struct GatedLayout {
+    size_t rows, part, total;
+};
+GatedLayout gated_layout(int64_t M, int64_t d, int64_t ff) {
+    GatedLayout L;
+    int64_t steps;
+    const int64_t splits = gated_splits(M, d, 2 * ff, &steps);
+    L.rows = up((size_t)(M * ff) * 4);
+    L.part = L.rows + up((size_t)(M * d) * 2);
+    L.total = L.part + (splits > 1 ? up((size_t)(splits * M * d) * 4) : 0);
+    return L;
+}
 bool half_type(int t) { return t == BLR_F16 || t == BLR_BF16; }
 }  // namespace
 
@@ -1174,7 +1185,7 @@ int blr_gated_forward(int64_t M, int64_t d, int64_t ff, int dtype, int ht, const
 }
 
 size_t blr_gated_workspace_bytes(int64_t M, int64_t d, int64_t ff) {
-    return gated_shape_ok(M, d, ff) ? gated_rows_at(M, ff) + up((size_t)(M * d) * 2) : 0;
+    return gated_shape_ok(M, d, ff) ? gated_layout(M, d, ff).total : 0;
 }
 
 int blr_gated_backward(int64_t M, int64_t d, int64_t ff, int dtype, int ht, int gt, const void *x, const int8_t *x_q,
@@ -1191,7 +1202,8 @@ int blr_gated_backward(int64_t M, int64_t d, int64_t ff, int dtype, int ht, int 
         return BLR_ERR_DTYPE;
     if (!gated_shape_ok(M, d, ff)) return BLR_ERR_SHAPE;
     if (!pow2_scale_ok(gscale)) return BLR_ERR_SCALE;
-    const size_t need = blr_gated_workspace_bytes(M, d, ff);
+    const GatedLayout L = gated_layout(M, d, ff);
+    const size_t need = L.total;
     if (workspace == nullptr || workspace_bytes < need) return BLR_ERR_WORKSPACE;
     const size_t n = (size_t)(ff * d), mid = (size_t)(M * ff), rows = (size_t)(M * d);
     const Span arrays[] = {{x, rows * 2, false}, {x_q, rows, false}, {dh, mid * size_of(ht), false},
@@ -1204,7 +1216,7 @@ int blr_gated_backward(int64_t M, int64_t d, int64_t ff, int dtype, int ht, int 
     if (st != BLR_OK) return st;
     hipStream_t s = (hipStream_t)stream;
     if (x_q && (dw_gate || !tape_q)) {
-        void *rows_x = (char *)workspace + gated_rows_at(M, ff);
+        void *rows_x = (char *)workspace + L.rows;
         const Checkpoint c = {rows_x, const_cast<int8_t *>(x_q), const_cast<uint8_t *>(x_b), M * d, dtype};
         BLR_TRY(launch_checkpoint(c, false, s));
         x = rows_x;
@@ -1241,6 +1253,7 @@ int blr_gated_backward(int64_t M, int64_t d, int64_t ff, int dtype, int ht, int 
         v.out = dx;
         v.M = M;
         v.K = 2 * ff;
+        v.part = (float *)((char *)workspace + L.part);
         v.acc = accumulate_dx ? 1 : 0;
         BLR_TRY(launch_gated_dx(v, s));
     }

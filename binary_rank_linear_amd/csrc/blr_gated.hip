@@ -19,6 +19,8 @@
 // back 8 contracted values to a lane, the second through the LDS's transposing
 // reads. Lanes copy their 16 bytes from a place XORed with the row, so that
 // neither read meets the same bank twice.
+#include <type_traits>
+
 #include "blr_internal.h"
 #include "blr_keep8.h"
 
@@ -99,7 +101,11 @@ __device__ __forceinline__ void copy_to_lds(i32x4 rsrc, int voff, uint32_t lds) 
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(rsrc)
                  : "memory", "m0");
 }
-__device__ __forceinline__ void wait_all() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+// All but the last N copies have arrived, and every read of LDS.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void barrier() {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -113,7 +119,29 @@ enum Role { FORWARD, AGAIN, DX, DW };
 __device__ __forceinline__ int twist_m(int k) { return ((k & 3) | ((k >> 1) & 4)) << 1; }
 __device__ __forceinline__ int twist_n(int k) { return (k & 1) | (k & 8); }
 
-template <typename T, Role R, int BM, int BN>
+// Eight elements of a product go out, scaled, and added to what is there where
+// the call says so.
+template <typename T>
+__device__ __forceinline__ void put_product(const GatedGemm &a, char *out, int64_t at, float *v) {
+    float o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= a.scale;
+    auto put = [&](auto *q) {
+        using O = typename std::remove_pointer<decltype(q)>::type;
+        if (a.acc) {
+            widen8(raw8(q), o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += o[e];
+        }
+        put8(q, narrow8<O>(v));
+    };
+    if (a.out_f32)
+        put((float *)out + at);
+    else
+        put((T *)out + at);
+}
+
+template <typename T, Role R, int BM, int BN, int STEPS>
 struct Tile {
     static constexpr bool gated = R == FORWARD || R == AGAIN;
     static constexpr bool a_inner = R != DW, b_inner = gated;  // contracted index innermost
@@ -123,10 +151,10 @@ struct Tile {
     static_assert(A_BYTES == COPIES * WAVES * 1024 && B_BYTES == COPIES * WAVES * 1024, "copies fill the tiles");
 };
 
-template <typename T, Role R, int BM, int BN>
+template <typename T, Role R, int BM, int BN, int STEPS>
 __global__ __launch_bounds__(128 * (BN / 64)) void gated_kernel(GatedGemm a) {
-    using G = Tile<T, R, BM, BN>;
-    __shared__ __attribute__((aligned(1024))) char smem[2 * G::STAGE];
+    using G = Tile<T, R, BM, BN, STEPS>;
+    __shared__ __attribute__((aligned(1024))) char smem[STEPS * G::STAGE];
     const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS_PTR(char))smem;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wn = w % G::WN, wm = w / G::WN, p = lane & 15, g4 = lane >> 4;
@@ -137,6 +165,8 @@ __global__ __launch_bounds__(128 * (BN / 64)) void gated_kernel(GatedGemm a) {
         const int64_t total = gridDim.x, per = total / 8, rest = total % 8, x = tile % 8;
         tile = x * per + (x < rest ? x : rest) + tile / 8;
     }
+    const int64_t split = R == DX ? tile / (a.tiles_m * a.tiles_n) : 0;
+    tile -= split * a.tiles_m * a.tiles_n;
     const int64_t group = tile / (a.group * a.tiles_n), in_group = tile % (a.group * a.tiles_n);
     const int64_t first = group * a.group, rows = a.tiles_m - first < a.group ? a.tiles_m - first : a.group;
     const int64_t m0 = (first + in_group % rows) * BM;
@@ -174,28 +204,41 @@ __global__ __launch_bounds__(128 * (BN / 64)) void gated_kernel(GatedGemm a) {
     const char *pb = (const char *)(G::b_inner && (w & 1) ? a.B2 : a.B) + (G::b_inner ? (int64_t)n0 * a.ldb * 2 : (int64_t)n0 * 2);
     const int64_t hop = (const char *)a.B2 - (const char *)a.B;
 
-    auto stage = [&](int64_t k0, int buf) {
-        const uint32_t at = lds0 + buf * G::STAGE + w * G::COPIES * 1024;
+    // where a step's copies come from and go to
+    struct Source {
+        i32x4 a, b;
+        uint32_t to;
+    };
+    auto source = [&](int64_t k0, int buf) {
+        Source q;
+        q.to = lds0 + buf * G::STAGE + w * G::COPIES * 1024;
         const int64_t left = a.K - k0 < BK ? a.K - k0 : BK;
-        i32x4 ra = G::a_inner ? resource(pa + k0 * 2, 0x7ffffffe)
-                                    : resource(pa + k0 * a.lda * 2, (uint32_t)((left * a.lda - m0) * 2));
+        q.a = G::a_inner ? resource(pa + k0 * 2, 0x7ffffffe)
+                         : resource(pa + k0 * a.lda * 2, (uint32_t)((left * a.lda - m0) * 2));
         const char *b = pb;
-        i32x4 rb;
         if constexpr (G::b_inner) {
-            rb = resource(b + k0 * 2, 0x7ffffffe);
+            q.b = resource(b + k0 * 2, 0x7ffffffe);
         } else {
             // dx: the contraction runs through Wg, then Wu
             int64_t kb = k0;
             if (R == DX && k0 >= a.K / 2) b += hop, kb -= a.K / 2;
-            rb = resource(b + kb * a.ldb * 2, (uint32_t)((left * a.ldb - n0) * 2));
+            q.b = resource(b + kb * a.ldb * 2, (uint32_t)((left * a.ldb - n0) * 2));
         }
         // a vector instruction may have written them last, and the copies, which
         // the compiler does not see as loads, need five cycles' distance from it
-        asm volatile("s_nop 4" : "+s"(ra), "+s"(rb));
+        asm volatile("s_nop 4" : "+s"(q.a), "+s"(q.b));
+        return q;
+    };
+    auto copy = [&](const Source &q, int i) {
+        if (i < G::COPIES)
+            copy_to_lds(q.a, off_a[i], q.to + i * 1024);
+        else
+            copy_to_lds(q.b, off_b[i - G::COPIES], q.to + G::A_BYTES + (i - G::COPIES) * 1024);
+    };
+    auto stage = [&](int64_t k0, int buf) {
+        const Source q = source(k0, buf);
 #pragma unroll
-        for (int i = 0; i < G::COPIES; ++i) copy_to_lds(ra, off_a[i], at + i * 1024);
-#pragma unroll
-        for (int i = 0; i < G::COPIES; ++i) copy_to_lds(rb, off_b[i], at + G::A_BYTES + i * 1024);
+        for (int i = 0; i < 2 * G::COPIES; ++i) copy(q, i);
     };
 
     // an operand's 16 x 32 piece: lane = row (p), 8 contracted values (8 g4 on)
@@ -244,41 +287,83 @@ __global__ __launch_bounds__(128 * (BN / 64)) void gated_kernel(GatedGemm a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = vf4{};
 
-    const int64_t steps = (a.K + BK - 1) / BK;
+    // this workgroup's steps of the contraction: all, or a split's
+    const int64_t k_first = split * a.split_steps * BK;
+    int steps = (int)((a.K - k_first + BK - 1) / BK);
+    if (R == DX && steps > a.split_steps) steps = (int)a.split_steps;
     s16x8 xa[G::MT], xb[4], ya[G::MT], yb[4];
-    auto read = [&](s16x8 *fa, s16x8 *fb, int buf, int kk) {
+    // piece r of a half step's operands: n's four, then m's
+    auto read = [&](s16x8 *fa, s16x8 *fb, int buf, int kk, int r) {
         const char *s = smem + buf * G::STAGE;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) fb[j] = frag_b(s + G::A_BYTES, j, kk);
-#pragma unroll
-        for (int i = 0; i < G::MT; ++i) fa[i] = frag_a(s, i, kk);
+        if (r < 4)
+            fb[r] = frag_b(s + G::A_BYTES, r, kk);
+        else if (r < 4 + G::MT)
+            fa[r - 4] = frag_a(s, r - 4, kk);
     };
-    auto multiply = [&](const s16x8 *fa, const s16x8 *fb) {
+    auto multiply = [&](const s16x8 *fa, const s16x8 *fb, int i) {
 #pragma unroll
-        for (int i = 0; i < G::MT; ++i)
+        for (int j = 0; j < 4; ++j) acc[i][j] = mma(fb[j], fa[i], acc[i][j], T());
+    };
+    // Reads and copies are handed out among the products, so that the matrix
+    // units start at once after the barrier; the order is the one written.
+    constexpr int ROWS = G::a_inner ? G::MT / 2 : G::MT * 3 / 4;  // rows of products that take reads
+    constexpr int READS = (4 + G::MT + ROWS - 1) / ROWS;
+    constexpr int COPIES = 2 * G::COPIES / (G::MT / 2);
+    auto step = [&](int t, auto copies, auto reads) {
+        const int buf = t % STEPS, next = (t + 1) % STEPS;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = mma(fb[j], fa[i], acc[i][j], T());
+        for (int i = 0; i < G::MT; ++i) {
+            if (i < ROWS)
+#pragma unroll
+                for (int r = 0; r < READS; ++r) read(ya, yb, buf, 1, i * READS + r);
+            multiply(xa, xb, i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        // of the steps after the next one, as many as there are may be on their way
+        if constexpr (decltype(copies)::value)
+            wait_copies<2 * G::COPIES *(STEPS - 2)>();
+        else if (STEPS > 3 && t + 3 < steps)
+            wait_copies<4 * G::COPIES>();
+        else if (STEPS > 2 && t + 2 < steps)
+            wait_copies<2 * G::COPIES>();
+        else
+            wait_copies<0>();
+        barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        Source q;
+        if constexpr (decltype(copies)::value) q = source(k_first + (int64_t)(t + STEPS) * BK, buf);
+#pragma unroll
+        for (int i = 0; i < G::MT; ++i) {
+            if (decltype(copies)::value && i < G::MT / 2)
+#pragma unroll
+                for (int c = 0; c < COPIES; ++c) copy(q, i * COPIES + c);
+            if (decltype(reads)::value && i < ROWS)
+#pragma unroll
+                for (int r = 0; r < READS; ++r) read(xa, xb, next, 0, i * READS + r);
+            multiply(ya, yb, i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
 
     // A step's second half is read while the first multiplies, the next step's
     // first half while the second does; between them one barrier, at which the
-    // step's buffer is free and the next one's copies have arrived. Its own
-    // copies then have a whole step to arrive in.
-    stage(0, 0);
-    wait_all();
+    // step's buffer is free and the next one's copies have arrived. With STEPS
+    // buffers a step's copies have STEPS - 1 steps to arrive in.
+    using Yes = std::true_type;
+    using No = std::false_type;
+    static_assert(STEPS <= 4, "the waits at the end tell up to three steps apart");
+    for (int i = 0; i < STEPS && i < steps; ++i) stage(k_first + (int64_t)i * BK, i);
+    if (steps < STEPS)
+        wait_copies<0>();
+    else
+        wait_copies<2 * G::COPIES *(STEPS - 1)>();
     barrier();
-    if (steps > 1) stage(BK, 1);
-    read(xa, xb, 0, 0);
-    for (int64_t t = 0; t < steps; ++t) {
-        const int buf = (int)(t & 1);
-        read(ya, yb, buf, 1);
-        multiply(xa, xb);
-        wait_all();
-        barrier();
-        if (t + 2 < steps) stage((t + 2) * BK, buf);
-        if (t + 1 < steps) read(xa, xb, buf ^ 1, 0);
-        multiply(ya, yb);
-    }
+#pragma unroll
+    for (int r = 0; r < 4 + G::MT; ++r) read(xa, xb, 0, 0, r);
+    int t = 0;
+    for (; t + STEPS < steps; ++t) step(t, Yes(), Yes());
+    for (; t + 1 < steps; ++t) step(t, No(), Yes());
+    step(t, No(), No());
 
     // lane: row m, columns from n on
 #pragma unroll
@@ -335,37 +420,42 @@ __global__ __launch_bounds__(128 * (BN / 64)) void gated_kernel(GatedGemm a) {
         } else {
             const int n = n0 + wn * 64 + g4 * 16;
             if (n >= a.N) continue;  // N is a multiple of 16
+            if (R == DX && a.splits > 1) {
+                float *q = a.part + (split * a.M + m) * a.N + n;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) ((vf4 *)q)[j] = acc[i][j];
+                continue;
+            }
             char *out = (char *)a.out;
             int64_t row = m;
             if (R == DW && m >= a.M / 2) {
                 out = (char *)a.out2;
                 row -= a.M / 2;
             }
-            const int64_t at = row * a.N + n;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float v[8], o[8];
+                float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = acc[i][2 * h + (e >> 2)][e & 3] * a.scale;
-                if (a.out_f32) {
-                    float *q = (float *)out + at + 8 * h;
-                    if (a.acc) {
-                        widen8(raw8(q), o);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] += o[e];
-                    }
-                    put8(q, narrow8<float>(v));
-                } else {
-                    T *q = (T *)out + at + 8 * h;
-                    if (a.acc) {
-                        widen8(raw8(q), o);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] += o[e];
-                    }
-                    put8(q, narrow8<T>(v));
-                }
+                for (int e = 0; e < 8; ++e) v[e] = acc[i][2 * h + (e >> 2)][e & 3];
+                put_product<T>(a, out, row * a.N + n + 8 * h, v);
             }
         }
+    }
+}
+
+// The splits' products summed in order.
+template <typename T>
+__global__ __launch_bounds__(256) void gated_sum_kernel(GatedGemm a) {
+    const int64_t n = a.M * a.N, grid = (int64_t)gridDim.x * 2048;
+    for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; at < n; at += grid) {
+        float v[8], o[8];
+        widen8(raw8(a.part + at), v);
+        for (int q = 1; q < a.splits; ++q) {
+            widen8(raw8(a.part + q * n + at), o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += o[e];
+        }
+        put_product<T>(a, (char *)a.out, at, v);
     }
 }
 
@@ -399,29 +489,69 @@ __global__ __launch_bounds__(256) void gated_gradients_kernel(GatedGemm a) {
 
 constexpr int64_t GROUP = 8;
 
-template <typename T, Role R, int B>
+template <typename T, Role R, int B, int STEPS>
 hipError_t contract(int id, GatedGemm a, hipStream_t s) {
+    using G = Tile<T, R, B, B, STEPS>;
     a.tiles_m = (a.M + B - 1) / B;
-    const int64_t cols = Tile<T, R, B, B>::gated ? B / 2 : B, N = Tile<T, R, B, B>::gated ? a.ff : a.N;
+    const int64_t cols = G::gated ? B / 2 : B, N = G::gated ? a.ff : a.N;
     a.tiles_n = (N + cols - 1) / cols;
     a.group = a.tiles_m < GROUP ? a.tiles_m : GROUP;
     prof_begin(id, s);
-    gated_kernel<T, R, B, B><<<dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(128 * (B / 64)), 0, s>>>(a);
+    gated_kernel<T, R, B, B, STEPS><<<dim3((unsigned)(a.tiles_m * a.tiles_n * a.splits)), dim3(64 * G::WAVES), 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     prof_end(s);
     return e;
 }
 
+int64_t tiles(int64_t m, int64_t n, int64_t b) { return (m + b - 1) / b * ((n + b - 1) / b); }
+
+template <typename T, Role R>
+hipError_t contract(int id, GatedGemm a, hipStream_t s) {
+    const bool gated = R == FORWARD || R == AGAIN;
+    const int64_t N = gated ? 2 * a.ff : a.N;
+    a.splits = 1;
+    a.split_steps = (a.K + BK - 1) / BK;
+    // A round is one tile of 256 on every CU, or two of 128, which together take
+    // 0.62 of its time (8192 rows, 4096 x 12288: 1.27 PFLOP/s against 1.06).
+    const int64_t large = (tiles(a.M, N, 256) + 255) / 256, small = (tiles(a.M, N, 128) + 511) / 512;
+    if (8 * large <= 5 * small) return contract<T, R, 256, 2>(id, a, s);
+    if constexpr (R == FORWARD || R == AGAIN) {
+        // few rows: narrow tiles, all on the chip at once, and three steps on
+        // their way (64 rows, 2048 -> 5504: 15 us against 25)
+        if (tiles(a.M, N, 64) <= 512) return contract<T, R, 64, 4>(id, a, s);
+    }
+    if constexpr (R == DX) {
+        a.splits = gated_splits(a.M, a.N, a.K, &a.split_steps);
+        if (a.splits > 1) {
+            const hipError_t e = contract<T, R, 128, 2>(id, a, s);
+            if (e != hipSuccess) return e;
+            const int64_t n = (a.M * a.N / 8 + 255) / 256;
+            prof_begin(K_GATED_SUM, s);
+            gated_sum_kernel<T><<<dim3((unsigned)(n < 8192 ? n : 8192)), dim3(256), 0, s>>>(a);
+            const hipError_t e2 = hipGetLastError();
+            prof_end(s);
+            return e2;
+        }
+    }
+    return contract<T, R, 128, 2>(id, a, s);
+}
+
 template <Role R>
 hipError_t contract(int id, const GatedGemm &a, hipStream_t s) {
-    const bool gated = R == FORWARD || R == AGAIN;
-    const int64_t tiles = ((a.M + 255) / 256) * (((gated ? 2 * a.ff : a.N) + 255) / 256);
-    if (tiles >= 256)
-        return a.dtype == 1 ? contract<_Float16, R, 256>(id, a, s) : contract<__bf16, R, 256>(id, a, s);
-    return a.dtype == 1 ? contract<_Float16, R, 128>(id, a, s) : contract<__bf16, R, 128>(id, a, s);
+    return a.dtype == 1 ? contract<_Float16, R>(id, a, s) : contract<__bf16, R>(id, a, s);
 }
 
 }  // namespace
+
+int64_t gated_splits(int64_t M, int64_t N, int64_t K, int64_t *steps) {
+    // two tiles of 128 on every CU, none of fewer than eight steps
+    const int64_t all = (K + BK - 1) / BK, t = tiles(M, N, 128);
+    int64_t most = 512 / t;
+    if (most > all / 8) most = all / 8;
+    if (most < 1) most = 1;
+    *steps = (all + most - 1) / most;
+    return (all + *steps - 1) / *steps;
+}
 
 hipError_t launch_gated_forward(const GatedGemm &a, hipStream_t s) { return contract<FORWARD>(K_GATED, a, s); }
 hipError_t launch_gated_again(const GatedGemm &a, hipStream_t s) { return contract<AGAIN>(K_GATED_AGAIN, a, s); }

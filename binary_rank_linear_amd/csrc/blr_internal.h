@@ -57,6 +57,7 @@ enum KernelId {
     K_GATED_AGAIN,  // both projections again, dg and du
     K_GATED_GRADIENTS, // dg and du from the projections in 8 bits
     K_GATED_DX,     // dx = dg Wg + du Wu
+    K_GATED_SUM,    // dx: the splits' products summed in order
     K_GATED_DW,     // dWg, dWu = dg^T x, du^T x
     K_COUNT
 };
@@ -385,12 +386,16 @@ struct GatedGemm {
     uint8_t *tape_b;
     int64_t M, K, lda, ldb;
     int64_t tiles_m, tiles_n, group;  // filled by the launcher
+    int64_t splits, split_steps;      // dx: of the contraction; by the launcher too
+    float *part;                      // dx: [splits][M][N], sums of several splits
     int64_t ff;
     int N, dtype, kind;
     int out_f32;  // out (again, gradients: dh) is f32, not dtype
     int acc;      // dx, dw: added to what out holds
     float scale;  // of the product (again, gradients: of dh)
 };
+// Splits of dx's contraction, and the steps of 64 of one.
+int64_t gated_splits(int64_t M, int64_t N, int64_t K, int64_t *steps);
 hipError_t launch_gated_forward(const GatedGemm &a, hipStream_t s);
 hipError_t launch_gated_again(const GatedGemm &a, hipStream_t s);
 hipError_t launch_gated_gradients(const GatedGemm &a, hipStream_t s);

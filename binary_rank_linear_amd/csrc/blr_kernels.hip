@@ -2121,6 +2121,7 @@ const char *kernel_name(int id) {
         case K_GATED_AGAIN: return "gated_again";
         case K_GATED_GRADIENTS: return "gated_gradients";
         case K_GATED_DX: return "gated_dx";
+        case K_GATED_SUM: return "gated_sum";
         case K_GATED_DW: return "gated_dw";
     }
     return "?";
