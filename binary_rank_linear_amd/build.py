@@ -15,7 +15,7 @@ SOURCES = [os.path.join(HERE, "csrc", f) for f in ("blr_kernels.hip", "blr_route
                                                      "blr_adapters_backward.hip", "blr_norm.hip", "blr_gated.hip",
                                                      "blr_api.hip")]
 HEADERS = [os.path.join(HERE, "csrc", f) for f in ("blr_internal.h", "blr_plan.h", "blr_vec.h", "blr_adapters.h",
-                                                     "blr_keep8.h")] + \
+                                                     "blr_keep8.h", "blr_math.h")] + \
     [os.path.join(ROOT, "include", "blr.h")]
 LIB = os.path.join(HERE, "libblr.so")
 ARCH = "gfx950"

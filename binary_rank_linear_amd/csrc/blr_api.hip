@@ -966,18 +966,18 @@ bool norm_types_ok(int xt, int ft, int nt) {
     return dtype_ok(xt) && dtype_ok(ft) && dtype_ok(nt) && (xt == BLR_F32 || (ft == xt && nt == xt));
 }
 
-// Sums of ranges: of dw, of dw_after, and two gates' parts where rows share gates.
+// Sums of workgroups: of dw, of dw_after; of ranges, two gates' parts, where
+// rows share gates.
 struct NormLayout {
     size_t part_a, part_z, total;
-    int64_t per, ranges;
+    NormSplit split;
 };
 NormLayout norm_layout(int64_t M, int64_t d, int64_t span) {
     NormLayout L;
-    L.ranges = norm_ranges(M, d, &L.per);
-    const size_t one = up((size_t)(L.ranges * d) * 4);
-    L.part_a = one;
-    L.part_z = 2 * one;
-    L.total = (span > 1 ? 4 : 2) * one;
+    L.split = norm_split(M, d);
+    L.part_a = up((size_t)(L.split.blocks * d) * 4);
+    L.part_z = 2 * L.part_a;
+    L.total = L.part_z + (span > 1 ? up((size_t)(2 * L.split.ranges * d) * 4) : 0);
     return L;
 }
 
@@ -1112,8 +1112,9 @@ int blr_norm_backward(int64_t M, int64_t d, int xt, int ft, int nt, const void *
     a.part_z = (float *)((char *)workspace + L.part_z);
     a.M = M;
     a.d = d;
-    a.per = L.per;
-    a.ranges = L.ranges;
+    a.per = L.split.per;
+    a.ranges = L.split.ranges;
+    a.blocks = L.split.blocks;
     a.span = (uint32_t)span;
     a.xt = xt;
     a.ft = ft;

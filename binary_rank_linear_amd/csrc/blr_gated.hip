@@ -23,6 +23,7 @@
 
 #include "blr_internal.h"
 #include "blr_keep8.h"
+#include "blr_math.h"
 
 namespace blr {
 
@@ -40,19 +41,6 @@ __device__ __forceinline__ vf4 mma(s16x8 a, s16x8 b, vf4 c, __bf16) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(vb8, a), __builtin_bit_cast(vb8, b), c, 0, 0, 0);
 }
 
-// exp(v) to about 1e-7: the product with log2(e) is kept to twice its length,
-// whose tail enters as 1 + tail ln 2.
-__device__ __forceinline__ float exp_of(float v) {
-    const float L = 1.44269504088896340736f;
-    const float t = v * L, tail = fmaf(v, L, -t) + v * 1.92596299112661746887e-8f;
-    const float e = __builtin_amdgcn_exp2f(t);
-    return fmaf(e, tail * 0.69314718055994530942f, e);
-}
-// 1 / v, v >= 1, with one Newton step.
-__device__ __forceinline__ float inverse(float v) {
-    const float r = __builtin_amdgcn_rcpf(v);
-    return fmaf(fmaf(-v, r, 1.0f), r, r);
-}
 // act(g) and its slope. gelu is the form with tanh: 0.5 g (1 + tanh y) is
 // g sigmoid(2 y), y = sqrt(2 / pi) (g + 0.044715 g^3). Both ends stay finite:
 // the exponential is of -|.|.

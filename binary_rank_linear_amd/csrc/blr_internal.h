@@ -349,20 +349,24 @@ struct NormBackward {
     const float *w, *w_after, *stats;
     void *dx, *df, *dgate;
     float *dw, *dw_after;
-    // sums of ranges: [ranges][d] each, and [ranges][2][d] of the gates that a
-    // range has only a part of
+    // sums of workgroups: [blocks][d] each, and of ranges [ranges][2][d], of the
+    // gates that a range has only a part of
     float *part_w, *part_a, *part_z;
-    int64_t M, d, per, ranges;
+    int64_t M, d, per, ranges, blocks;
     uint32_t span;
     int xt, ft, nt, gate_kind, norm_f, acc;
     bool need_f;  // f's values take part
     bool summed;  // dgate is f32, a sum over the rows of each gate (also where that is one row)
+    bool by_gate; // the gates' sums: a workgroup for each gate; filled by the launcher
     float skip, scale;
 };
 hipError_t launch_norm_forward(const NormForward &a, hipStream_t s);
-hipError_t launch_norm_backward(const NormBackward &a, hipStream_t s);
-// Ranges of rows of the backward, and the rows of one.
-int64_t norm_ranges(int64_t M, int64_t d, int64_t *per);
+hipError_t launch_norm_backward(NormBackward a, hipStream_t s);
+// The backward's ranges of rows, the rows of one, and its workgroups.
+struct NormSplit {
+    int64_t per, ranges, blocks;
+};
+NormSplit norm_split(int64_t M, int64_t d);
 struct Checkpoint {
     void *x;  // read by save, written by load
     int8_t *q;

@@ -82,12 +82,12 @@ __device__ __forceinline__ uint2 keep8(const float *v, int b) {
     };
     return make_uint2(four(k[0], k[1], k[2], k[3]), four(k[4], k[5], k[6], k[7]));
 }
+// The values of eight of them: the step itself is a float (a subnormal one for
+// b < 7), and its products are exact.
 __device__ __forceinline__ void kept8(uint2 q, int b, float *o) {
+    const float step = b == 255 ? __builtin_nanf("") : ldexpf(1.0f, b - 133);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float k = (float)(int8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
-        o[i] = b == 255 ? __builtin_nanf("") : ldexpf(k, b - 133);
-    }
+    for (int i = 0; i < 8; ++i) o[i] = (float)(int8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3))) * step;
 }
 
 }  // namespace blr
