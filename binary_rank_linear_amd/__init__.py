@@ -452,15 +452,22 @@ def _shape(t, name, dims):
     raise ValueError(f"{name} has shape {tuple(shape)}, expected {dims} dimensions")
 
 
+_gpus = {}  # number of a GPU: (torch.empty, its device)
+
+
 def _new(shape, dtype, dev, stream):
     """Memory for a call on `stream` (None: the current one): the allocator
     hands out and takes back a tensor in the order of the stream it was made
     on, so it is made on the one that the kernels run on."""
-    import torch
+    at = _gpus.get(dev)
+    if at is None:
+        import torch
+        at = _gpus[dev] = (torch.empty, torch.device("cuda", dev))
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+        return at[0](shape, dtype=dtype, device=at[1])
+    import torch
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+        return torch.empty(shape, dtype=dtype, device=at[1])
 
 
 def _out(t, name, dtype, shape, dev, stream):
@@ -496,18 +503,23 @@ def _device(t, name, dtypes, stream):
     return dev
 
 
+_current = None  # (stream of a GPU, number of the current GPU)
+
+
 def _launch(name, dev, stream, *args):
     """The C call `name` on the tensors' own device, on its current stream
     unless one is given."""
-    import torch
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        handle = stream.cuda_stream
+    global _current
+    if _current is None:
+        import torch
+        torch.cuda.current_device()  # starts torch's side of the device, which the calls below take for granted
+        _current = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+    handle = _current[0](dev) if stream is None else stream.cuda_stream
     fn = getattr(_lib or load(), name)
-    if torch.cuda.current_device() == dev:
+    if _current[1]() == dev:
         status = fn(*args, handle)
     else:
+        import torch
         with torch.cuda.device(dev):
             status = fn(*args, handle)
     if status != 0:
