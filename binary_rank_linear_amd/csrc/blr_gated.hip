@@ -44,9 +44,10 @@ __device__ __forceinline__ vf4 mma(s16x8 a, s16x8 b, vf4 c, __bf16) {
 // act(g) and its slope. gelu is the form with tanh: 0.5 g (1 + tanh y) is
 // g sigmoid(2 y), y = sqrt(2 / pi) (g + 0.044715 g^3). Both ends stay finite:
 // the exponential is of -|.|.
-__device__ __forceinline__ float act(int kind, float g, float *slope) {
+template <bool GELU>
+__device__ __forceinline__ float act(float g, float *slope) {
     float y = g, dy = 1.0f;
-    if (kind) {
+    if constexpr (GELU) {
         const float a = 1.59576912160573071176f, b = 0.044715f;  // 2 sqrt(2 / pi)
         const float gg = g * g;
         y = a * g * fmaf(b, gg, 1.0f);
@@ -60,6 +61,35 @@ __device__ __forceinline__ float act(int kind, float g, float *slope) {
     const float r = big * small;
     *slope = r == 0.0f ? s : fmaf(g * dy, r, s);
     return g * s;
+}
+// h = act(g) u of eight columns, in place of g. The kind is looked at once, so
+// that the eight go through the long chain side by side.
+__device__ __forceinline__ void products8(int kind, float *g, const float *u) {
+    auto all = [&](auto gelu) {
+        float unused;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = act<decltype(gelu)::value>(g[i], &unused) * u[i];
+    };
+    if (kind)
+        all(std::true_type());
+    else
+        all(std::false_type());
+}
+// dg = v u act'(g) and du = v act(g), in place of g and u.
+__device__ __forceinline__ void gradients8(int kind, const float *v, float *g, float *u) {
+    auto all = [&](auto gelu) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float slope;
+            const float a = act<decltype(gelu)::value>(g[i], &slope);
+            g[i] = v[i] * u[i] * slope;
+            u[i] = v[i] * a;
+        }
+    };
+    if (kind)
+        all(std::true_type());
+    else
+        all(std::false_type());
 }
 
 // ------------------------------------------------------------ contraction --
@@ -360,7 +390,7 @@ __global__ __launch_bounds__(128 * (BN / 64)) void gated_kernel(GatedGemm a) {
         if (m >= a.M) continue;  // whole quads of lanes with the same p
         if constexpr (G::gated) {
             const int n = n0 + wn * 32 + g4 * 8;
-            float gate[8], up[8], o[8];
+            float gate[8], up[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 gate[e] = acc[i][e >> 2][e & 3];
@@ -368,18 +398,11 @@ __global__ __launch_bounds__(128 * (BN / 64)) void gated_kernel(GatedGemm a) {
             }
             const int64_t at = m * a.ff + n;
             if constexpr (R == FORWARD) {
-                float unused;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = act(a.kind, gate[e], &unused) * up[e];
-                if (a.out_f32)
-                    put8((float *)a.out + at, narrow8<float>(o));
-                else
-                    put8((T *)a.out + at, narrow8<T>(o));
                 if (a.tape_q) {
                     // the 32 columns of a block are those of the four lanes with this row
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        float *v = h ? up : gate;
+                        const float *v = h ? up : gate;
                         uint32_t top = top8(v);
                         top = max(top, (uint32_t)__shfl_xor((int)top, 16));
                         top = max(top, (uint32_t)__shfl_xor((int)top, 32));
@@ -388,22 +411,23 @@ __global__ __launch_bounds__(128 * (BN / 64)) void gated_kernel(GatedGemm a) {
                         if (g4 == 0) a.tape_b[(h * a.M * a.ff + at) / 32] = (uint8_t)b;
                     }
                 }
+                products8(a.kind, gate, up);
+                if (a.out_f32)
+                    put8((float *)a.out + at, narrow8<float>(gate));
+                else
+                    put8((T *)a.out + at, narrow8<T>(gate));
             } else {
-                float dh[8], q[8];
+                float dh[8];
                 if (a.out_f32)
                     widen8(raw8((const float *)a.dh + at), dh);
                 else
                     widen8(raw8((const T *)a.dh + at), dh);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float slope;
-                    const float v = dh[e] * a.scale;
-                    q[e] = v * act(a.kind, gate[e], &slope);
-                    o[e] = v * up[e] * slope;
-                }
+                for (int e = 0; e < 8; ++e) dh[e] *= a.scale;
+                gradients8(a.kind, dh, gate, up);
                 T *d = (T *)a.out + m * 2 * a.ff + n;
-                put8(d, narrow8<T>(o));
-                put8(d + a.ff, narrow8<T>(q));
+                put8(d, narrow8<T>(gate));
+                put8(d + a.ff, narrow8<T>(up));
             }
         } else {
             const int n = n0 + wn * 64 + g4 * 16;
@@ -455,7 +479,7 @@ __global__ __launch_bounds__(256) void gated_gradients_kernel(GatedGemm a) {
     if (n >= a.ff) return;
     for (int64_t row = blockIdx.y; row < a.M; row += gridDim.y) {
         const int64_t at = row * a.ff + n;
-        float gate[8], up[8], dh[8], o[8], q[8];
+        float gate[8], up[8], dh[8];
         if (a.out_f32)
             widen8(raw8((const float *)a.dh + at), dh);
         else
@@ -463,15 +487,11 @@ __global__ __launch_bounds__(256) void gated_gradients_kernel(GatedGemm a) {
         kept8(*(const uint2 *)(a.tape_q + at), a.tape_b[at / 32], gate);
         kept8(*(const uint2 *)(a.tape_q + ups + at), a.tape_b[(ups + at) / 32], up);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float slope;
-            const float v = dh[e] * a.scale;
-            q[e] = v * act(a.kind, gate[e], &slope);
-            o[e] = v * up[e] * slope;
-        }
+        for (int e = 0; e < 8; ++e) dh[e] *= a.scale;
+        gradients8(a.kind, dh, gate, up);
         T *d = (T *)a.out + row * 2 * a.ff + n;
-        put8(d, narrow8<T>(o));
-        put8(d + a.ff, narrow8<T>(q));
+        put8(d, narrow8<T>(gate));
+        put8(d + a.ff, narrow8<T>(up));
     }
 }
 
