@@ -165,8 +165,9 @@ struct Tile {
     static constexpr bool a_inner = R != DW, b_inner = gated;  // contracted index innermost
     static constexpr int WN = BN / 64, WAVES = 2 * WN, MT = BM / 32;
     static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, STAGE = A_BYTES + B_BYTES;
-    static constexpr int COPIES = 4;  // of either operand, by each wave
-    static_assert(A_BYTES == COPIES * WAVES * 1024 && B_BYTES == COPIES * WAVES * 1024, "copies fill the tiles");
+    // copies of 1 KB by each wave: of either operand, and of both
+    static constexpr int A_COPIES = A_BYTES / WAVES / 1024, B_COPIES = B_BYTES / WAVES / 1024, COPIES = A_COPIES + B_COPIES;
+    static_assert(A_BYTES == A_COPIES * WAVES * 1024 && B_COPIES == 4, "copies fill the tiles, four of 8 rows of n each");
 };
 
 template <typename T, Role R, int BM, int BN, int STEPS>
@@ -191,10 +192,10 @@ __global__ __launch_bounds__(128 * (BN / 64)) void gated_kernel(GatedGemm a) {
     const int n0 = (int)(in_group / rows) * (G::gated ? BN / 2 : BN);
 
     // what each lane copies: byte offsets from the tile's corner
-    int off_a[G::COPIES], off_b[G::COPIES];
+    int off_a[G::A_COPIES], off_b[G::B_COPIES];
 #pragma unroll
-    for (int i = 0; i < G::COPIES; ++i) {
-        const int c = w * G::COPIES + i;  // 1 KB of the tile
+    for (int i = 0; i < G::A_COPIES; ++i) {
+        const int c = w * G::A_COPIES + i;  // 1 KB of the tile
         if constexpr (G::a_inner) {
             const int row = c * 8 + (lane >> 3), at = (lane & 7) ^ (row & 7);
             const int64_t left = a.M - 1 - m0;
@@ -206,6 +207,10 @@ __global__ __launch_bounds__(128 * (BN / 64)) void gated_kernel(GatedGemm a) {
             off_a[i] = (int)(k * a.lda * 2 + at * 16);
             if (m0 + at * 8 >= a.M) off_a[i] = 0x7fffffff;  // past every resource's end: zeros
         }
+    }
+#pragma unroll
+    for (int i = 0; i < G::B_COPIES; ++i) {
+        const int c = w * G::B_COPIES + i;
         if constexpr (G::b_inner) {
             const int row = c * 8 + (lane >> 3), at = (lane & 7) ^ (row & 7);
             const int n = (row >> 6) * 32 + col_of(true, (row >> 4) & 3, row & 15);
@@ -229,7 +234,7 @@ __global__ __launch_bounds__(128 * (BN / 64)) void gated_kernel(GatedGemm a) {
     };
     auto source = [&](int64_t k0, int buf) {
         Source q;
-        q.to = lds0 + buf * G::STAGE + w * G::COPIES * 1024;
+        q.to = lds0 + buf * G::STAGE;
         const int64_t left = a.K - k0 < BK ? a.K - k0 : BK;
         q.a = G::a_inner ? resource(pa + k0 * 2, 0x7ffffffe)
                          : resource(pa + k0 * a.lda * 2, (uint32_t)((left * a.lda - m0) * 2));
@@ -248,15 +253,15 @@ __global__ __launch_bounds__(128 * (BN / 64)) void gated_kernel(GatedGemm a) {
         return q;
     };
     auto copy = [&](const Source &q, int i) {
-        if (i < G::COPIES)
-            copy_to_lds(q.a, off_a[i], q.to + i * 1024);
-        else
-            copy_to_lds(q.b, off_b[i - G::COPIES], q.to + G::A_BYTES + (i - G::COPIES) * 1024);
+        if (i < G::A_COPIES)
+            copy_to_lds(q.a, off_a[i], q.to + (w * G::A_COPIES + i) * 1024);
+        else if (i < G::COPIES)
+            copy_to_lds(q.b, off_b[i - G::A_COPIES], q.to + G::A_BYTES + (w * G::B_COPIES + i - G::A_COPIES) * 1024);
     };
     auto stage = [&](int64_t k0, int buf) {
         const Source q = source(k0, buf);
 #pragma unroll
-        for (int i = 0; i < 2 * G::COPIES; ++i) copy(q, i);
+        for (int i = 0; i < G::COPIES; ++i) copy(q, i);
     };
 
     // an operand's 16 x 32 piece: lane = row (p), 8 contracted values (8 g4 on)
@@ -326,7 +331,7 @@ __global__ __launch_bounds__(128 * (BN / 64)) void gated_kernel(GatedGemm a) {
     // units start at once after the barrier; the order is the one written.
     constexpr int ROWS = G::a_inner ? G::MT / 2 : G::MT * 3 / 4;  // rows of products that take reads
     constexpr int READS = (4 + G::MT + ROWS - 1) / ROWS;
-    constexpr int COPIES = 2 * G::COPIES / (G::MT / 2);
+    constexpr int COPIES = (G::COPIES + G::MT / 2 - 1) / (G::MT / 2);
     auto step = [&](int t, auto copies, auto reads) {
         const int buf = t % STEPS, next = (t + 1) % STEPS;
 #pragma unroll
@@ -339,11 +344,11 @@ __global__ __launch_bounds__(128 * (BN / 64)) void gated_kernel(GatedGemm a) {
         }
         // of the steps after the next one, as many as there are may be on their way
         if constexpr (decltype(copies)::value)
-            wait_copies<2 * G::COPIES *(STEPS - 2)>();
+            wait_copies<G::COPIES *(STEPS - 2)>();
         else if (STEPS > 3 && t + 3 < steps)
-            wait_copies<4 * G::COPIES>();
-        else if (STEPS > 2 && t + 2 < steps)
             wait_copies<2 * G::COPIES>();
+        else if (STEPS > 2 && t + 2 < steps)
+            wait_copies<G::COPIES>();
         else
             wait_copies<0>();
         barrier();
@@ -374,7 +379,7 @@ __global__ __launch_bounds__(128 * (BN / 64)) void gated_kernel(GatedGemm a) {
     if (steps < STEPS)
         wait_copies<0>();
     else
-        wait_copies<2 * G::COPIES *(STEPS - 1)>();
+        wait_copies<G::COPIES *(STEPS - 1)>();
     barrier();
 #pragma unroll
     for (int r = 0; r < 4 + G::MT; ++r) read(xa, xb, 0, 0, r);
@@ -497,41 +502,47 @@ __global__ __launch_bounds__(256) void gated_gradients_kernel(GatedGemm a) {
 
 constexpr int64_t GROUP = 8;
 
-template <typename T, Role R, int B, int STEPS>
+template <typename T, Role R, int BM, int BN, int STEPS>
 hipError_t contract(int id, GatedGemm a, hipStream_t s) {
-    using G = Tile<T, R, B, B, STEPS>;
-    a.tiles_m = (a.M + B - 1) / B;
-    const int64_t cols = G::gated ? B / 2 : B, N = G::gated ? a.ff : a.N;
+    using G = Tile<T, R, BM, BN, STEPS>;
+    a.tiles_m = (a.M + BM - 1) / BM;
+    const int64_t cols = G::gated ? BN / 2 : BN, N = G::gated ? a.ff : a.N;
     a.tiles_n = (N + cols - 1) / cols;
     a.group = a.tiles_m < GROUP ? a.tiles_m : GROUP;
     prof_begin(id, s);
-    gated_kernel<T, R, B, B, STEPS><<<dim3((unsigned)(a.tiles_m * a.tiles_n * a.splits)), dim3(64 * G::WAVES), 0, s>>>(a);
+    gated_kernel<T, R, BM, BN, STEPS><<<dim3((unsigned)(a.tiles_m * a.tiles_n * a.splits)), dim3(64 * G::WAVES), 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     prof_end(s);
     return e;
 }
 
-int64_t tiles(int64_t m, int64_t n, int64_t b) { return (m + b - 1) / b * ((n + b - 1) / b); }
+int64_t tiles(int64_t m, int64_t n, int64_t bm, int64_t bn) { return (m + bm - 1) / bm * ((n + bn - 1) / bn); }
 
+// Which tiles: times in us of the forward, 2048 -> 5504 bf16, for 64, 300, 400, 600
+// and 1000 rows:
+//   64 x 64, 4 buffers     15  30  41  54  79    256 x 256   46  53  --  --  57
+//   64 x 128, 2 buffers    22  24  31  47  59
+//   128 x 128, 2 buffers   25  30  32  34  53
 template <typename T, Role R>
 hipError_t contract(int id, GatedGemm a, hipStream_t s) {
-    const bool gated = R == FORWARD || R == AGAIN;
+    constexpr bool gated = R == FORWARD || R == AGAIN;
     const int64_t N = gated ? 2 * a.ff : a.N;
     a.splits = 1;
     a.split_steps = (a.K + BK - 1) / BK;
     // A round is one tile of 256 on every CU, or two of 128, which together take
     // 0.62 of its time (8192 rows, 4096 x 12288: 1.27 PFLOP/s against 1.06).
-    const int64_t large = (tiles(a.M, N, 256) + 255) / 256, small = (tiles(a.M, N, 128) + 511) / 512;
-    if (8 * large <= 5 * small) return contract<T, R, 256, 2>(id, a, s);
-    if constexpr (R == FORWARD || R == AGAIN) {
-        // few rows: narrow tiles, all on the chip at once, and three steps on
-        // their way (64 rows, 2048 -> 5504: 15 us against 25)
-        if (tiles(a.M, N, 64) <= 512) return contract<T, R, 64, 4>(id, a, s);
+    const int64_t large = (tiles(a.M, N, 256, 256) + 255) / 256, small = (tiles(a.M, N, 128, 128) + 511) / 512;
+    if (8 * large <= 5 * small) return contract<T, R, 256, 256, 2>(id, a, s);
+    if constexpr (gated) {
+        // few rows: small tiles, all on the chip at once; the smallest, two on a
+        // CU, with three steps on their way
+        if (tiles(a.M, N, 64, 64) <= 512) return contract<T, R, 64, 64, 4>(id, a, s);
+        if (tiles(a.M, N, 64, 128) <= 768) return contract<T, R, 64, 128, 2>(id, a, s);
     }
     if constexpr (R == DX) {
         a.splits = gated_splits(a.M, a.N, a.K, &a.split_steps);
         if (a.splits > 1) {
-            const hipError_t e = contract<T, R, 128, 2>(id, a, s);
+            const hipError_t e = contract<T, R, 128, 128, 2>(id, a, s);
             if (e != hipSuccess) return e;
             const int64_t n = (a.M * a.N / 8 + 255) / 256;
             prof_begin(K_GATED_SUM, s);
@@ -541,7 +552,7 @@ hipError_t contract(int id, GatedGemm a, hipStream_t s) {
             return e2;
         }
     }
-    return contract<T, R, 128, 2>(id, a, s);
+    return contract<T, R, 128, 128, 2>(id, a, s);
 }
 
 template <Role R>
@@ -553,7 +564,7 @@ hipError_t contract(int id, const GatedGemm &a, hipStream_t s) {
 
 int64_t gated_splits(int64_t M, int64_t N, int64_t K, int64_t *steps) {
     // two tiles of 128 on every CU, none of fewer than eight steps
-    const int64_t all = (K + BK - 1) / BK, t = tiles(M, N, 128);
+    const int64_t all = (K + BK - 1) / BK, t = tiles(M, N, 128, 128);
     int64_t most = 512 / t;
     if (most > all / 8) most = all / 8;
     if (most < 1) most = 1;

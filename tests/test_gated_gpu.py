@@ -129,6 +129,16 @@ def test_backward(dev, t, M, d, ff):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,d,ff", [(200, 256, 5504), (130, 128, 8192), (700, 256, 4224)])
+def test_middle_tiles(dev, M, d, ff):
+    """Rows between the smallest tiles' and the largest's."""
+    v = case(dev, M, d, ff, BF16, dh_sigma=1e-2)
+    say(f"gated {M}x{d}x{ff}")
+    _, tape = check_forward(v, GELU, BF16, keep=True)
+    check_backward(v, GELU, None)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("t", [F16, BF16])
 @pytest.mark.parametrize("M,d,ff", [(2100, 1024, 2176), (4200, 2176, 1024)])
 def test_large_tiles(dev, t, M, d, ff):
