@@ -1133,8 +1133,9 @@ int blr_norm_backward(int64_t M, int64_t d, int xt, int ft, int nt, const void *
 // ---------------------------------------------------- gated feed-forward --
 namespace {
 bool gated_shape_ok(int64_t M, int64_t d, int64_t ff) {
+    const int64_t most = (int64_t)1 << 24;  // tiles of 256 threads: a grid has room for 2^32
     return rows_ok(M) && d >= 128 && d % 128 == 0 && d <= MAX_WIDTH && ff >= 128 && ff % 128 == 0 && ff <= MAX_WIDTH &&
-           ceil_div(M, 128) * (ff / 64) < ((int64_t)1 << 31);
+           ceil_div(M, 128) * (ff / 64) < most && ceil_div(M, 128) * (d / 128) < most;
 }
 // dg and du side by side, x out of its checkpoint, the sums of dx's splits.
 struct GatedLayout {

@@ -103,7 +103,7 @@ template <typename XT, typename FT, typename NT, int C>
 __global__ __launch_bounds__(64 * MAX_WAVES) void norm_forward_kernel(NormForward a) {
     __shared__ float red[2 * MAX_WAVES];
     const Team t;
-    const int64_t row = (int64_t)blockIdx.x * blockDim.y + t.team;
+    const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.y + t.team;
     if (row >= a.M) return;  // whole waves: a workgroup of several rows has one wave for each
     const int d = (int)a.d, chunks = d / 8, step = 64 * t.waves;
     const float inv_d = 1.0f / (float)d;
@@ -544,7 +544,10 @@ hipError_t launch(int id, K kernel, dim3 grid, dim3 block, const A &a, hipStream
 
 hipError_t launch_norm_forward(const NormForward &a, hipStream_t s) {
     const Shape sh = shape_of(a.d, chunks_of(a.d));
-    const dim3 block(64 * sh.waves, sh.teams), grid((unsigned)((a.M + sh.teams - 1) / sh.teams));
+    // a row (or four) to a workgroup; a grid has room for 2^32 threads along x
+    const int64_t groups = (a.M + sh.teams - 1) / sh.teams, most = 1 << 20;
+    const dim3 block(64 * sh.waves, sh.teams);
+    const dim3 grid((unsigned)(groups < most ? groups : most), (unsigned)((groups + most - 1) / most));
     return with_types(a.xt, a.ft, a.nt, [&](auto x, auto f, auto n) {
         using X = decltype(x);
         using F = decltype(f);

@@ -372,8 +372,8 @@ typedef enum { BLR_GATE_LINEAR = 0, BLR_GATE_SIGMOID = 1, BLR_GATE_SILU = 2 } bl
  * overwrites dw, dw_after and the dgate of a span over 1, 1 adds to them.
  *
  * d a multiple of 8 up to 16384, 1 <= M < 2^31 - 65536; row arrays, q and
- * weights 16-byte aligned, stats 4-byte. All arithmetic is f32, outputs of 16
- * bits are rounded once. Results are the same on every run. Workspace of the
+ * weights 16-byte aligned, stats 4-byte. All arithmetic is f32 (a row's squares
+ * too, whose sum has to stay in its range), outputs of 16 bits are rounded once. Results are the same on every run. Workspace of the
  * backward: blr_norm_workspace_bytes, 0 for invalid sizes.
  */
 int blr_norm_forward(int64_t M, int64_t d, int xt, int ft, int nt, const void *x, const void *f, int norm_f,
@@ -414,8 +414,8 @@ typedef enum { BLR_ACT_SILU = 0, BLR_ACT_GELU = 1 } blr_act;
  *     bf16 1 does.
  *   dx or the pair dw_gate, dw_up may be NULL (not formed). accumulate_dx and
  *     accumulate_grads = 0 overwrite, 1 adds (in f32, then rounds).
- * d, ff multiples of 128 up to 2^20, 1 <= M < 2^31 - 65536, with M / 128 ff / 64
- * below 2^31. Products are exact and sums f32; h and the gradients are rounded
+ * d, ff multiples of 128 up to 2^20, 1 <= M < 2^31 - 65536, with (M / 128)
+ * (ff / 64) and (M / 128) (d / 128), rounded up, below 2^24. Products are exact and sums f32; h and the gradients are rounded
  * once, and between the backward's contractions dg and du are of dtype. Rows do
  * not touch each other in h and dx, whatever they hold. Results are the same
  * on every run. Arrays 16-byte aligned (tape_b and x_b any). The backward's

@@ -162,7 +162,8 @@ def test_gated_refuses(caller):
                dict(kind=-1)):
         assert caller(**kw) == E_DTYPE, kw
     for M, d, ff in [(0, 128, 128), ((1 << 31) - 65536, 128, 128), (4, 64, 128), (4, 192, 128), (4, 128, 0),
-                     (4, 128, 160), (4, (1 << 20) + 128, 128), (4, 128, (1 << 20) + 128), (1 << 30, 128, 1 << 20)]:
+                     (4, 128, 160), (4, (1 << 20) + 128, 128), (4, 128, (1 << 20) + 128), (1 << 30, 128, 1 << 20),
+                     (1 << 30, 1 << 20, 128)]:
         assert caller(M, d, ff) == E_SHAPE, (M, d, ff)
         assert blr.load().blr_gated_workspace_bytes(M, d, ff) == 0
     for k in ("w_gate", "w_up", "tape_q", "tape_b"):

@@ -280,3 +280,24 @@ def test_captured(dev):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, [out, n, stats, *grads]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,M", [(8, (1 << 22) + 4099), (520, (1 << 20) + 1027)])
+def test_more_rows_than_a_grid_is_wide(dev, d, M):
+    """Rows in the grid's second line: every row has the result that it has
+    alone."""
+    import torch
+    g = torch.Generator(device=dev).manual_seed(1)
+    x = torch.randn((M, d), generator=g, device=dev).bfloat16()
+    w = torch.randn(d, generator=g, device=dev)
+    say(f"{M} rows of {d}")
+    _, n, stats, _ = blr.blr_norm_forward(x, None, w)
+    at = torch.cat([torch.arange(0, 700, device=dev), torch.arange(M - 6000, M, device=dev),
+                    torch.randint(0, M, (20000,), generator=g, device=dev)])
+    _, alone, s1, _ = blr.blr_norm_forward(x[at], None, w)
+    assert torch.equal(n[at], alone) and torch.equal(stats[0][at], s1[0])
+    want, r = ref.norm_before(f64(x[at]), f64(w), float(np.float32(1e-6)))
+    within(f64(alone), want, np.abs(want), ROW, BF16)
+    within(f64(stats[0]), 1 / np.sqrt((x.float() ** 2).mean(1).double().cpu().numpy() + float(np.float32(1e-6))),
+           f64(stats[0]), 2 * ROW)
