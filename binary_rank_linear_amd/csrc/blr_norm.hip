@@ -52,7 +52,7 @@ __device__ __forceinline__ float phi(int kind, float z, float *slope) {
     // past 200 the exponential is zero, and z may be infinite; a NaN stays one
     const float e = exp_of(fabsf(z) > 200.0f ? -200.0f : -fabsf(z)), big = inverse(1.0f + e), small = e * big;
     const float s = z >= 0.0f ? big : small, r = big * small;
-    *slope = kind == 1 ? r : s + z * r;
+    *slope = kind == 1 ? r : r == 0.0f ? s : s + z * r;  // z may be infinite where r is zero
     return kind == 1 ? s : z * s;
 }
 

@@ -180,8 +180,10 @@ def test_small_gradients_in_f16(dev):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("gt", [F32, BF16])
-def test_accumulates(dev, gt):
-    M, d, ff, t = 150, 384, 256, BF16
+@pytest.mark.parametrize("ff", [256, 2176])
+def test_accumulates(dev, gt, ff):
+    """Also where dx's contraction, over 2 ff, is made in several splits."""
+    M, d, t = 150, 384, BF16
     v = case(dev, M, d, ff, t, dh_sigma=1e-2)
     say(f"gradients added to what is there, {gt}")
     one = blr.blr_gated_backward(v["x"], v["dh"], v["w_gate"], v["w_up"], grad_dtype=dt(gt))

@@ -301,3 +301,44 @@ def test_more_rows_than_a_grid_is_wide(dev, d, M):
     within(f64(alone), want, np.abs(want), ROW, BF16)
     within(f64(stats[0]), 1 / np.sqrt((x.float() ** 2).mean(1).double().cpu().numpy() + float(np.float32(1e-6))),
            f64(stats[0]), 2 * ROW)
+
+
+@pytest.mark.gpu
+def test_parts_alone(dev):
+    """Each output by itself has the bits that it has among the others."""
+    import torch
+    types, M, d = (F32, BF16, F16), 77, 512
+    v = case(dev, M, d, types, gate=True, span=9, kind=1)
+    out, n, stats, kept = blr.blr_norm_forward(v["x"], v["f"], v["w"], n_dtype=torch.float16, keep=True, **v["how"])
+    say("forward: out alone, the checkpoint with it, n without statistics")
+    o = blr.blr_norm_forward(v["x"], v["f"], v["w"], need_n=False, need_stats=False, **v["how"])
+    assert torch.equal(o[0], out) and o[1:] == (None, None, None)
+    o = blr.blr_norm_forward(v["x"], v["f"], need_n=False, need_stats=False, keep=True, **v["how"])
+    assert torch.equal(o[0], out) and all(torch.equal(a, b) for a, b in zip(o[3], kept))
+    o = blr.blr_norm_forward(v["x"], v["f"], v["w"], n_dtype=torch.float16, need_stats=False, **v["how"])
+    assert torch.equal(o[1], n) and o[2] is None
+    whole = blr.blr_norm_backward(v["dn"], v["dout"], kept, v["f"], v["w"], stats, **v["how"])
+    say("backward: rows alone, the weights' gradients alone, dn alone from a checkpoint")
+    got = blr.blr_norm_backward(v["dn"], v["dout"], kept, v["f"], v["w"], stats, grads=False, **v["how"])
+    assert torch.equal(got[0], whole[0]) and torch.equal(got[1], whole[1]) and got[2:] == (None, None, None)
+    got = blr.blr_norm_backward(v["dn"], v["dout"], kept, v["f"], v["w"], stats, need_dx=False, need_df=False, **v["how"])
+    assert got[:2] == (None, None) and all(torch.equal(a, b) for a, b in zip(got[2:], whole[2:]))
+    check_backward(v, types, kept, stats, M, dout=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,high,low", [(1, (1.0, 0.0), (0.0, 0.0)), (2, (np.inf, 1.0), (0.0, 0.0))])
+def test_gates_far_out(dev, kind, high, low):
+    """Gates at the ends: sigmoid 0 and 1, silu z and 0, and their slopes."""
+    import torch
+    v = case(dev, 4, 64, (F32, F32, F32), norm_f=False, after=False, gate=True, kind=kind)
+    v["gate"][0], v["gate"][1], v["gate"][2] = 1e4, -1e4, 3e38
+    v["f"].fill_(1.0)
+    how = {**v["how"], "skip": 0.0, "scale": 1.0}
+    out, _, stats, _ = blr.blr_norm_forward(v["x"], v["f"], None, **how)
+    far = {1: (1.0, 0.0, 1.0), 2: (1e4, 0.0, 3e38)}[kind]
+    for i, want in enumerate(far):
+        assert torch.equal(out[i], torch.full_like(out[i], want)), i
+    _, _, dz, _, _ = blr.blr_norm_backward(None, v["dout"], None, v["f"], None, None, **how)
+    for i, slope in enumerate((high[1], low[1], high[1])):
+        assert torch.equal(dz[i], v["dout"][i] * slope), i
