@@ -312,3 +312,31 @@ def test_captured(dev, M):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, [h, *tape, *out]))
+
+
+@pytest.mark.gpu
+def test_past_32_bits(dev):
+    """More than 2^32 values of h: the far rows against the formula, and nothing
+    of the rows before them, which are zero, in the weights' gradients."""
+    import torch
+    d, ff, t = 128, 16384, BF16
+    M = (1 << 32) // ff + 91
+    v = case(dev, 60, d, ff, t, dh_sigma=1e-2)
+    x = torch.zeros((M, d), dtype=dt(t), device=dev)
+    dh = torch.zeros((M, ff), dtype=dt(t), device=dev)
+    x[-60:], dh[-60:] = v["x"], v["dh"]
+    say(f"gated {M}x{d}x{ff}")
+    h, tape = blr.blr_gated_forward(x, v["w_gate"], v["w_up"], keep=True)
+    h1, tape1 = check_forward(v, SILU, t, keep=True)
+    assert not bool(h[:-60].any())
+    got, one = h[-60:].double(), h1.double()
+    assert bool(((got - one).abs() <= 2 * HALF[t] * one.abs() + 1e-6).all())  # a sum's order may round it the other way
+    q, b = tape[0][:, -60:], tape[1][:, -60:]
+    assert int((b != tape1[1]).sum()) <= 4 and int((q.int() - tape1[0].int()).abs().max()) <= 64
+    say("backward")
+    dx, dwg, dwu = blr.blr_gated_backward(x, dh, v["w_gate"], v["w_up"], tape)
+    dx1, dwg1, dwu1 = blr.blr_gated_backward(v["x"], v["dh"], v["w_gate"], v["w_up"], (q.contiguous(), b.contiguous()))
+    assert not bool(dx[:-60].any())
+    for a, c in ((dx[-60:], dx1), (dwg, dwg1), (dwu, dwu1)):
+        a, c = a.double(), c.double()
+        assert bool(((a - c).abs() <= 2 * HALF[t] * c.abs() + 1e-5 * c.abs().max()).all())

@@ -103,7 +103,7 @@ def check_backward(v, types, out, stats, M, *, dn=True, dout=True, f=None, **mor
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("types", TYPES)
-@pytest.mark.parametrize("M,d", [(1, 128), (5, 8), (67, 520), (3, 4096), (2, 8200), (131, 1096)])
+@pytest.mark.parametrize("M,d", [(1, 128), (5, 8), (67, 520), (3, 4096), (2, 8200), (3, 6152), (2, 8192), (131, 1096)])
 def test_sandwich(dev, types, M, d):
     say(f"norm {types} {M}x{d}")
     v = case(dev, M, d, types, gate=True, kind=2)
@@ -342,3 +342,30 @@ def test_gates_far_out(dev, kind, high, low):
     _, _, dz, _, _ = blr.blr_norm_backward(None, v["dout"], None, v["f"], None, None, **how)
     for i, slope in enumerate((high[1], low[1], high[1])):
         assert torch.equal(dz[i], v["dout"][i] * slope), i
+
+
+@pytest.mark.gpu
+def test_past_32_bits(dev):
+    """More than 2^32 values: the far rows have the results that they have alone."""
+    import torch
+    d = 4096
+    M = (1 << 32) // d + 37
+    g = torch.Generator(device=dev).manual_seed(4)
+    tail = [torch.randn((50, d), generator=g, device=dev).bfloat16() for _ in range(4)]
+
+    def rows(t):
+        big = torch.ones((M, d), dtype=torch.bfloat16, device=dev)
+        big[-50:] = t
+        return big
+
+    w = torch.randn(d, generator=g, device=dev)
+    how = dict(norm_f=True, w_after=w, skip=0.5, scale=2.0)
+    say(f"norm {M}x{d}")
+    x, f, dn, dout = (rows(t) for t in tail)
+    out, n, stats, kept = blr.blr_norm_forward(x, f, w, keep=True, **how)
+    o1, n1, s1, k1 = blr.blr_norm_forward(tail[0], tail[1], w, keep=True, **how)
+    assert torch.equal(out[-50:], o1) and torch.equal(n[-50:], n1) and torch.equal(stats[:, -50:], s1)
+    assert torch.equal(kept[0][-50:], k1[0]) and torch.equal(kept[1][-50:], k1[1])
+    dx, df, _, _, _ = blr.blr_norm_backward(dn, dout, kept, f, w, stats, **how)
+    dx1, df1, _, _, _ = blr.blr_norm_backward(tail[2], tail[3], k1, tail[1], w, s1, **how)
+    assert torch.equal(dx[-50:], dx1) and torch.equal(df[-50:], df1)
