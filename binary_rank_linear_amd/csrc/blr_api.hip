@@ -127,8 +127,9 @@ bool shape_ok(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_t P = 1) 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 
+// Products are divided by s, as a product with its inverse: f32 has none below 2^-127.
 bool pow2_scale_ok(float s) {
-    if (!(s > 0.0f) || !isfinite(s)) return false;
+    if (!(s > 0.0f) || !isfinite(s) || !isfinite(1.0f / s)) return false;
     int e;
     return frexpf(s, &e) == 0.5f;
 }
@@ -162,7 +163,7 @@ const char *blr_status_string(int status) {
         case BLR_OK: return "ok";
         case BLR_ERR_NULL: return "a required pointer is NULL";
         case BLR_ERR_SHAPE: return "invalid shape (d_in, d_out, r must be multiples of 128; M >= 1)";
-        case BLR_ERR_SCALE: return "gscale must be a positive finite power of two";
+        case BLR_ERR_SCALE: return "gscale must be a power of two from 2^-127 to 2^127";
         case BLR_ERR_WORKSPACE: return "workspace missing or smaller than blr_workspace_bytes()";
         case BLR_ERR_DEVICE: return "the current device is not gfx950";
         case BLR_ERR_HIP: return "HIP runtime error";

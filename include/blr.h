@@ -54,7 +54,7 @@ typedef enum {
     BLR_OK = 0,
     BLR_ERR_NULL = -1,      /* a required pointer is NULL */
     BLR_ERR_SHAPE = -2,     /* a size is out of range or breaks the multiple-of-128 rule */
-    BLR_ERR_SCALE = -3,     /* gscale is not a positive finite power of two */
+    BLR_ERR_SCALE = -3,     /* gscale is not a power of two from 2^-127 to 2^127 */
     BLR_ERR_WORKSPACE = -4, /* workspace NULL or smaller than blr_workspace_bytes() */
     BLR_ERR_DEVICE = -5,    /* current device is not gfx950 */
     BLR_ERR_HIP = -6,       /* the HIP runtime reported an error */
@@ -135,7 +135,8 @@ int blr_forward_noalloc(int64_t M, int64_t d_in, int64_t d_out, int64_t r, const
  *     the forward stored none (then c is recomputed from tape_a).
  *   gscale: the power of two the gradients are staged under in f16 (dy.h
  *     and db.l are multiplied by it before rounding to f16; the products are
- *     divided by it in f32, exactly). Must be a positive finite power of two.
+ *     divided by it in f32, exactly). Must be a power of two from 2^-127 to
+ *     2^127 (below, its inverse is infinite).
  *   dh [d_out], dl [r], dg [d_in]: always accumulate (+=); zero them first
  *     for a plain gradient.
  *   dx [M][d_in]: accumulate_dx = 0 writes dx = g.dx', 1 adds.
@@ -201,7 +202,7 @@ int blr_backward_paths(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int64_
  * Dense frozen linear (page: `plane_linear`): y [M][n] = (f16(x * scale)
  * . plane^T) / scale, x [M][k] f32, plane [n][k] f16 (IEEE binary16 bit
  * patterns), through the same staging and MFMA contraction as the layer
- * (f32 accumulation; y overwritten). scale is a positive finite power of two
+ * (f32 accumulation; y overwritten). scale is a power of two from 2^-127 to 2^127
  * (the page stages gradients under a gradient scale when it runs this for
  * the input gradient with the transposed plane). n and k multiples of 128,
  * M >= 1; x, plane and y 16-byte aligned.
@@ -408,7 +409,7 @@ typedef enum { BLR_ACT_SILU = 0, BLR_ACT_GELU = 1 } blr_act;
  *   The backward's x as rows, or as a checkpoint (x_q, x_b, with x NULL), whose
  *     values it takes in dtype; none where g and u come from the tape and no
  *     weights' gradients are formed.
- *   gscale, a positive finite power of two: dg and du are rounded to dtype
+ *   gscale, a power of two from 2^-127 to 2^127: dg and du are rounded to dtype
  *     times gscale, and the products after them are divided by it, as in
  *     blr_backward. In f16 it keeps small gradients out of the subnormals; in
  *     bf16 1 does.
