@@ -163,7 +163,7 @@ const char *blr_status_string(int status) {
         case BLR_OK: return "ok";
         case BLR_ERR_NULL: return "a required pointer is NULL";
         case BLR_ERR_SHAPE: return "invalid shape (d_in, d_out, r must be multiples of 128; M >= 1)";
-        case BLR_ERR_SCALE: return "gscale must be a power of two from 2^-127 to 2^127";
+        case BLR_ERR_SCALE: return "gscale must be a power of two from 2^-127 to 2^127, eps finite and not below zero";
         case BLR_ERR_WORKSPACE: return "workspace missing or smaller than blr_workspace_bytes()";
         case BLR_ERR_DEVICE: return "the current device is not gfx950";
         case BLR_ERR_HIP: return "HIP runtime error";
@@ -1010,6 +1010,7 @@ int blr_norm_forward(int64_t M, int64_t d, int xt, int ft, int nt, const void *x
     if (!f && !n && !stats && !q) return BLR_ERR_NULL;
     if (!norm_types_ok(xt, ft, nt) || gate_kind < BLR_GATE_LINEAR || gate_kind > BLR_GATE_SILU) return BLR_ERR_DTYPE;
     if (!norm_shape_ok(M, d, span) || (q && d % 32)) return BLR_ERR_SHAPE;
+    if (!(eps >= 0.0f) || !isfinite(eps)) return BLR_ERR_SCALE;
     if (!aligned4(stats)) return BLR_ERR_ALIGN;
     if (!f) w_after = nullptr, gate = nullptr, norm_f = 0;
     if (span > M) span = M;

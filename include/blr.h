@@ -54,7 +54,7 @@ typedef enum {
     BLR_OK = 0,
     BLR_ERR_NULL = -1,      /* a required pointer is NULL */
     BLR_ERR_SHAPE = -2,     /* a size is out of range or breaks the multiple-of-128 rule */
-    BLR_ERR_SCALE = -3,     /* gscale is not a power of two from 2^-127 to 2^127 */
+    BLR_ERR_SCALE = -3,     /* gscale is not a power of two from 2^-127 to 2^127, or eps not finite and >= 0 */
     BLR_ERR_WORKSPACE = -4, /* workspace NULL or smaller than blr_workspace_bytes() */
     BLR_ERR_DEVICE = -5,    /* current device is not gfx950 */
     BLR_ERR_HIP = -6,       /* the HIP runtime reported an error */
@@ -341,7 +341,7 @@ typedef enum { BLR_GATE_LINEAR = 0, BLR_GATE_SIGMOID = 1, BLR_GATE_SILU = 2 } bl
  * the rows n that the next block reads are normed (root mean square):
  *   v = f rstd_f w_after (norm_f = 1) or f w_after (norm_f = 0)
  *   out = skip x + scale phi(z) v          n = out rstd w
- *   rstd = 1 / sqrt(mean(out^2) + eps), rstd_f of f likewise
+ *   rstd = 1 / sqrt(mean(out^2) + eps), rstd_f of f likewise; eps >= 0, finite
  * x, out have type xt, f and the gate z type ft, n type nt: xt = BLR_F32 with
  * any ft and nt, or all three the same 16-bit type. Weights are f32 [d], NULL
  * for ones.

@@ -4,7 +4,8 @@ import ctypes
 
 import binary_rank_linear_amd as blr
 from test_abi import E_SCALE, bwd, ptrs  # noqa: F401  (ptrs: a fixture)
-from test_block_abi import NO_GPU, gated_backward
+from test_block_abi import FWD, NO_GPU, call, gated_backward
+from test_operators_abi import F32
 
 # the least power of two whose inverse f32 holds is 2^-127; 2^-149 is f32's least
 SMALLEST, TOO_SMALL = 2.0 ** -127, (2.0 ** -128, 2.0 ** -140, 2.0 ** -149)
@@ -26,3 +27,17 @@ def test_a_scale_without_an_inverse(ptrs):  # noqa: F811
         assert gated_backward(gscale=s) in NO_GPU, s
         assert bwd(lib, 128, 256, 256, 128, ptrs, gscale=s) in NO_GPU, s
         assert plane(s, ptrs) in NO_GPU, s
+
+
+def test_eps():
+    """1 / sqrt(mean + eps) has no value for an eps below zero or NaN, and only
+    zero for an infinite one."""
+    def norm(eps):
+        return call("blr_norm_forward", (4, 64, F32, F32, F32, "x", None, 0, None, None, 0, 1, ctypes.c_float(1),
+                                         ctypes.c_float(1), "w", ctypes.c_float(eps), None, "n", "stats", None, None),
+                    FWD, {})
+
+    for eps in (-1e-6, -1.0, float("nan"), float("inf"), float("-inf")):
+        assert norm(eps) == E_SCALE, eps
+    for eps in (0.0, -0.0, 1e-45, 1e-6, 1.0):
+        assert norm(eps) in NO_GPU, eps
