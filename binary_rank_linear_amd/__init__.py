@@ -766,8 +766,18 @@ def blr_checkpoint_load(q, b, dtype, *, x=None, stream=None):
 GATE_LINEAR, GATE_SIGMOID, GATE_SILU = 0, 1, 2
 
 
+def _number(v, lo, hi, status, where):
+    """v in lo .. hi: ctypes cuts what C's type does not hold to its low bits."""
+    if not lo <= v <= hi:
+        raise BlrError(status, where)
+
+
+_SPAN = (1 << 63) - 1
+
+
 def workspace_norm(M: int, d: int, span: int = 1, device=None):
     import torch
+    _number(span, 1, _SPAN, -2, "blr_norm_workspace_bytes")
     n = int(load().blr_norm_workspace_bytes(M, d, span))
     if n == 0:
         raise BlrError(-2, "blr_norm_workspace_bytes")
@@ -793,6 +803,8 @@ def blr_norm_forward(x, f=None, w=None, *, norm_f=False, w_after=None, gate=None
     `keep` (or a pair `kept` to write to) the checkpoint of out, or of x without
     f, is formed too. Returns (out, n, stats, kept), None for what was not
     formed."""
+    _number(span, 1, _SPAN, -2, "blr_norm_forward")
+    _number(gate_kind, GATE_LINEAR, GATE_SILU, -9, "blr_norm_forward")
     code, M, d, dev = _rows(x, "x", stream)
     f32, _, wide, _, codes = _types()
     at_x = _at(x, "x", (x.dtype,), (M, d), dev)
@@ -804,8 +816,6 @@ def blr_norm_forward(x, f=None, w=None, *, norm_f=False, w_after=None, gate=None
         at_f = _at(f, "f", wide, (M, d), dev)
     elif out is not None or gate is not None or w_after is not None or norm_f:
         raise ValueError("out, gate, w_after and norm_f need f")
-    if span < 1:
-        raise BlrError(-2, "blr_norm_forward")
     if n_dtype not in codes:
         raise TypeError(f"n_dtype is {n_dtype}, expected one of {wide}")
     at_w, at_after, at_gate = _norm_columns(d, w, w_after, gate, -(-M // span), ft, dev)
@@ -836,6 +846,8 @@ def blr_norm_backward(dn, dout, out, f=None, w=None, stats=None, *, has_f=None, 
     the gradients of w, w_after and gate are formed where these are given and
     take part; overwritten unless accumulate_grads (dgate of span 1 always is).
     Returns (dx, df, dgate, dw, dw_after), None for what was not formed."""
+    _number(span, 1, _SPAN, -2, "blr_norm_backward")
+    _number(gate_kind, GATE_LINEAR, GATE_SILU, -9, "blr_norm_backward")
     f32, _, wide, _, codes = _types()
     rows, name = (dout, "dout") if dn is None else (dn, "dn")
     code, M, d, dev = _rows(rows, name, stream)
@@ -849,8 +861,6 @@ def blr_norm_backward(dn, dout, out, f=None, w=None, stats=None, *, has_f=None, 
     if (dw is not None and (w is None or dn is None)) or (dw_after is not None and w_after is None) or \
             (dgate is not None and gate is None):
         raise ValueError("dw needs w and dn, dw_after w_after, and dgate gate")
-    if span < 1:
-        raise BlrError(-2, "blr_norm_backward")
     nt = rows.dtype if dn is not None else None
     xt = dout.dtype if dout is not None else getattr(out, "dtype", None) or x_dtype
     ft = getattr(f, "dtype", None) or f_dtype or (xt if not has_f else None)
@@ -932,6 +942,7 @@ def blr_gated_forward(x, w_gate, w_up, *, kind=ACT_SILU, h_dtype=None, h=None, k
     (or a pair `tape` to write to) the two projections are kept in 8 bits for
     the backward: tape = (q [2][M][ff], b [2][M][ff / 32]). Returns (h, tape),
     tape None when not kept."""
+    _number(kind, ACT_SILU, ACT_GELU, -9, "blr_gated_forward")
     ff, d, t, code, dev, at_w = _gated_weights(w_gate, w_up, stream)
     codes = _types()[4]
     M = _shape(x, "x", 2)[0]
@@ -961,6 +972,7 @@ def blr_gated_backward(x, dh, w_gate, w_up, tape=None, *, kind=ACT_SILU, gscale=
     not given are allocated; overwritten unless accumulate_dx /
     accumulate_grads. Returns (dx, dw_gate, dw_up), None for what was not
     formed."""
+    _number(kind, ACT_SILU, ACT_GELU, -9, "blr_gated_backward")
     if (accumulate_grads and (dw_gate is None or dw_up is None)) or (accumulate_dx and dx is None):
         raise ValueError("what is accumulated into has to be given")
     if not grads and (dw_gate is not None or dw_up is not None):
