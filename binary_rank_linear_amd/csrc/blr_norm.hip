@@ -14,6 +14,8 @@
 // by lane moves, over the row's waves through LDS, in a fixed order. The forward
 // of 8192 x 4096, f32 stream and f, a gate a row, bf16 n takes 110 us (5.5 TB/s);
 // a 2 GiB copy runs at 4.9.
+#include <cfloat>
+
 #include "blr_internal.h"
 #include "blr_keep8.h"
 #include "blr_math.h"
@@ -53,7 +55,7 @@ __device__ __forceinline__ float phi(int kind, float z, float *slope) {
     const float e = exp_of(fabsf(z) > 200.0f ? -200.0f : -fabsf(z)), big = inverse(1.0f + e), small = e * big;
     const float s = z >= 0.0f ? big : small, r = big * small;
     *slope = kind == 1 ? r : r == 0.0f ? s : s + z * r;  // z may be infinite where r is zero
-    return kind == 1 ? s : z * s;
+    return kind == 1 ? s : fmaxf(z, -FLT_MAX) * s;  // and s zero where z is minus infinity
 }
 
 // phi of eight values, and their slopes where asked for, both times scale; the

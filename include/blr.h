@@ -332,7 +332,8 @@ int blr_adapters_backward(int64_t M, int64_t d_in, int64_t d_out, int64_t r, int
 int blr_checkpoint_save(int64_t M, int64_t d, int dtype, const void *x, int8_t *q, uint8_t *b, void *stream);
 int blr_checkpoint_load(int64_t M, int64_t d, int dtype, const int8_t *q, const uint8_t *b, void *x, void *stream);
 
-/* How a gate opens: phi(z) = z, 1 / (1 + exp(-z)), z / (1 + exp(-z)). */
+/* How a gate opens: phi(z) = z, 1 / (1 + exp(-z)), z / (1 + exp(-z)). At an
+ * infinite z phi and its slope are what they tend to: silu 0 at -inf. */
 typedef enum { BLR_GATE_LINEAR = 0, BLR_GATE_SIGMOID = 1, BLR_GATE_SILU = 2 } blr_gate;
 
 /*
