@@ -27,6 +27,7 @@
 // 8 and 14 % faster, no copies at all 15, 16 and 24 %: what is left is the matrix
 // units' own rate, the LDS's, and the ends of tiles. One row of 4096 -> 12288 takes
 // 40 us, its weights' bytes at 5.0 TB/s.
+#include <cfloat>
 #include <type_traits>
 
 #include "blr_internal.h"
@@ -68,7 +69,7 @@ __device__ __forceinline__ float act(float g, float *slope) {
     // far out the slope's second term is zero, whatever y has grown to
     const float r = big * small;
     *slope = r == 0.0f ? s : fmaf(g * dy, r, s);
-    return g * s;
+    return fmaxf(g, -FLT_MAX) * s;  // s is zero where g is minus infinity
 }
 // h = act(g) u of eight columns, in place of g. The kind is looked at once, so
 // that the eight go through the long chain side by side.

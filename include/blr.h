@@ -391,7 +391,8 @@ int blr_norm_backward(int64_t M, int64_t d, int xt, int ft, int nt, const void *
                       size_t workspace_bytes, void *stream);
 
 /* The gated feed-forward's activation: g / (1 + exp(-g)), or 0.5 g (1 +
- * tanh(sqrt(2 / pi) (g + 0.044715 g^3))). */
+ * tanh(sqrt(2 / pi) (g + 0.044715 g^3))). At an infinite g act and its slope
+ * are what they tend to: 0 at -inf. */
 typedef enum { BLR_ACT_SILU = 0, BLR_ACT_GELU = 1 } blr_act;
 
 /*
