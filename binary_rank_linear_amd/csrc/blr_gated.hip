@@ -84,14 +84,15 @@ __device__ __forceinline__ void products8(int kind, float *g, const float *u) {
     else
         all(std::false_type());
 }
-// dg = v u act'(g) and du = v act(g), in place of g and u.
+// dg = v u act'(g) and du = v act(g), in place of g and u. The slope is at most
+// 1.13, so that its product with u stays in range where v u may not.
 __device__ __forceinline__ void gradients8(int kind, const float *v, float *g, float *u) {
     auto all = [&](auto gelu) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float slope;
             const float a = act<decltype(gelu)::value>(g[i], &slope);
-            g[i] = v[i] * u[i] * slope;
+            g[i] = v[i] * (u[i] * slope);
             u[i] = v[i] * a;
         }
     };
