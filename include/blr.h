@@ -414,7 +414,9 @@ typedef enum { BLR_ACT_SILU = 0, BLR_ACT_GELU = 1 } blr_act;
  *   gscale, a power of two from 2^-127 to 2^127: dg and du are rounded to dtype
  *     times gscale, and the products after them are divided by it, as in
  *     blr_backward. In f16 it keeps small gradients out of the subnormals; in
- *     bf16 1 does.
+ *     bf16 1 does. dg or du times gscale past dtype's largest value (65504 in
+ *     f16) is infinite, as in blr_backward: its row of dx, and the weights'
+ *     gradients, are then not finite, and gscale is too large.
  *   dx or the pair dw_gate, dw_up may be NULL (not formed). accumulate_dx and
  *     accumulate_grads = 0 overwrite, 1 adds (in f32, then rounds).
  * d, ff multiples of 128 up to 2^20, 1 <= M < 2^31 - 65536, with (M / 128)
