@@ -8,8 +8,10 @@
 //
 // Products of 16-bit values are exact in the matrix instructions' f32 sums. D
 // is rounded to the rows' type once (times gscale, as f16 needs it for small
-// gradients): the products after it are of 16 bits, and its rounding is of
-// the size of the results' own.
+// gradients): the products after it are of 16 bits. Its rounding, 1.7e-3 (bf16)
+// or 2.1e-4 (f16) of a gradient in the 2-norm, is of the size of 16-bit results'
+// own, which are off by 2.3e-3 or 2.9e-4 in all; in f32 gradients it is what
+// is left.
 //
 // All three contractions are one kernel over tiles in LDS, bound by the matrix
 // units. An operand lies in memory with the contracted index innermost (x and
@@ -21,12 +23,14 @@
 // the first kind's reads over all banks; the second's of n take half the banks
 // at a time (a quarter of dx's and dw's LDS cycles, by the counters).
 //
-// 8192 rows of bf16, 4096 -> 12288, HIP events: forward 1.30 ms (1.27 PFLOP/s; the
-// library's product without the activation 1.29), dx 1.21 (1.36; 1.32), the weights'
-// gradients 1.32 (1.25; 1.15). Copies that always come out of L2 would make them 5,
+// 8192 rows of bf16, 4096 -> 12288, HIP events: forward 1.31 ms (1.26 PFLOP/s; the
+// library's product without the activation 1.29), dx 1.20 (1.37; 1.32), the weights'
+// gradients 1.31 (1.26; 1.15); f16 1.37, 1.26 and 1.36. 30000 x 5120 -> 17408, bf16:
+// 8.6 ms (1.24), 9.2 with a tape (1.16), dx 8.8 (1.21), the weights' 9.2 (1.16). Some
+// cards are 5 % slower in all of them. Copies that always come out of L2 would make them 5,
 // 8 and 14 % faster, no copies at all 15, 16 and 24 %: what is left is the matrix
 // units' own rate, the LDS's, and the ends of tiles. One row of 4096 -> 12288 takes
-// 40 us, its weights' bytes at 5.0 TB/s.
+// 39 us, its weights' bytes at 5.2 TB/s, one of 5120 -> 17408 84 (4.2).
 #include <cfloat>
 #include <type_traits>
 
@@ -537,6 +541,9 @@ int64_t tiles(int64_t m, int64_t n, int64_t bm, int64_t bn) { return (m + bm - 1
 //   64 x 64, 4 buffers     15  30  41  54  79    256 x 256   46  53  --  --  57
 //   64 x 128, 2 buffers    22  24  31  47  59
 //   128 x 128, 2 buffers   25  30  32  34  53
+// Up to 64 rows the first line ends at ff = 16384. Past it, the first two, bf16:
+// 5120 -> 17408 82 against 84 (1 row), 94 against 97 (64); 8192 -> 28672 171 against 174
+// and 187 against 169.
 template <typename T, Role R>
 hipError_t contract(int id, GatedGemm a, hipStream_t s) {
     constexpr bool gated = R == FORWARD || R == AGAIN;

@@ -5,8 +5,9 @@
 
 namespace blr {
 
-// exp(v) to about 1e-7: the product with log2(e) is kept to twice its length,
-// whose tail enters as 1 + tail ln 2.
+// exp(v) to about 1e-7, and zero below -87.4, where it would be subnormal: the
+// product with log2(e) is kept to twice its length, whose tail enters as 1 +
+// tail ln 2.
 __device__ __forceinline__ float exp_of(float v) {
     const float L = 1.44269504088896340736f;
     const float t = v * L, tail = fmaf(v, L, -t) + v * 1.92596299112661746887e-8f;

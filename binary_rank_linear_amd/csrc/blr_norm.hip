@@ -12,8 +12,8 @@
 // thread 8 C of its columns, in registers from the load to the last store, so
 // that every array crosses memory once. Sums over a row are f32: along a wave
 // by lane moves, over the row's waves through LDS, in a fixed order. The forward
-// of 8192 x 4096, f32 stream and f, a gate a row, bf16 n takes 110 us (5.5 TB/s);
-// a 2 GiB copy runs at 4.9.
+// of 8192 x 4096, f32 stream and f, a gate a row, bf16 n takes 110 us (18 bytes a
+// value, 5.5 TB/s); a 2 GiB copy runs at 5.0.
 #include <cfloat>
 
 #include "blr_internal.h"
@@ -44,8 +44,8 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // phi(z) and its slope. With e = exp(-|z|), 1 / (1 + e) and e / (1 + e) are
-// sigmoid(|z|) and sigmoid(-|z|), so that s (1 - s) loses nothing at the far
-// ends, and nothing overflows.
+// sigmoid(|z|) and sigmoid(-|z|), so that s (1 - s) loses nothing far out (it is
+// zero where e is), and nothing overflows.
 __device__ __forceinline__ float phi(int kind, float z, float *slope) {
     if (kind == 0) {
         *slope = 1.0f;
@@ -304,8 +304,11 @@ __device__ __forceinline__ void put_sums(float *p, const float *v, bool add) {
 // thread that is more than the 128 registers of 16 waves on a CU, and the row is
 // read a second time, out of the caches. AHEAD: the next row is loaded
 // meanwhile, which leaves no room for a gate.
-// 8192 x 4096, f32 stream and f, bf16 n: 117 us from checkpoints (4.3 TB/s), 152 from
-// rows (4.6), 227 with a gate a row (4.3).
+// 8192 x 4096, f32 stream and f, bf16 n, the bytes of its rows: 117 us from
+// checkpoints (16.06 bytes a value, 4.6 TB/s), 152 from rows (22, 4.8), 225 with a
+// gate a row (30, 4.5); the finish takes 7 to 9 more. Wider rows are slower: 5120 bf16
+// columns, ten of a CU's sixteen waves, 3.8 TB/s; 8192 f32 with a gate, 36 registers
+// in memory, 640 us (3.1); 2048 x 16384 f32 with a gate, 168 of them, 680 us (1.5).
 template <typename XT, typename FT, typename NT, int C, bool GATE, int WAVES = MAX_WAVES>
 __global__ __launch_bounds__(64 * WAVES) void norm_backward_kernel(NormBackward a) {
     constexpr bool HOLD = C == 1, AHEAD = HOLD && !GATE;
